@@ -416,6 +416,166 @@ ttt_status ttt_lm_target(const ttt_desc* desc, const void* X0,
                          void* V, void* workspace, size_t workspace_bytes,
                          void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder block: rotary positions, a paged key/value
+ * cache held in 4 bits, and attention over it. Conventions (validation before
+ * any launch, asynchrony, no allocation, errors, aliasing) as above.
+ *
+ * Rows of heads: element i of head h of token n is data[n * token_stride +
+ * h * head_stride + i], in elements of act_dtype; both strides are multiples
+ * of 16 bytes (parts of a fused projection, head-major tensors and, for
+ * inputs, strides of 0 are all fine). Outputs may not overlap themselves. */
+typedef struct ttt_rows {
+  void* data;            /* 16-byte aligned */
+  int64_t token_stride;  /* elements */
+  int64_t head_stride;   /* elements */
+  int32_t heads;         /* 1 .. 1024 */
+  int32_t reserved;      /* must be 0 */
+} ttt_rows;
+
+/* Rotary positions. Pair i of a head's first rot_dim values is turned by the
+ * angle pos * w_i: (a, b) -> (a c - b s, b c + a s). Pairs are the halves
+ * (i, i + rot_dim / 2), or with TTT_ROPE_INTERLEAVED the neighbours
+ * (2i, 2i + 1). Values from rot_dim on are copied. c and s come from a
+ * caller-owned fp32 table [max_pos][rot_dim / 2][2] of (cos, sin); a position
+ * outside [0, max_pos) gives NaN in the rotated values. */
+enum { TTT_ROPE_INTERLEAVED = 1u << 0 };
+typedef struct ttt_rope {
+  const float* table;
+  int32_t rot_dim;       /* a multiple of 16, at most head_dim */
+  int32_t max_pos;
+  uint32_t flags;        /* TTT_ROPE_* */
+  uint32_t reserved;     /* must be 0 */
+} ttt_rope;
+
+/* Fills a table (in 64 bits, rounded once): w_i = base^(-2i / rot_dim), and
+ * for contexts longer than the trained one
+ *   LINEAR  w_i / factor
+ *   BASE    base * factor^(rot_dim / (rot_dim - 2)) in base's place
+ *   YARN    w_i for pairs that turn more than `high` times over `original`
+ *           positions, w_i / factor below `low` turns, and between (as whole
+ *           pair indices, rounded outwards) a linear mix in i
+ *   BANDS   the same ends, and between a mix linear in the pair's turns
+ * Every cos and sin is multiplied by amplitude (1 without scaling).
+ *   scaling may be NULL (PLAIN); rot_dim a multiple of 16, at most 1024 */
+typedef enum ttt_rope_kind {
+  TTT_ROPE_PLAIN = 0, TTT_ROPE_LINEAR = 1, TTT_ROPE_BASE = 2, TTT_ROPE_YARN = 3, TTT_ROPE_BANDS = 4
+} ttt_rope_kind;
+typedef struct ttt_rope_scaling {
+  int32_t kind;          /* ttt_rope_kind */
+  int32_t reserved;      /* must be 0 */
+  double factor;         /* >= 1 */
+  double original;       /* trained context, for YARN and BANDS */
+  double low, high;      /* turns, 0 < low < high, for YARN and BANDS */
+  double amplitude;      /* > 0 */
+} ttt_rope_scaling;
+ttt_status ttt_rope_table(float* table, int32_t max_pos, int32_t rot_dim, double base,
+                          const ttt_rope_scaling* scaling, void* stream);
+
+/* Rotates queries and keys in one launch.
+ *   tokens     rows of q and k; 0 is a valid call that does nothing
+ *   positions  [tokens] int32, or NULL: row n stands at n % seq_len
+ *   head_dim   a multiple of 16, at most 1024
+ *   k, k_out   may be NULL together
+ * An output may be its own input (same data and strides). The products are
+ * rounded to fp32 before they are added; the result is rounded once. The
+ * backward takes the gradients of the outputs and writes those of the inputs
+ * (the transposed rotation; the table gets no gradient). */
+ttt_status ttt_rope_forward(int32_t tokens, int32_t seq_len, int32_t head_dim, int32_t act_dtype,
+                            const ttt_rope* rope, const int32_t* positions, const ttt_rows* q,
+                            const ttt_rows* k, const ttt_rows* q_out, const ttt_rows* k_out,
+                            void* stream);
+ttt_status ttt_rope_backward(int32_t tokens, int32_t seq_len, int32_t head_dim, int32_t act_dtype,
+                             const ttt_rope* rope, const int32_t* positions, const ttt_rows* dq_out,
+                             const ttt_rows* dk_out, const ttt_rows* dq, const ttt_rows* dk,
+                             void* stream);
+
+/* The cache. A pool of n_pages pages of page_size tokens; page p of sequence
+ * b is page_table[b][p]. An entry outside [0, n_pages) is no page: what would
+ * go there is not written, and no row sees its tokens. kv_lens[b] counts
+ * sequence b's tokens, this call's included; its new tokens are rows
+ * q_starts[b] .. q_starts[b + 1] - 1 and stand at the end of its kv_lens[b].
+ * These four arrays are device memory, read while the kernels run. Rows that
+ * no sequence claims are not appended, and their outputs are unspecified.
+ *
+ * A value is held as a sign and one of 0, .5, 1, 1.5, 2, 3, 4, 6 times a
+ * power of two that 32 neighbouring values of a head share (the 4-bit E2M1
+ * blocks of the OCP Microscaling formats: 4.25 bits a value). The power is
+ * the least 2^e, -125 <= e <= 125, with max |x| <= 7 * 2^e; values are
+ * rounded to nearest, ties to the even code, saturating. A NaN or an infinity
+ * anywhere in a token's head makes that whole head vector NaN.
+ *
+ * Inside a page every head has its own block of page_size * (D + D / 16)
+ * bytes, D = head_dim:
+ *   K codes   [page_size][D / 2]            byte j: value 2j low, 2j + 1 high
+ *   V codes   [page_size / 4][D / 8][4][4]  of four tokens: 8 values of each
+ *   K scales  [page_size][D / 32]           e + 127; above 252: NaN
+ *   V scales  [D / 32][page_size] */
+typedef struct ttt_cache {
+  void* pages;                /* 16-byte aligned */
+  int64_t page_stride;        /* bytes, a multiple of 16, >= ttt_kv_page_bytes() */
+  const int32_t* page_table;  /* [batch][max_pages] */
+  const int32_t* kv_lens;     /* [batch] */
+  const int32_t* q_starts;    /* [batch + 1], or NULL: tokens / batch each */
+  int32_t batch, max_pages, n_pages;
+  int32_t page_size;          /* a multiple of 16, at most 4096 */
+  int32_t kv_heads;
+  int32_t head_dim;           /* 64, 128 or 256 */
+  int32_t reserved;           /* must be 0 */
+} ttt_cache;
+ttt_status ttt_kv_page_bytes(int32_t page_size, int32_t kv_heads, int32_t head_dim, size_t* bytes);
+
+/* Appends the new tokens' keys and values, the keys rotated on the way, and
+ * rotates the queries beside them.
+ *   rope       NULL: no rotation (keys already rotated, or none wanted)
+ *   positions  [tokens] int32, or NULL: the token's index in its sequence
+ *   q, q_out   NULL together, or rotated as ttt_rope_forward does (q_out may
+ *              be q); needs rope */
+ttt_status ttt_kv_append(const ttt_cache* cache, int32_t tokens, int32_t act_dtype,
+                         const ttt_rows* k, const ttt_rows* v, const ttt_rows* q,
+                         const ttt_rows* q_out, const ttt_rope* rope, const int32_t* positions,
+                         void* stream);
+
+/* What the cache holds of the same tokens (those that ttt_kv_append with
+ * these arrays has written): exact in either type, 0 where there is no page. */
+ttt_status ttt_kv_read(const ttt_cache* cache, int32_t tokens, int32_t act_dtype,
+                       const ttt_rows* k_out, const ttt_rows* v_out, void* stream);
+
+/* Attention of the new tokens' rows over the cache. Row t of sequence b
+ * (t < new = q_starts[b + 1] - q_starts[b]) stands at position kv_lens[b] -
+ * new + t and sees the keys up to its own position, with window > 0 the last
+ * `window` of them only; with TTT_ATTN_ALL_KEYS every key of the sequence.
+ * Query head h reads kv head h / (q heads / kv heads).
+ *   o    softmax(scale q k^T) v, act_dtype
+ *   lse  [tokens][q heads] fp32, or NULL: log of the sum of exponentials
+ * A row that sees nothing gives o = 0 and lse = -inf. A NaN or infinity that a
+ * row does not see does not reach it.
+ *   max_new  an upper bound of the sequences' new tokens, and
+ *   max_kv   of their kv_lens: they size the launch; wrong ones cost time,
+ *            not results
+ *   workspace  ttt_kv_attention_workspace_size() bytes, 256-byte aligned (may
+ *            be NULL where that is 0)
+ * Arithmetic: products of bf16 operands accumulated in fp32 (the cache's
+ * values are exact in bf16). For bf16 rows the weights are rounded to bf16
+ * before they meet the values; for fp32 rows queries and weights enter as
+ * three bf16 terms each (24 bits). Maxima, sums and joins are fp32, in a fixed
+ * order. */
+enum { TTT_ATTN_ALL_KEYS = 1u << 0 };
+typedef struct ttt_attn {
+  float scale;
+  int32_t window;        /* 0: none */
+  int32_t max_new;       /* >= 1 */
+  int32_t max_kv;        /* >= 1 */
+  uint32_t flags;        /* TTT_ATTN_* */
+  uint32_t reserved;     /* must be 0 */
+} ttt_attn;
+ttt_status ttt_kv_attention_workspace_size(const ttt_attn* attn, int32_t batch, int32_t tokens,
+                                           int32_t kv_heads, int32_t q_heads, int32_t head_dim,
+                                           size_t* bytes);
+ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_t tokens,
+                            int32_t act_dtype, const ttt_rows* q, const ttt_rows* o, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* The name of a status code ("TTT_OK", "TTT_ERR_INVALID_ARG", ...; codes
  * outside ttt_status give "TTT_ERR_UNKNOWN"). The string is static. */
 const char* ttt_status_string(int32_t status);

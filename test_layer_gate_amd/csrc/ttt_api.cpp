@@ -351,6 +351,12 @@ namespace tttk_api {
 __attribute__((visibility("hidden"))) ttt_status set_error(ttt_status s, const std::string& msg) {
   return fail(s, msg);
 }
+// One of their launches, timed like this file's own.
+__attribute__((visibility("hidden"))) hipError_t timed_launch(const char* name, hipStream_t s,
+                                                              hipError_t (*launch)(const void*, hipStream_t),
+                                                              const void* args) {
+  return timed(name, s, [&]() { return launch(args, s); });
+}
 }  // namespace tttk_api
 
 extern "C" {

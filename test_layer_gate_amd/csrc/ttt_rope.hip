@@ -1,0 +1,141 @@
+// gfx950 kernels of the rotary positions: y = R(pos) x on the first `rot`
+// values of every head, its transpose for the gradient, and the table of
+// cosines and sines they read.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ttt_serve_device.h"
+
+namespace tttk {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+// A unit is 16 values of one head: 8 pairs of the rotated part (halves i and
+// i + rot / 2, or 16 neighbours), or 16 values of the part that is copied. A
+// thread takes one unit of a token and walks over heads with it, so that the
+// 8 cosines and sines (64 bytes) are loaded once for them. Bound by HBM: each
+// value is read once and written once, in 16-byte pieces.
+template <bool F32>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeLaunch a, int units, int lanes,
+                                                            int64_t total) {
+  const int64_t id = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+  if (id >= total) return;
+  const int u = (int)(id % units);
+  const int64_t r = id / units;
+  const int h0 = (int)(r % lanes);
+  const int n = (int)(r / lanes);
+  const RopeArgs& rope = a.rope;
+  const int rot_units = rope.rot >> 4;
+  const bool turned = u < rot_units;
+  // first and second 8 values of the unit
+  const int i0 = !turned ? u * 16 : rope.interleaved ? u * 16 : u * 8;
+  const int i1 = !turned || rope.interleaved ? i0 + 8 : i0 + (rope.rot >> 1);
+  float c[8], s[8];
+  if (turned) {
+    const int pos = a.positions ? a.positions[n] : n % a.seq_len;
+    load_cs8(rope, pos, u * 8, c, s);
+  }
+  const int heads = a.x[0].heads + a.x[1].heads;
+  for (int h = h0; h < heads; h += lanes) {
+    const int t = h >= a.x[0].heads;
+    const int hh = t ? h - a.x[0].heads : h;
+    const int64_t xi = n * a.x[t].ts + hh * a.x[t].hs, yi = n * a.y[t].ts + hh * a.y[t].hs;
+    float p[8], q[8];
+    load8<F32>(a.x[t].p, xi + i0, p);
+    load8<F32>(a.x[t].p, xi + i1, q);
+    if (turned) {
+      if (rope.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          turn(p[2 * e], p[2 * e + 1], c[e], s[e], &p[2 * e], &p[2 * e + 1]);
+          turn(q[2 * e], q[2 * e + 1], c[4 + e], s[4 + e], &q[2 * e], &q[2 * e + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn(p[e], q[e], c[e], s[e], &p[e], &q[e]);
+      }
+    }
+    store8<F32>(a.y[t].p, yi + i0, p);
+    store8<F32>(a.y[t].p, yi + i1, q);
+  }
+}
+
+// The angle step of pair i: w = base^(-2i / rot), changed for long contexts.
+//   1 linear: w / factor
+//   2 by base: base * factor^(rot / (rot - 2)), which leaves the fastest pair
+//     alone and divides the slowest one's step by factor
+//   3 by parts (YaRN): pairs that turn more than `hi` times over the original
+//     context keep w, those below `lo` turns take w / factor, a linear ramp
+//     in the pair's index lies between
+//   4 bands: the same two ends by wavelength (orig / hi and orig / lo), a
+//     linear ramp in orig / wavelength between
+__device__ double angle_step(int i, int rot, double base, int kind, double factor, double orig,
+                             double lo, double hi) {
+  const double two_pi = 6.283185307179586476925286766559;
+  if (kind == 2) base *= pow(factor, (double)rot / (rot - 2));
+  const double w = pow(base, -2.0 * i / rot);
+  if (kind == 1) return w / factor;
+  if (kind == 3) {
+    // the (real) index of the pair that turns r times: w orig = 2 pi r
+    const double lg = log(base);
+    double first = floor(rot * log(orig / (hi * two_pi)) / (2 * lg));
+    double last = ceil(rot * log(orig / (lo * two_pi)) / (2 * lg));
+    first = fmax(first, 0.0);
+    last = fmin(last, rot - 1.0);
+    if (first == last) last += 0.001;
+    const double ramp = fmin(fmax((i - first) / (last - first), 0.0), 1.0);
+    return w * (1.0 - ramp) + w / factor * ramp;
+  }
+  if (kind == 4) {
+    const double turns = orig * w / two_pi;
+    if (turns > hi) return w;
+    if (turns < lo) return w / factor;
+    const double keep = (turns - lo) / (hi - lo);
+    return (1.0 - keep) * w / factor + keep * w;
+  }
+  return w;
+}
+
+// Angles and their functions in 64 bits: pos * w reaches 10^6 rad, where a
+// 32-bit product is off by several hundredths. Run once for a model.
+__global__ __launch_bounds__(kRopeThreads) void rope_table_kernel(
+    float* __restrict__ table, int64_t total, int half, int rot, double base, int kind,
+    double factor, double orig, double lo, double hi, double mul) {
+  const int64_t id = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+  if (id >= total) return;
+  const int i = (int)(id % half);
+  const double w = angle_step(i, rot, base, kind, factor, orig, lo, hi);
+  double s, c;
+  sincos((double)(id / half) * w, &s, &c);
+  table[2 * id] = (float)(c * mul);
+  table[2 * id + 1] = (float)(s * mul);
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeLaunch& a, hipStream_t s) {
+  const int units = a.dim / 16, heads = a.x[0].heads + a.x[1].heads;
+  // Heads that a thread walks over: as many as leave the chip full.
+  int lanes = heads;
+  const int64_t one = (int64_t)a.tokens * units;
+  while (lanes > 1 && one * ((lanes + 1) / 2) >= (int64_t)256 * 2048) lanes = (lanes + 1) / 2;
+  const int64_t total = one * lanes;
+  const int64_t grid = (total + kRopeThreads - 1) / kRopeThreads;
+  if (a.f32)
+    rope_kernel<true><<<(uint32_t)grid, kRopeThreads, 0, s>>>(a, units, lanes, total);
+  else
+    rope_kernel<false><<<(uint32_t)grid, kRopeThreads, 0, s>>>(a, units, lanes, total);
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_table(float* table, int max_pos, int rot, double base, int kind,
+                             double factor, double orig, double lo, double hi, double mul,
+                             hipStream_t s) {
+  const int64_t total = (int64_t)max_pos * (rot / 2);
+  rope_table_kernel<<<(uint32_t)((total + kRopeThreads - 1) / kRopeThreads), kRopeThreads, 0, s>>>(
+      table, total, rot / 2, rot, base, kind, factor, orig, lo, hi, mul);
+  return hipGetLastError();
+}
+
+}  // namespace tttk

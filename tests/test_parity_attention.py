@@ -1,0 +1,241 @@
+"""GPU parity of attention over the paged 4-bit cache against the float64
+oracle on the same cache bytes.
+
+Tolerances (per output value, w = sum_j p_j |v_j| from the oracle). A weight
+p_j carries the relative error of its exponent: a score is a sum of D exact
+products (bf16 times bf16) accumulated in fp32, so at most D 2^-24 sum |q k|
+scale, typically its square root; then the exponential's own 2^-22. Rounding
+p to bf16 (8 significant bits) is at most 2^-8 of it, the output's own rounding
+2^-8 of the value. fp32
+rows take neither; their three-term queries and weights leave 2^-24 each.
+Accumulating n weighted values in fp32 adds at most 2^-24 n w, typically its
+square root (held to 4 sqrt(n) below)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.serve_oracle as so
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ttt():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test run without a GPU")
+    import test_layer_gate_amd as m
+    m.lib()
+    return m
+
+
+def host(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def pool_of(rng, lens, page, hk, dim, garbage=True):
+    """Pages holding Gaussian keys and values; whatever no token fills is
+    random bytes, NaN scales among them."""
+    need = [-(-int(x) // page) for x in lens]
+    n_pages = sum(need) + 2
+    ids = rng.permutation(n_pages)
+    table = np.full((len(lens), max(max(need), 1)), -1, np.int64)
+    at = 0
+    pages = rng.integers(0, 256, (n_pages, hk, page * dim * 17 // 16)).astype(np.uint8)
+    for b, m in enumerate(need):
+        table[b, :m] = ids[at:at + m]
+        at += m
+    k = [rng.standard_normal((int(x), hk, dim)) * (1 + 2 * (rng.random((1, hk, dim)) > 0.95))
+         for x in lens]
+    v = [rng.standard_normal((int(x), hk, dim)) for x in lens]
+    where = [(b, j) for b, x in enumerate(lens) for j in range(int(x))]
+    if where:
+        pages = so.put(pages, table, where, np.concatenate(k), np.concatenate(v))
+    return pages, table
+
+
+def check(ttt, dtype, page, hk, hq, dim, news, lens, *, window=0, causal=True, seed=0, sharp=1.5,
+          pages=None, table=None, q=None, no_starts=False, **kw):
+    rng = np.random.default_rng(seed)
+    if pages is None:
+        pages, table = pool_of(rng, lens, page, hk, dim)
+    n = sum(news)
+    if q is None:
+        q = torch.from_numpy(sharp * rng.standard_normal((n, hq, dim))).to(dtype).cuda()
+    starts = np.concatenate([[0], np.cumsum(news)])
+    scale = dim ** -0.5
+    o, lse = ttt.kv_attention(q, torch.from_numpy(pages).cuda(), ints(table), ints(lens),
+                              q_starts=None if no_starts else ints(starts), window=window,
+                              causal=causal, with_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert o.dtype == dtype and o.shape == q.shape
+    o, lse, qh = host(o), host(lse), host(q)
+    for b, (m, length) in enumerate(zip(news, lens)):
+        r = slice(starts[b], starts[b + 1])
+        k, v, have = so.gather(pages, table, b, int(length), dim)
+        ref, lref, w = so.attend(qh[r], k, v, have, int(length), scale, window, causal)
+        ks = np.abs(np.nan_to_num(k)).repeat(hq // hk, 1)
+        terms = scale * np.einsum("thd,jhd->thj", np.abs(qh[r]), ks).max(-1) if length else 0.0
+        rel = (4 * np.sqrt(dim) * 2 ** -24 * terms + 2 ** -21 + 4 * np.sqrt(max(length, 1)) * 2 ** -24)
+        rel = np.broadcast_to(rel, lref.shape)
+        tol = (rel[..., None] + (2 ** -8 if dtype == BF else 2 ** -23)) * w
+        tol = tol + (2 ** -8 * 1.01 if dtype == BF else 2 ** -23) * np.abs(ref) + 1e-30
+        assert np.array_equal(np.isnan(o[r]), np.isnan(ref)), b
+        err = np.abs(o[r] - ref)
+        assert not (err > tol).any(), (b, float(np.nanmax(err / tol)), np.argwhere(err > tol)[:3])
+        empty = np.isneginf(lref)
+        assert np.array_equal(np.isneginf(lse[r]), empty)
+        assert not o[r][empty].any()
+        d = np.abs(lse[r] - lref)[~empty & ~np.isnan(lref)]
+        room = (rel + 2 ** -22 * (1 + np.abs(lref)))[~empty & ~np.isnan(lref)]
+        assert (d <= room).all(), (b, float((d / room).max()))
+    return o
+
+
+LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 255, 300]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_single_tokens_of_every_length(ttt, dtype, dim):
+    check(ttt, dtype, 32, 2, 8, dim, [1] * len(LENGTHS), LENGTHS, no_starts=True)
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 112, 256])
+@pytest.mark.parametrize("hk,hq", [(1, 1), (2, 2), (1, 5), (2, 32), (1, 17), (4, 8)])
+def test_head_layouts_and_pages(ttt, page, hk, hq):
+    check(ttt, BF, page, hk, hq, 128, [1, 3, 1], [200, 77, 513], seed=page + hq)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim,hk,hq", [(64, 2, 4), (128, 1, 4), (128, 2, 10), (256, 1, 3)])
+@pytest.mark.parametrize("news,lens", [
+    ([5], [5]), ([64], [64]), ([65, 1, 130], [65, 100, 260]), ([100, 33], [333, 33]),
+    ([257], [700])])
+def test_segments(ttt, dtype, dim, hk, hq, news, lens):
+    check(ttt, dtype, 48, hk, hq, dim, news, lens, seed=dim + sum(news))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [1, 2, 31, 64, 100, 5000])
+def test_windows(ttt, dtype, window):
+    check(ttt, dtype, 32, 2, 8, 128, [70, 1, 1, 9], [300, 300, 40, 9], window=window, seed=window)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_all_keys(ttt, dtype):
+    check(ttt, dtype, 32, 2, 4, 64, [70, 1, 9], [300, 40, 9], causal=False)
+    check(ttt, dtype, 32, 2, 4, 128, [130, 3], [130, 300], causal=False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_that_see_nothing(ttt, dtype, dim):
+    """No keys, fewer keys than rows, no rows, and rows whose pages are gone."""
+    check(ttt, dtype, 16, 2, 4, dim, [3, 20, 0, 1, 40], [0, 7, 50, 1, 3], seed=3)
+    rng = np.random.default_rng(4)
+    pages, table = pool_of(rng, [100, 200], 32, 2, dim)
+    table[0, :] = -1                   # the whole sequence
+    table[1, :5] = [-1, 99, -1, -1, -7]   # everything but the last 40 tokens
+    check(ttt, dtype, 32, 2, 4, dim, [50, 70], [100, 200], pages=pages, table=table)
+    check(ttt, dtype, 32, 2, 4, dim, [1, 1], [100, 200], pages=pages, table=table, window=64)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news,where", [([1], [70]), ([40], [170, 185]), ([200], [3, 100, 199])])
+def test_nan_reaches_only_the_rows_that_see_it(ttt, dtype, dim, news, where):
+    length = 200
+    for part in ("k", "v"):
+        rng = np.random.default_rng(5)
+        pages, table = pool_of(rng, [length], 16, 1, dim)
+        k, v = (rng.standard_normal((length, 1, dim)) for _ in range(2))
+        for j in where:
+            (k if part == "k" else v)[j, 0, dim // 2] = np.nan
+        pages = so.put(pages, table, [(0, j) for j in range(length)], k, v)
+        o = check(ttt, dtype, 16, 1, 4, dim, news, [length], pages=pages, table=table)
+        first = min(where)
+        seen = np.arange(length - news[0], length) >= first
+        assert np.isnan(o[seen]).all() and np.isfinite(o[~seen]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_caches_and_sharp_rows(ttt, dtype):
+    """Long enough to be split over many workgroups; rows that all but pick
+    one key, and rows over scores of hundreds."""
+    check(ttt, dtype, 64, 1, 4, 128, [1], [9001], seed=1)
+    check(ttt, dtype, 64, 1, 4, 128, [3], [2500], seed=2, sharp=30.0)
+    check(ttt, dtype, 64, 2, 4, 64, [1, 1], [4097, 5], seed=3, sharp=300.0)
+
+
+def test_bounds_are_hints(ttt):
+    """max_new and max_kv size the launch; wrong ones change no result."""
+    rng = np.random.default_rng(6)
+    pages, table = pool_of(rng, [3000, 40], 64, 2, 128)
+    for kw in (dict(max_new=1, max_kv=1), dict(max_new=64, max_kv=64), dict(max_new=9999, max_kv=10 ** 8)):
+        check(ttt, BF, 64, 2, 8, 128, [37, 5], [3000, 40], pages=pages, table=table, **kw)
+
+
+def test_strided_rows_other_streams_and_outputs(ttt):
+    rng = np.random.default_rng(7)
+    pages, table = pool_of(rng, [500, 61], 64, 2, 128)
+    x = torch.from_numpy(rng.standard_normal((50, 12, 128))).to(BF).cuda()
+    q = x[:, :8]
+    ref = check(ttt, BF, 64, 2, 8, 128, [45, 5], [500, 61], pages=pages, table=table, q=q)
+    p, t, n, st = torch.from_numpy(pages).cuda(), ints(table), ints([500, 61]), ints([0, 45, 50])
+    out = torch.full((8, 50, 128), 7.0, dtype=BF, device="cuda")     # head-major
+    ws = torch.empty(ttt.kv_attention_workspace_size(2, 50, 2, 8, 128, max_new=50, max_kv=t.shape[1] * 64),
+                     dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = ttt.kv_attention(q, p, t, n, q_starts=st, out=out.transpose(0, 1), workspace=ws, stream=s)
+    s.synchronize()
+    assert np.array_equal(host(got), ref)
+    e = ttt.kv_attention(q[:0], p, t, n, q_starts=ints([0, 0, 0]))
+    assert e.shape == (0, 8, 128)
+
+
+def test_captured_step_follows_the_lengths(ttt):
+    """Append and attention of one token in a graph: each replay reads the
+    lengths, pages and rows as they are then."""
+    hk, hq, dim, page = 2, 8, 128, 16
+    rng = np.random.default_rng(8)
+    pages = ttt.kv_pages(9, page, hk, dim)
+    table = ints([[4, 2, 7, 0], [1, 8, 3, 5]])
+    rope = ttt.rope_table(64, dim, 1e4)
+    xs = torch.from_numpy(rng.standard_normal((40, 2, hq + 2 * hk, dim))).to(BF).cuda()
+    x, lens = xs[0].clone(), ints([1, 3])
+    ws = torch.empty(max(1, ttt.kv_attention_workspace_size(2, 2, hk, hq, dim, max_new=1, max_kv=64)),
+                     dtype=torch.uint8, device="cuda")
+    q, o = torch.empty((2, 2, hq, dim), dtype=BF, device="cuda")
+
+    def step(pool):
+        ttt.kv_append(pool, table, lens, x[:, hq:hq + hk], x[:, hq + hk:], q=x[:, :hq],
+                      rope_table=rope, q_out=q)
+        ttt.kv_attention(q, pool, table, lens, max_kv=64, out=o, workspace=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(pages)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(pages)
+    pages.zero_()
+    eager = ttt.kv_pages(9, page, hk, dim)
+    for t in range(40):
+        x.copy_(xs[t])
+        lens.copy_(ints([t + 1, t + 3]))
+        g.replay()
+        torch.cuda.synchronize()
+        got = o.clone()
+        o.zero_()
+        step(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(got, o), t
+        assert torch.equal(pages, eager), t
