@@ -570,8 +570,8 @@ typedef struct ttt_attn {
   uint32_t reserved;     /* must be 0 */
 } ttt_attn;
 ttt_status ttt_kv_attention_workspace_size(const ttt_attn* attn, int32_t batch, int32_t tokens,
-                                           int32_t kv_heads, int32_t q_heads, int32_t head_dim,
-                                           size_t* bytes);
+                                           int32_t act_dtype, int32_t kv_heads, int32_t q_heads,
+                                           int32_t head_dim, size_t* bytes);
 ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_t tokens,
                             int32_t act_dtype, const ttt_rows* q, const ttt_rows* o, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream);

@@ -64,7 +64,7 @@ def _L():
     L.ttt_kv_page_bytes.argtypes = [_I, _I, _I, Z]
     L.ttt_kv_append.argtypes = [C, _I, _I, R, R, R, R, T, _P, _P]
     L.ttt_kv_read.argtypes = [C, _I, _I, R, R, _P]
-    L.ttt_kv_attention_workspace_size.argtypes = [A, _I, _I, _I, _I, _I, Z]
+    L.ttt_kv_attention_workspace_size.argtypes = [A, _I, _I, _I, _I, _I, _I, Z]
     L.ttt_kv_attention.argtypes = [C, A, _I, _I, R, R, _P, _P, ctypes.c_size_t, _P]
     for fn in ("rope_table", "rope_forward", "rope_backward", "kv_page_bytes", "kv_append",
                "kv_read", "kv_attention_workspace_size", "kv_attention"):
@@ -291,12 +291,13 @@ def _attn(scale, window, max_new, max_kv, causal, dim):
                 0 if causal else ATTN_ALL_KEYS, 0)
 
 
-def kv_attention_workspace_size(batch, rows, kv_heads, q_heads, head_dim, *, max_new, max_kv,
-                                window=0) -> int:
+def kv_attention_workspace_size(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bfloat16, *,
+                                max_new, max_kv, window=0) -> int:
     n = ctypes.c_size_t(0)
     a = _attn(None, window, max_new, max_kv, True, head_dim)
-    _b._check(_L().ttt_kv_attention_workspace_size(ctypes.byref(a), batch, rows, kv_heads, q_heads,
-                                                   head_dim, ctypes.byref(n)))
+    act = _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16
+    _b._check(_L().ttt_kv_attention_workspace_size(ctypes.byref(a), batch, rows, act, kv_heads,
+                                                   q_heads, head_dim, ctypes.byref(n)))
     return n.value
 
 
@@ -331,8 +332,8 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     L, ref = _L(), ctypes.byref
     if workspace is None:
         need = ctypes.c_size_t(0)
-        st = L.ttt_kv_attention_workspace_size(ref(a), cache.batch, n, cache.kv_heads, rq.heads,
-                                               dim, ref(need))
+        st = L.ttt_kv_attention_workspace_size(ref(a), cache.batch, n, act, cache.kv_heads,
+                                               rq.heads, dim, ref(need))
         if st:
             _b._check(st)
         if need.value:

@@ -20,6 +20,7 @@ LIB_NAME = "libttt_layer.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["ttt_kernels.hip", "ttt_decode.hip", "ttt_backward.hip", "ttt_noalloc.hip",
            "ttt_rope.hip", "ttt_cache.hip", "ttt_attention.hip",
+           "ttt_attend_many.hip",
            "ttt_api.cpp", "ttt_serve_api.cpp"]
 ARCH = "gfx950"
 

@@ -1,0 +1,421 @@
+// gfx950 kernel of attention over the paged 4-bit cache for many rows
+// (prompts and segments); the method and the few-row kernel are in
+// ttt_attention.hip.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ttt_attention.h"
+
+namespace tttk {
+namespace {
+
+// A workgroup of 8 waves takes 256 rows of one key head, 32 a wave, and walks
+// over its keys 64 at a time. Codes are turned into bf16 once for all of the
+// rows: waves 0-3 decode the tile's keys, waves 4-7 its values (each 16
+// tokens), and leave them in LDS in the order in which the matrix
+// instructions read them, 1 KB a fragment, so that a fragment is one
+// contiguous read. Two tiles' buffers alternate; raw codes are fetched two
+// tiles ahead and page numbers three.
+//
+// S^T = K Q^T with 32x32x16: a lane holds, of one row, the keys 8 (i / 4) + 4
+// (lane / 32) + i % 4 of a 32-key tile. Taken eight at a time these are what
+// the second product O^T = V^T P^T wants from that lane if V's fragments
+// list the keys of 16 in the order 0-3, 8-11 | 4-7, 12-15, which is how they
+// are written. The rows of V^T are numbered so that a lane of O^T holds
+// neighbouring values: fragment t, row i is value i D / 32 + t.
+//
+// Wide heads and fp32 rows need more than the 256 registers that two waves a
+// SIMD have: they take 4 waves (128 rows), each of which decodes keys and
+// values both.
+constexpr int kManyKeys = 64;
+
+// Which of a tile's keys have no page, are NaN, or have a NaN value: one bit a
+// key, 32 keys a word.
+struct TileMarks {
+  uint32_t absent[2], knan[2], vnan[2];
+};
+
+// Bits [a, b) of a word.
+__device__ __forceinline__ uint32_t bits_between(int a, int b) {
+  a = min(max(a, 0), 32), b = min(max(b, 0), 32);
+  const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
+  const uint32_t below_a = a == 32 ? ~0u : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
+// All ones where bit k of w is set.
+__device__ __forceinline__ uint32_t spread(uint32_t w, int k) {
+  return (uint32_t)__builtin_amdgcn_sbfe((int)w, k, 1);
+}
+constexpr uint32_t kNanBits = 0x7fc00000u, kNoneBits = 0xff800000u;
+
+template <int D>
+struct Raw {  // a lane's share of 16 tokens' codes, and their scales
+  static constexpr int kUnits = D == 256 ? 2 : 1;
+  uint4 w[kUnits];
+  uint32_t s[kUnits];
+  bool have;
+};
+
+// D = 64: half the lanes have no unit.
+template <int D>
+__device__ __forceinline__ bool unit_live(int lane) { return D >= 128 || lane < 32; }
+
+// Keys: unit (block of 32 values c, token t), lane = 16 c + t (+ 64 a unit).
+// Values: unit (four tokens q, 8 values c), lane = (D / 8) q + c.
+template <int D>
+__device__ __forceinline__ void fetch(Raw<D>& r, const AttnLaunch& a, bool is_v, int hk, int id,
+                                      int off, bool have, int lane) {
+  r.have = have && (uint32_t)id < (uint32_t)a.pool.n_pages;
+  if (!r.have || !unit_live<D>(lane)) return;
+  const int page = a.pool.page;
+  const uint8_t* p = a.pool.pages + id * a.pool.page_stride + hk * head_block_bytes(page, D);
+#pragma unroll
+  for (int u = 0; u < Raw<D>::kUnits; ++u) {
+    const int n = lane + 64 * u;
+    if (is_v) {
+      const int q = n / (D / 8), c = n % (D / 8);
+      r.w[u] = *reinterpret_cast<const uint4*>(p + page * (D / 2) + off * (D / 2) + n * 16);
+      r.s[u] = *reinterpret_cast<const uint32_t*>(p + page * D + page * (D / 32) + (c >> 2) * page +
+                                                  off + 4 * q);
+    } else {
+      const int c = n >> 4, t = n & 15;
+      r.w[u] = *reinterpret_cast<const uint4*>(p + (off + t) * (D / 2) + c * 16);
+      r.s[u] = p[page * D + (off + t) * (D / 32) + c];
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t* kbuf, uint8_t* vbuf,
+                                       TileMarks* marks, int lane) {
+  if (!r.have) {  // no such page, or past the end: zeros, which no row counts
+#pragma unroll
+    for (int u = 0; u < Raw<D>::kUnits; ++u) {
+      r.w[u] = make_uint4(0, 0, 0, 0);
+      r.s[u] = 0x7f7f7f7fu;
+    }
+    if (lane == 0 && !is_v) atomicOr(&marks->absent[piece >> 1], 0xffffu << (16 * (piece & 1)));
+  }
+#pragma unroll
+  for (int u = 0; u < Raw<D>::kUnits; ++u) {
+    const int n = lane + 64 * u;
+    if (is_v) {
+      static_assert(kScaleMax == 252, "bytes from 253 on");
+      const bool live = unit_live<D>(lane);
+      uint32_t bad = live ? ((r.s[u] & 0x7f7f7f7fu) + 0x03030303u) & r.s[u] & 0x80808080u : 0u;
+      const int q = n / (D / 8), c = n % (D / 8);
+      uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
+      if (__any(bad != 0)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (bad >> (8 * e + 7) & 1) {
+            atomicOr(&marks->vnan[piece >> 1], 1u << (16 * (piece & 1) + 4 * q + e));
+            w[e] = 0;
+            r.s[u] = (r.s[u] & ~(255u << (8 * e))) | (127u << (8 * e));
+          }
+      }
+      if (!live) continue;
+      uint32_t d[4][4];  // [token][value pair]
+#pragma unroll
+      for (int e = 0; e < 4; ++e) decode8(w[e], scale_value((r.s[u] >> (8 * e)) & 255u), d[e]);
+      constexpr int T = D / 32;  // fragments; value 8c + j is row (8c + j) / T of fragment j % T
+      uint8_t* at = vbuf + piece * (T * 1024) + (q & 1) * 512 + (q >> 1) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+        const uint2 x = make_uint2(__builtin_amdgcn_perm(d[1][j >> 1], d[0][j >> 1], sel),
+                                   __builtin_amdgcn_perm(d[3][j >> 1], d[2][j >> 1], sel));
+        *reinterpret_cast<uint2*>(at + (j % T) * 1024 + (8 * c / T + j / T) * 16) = x;
+      }
+    } else {
+      const bool live = unit_live<D>(lane);
+      const int c = n >> 4, t = n & 15;
+      if (__any(live && r.s[u] > kScaleMax) && live && r.s[u] > kScaleMax)
+        atomicOr(&marks->knan[piece >> 1], 1u << (16 * (piece & 1) + t));
+      if (!live) continue;
+      const float sc = scale_value(r.s[u] & 255u);
+      const uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
+      constexpr int S = D / 16;  // steps; values 32c + 8j .. are half j % 2 of step 2c + j / 2
+      uint8_t* at = kbuf + ((piece >> 1) * S + 2 * c) * 1024 + ((piece & 1) * 16 + t) * 16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t d[4];
+        decode8(w[j], sc, d);
+        *reinterpret_cast<uint4*>(at + (j >> 1) * 1024 + (j & 1) * 512) = make_uint4(d[0], d[1], d[2], d[3]);
+      }
+    }
+  }
+}
+
+template <int D, int T, bool F32>
+__global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(AttnLaunch a, int row_tiles) {
+  constexpr int NW = many_waves(D, F32), kManyRows = 32 * NW;
+  constexpr int KINDS = 8 / NW;          // of keys and values, what one wave decodes
+  constexpr int KS = D / 16;             // steps of the first product
+  constexpr int NT = D / 32;             // fragments of V^T
+  constexpr int SUB = 2;                 // 32-key tiles whose scores are held at once
+  __shared__ __attribute__((aligned(16))) uint8_t kbuf[2][kManyKeys * D * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t vbuf[2][kManyKeys * D * 2];
+  __shared__ TileMarks marks[3];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i32 = lane & 31, half = lane >> 5;
+  const int b = blockIdx.y;
+  int id = blockIdx.x;
+  const int hk = id % a.pool.heads;
+  id /= a.pool.heads;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int group = a.q.heads / a.pool.heads, page = a.pool.page;
+  const Seq seq = seq_of(a.pool, b);
+  if (seq.news <= 0) return;
+  const int rows = seq.news * group;
+  const int piece = wave & 3;
+  const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+  const float grown = 8.f / sc;
+
+  // Tiles of rows from the last, which sees most, to the first.
+  for (int tile = row_tiles - 1 - id; tile * kManyRows < rows; tile += row_tiles) {
+    const int r = tile * kManyRows + wave * 32 + i32;
+    const bool live = r < rows;
+    const int t = min(r, rows - 1) / group;
+    const int head = hk * group + min(r, rows - 1) % group;
+    const Span sp = span_of(a, seq.len, seq.news, t);
+    const Span tile_first = span_of(a, seq.len, seq.news, tile * kManyRows / group);
+    const Span tile_last = span_of(a, seq.len, seq.news, min(tile * kManyRows + kManyRows - 1, rows - 1) / group);
+    const int w0 = min(tile * kManyRows + wave * 32, rows - 1), w1 = min(w0 + 31, rows - 1);
+    const Span first = span_of(a, seq.len, seq.news, w0 / group);
+    const Span last = span_of(a, seq.len, seq.news, w1 / group);
+    const int lo = tile_first.lo & ~(kManyKeys - 1), hi = tile_last.hi;
+    int each = (max(hi - lo, 0) + a.splits - 1) / a.splits;
+    each = (each + kManyKeys - 1) & ~(kManyKeys - 1);
+    const int s0 = lo + split * each, s1 = min(hi, s0 + each);
+
+    uint32_t qf[T][KS][4];
+    {
+      const int64_t at = (int64_t)(seq.row0 + t) * a.q.ts + head * a.q.hs + half * 8;
+      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float v[8];
+        load8<F32>(a.q.p, at + 16 * s, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[T];
+          split2<T>(v[2 * e], v[2 * e + 1], w);
+#pragma unroll
+          for (int x = 0; x < T; ++x) qf[x][s][e] = w[x] ^ flip;
+        }
+      }
+    }
+    f32x16_t o[NT];
+#pragma unroll
+    for (int f = 0; f < NT; ++f)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[f][e] = 0.f;
+    float m = kNone, ms = 0.f, l = 0.f;  // maximum (unscaled), its scaled value (0 for none), sum
+
+    // This wave's 16 tokens of the tile at key j.
+    auto lookup = [&](int j, int* off) {
+      const int key = j + 16 * piece, pg = key / page;
+      *off = key - pg * page;
+      return key < s1 && pg < a.pool.max_pages ? a.pool.table[(int64_t)b * a.pool.max_pages + pg] : -1;
+    };
+
+    __syncthreads();  // the last tile of rows is done with LDS
+    if (threadIdx.x < 3) marks[threadIdx.x] = TileMarks{};
+    __syncthreads();
+    Raw<D> raw[KINDS];
+    int off, next = lookup(s0, &off);
+    auto fetch_all = [&]() {
+#pragma unroll
+      for (int z = 0; z < KINDS; ++z)
+        fetch<D>(raw[z], a, KINDS == 2 ? z == 1 : wave >= 4, hk, next, off, next >= 0, lane);
+    };
+    auto unpack_all = [&](int buf, int mk) {
+#pragma unroll
+      for (int z = 0; z < KINDS; ++z)
+        unpack<D>(raw[z], KINDS == 2 ? z == 1 : wave >= 4, piece, kbuf[buf], vbuf[buf], &marks[mk], lane);
+    };
+    if (s0 < s1) {
+      fetch_all();
+      unpack_all(0, 0);
+      next = lookup(s0 + kManyKeys, &off);
+      fetch_all();
+      next = lookup(s0 + 2 * kManyKeys, &off);
+    }
+    int cur = 0, mk = 0;
+    for (int j = s0; j < s1; j += kManyKeys, cur ^= 1, mk = mk == 2 ? 0 : mk + 1) {
+      __syncthreads();  // tile j is in LDS; the buffers of the one before are free
+      const int mk1 = mk == 2 ? 0 : mk + 1, mk2 = mk1 == 2 ? 0 : mk1 + 1;
+      if (threadIdx.x == 0) marks[mk2] = TileMarks{};
+      if (j + kManyKeys < s1) {
+        unpack_all(cur ^ 1, mk1);
+        fetch_all();
+        next = lookup(j + 3 * kManyKeys, &off);
+      }
+      if (j >= last.hi || j + kManyKeys <= first.lo) continue;
+      const TileMarks mark = marks[mk];
+      const bool odd = __builtin_amdgcn_readfirstlane(
+          (mark.absent[0] | mark.absent[1] | mark.knan[0] | mark.knan[1] | mark.vnan[0] | mark.vnan[1]) != 0 ||
+          j < last.lo || j + kManyKeys > first.hi);
+#pragma unroll
+      for (int sub = 0; sub < 2 / SUB; ++sub) {
+        f32x16_t s[SUB];
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[x][e] = 0.f;
+          const uint8_t* at = kbuf[cur] + (sub * SUB + x) * (KS * 1024) + lane * 16;
+#pragma unroll
+          for (int q = 0; q < KS; ++q) {
+            const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(at + q * 1024);
+#pragma unroll
+            for (int y = T - 1; y >= 0; --y)
+              s[x] = mfma32(kf, frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), s[x]);
+          }
+        }
+        uint32_t poison[SUB] = {};  // keys that this row sees whose value is NaN
+        if (odd) {
+#pragma unroll
+          for (int x = 0; x < SUB; ++x) {
+            const int y = sub * SUB + x, j0 = j + 32 * y;
+            const uint32_t seen =
+                (bits_between(sp.lo - j0, sp.hi - j0) & ~(y ? mark.absent[1] : mark.absent[0])) >> (4 * half);
+            const uint32_t nan = ((y ? mark.knan[1] : mark.knan[0]) >> (4 * half)) & seen;
+            poison[x] = ((y ? mark.vnan[1] : mark.vnan[0]) >> (4 * half)) & seen;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int k = 8 * (e >> 2) + (e & 3);
+              const uint32_t keep = spread(seen, k);
+              s[x][e] = __uint_as_float((__float_as_uint(s[x][e]) & keep) | (kNoneBits & ~keep) |
+                                        (spread(nan, k) & kNanBits));
+            }
+          }
+        }
+        float mx = kNone;
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[x][e]);
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        // The maximum is only followed when it has grown by more than a
+        // factor 2^8 of the weights: until then they stay below 2^8, which
+        // fp32 and bf16 hold as well as 1, and nothing has to be rescaled.
+        if (__any(mx > m + grown)) {
+          const float mn = fmaxf(m, mx);
+          const float n0 = mn == kNone ? 0.f : mn * sc;
+          const float al = m == kNone ? 0.f : __builtin_amdgcn_exp2f(ms - n0);
+          m = mn, ms = n0;
+          l *= al;
+#pragma unroll
+          for (int f = 0; f < NT; ++f)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[f][e] *= al;
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            s[x][e] = __builtin_amdgcn_exp2f(fmaf(s[x][e], sc, -ms));
+            sum[e & 3] += s[x][e];
+          }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (odd) {
+          // A NaN value is out of V, where it would reach every row: it enters
+          // the weight of the rows that see it.
+#pragma unroll
+          for (int x = 0; x < SUB; ++x)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              s[x][e] = __uint_as_float(__float_as_uint(s[x][e]) |
+                                        (spread(poison[x], 8 * (e >> 2) + (e & 3)) & kNanBits));
+        }
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t pw[T][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[T];
+              split2<T>(s[x][8 * g + 2 * e], s[x][8 * g + 2 * e + 1], w);
+#pragma unroll
+              for (int y = 0; y < T; ++y) pw[y][e] = w[y];
+            }
+            const uint8_t* at = vbuf[cur] + (2 * (sub * SUB + x) + g) * (NT * 1024) + lane * 16;
+#pragma unroll
+            for (int f = 0; f < NT; ++f) {
+              const bf16x8_t vf = *reinterpret_cast<const bf16x8_t*>(at + f * 1024);
+#pragma unroll
+              for (int y = T - 1; y >= 0; --y)
+                o[f] = mfma32(vf, frag(pw[y][0], pw[y][1], pw[y][2], pw[y][3]), o[f]);
+            }
+          }
+      }
+    }
+    l += __shfl_xor(l, 32);
+    if (!live) continue;
+    const int64_t row = (int64_t)(seq.row0 + t) * a.q.heads + head;
+    const float m2 = m == kNone ? kNone : ms;
+    // lane (row, half): fragment f, register e is value NT (8 (e / 4) + 4 half + e % 4) + f
+    if (a.splits > 1) {
+      const int64_t at = (int64_t)split * a.pool.tokens * a.q.heads + row;
+      if (half == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m2, l);
+      float* dst = a.part + at * D;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float* x = dst + NT * (8 * (e >> 2) + 4 * half + (e & 3));
+        if constexpr (NT == 2) {
+          *reinterpret_cast<float2*>(x) = make_float2(o[0][e], o[1][e]);
+        } else {
+#pragma unroll
+          for (int f = 0; f < NT; f += 4)
+            *reinterpret_cast<float4*>(x + f) = make_float4(o[f][e], o[f + 1][e], o[f + 2][e], o[f + 3][e]);
+        }
+      }
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (a.lse != nullptr && half == 0)
+        a.lse[row] = l == 0.f ? kNone : (m2 + __builtin_amdgcn_logf(l)) * kLn2;
+      const int64_t at = (int64_t)(seq.row0 + t) * a.o.ts + head * a.o.hs;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t x = at + NT * (8 * (e >> 2) + 4 * half + (e & 3));
+#pragma unroll
+        for (int f = 0; f < NT; f += 2) {
+          if constexpr (F32)
+            *reinterpret_cast<float2*>(static_cast<float*>(a.o.p) + x + f) =
+                make_float2(o[f][e] * inv, o[f + 1][e] * inv);
+          else
+            *reinterpret_cast<uint32_t*>(static_cast<u16*>(a.o.p) + x + f) =
+                pack_bf16(o[f][e] * inv, o[f + 1][e] * inv);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attend_many(const AttnLaunch& a, hipStream_t s) {
+  const int group = a.q.heads / a.pool.heads;
+  const int waves = many_waves(a.pool.dim, a.f32);
+  int64_t tiles = ((int64_t)a.max_new * group + 32 * waves - 1) / (32 * waves);
+  const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads);
+  if (tiles > most) tiles = most;  // a workgroup then takes several
+  const dim3 grid((uint32_t)(tiles * a.splits * a.pool.heads), a.pool.batch);
+#define TTT_CALL(D, T, F) attend_many_kernel<D, T, F><<<grid, 64 * waves, 0, s>>>(a, (int)tiles)
+  switch (a.pool.dim) {
+    case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
+    case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
+    default: if (a.f32) { TTT_CALL(256, 3, true); } else { TTT_CALL(256, 1, false); } break;
+  }
+#undef TTT_CALL
+  return hipGetLastError();
+}
+
+}  // namespace tttk

@@ -1,0 +1,72 @@
+// Device helpers of the attention kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ttt_fp4.h"
+#include "ttt_serve_device.h"
+
+namespace tttk {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -__builtin_huge_valf();
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+struct U4 {
+  uint32_t v[4];
+};
+__device__ __forceinline__ bf16x8_t frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8_t, U4{{a, b, c, d}});
+}
+
+// x as T bf16 terms (T = 1: rounded to nearest; T = 3: 24 bits, exact but for
+// the last term's rounding), pairs packed.
+template <int T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&w)[T]) {
+  w[0] = pack_bf16(x, y);
+#pragma unroll
+  for (int t = 1; t < T; ++t) {
+    x -= __uint_as_float(w[t - 1] << 16);
+    y -= __uint_as_float(w[t - 1] & 0xffff0000u);
+    w[t] = pack_bf16(x, y);
+  }
+}
+
+// The keys that row r of a tile sees: [lo, hi).
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span span_of(const AttnLaunch& a, int len, int news, int t) {
+  const int p = len - news + t;
+  Span s;
+  s.hi = a.causal ? min(p + 1, len) : len;
+  s.lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  return s;
+}
+
+// Sequence b's rows, and its keys.
+struct Seq {
+  int row0, news, len;
+};
+__device__ __forceinline__ Seq seq_of(const Pool& p, int b) {
+  const int each = p.tokens / p.batch;
+  const int r0 = p.starts ? p.starts[b] : b * each;
+  const int r1 = p.starts ? p.starts[b + 1] : r0 + each;
+  Seq s;
+  s.row0 = r0;
+  s.news = r0 < 0 ? 0 : min(r1, p.tokens) - r0;
+  s.len = min(p.lens[b], p.max_pages * p.page);
+  return s;
+}
+
+}  // namespace tttk

@@ -13,51 +13,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "ttt_fp4.h"
-#include "ttt_serve_device.h"
+#include "ttt_attention.h"
 
 namespace tttk {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNone = -__builtin_huge_valf();
-
-__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-struct U4 {
-  uint32_t v[4];
-};
-__device__ __forceinline__ bf16x8_t frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __builtin_bit_cast(bf16x8_t, U4{{a, b, c, d}});
-}
-
-// x as T bf16 terms (T = 1: rounded to nearest; T = 3: 24 bits, exact but for
-// the last term's rounding), pairs packed.
-template <int T>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&w)[T]) {
-  w[0] = pack_bf16(x, y);
-#pragma unroll
-  for (int t = 1; t < T; ++t) {
-    x -= __uint_as_float(w[t - 1] << 16);
-    y -= __uint_as_float(w[t - 1] & 0xffff0000u);
-    w[t] = pack_bf16(x, y);
-  }
-}
-
-// The keys that row r of a tile sees: [lo, hi).
-struct Span {
-  int lo, hi;
-};
-__device__ __forceinline__ Span span_of(const AttnLaunch& a, int len, int news, int t) {
-  const int p = len - news + t;
-  Span s;
-  s.hi = a.causal ? min(p + 1, len) : len;
-  s.lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  return s;
-}
 
 // ---------------------------------------------------------------------------
 // Few rows. A wave takes 16 rows (query heads of one key head, times tokens)
@@ -85,11 +44,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
   const int group = a.q.heads / a.pool.heads;
   const int page = a.pool.page, gpp = page >> 4;  // 16-key pieces a page
 
-  const int row0 = a.pool.starts ? a.pool.starts[b] : b * (a.pool.tokens / a.pool.batch);
-  const int row1 = a.pool.starts ? a.pool.starts[b + 1] : row0 + a.pool.tokens / a.pool.batch;
-  const int news = min(row1, a.pool.tokens) - max(row0, 0);
-  if (news <= 0 || row0 < 0) return;
-  const int len = min(a.pool.lens[b], a.pool.max_pages * page);
+  const Seq seq = seq_of(a.pool, b);
+  if (seq.news <= 0) return;
+  const int row0 = seq.row0, news = seq.news, len = seq.len;
   const int rows = news * group;
 
   for (int tile = blockIdx.y / a.pool.heads; tile * 16 < rows; tile += row_tiles) {
@@ -417,18 +374,38 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
 
 }  // namespace
 
-int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window) {
-  const int64_t tiles = ((int64_t)max_new * (q_heads / kv_heads) + 15) / 16 * kv_heads * batch;
+namespace {
+
+// Rows of one sequence and key head from which the many-row kernel is taken.
+constexpr int kManyFrom = 64;
+
+}  // namespace
+
+int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
+                int dim) {
+  const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
   int64_t keys = max_kv;
-  if (window > 0) keys = keys < window + max_new ? keys : window + max_new;
+  if (window > 0) keys = keys < (int64_t)window + max_new ? keys : (int64_t)window + max_new;
+  if (attn_many(rows, f32, dim)) {
+    const int per = 32 * many_waves(dim, f32);
+    const int64_t groups = (rows + per - 1) / per * kv_heads * batch;
+    const int64_t most = (keys + 511) / 512;
+    int64_t want = 256 / groups;
+    if (want > most) want = most;
+    return (int)(want < 1 ? 1 : want);
+  }
+  const int64_t tiles = (rows + 15) / 16 * kv_heads * batch;
   const int64_t most = (keys + 255) / 256;   // no fewer than 64 keys a wave
   int64_t want = (1024 + tiles - 1) / tiles;  // four workgroups a CU
   if (want > most) want = most;
   return (int)(want < 1 ? 1 : want);
 }
 
+bool attn_many(int64_t rows, bool f32, int dim) { return rows >= kManyFrom && !(f32 && dim == 256); }
+
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int group = a.q.heads / a.pool.heads;
+  if (attn_many((int64_t)a.max_new * group, a.f32, a.pool.dim)) return launch_attend_many(a, s);
   int64_t tiles = ((int64_t)a.max_new * group + 15) / 16;
   if (tiles * a.pool.heads > 65535) tiles = 65535 / a.pool.heads;
   const dim3 grid(a.splits, (uint32_t)(tiles * a.pool.heads), a.pool.batch);

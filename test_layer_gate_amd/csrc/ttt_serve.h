@@ -81,8 +81,14 @@ hipError_t launch_rope_table(float* table, int max_pos, int rot, double base, in
 hipError_t launch_append(const AppendLaunch& a, hipStream_t s);
 hipError_t launch_read(const ReadLaunch& a, hipStream_t s);
 // How many parts each sequence's keys are cut into.
-int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window);
+int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
+                int dim);
+// Whether `rows` rows a sequence and key head go to the many-row kernel, and
+// how many waves of 32 rows its workgroups have.
+bool attn_many(int64_t rows, bool f32, int dim);
+constexpr int many_waves(int dim, bool f32) { return dim == 256 || f32 ? 4 : 8; }
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s);
+hipError_t launch_attend_many(const AttnLaunch& a, hipStream_t s);
 hipError_t launch_attention_join(const AttnLaunch& a, hipStream_t s);
 
 }  // namespace tttk

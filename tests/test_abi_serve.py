@@ -187,7 +187,7 @@ def test_attention_refusals(L, kw, code):
 def test_attention_workspace(L):
     def size(tokens, batch=1, hk=8, hq=32, dim=128, **kw):
         n = ctypes.c_size_t(0)
-        st = L.ttt_kv_attention_workspace_size(ref(attn(**kw)), batch, tokens, hk, hq, dim, ref(n))
+        st = L.ttt_kv_attention_workspace_size(ref(attn(**kw)), batch, tokens, 0, hk, hq, dim, ref(n))
         return st, n.value
     st, n = size(1, max_new=1, max_kv=131072)
     assert st == OK and n >= 32 * 128 * 4 * 2
@@ -196,7 +196,7 @@ def test_attention_workspace(L):
     for kw, code in BAD_ATTN:
         assert size(1, **kw)[0] == code
     assert size(-1)[0] == INVALID and size(1, hq=9)[0] == INVALID and size(1, dim=80)[0] == UNSUPPORTED
-    assert L.ttt_kv_attention_workspace_size(ref(attn()), 1, 1, 8, 32, 128, None) == INVALID
+    assert L.ttt_kv_attention_workspace_size(ref(attn()), 1, 1, 0, 8, 32, 128, None) == INVALID
 
 
 def test_struct_layouts_match_the_header():
