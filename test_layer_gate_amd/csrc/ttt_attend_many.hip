@@ -173,8 +173,7 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
   if (seq.news <= 0) return;
   const int rows = seq.news * group;
   const int piece = wave & 3;
-  const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
-  const float grown = 8.f / sc;
+  const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1.2e-38f), grown = fminf(8.f / sc, 1e38f);
 
   // Tiles of rows from the last, which sees most, to the first.
   for (int tile = row_tiles - 1 - id; tile * kManyRows < rows; tile += row_tiles) {

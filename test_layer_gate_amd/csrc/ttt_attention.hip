@@ -4,12 +4,15 @@
 // keys j with max(0, p - window + 1) <= j <= p (causal; else j < len):
 //   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  s_j = scale q . k_j,
 // in one pass over the keys with the running maximum m, sum and weighted sum
-// (rescaled whenever m grows).
+// (rescaled whenever m has grown by more than a factor 2^8 of the weights).
 //
 // Codes times their power-of-two scale are exact in bf16, so keys and values
 // enter the matrix instructions without a rounding; what is rounded is the
 // weights p (to bf16), and, for fp32 rows, nothing: q and p are then three
-// bf16 terms each, whose products are all accumulated in fp32.
+// bf16 terms each. Everything accumulates in fp32. (The scaled matrix
+// instructions would take keys as codes against 8-bit terms of q, in the same
+// time and without decoding; they keep about 17 bits of a sum of 8 products,
+// which left scores and lse off by 1e-4, and were not taken.)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -20,24 +23,33 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Few rows. A wave takes 16 rows (query heads of one key head, times tokens)
-// and a stretch of the keys, 32 at a time. S^T = K Q^T with 16x16x32: lane
-// (i, g) = (lane % 16, lane / 16) brings D / 4 neighbouring values of key i;
-// of the result it holds, for row i, keys 4g .. 4g + 3 of either 16. Those
-// eight are what the second product O^T = V^T P^T asks of it (the order of
-// the contraction is free as long as V agrees), so P goes over without a
-// move between lanes. Of V it brings the same eight keys' values
-// i D / 16 .. + D / 16 - 1.
+// and a stretch of the keys, 32 at a time, the next 32 on their way meanwhile.
+// S^T = K Q^T with 16x16x32: lane (i, g) = (lane % 16, lane / 16) brings D / 4
+// neighbouring values of key i; of the result it holds, for row i, keys 4g .. 4g + 3 of either 16. Those eight are what the second product
+// O^T = V^T P^T (16x16x32) asks of it: the order of the contraction is free as
+// long as V agrees, so P goes over without a move between lanes. Of V it
+// brings the same eight keys' values i D / 16 .. + D / 16 - 1.
 constexpr int kFewWaves = 4;
 
+// One lane's share of 32 keys (two pieces of 16): raw codes and scales.
+template <int D>
+struct FewTile {
+  static constexpr int kN = D == 256 ? 2 : 1;
+  uint4 kw[2][kN], vw[2][kN];
+  uint32_t ks[2], vs[2];  // of K the word that holds the lane's scale bytes
+  bool have[2];
+};
+
 template <int D, int T, bool F32>
-__global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a, int row_tiles) {
-  constexpr int NB = D / 64;        // 16-byte pieces (D = 64: half a piece) of K per lane
-  constexpr int KS = D / 32;        // steps of the first product
-  constexpr int F = D / 16;         // V fragments = values per lane
+__global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void attend_few_kernel(AttnLaunch a, int row_tiles) {
+  constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
+  constexpr int KS = D / 32;            // steps of the first product
+  constexpr int F = D / 16;             // V fragments = values per lane
   __shared__ float red_o[kFewWaves - 1][16][D + 4];
   __shared__ float red_ml[kFewWaves][16][2];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int b = blockIdx.z, split = blockIdx.x;
   const int hk = blockIdx.y % a.pool.heads;
@@ -55,16 +67,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
     const int t = min(r, rows - 1) / group;
     const int head = hk * group + min(r, rows - 1) % group;
     const Span sp = span_of(a, len, news, t);
-    // the tile's keys, and this split's part of them
+    // the tile's keys
     const Span first = span_of(a, len, news, tile * 16 / group);
     const Span last = span_of(a, len, news, min(tile * 16 + 15, rows - 1) / group);
     const int lo = first.lo & ~31, hi = last.hi;
     const int all_lo = last.lo, all_hi = first.hi;  // keys that every row sees
-    int each = max(128 * kFewWaves / 4, (hi - lo + a.splits - 1) / a.splits);
-    each = (each + 127) & ~127;
-    const int s0 = lo + split * each, s1 = min(hi, s0 + each);
-    const int per = ((s1 - s0 + kFewWaves - 1) / kFewWaves + 31) & ~31;
-    const int k0 = s0 + wave * per, k1 = min(s1, k0 + per);
 
     // Q as the first product's B operand: step s, values (D / 4) g + 8 s ..
     uint32_t qf[T][KS][4];
@@ -77,68 +84,83 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t w[T];
-          split2<T>(live ? v[2 * e] : 0.f, live ? v[2 * e + 1] : 0.f, w);
+          split2<T>(v[2 * e], v[2 * e + 1], w);
 #pragma unroll
-          for (int x = 0; x < T; ++x) qf[x][s][e] = w[x];
+          for (int x = 0; x < T; ++x) qf[x][s][e] = w[x] ^ (a.scale < 0.f ? 0x80008000u : 0u);
         }
       }
     }
+    const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1.2e-38f), grown = fminf(8.f / sc, 1e38f);
     f32x4_t o[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) o[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float m = kNone, l = 0.f;
-    const float sc = a.scale * kLog2e;
+    float m = kNone, ms = 0.f, l = 0.f;  // maximum (unscaled), its scaled value (0 for none), sum
 
-    for (int base = k0; base < k1; base += 1024) {
-      // Where the next 64 pieces of 16 keys lie: one a lane.
-      int64_t my_block = -1;
+    const int k_lane = i16 * (D / 2) + (D == 64 ? g >> 1 : g * NP) * 16;
+    const int v_lane = page * (D / 2) + g * (2 * D) + (D == 64 ? (i16 >> 1) * 16 : i16 * (D / 8));
+    // K's scales are read as words (a byte load's widening would be waited for
+    // at once) and cut to the lane's byte where they are used.
+    const int ks_lane = page * D + (D == 64 ? (i16 >> 1) * 4 : D == 128 ? i16 * 4 : i16 * 8 + (g >> 1) * 4);
+    const int ks_shift = D == 64 ? 16 * (i16 & 1) + 8 * (g >> 1) : D == 128 ? 8 * g : 16 * (g & 1);
+    const int vs_lane = page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + 4 * g;
+
+    // This split's stretches of `each` keys, a quarter of each for every wave.
+    for (int s0 = lo + split * a.each; s0 < hi; s0 += a.splits * a.each) {
+      const int per = a.each / kFewWaves;
+      const int k0 = s0 + wave * per, k1 = min(hi, k0 + per);
+      int64_t my_block = 0;  // where 64 pieces of 16 keys lie: one a lane
       int my_off = 0;
-      {
+      uint64_t gone = 0;     // those that have no page, or are past the end
+      auto find = [&](int base) {
         const int piece = (base >> 4) + lane;
         const int pg = piece / gpp;
-        if (pg < a.pool.max_pages && piece * 16 < k1) {
+        my_block = 0, my_off = 0;
+        bool ok = pg < a.pool.max_pages && piece * 16 < k1;
+        if (ok) {
           const int id = a.pool.table[(int64_t)b * a.pool.max_pages + pg];
-          if ((uint32_t)id < (uint32_t)a.pool.n_pages) {
+          ok = (uint32_t)id < (uint32_t)a.pool.n_pages;
+          if (ok) {
             my_block = id * a.pool.page_stride + hk * head_block_bytes(page, D);
             my_off = (piece - pg * gpp) * 16;
           }
         }
-      }
-      const int stop = min(k1, base + 1024);
-      for (int j = base; j < stop; j += 32) {
-        uint32_t kw[2][KS], ks[2][NB], vw[2][4][D == 256 ? 2 : 1], vs[2];
-        bool have[2];
+        gone = __ballot(!ok);
+      };
+      auto fetch = [&](FewTile<D>& x, int src) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int src = ((j - base) >> 4) + x;
-          const int64_t blk = __shfl(my_block, src);
-          have[x] = blk >= 0;
-          const uint8_t* bp = a.pool.pages + (have[x] ? blk : 0);
-          const int off = have[x] ? __shfl(my_off, src) : 0;
-          const uint8_t* kc = bp + (off + i16) * (D / 2) + g * (D / 8);
-          const uint8_t* vc = bp + page * (D / 2) + ((off >> 2) + g) * (2 * D) +
-                              (D == 64 ? (i16 >> 1) * 16 : i16 * (D / 8));
-          const uint8_t* kp = bp + page * D + (off + i16) * (D / 32);
-          const uint8_t* vp = bp + page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + off + 4 * g;
-          if constexpr (D == 64) {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc);
-            kw[x][0] = w.x, kw[x][1] = w.y;
-            ks[x][0] = kp[g >> 1];
-          } else {
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)my_block, src + u);
+          const uint32_t hi32 = __builtin_amdgcn_readlane((int)(my_block >> 32), src + u);
+          const int off = __builtin_amdgcn_readlane(my_off, src + u);
+          x.have[u] = (gone >> (src + u) & 1) == 0;
+          const uint8_t* bp = a.pool.pages + ((uint64_t)hi32 << 32 | lo32);
+          const uint8_t* cp = bp + off * (D / 2);
 #pragma unroll
-            for (int p = 0; p < D / 128; ++p) {
-              const uint4 w = reinterpret_cast<const uint4*>(kc)[p];
-              kw[x][4 * p] = w.x, kw[x][4 * p + 1] = w.y, kw[x][4 * p + 2] = w.z, kw[x][4 * p + 3] = w.w;
-              ks[x][p] = kp[g * (D / 128) + p];
-            }
+          for (int p = 0; p < NP; ++p) {
+            x.kw[u][p] = *reinterpret_cast<const uint4*>(cp + k_lane + 16 * p);
+            x.vw[u][p] = *reinterpret_cast<const uint4*>(cp + v_lane + 16 * p);
           }
-#pragma unroll
-          for (int p = 0; p < (D == 256 ? 2 : 1); ++p) {
-            const uint4 w = reinterpret_cast<const uint4*>(vc)[p];
-            vw[x][0][p] = w.x, vw[x][1][p] = w.y, vw[x][2][p] = w.z, vw[x][3][p] = w.w;
-          }
-          vs[x] = *reinterpret_cast<const uint32_t*>(vp);
+          x.ks[u] = *reinterpret_cast<const uint32_t*>(bp + off * (D / 32) + ks_lane);
+          x.vs[u] = *reinterpret_cast<const uint32_t*>(bp + off + vs_lane);
         }
+      };
+      FewTile<D> cur, nxt;
+      if (k0 < k1) {
+        find(k0);
+        fetch(nxt, 0);
+      }
+      for (int j = k0; j < k1; j += 32) {
+        cur = nxt;
+        if (j + 32 < k1) {
+          const int ahead = (j + 32 - k0) & 1023;
+          if (ahead == 0) find(j + 32);
+          fetch(nxt, ahead >> 4);
+        }
+        uint32_t ks[2][NP];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int q = 0; q < NP; ++q) ks[x][q] = (cur.ks[x] >> (ks_shift + 8 * q)) & 255u;
         // S^T
         f32x4_t s[2];
 #pragma unroll
@@ -146,8 +168,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
           s[x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int q = 0; q < KS; ++q) {
+            const uint4 w = cur.kw[x][q >> 2];
+            uint32_t c = (q & 3) == 0 ? w.x : (q & 3) == 1 ? w.y : (q & 3) == 2 ? w.z : w.w;
+            // D = 64: a lane's 16 values are half of a block
+            if constexpr (D == 64) c = g & 1 ? (q == 0 ? w.z : w.w) : c;
             uint32_t d[4];
-            decode8(kw[x][q], scale_value(ks[x][D == 256 ? q >> 2 : 0]), d);
+            decode8(c, scale_value(ks[x][q >> 2]), d);
             const bf16x8_t kf = frag(d[0], d[1], d[2], d[3]);
 #pragma unroll
             for (int y = T - 1; y >= 0; --y)
@@ -156,20 +182,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
         }
         float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = s[e >> 2][e & 3] * sc;
+        for (int e = 0; e < 8; ++e) p[e] = s[e >> 2][e & 3];
         // Keys that some row does not see, that have no page, or that hold NaN
-        bool odd = j < all_lo || j + 32 > all_hi || !have[0] || !have[1];
-        {
-          uint32_t nan = 0;
+        uint32_t nan = 0;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int q = 0; q < (D == 256 ? 2 : 1); ++q) nan |= ks[x][q] > kScaleMax;
-            static_assert(kScaleMax == 252, "bytes from 253 on");
-            nan |= ((vs[x] & 0x7f7f7f7fu) + 0x03030303u) & vs[x] & 0x80808080u;
-          }
-          odd = odd || __any(nan != 0);
+          for (int q = 0; q < NP; ++q) nan |= ks[x][q] > kScaleMax;
+          static_assert(kScaleMax == 252, "bytes from 253 on");
+          nan |= ((cur.vs[x] & 0x7f7f7f7fu) + 0x03030303u) & cur.vs[x] & 0x80808080u;
         }
+        const bool odd = j < all_lo || j + 32 > all_hi || !cur.have[0] || !cur.have[1] || __any(nan != 0);
         uint32_t poison = 0;  // this row's keys whose value is NaN
         if (odd) {
 #pragma unroll
@@ -177,50 +200,56 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
             uint64_t kn = __ballot(ks[x][0] > kScaleMax);
             kn |= kn >> 32;
             kn |= kn >> 16;
+            uint32_t w[4 * NP];
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+              const uint4 y = cur.vw[x][q];
+              w[4 * q] = y.x, w[4 * q + 1] = y.y, w[4 * q + 2] = y.z, w[4 * q + 3] = y.w;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = j + 16 * x + 4 * g + e;
-              const bool seen = have[x] && key >= sp.lo && key < sp.hi;
-              const uint32_t vb = (vs[x] >> (8 * e)) & 255u;
+              const bool seen = cur.have[x] && key >= sp.lo && key < sp.hi;
+              const uint32_t vb = (cur.vs[x] >> (8 * e)) & 255u;
               float& pe = p[4 * x + e];
               pe = !seen ? kNone : (kn >> (4 * g + e)) & 1 ? __builtin_nanf("") : pe;
               // A NaN value must not reach the rows that do not see it (0 * NaN):
               // it goes out of V, and into the weight of those that do.
               if (seen && vb > kScaleMax) poison |= 1u << (4 * x + e);
-              if (!have[x] || vb > kScaleMax) {
-                vs[x] = (vs[x] & ~(255u << (8 * e))) | (127u << (8 * e));
+              if (!cur.have[x] || vb > kScaleMax) {
+                cur.vs[x] = (cur.vs[x] & ~(255u << (8 * e))) | (127u << (8 * e));
 #pragma unroll
-                for (int q = 0; q < (D == 256 ? 2 : 1); ++q) vw[x][e][q] = 0;
+                for (int q = 0; q < NP; ++q) w[4 * q + e] = 0;
               }
             }
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+              cur.vw[x][q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
           }
         }
-        // running maximum over the tile's keys of this row
-        float mx = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
-                         fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m, mx);
-        const float m0 = mn == kNone ? 0.f : mn;
-        const float al = __builtin_amdgcn_exp2f(m - m0);
-        m = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(p[e] - m0);
-          sum += p[e];
-        }
-        l = l * al + sum;
-        if (odd) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (poison >> e & 1) p[e] = __builtin_nanf("");
-        }
-        if (__any(al != 1.f)) {
+        // The maximum is only followed when a weight would pass 2^8: until
+        // then the lanes need not agree on a new one, and nothing is rescaled.
+        const float mx = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
+                               fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+        if (__any(mx > m + grown)) {
+          float mn = fmaxf(mx, __shfl_xor(mx, 16));
+          mn = fmaxf(fmaxf(mn, __shfl_xor(mn, 32)), m);
+          const float n0 = mn == kNone ? 0.f : mn * sc;
+          const float al = m == kNone ? 0.f : __builtin_amdgcn_exp2f(ms - n0);
+          m = mn, ms = n0;
+          l *= al;
 #pragma unroll
           for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[f][e] *= al;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], sc, -ms));
+        l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+        if (__any(poison != 0)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (poison >> e & 1) p[e] = __builtin_nanf("");
         }
         uint32_t pw[T][4];
 #pragma unroll
@@ -233,13 +262,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
         // O^T
         float vsc[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vsc[e] = scale_value((vs[e >> 2] >> (8 * (e & 3))) & 255u);
+        for (int e = 0; e < 8; ++e) vsc[e] = scale_value((cur.vs[e >> 2] >> (8 * (e & 3))) & 255u);
 #pragma unroll
-        for (int c = 0; c < (F + 7) / 8; ++c) {
+        for (int c = 0; c < NP; ++c) {
           uint32_t d[8][4];  // [key][value pair]
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            uint32_t w = vw[e >> 2][e & 3][c];
+            const uint4 y = cur.vw[e >> 2][c];
+            uint32_t w = (e & 3) == 0 ? y.x : (e & 3) == 1 ? y.y : (e & 3) == 2 ? y.z : y.w;
             if constexpr (D == 64) w >>= 16 * (i16 & 1);
             decode8(w, vsc[e], d[e]);
           }
@@ -259,6 +289,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    m = m == kNone ? kNone : ms;
 
     // Join the waves: all to the common maximum, then added in their order.
     __syncthreads();  // the last tile's readers are done
@@ -336,40 +367,66 @@ __global__ __launch_bounds__(64 * kFewWaves) void attend_few_kernel(AttnLaunch a
   }
 }
 
-// Joins the splits of every row, in their order: a wave takes one row.
-template <int D, bool F32>
+// Joins the splits of every row, in their order. ROWS rows a workgroup: each
+// has 256 / ROWS threads, D / 4 of which hold 4 values each of one split; the
+// others take every LANES-th split beside them and are added at the end. With
+// many splits there are few rows: one a workgroup.
+template <int D, bool F32, int ROWS>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
-  constexpr int V = D / 64;
-  const int lane = threadIdx.x & 63;
+  constexpr int TPR = 256 / ROWS, LANES = TPR / (D / 4);
+  static_assert(LANES == 1 || ROWS == 1, "threads of a row");
+  __shared__ float4 red[ROWS][LANES][D / 4];
+  __shared__ float red_l[ROWS][LANES];
+  const int rr = threadIdx.x / TPR, c = threadIdx.x % TPR % (D / 4), y = threadIdx.x % TPR / (D / 4);
   const int64_t rows = (int64_t)a.pool.tokens * a.q.heads;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= rows) return;
+  const int64_t row = min((int64_t)blockIdx.x * ROWS + rr, rows - 1);
   float m = kNone;
-  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
-  m = wave_max(m);
+  if constexpr (LANES > 1) {
+    // the maximum, one split a thread
+    for (int s = threadIdx.x; s < a.splits; s += 256) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+    m = wave_max(m);
+    __shared__ float red_m[4];
+    if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
+  } else {
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+  }
   const float m0 = m == kNone ? 0.f : m;
-  float l = 0.f, acc[V] = {};
-  for (int s = 0; s < a.splits; ++s) {
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = y; s < a.splits; s += LANES) {
     const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (s * rows + row));
-    if (ml.y == 0.f) continue;
+    const float4 v = *reinterpret_cast<const float4*>(a.part + (s * rows + row) * D + 4 * c);
     const float w = __builtin_amdgcn_exp2f(ml.x - m0);
     l += ml.y * w;
-    const float* p = a.part + (s * rows + row) * D + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] += p[v] * w;
+    acc.x += v.x * w, acc.y += v.y * w, acc.z += v.z * w, acc.w += v.w * w;
   }
+  if constexpr (LANES > 1) {
+    red[rr][y][c] = acc;
+    if (c == 0) red_l[rr][y] = l;
+    __syncthreads();
+    if (y > 0) return;
+#pragma unroll
+    for (int z = 1; z < LANES; ++z) {
+      const float4 v = red[rr][z][c];
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      l += red_l[rr][z];
+    }
+  }
+  if ((int64_t)blockIdx.x * ROWS + rr >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int n = (int)(row / a.q.heads), h = (int)(row % a.q.heads);
-  if (a.lse != nullptr && lane == 0)
+  if (a.lse != nullptr && c == 0)
     a.lse[row] = l == 0.f ? kNone : (m + __builtin_amdgcn_logf(l)) * kLn2;
-  const int64_t at = (int64_t)n * a.o.ts + h * a.o.hs + lane * V;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if constexpr (F32)
-      static_cast<float*>(a.o.p)[at + v] = acc[v] * inv;
-    else
-      static_cast<u16*>(a.o.p)[at + v] = bf16_rne(acc[v] * inv);
-  }
+  const int64_t at = (int64_t)n * a.o.ts + h * a.o.hs + 4 * c;
+  if constexpr (F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o.p) + at) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  else
+    *reinterpret_cast<uint2*>(static_cast<u16*>(a.o.p) + at) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace
@@ -382,7 +439,7 @@ constexpr int kManyFrom = 64;
 }  // namespace
 
 int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
-                int dim) {
+                int dim, int* each) {
   const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
   int64_t keys = max_kv;
   if (window > 0) keys = keys < (int64_t)window + max_new ? keys : (int64_t)window + max_new;
@@ -392,13 +449,20 @@ int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, i
     const int64_t most = (keys + 511) / 512;
     int64_t want = 256 / groups;
     if (want > most) want = most;
+    *each = 0;
     return (int)(want < 1 ? 1 : want);
   }
+  // Stretches that give about 2048 workgroups of four waves (eight a CU, so
+  // that sequences shorter than max_kv leave enough of them), of 512 keys or
+  // more where there are many and 128 at least.
   const int64_t tiles = (rows + 15) / 16 * kv_heads * batch;
-  const int64_t most = (keys + 255) / 256;   // no fewer than 64 keys a wave
-  int64_t want = (1024 + tiles - 1) / tiles;  // four workgroups a CU
-  if (want > most) want = most;
-  return (int)(want < 1 ? 1 : want);
+  int64_t e = keys * tiles / 2048;
+  const int64_t least = keys * tiles < 512 * 256 ? 128 : 512;
+  if (e < least) e = least;
+  if (e > (1 << 20)) e = 1 << 20;
+  e = (e + 127) & ~(int64_t)127;
+  *each = (int)e;
+  return (int)((keys + e - 1) / e);
 }
 
 bool attn_many(int64_t rows, bool f32, int dim) { return rows >= kManyFrom && !(f32 && dim == 256); }
@@ -421,8 +485,15 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
 
 hipError_t launch_attention_join(const AttnLaunch& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.pool.tokens * a.q.heads;
-  const uint32_t grid = (uint32_t)((rows + 3) / 4);
-#define TTT_CALL(D, F) attend_join_kernel<D, F><<<grid, 256, 0, s>>>(a)
+  // One row a workgroup has up to 16 splits in flight at once; with fewer
+  // than that to join, as many rows as have threads for one each.
+  const bool one = a.splits > 4 || rows < 512;
+#define TTT_CALL(D, F)                                                                        \
+  if (one)                                                                                    \
+    attend_join_kernel<D, F, 1><<<(uint32_t)rows, 256, 0, s>>>(a);                            \
+  else                                                                                        \
+    attend_join_kernel<D, F, 1024 / D>                                                        \
+        <<<(uint32_t)((rows + 1024 / D - 1) / (1024 / D)), 256, 0, s>>>(a)
   switch (a.pool.dim) {
     case 64: if (a.f32) { TTT_CALL(64, true); } else { TTT_CALL(64, false); } break;
     case 128: if (a.f32) { TTT_CALL(128, true); } else { TTT_CALL(128, false); } break;

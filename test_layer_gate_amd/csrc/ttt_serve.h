@@ -69,7 +69,7 @@ struct AttnLaunch {
   float scale;
   int causal, window, max_new, max_kv;
   bool f32;
-  int splits;            // attn_splits()
+  int splits, each;      // attn_splits()
   float* part;           // [splits][tokens * q heads][D] (splits > 1)
   float* part_ml;        // [splits][tokens * q heads][2]
 };
@@ -80,9 +80,10 @@ hipError_t launch_rope_table(float* table, int max_pos, int rot, double base, in
                              hipStream_t s);
 hipError_t launch_append(const AppendLaunch& a, hipStream_t s);
 hipError_t launch_read(const ReadLaunch& a, hipStream_t s);
-// How many parts each sequence's keys are cut into.
+// How many parts each sequence's keys are cut into; for the few-row kernel
+// *each keys a stretch, part s taking every splits-th stretch from the s-th.
 int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
-                int dim);
+                int dim, int* each);
 // Whether `rows` rows a sequence and key head go to the many-row kernel, and
 // how many waves of 32 rows its workgroups have.
 bool attn_many(int64_t rows, bool f32, int dim);
