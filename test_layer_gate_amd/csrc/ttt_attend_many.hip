@@ -35,20 +35,6 @@ struct TileMarks {
   uint32_t absent[2], knan[2], vnan[2];
 };
 
-// Bits [a, b) of a word.
-__device__ __forceinline__ uint32_t bits_between(int a, int b) {
-  a = min(max(a, 0), 32), b = min(max(b, 0), 32);
-  const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
-  const uint32_t below_a = a == 32 ? ~0u : (1u << a) - 1u;
-  return below_b & ~below_a;
-}
-
-// All ones where bit k of w is set.
-__device__ __forceinline__ uint32_t spread(uint32_t w, int k) {
-  return (uint32_t)__builtin_amdgcn_sbfe((int)w, k, 1);
-}
-constexpr uint32_t kNanBits = 0x7fc00000u, kNoneBits = 0xff800000u;
-
 template <int D>
 struct Raw {  // a lane's share of 16 tokens' codes, and their scales
   static constexpr int kUnits = D == 256 ? 2 : 1;
@@ -101,9 +87,8 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
   for (int u = 0; u < Raw<D>::kUnits; ++u) {
     const int n = lane + 64 * u;
     if (is_v) {
-      static_assert(kScaleMax == 252, "bytes from 253 on");
       const bool live = unit_live<D>(lane);
-      uint32_t bad = live ? ((r.s[u] & 0x7f7f7f7fu) + 0x03030303u) & r.s[u] & 0x80808080u : 0u;
+      const uint32_t bad = live ? nan_bytes(r.s[u]) : 0u;
       const int q = n / (D / 8), c = n % (D / 8);
       uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
       if (__any(bad != 0)) {
@@ -118,7 +103,7 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
       if (!live) continue;
       uint32_t d[4][4];  // [token][value pair]
 #pragma unroll
-      for (int e = 0; e < 4; ++e) decode8(w[e], scale_value((r.s[u] >> (8 * e)) & 255u), d[e]);
+      for (int e = 0; e < 4; ++e) decode8(w[e], scale_at(r.s[u], e), d[e]);
       constexpr int T = D / 32;  // fragments; value 8c + j is row (8c + j) / T of fragment j % T
       uint8_t* at = vbuf + piece * (T * 1024) + (q & 1) * 512 + (q >> 1) * 8;
 #pragma unroll
@@ -134,7 +119,7 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
       if (__any(live && r.s[u] > kScaleMax) && live && r.s[u] > kScaleMax)
         atomicOr(&marks->knan[piece >> 1], 1u << (16 * (piece & 1) + t));
       if (!live) continue;
-      const float sc = scale_value(r.s[u] & 255u);
+      const float sc = scale_at(r.s[u], 0);
       const uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
       constexpr int S = D / 16;  // steps; values 32c + 8j .. are half j % 2 of step 2c + j / 2
       uint8_t* at = kbuf + ((piece >> 1) * S + 2 * c) * 1024 + ((piece & 1) * 16 + t) * 16;

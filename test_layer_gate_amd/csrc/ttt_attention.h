@@ -42,6 +42,26 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&w)[T]) {
   }
 }
 
+// Bits [a, b) of a word.
+__device__ __forceinline__ uint32_t bits_between(int a, int b) {
+  a = min(max(a, 0), 32), b = min(max(b, 0), 32);
+  const uint32_t below_b = b == 32 ? ~0u : (1u << b) - 1u;
+  const uint32_t below_a = a == 32 ? ~0u : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
+// All ones where bit k of w is set.
+__device__ __forceinline__ uint32_t spread(uint32_t w, int k) {
+  return (uint32_t)__builtin_amdgcn_sbfe((int)w, k, 1);
+}
+constexpr uint32_t kNanBits = 0x7fc00000u, kNoneBits = 0xff800000u;
+
+// The bytes of four scales that stand for NaN, each as its top bit.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  static_assert(kScaleMax == 252, "bytes from 253 on");
+  return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u;
+}
+
 // The keys that row r of a tile sees: [lo, hi).
 struct Span {
   int lo, hi;

@@ -51,8 +51,15 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  const int b = blockIdx.z, split = blockIdx.x;
-  const int hk = blockIdx.y % a.pool.heads;
+  // Key heads vary fastest, then rows, sequences and at last splits: workgroups
+  // go round the XCDs in this order, and a split that short sequences do not
+  // have must not be one XCD's.
+  int id = blockIdx.x;
+  const int hk = id % a.pool.heads;
+  id /= a.pool.heads;
+  const int tile0 = id % row_tiles;
+  id /= row_tiles;
+  const int b = id % a.pool.batch, split = id / a.pool.batch;
   const int group = a.q.heads / a.pool.heads;
   const int page = a.pool.page, gpp = page >> 4;  // 16-key pieces a page
 
@@ -61,7 +68,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
   const int row0 = seq.row0, news = seq.news, len = seq.len;
   const int rows = news * group;
 
-  for (int tile = blockIdx.y / a.pool.heads; tile * 16 < rows; tile += row_tiles) {
+  for (int tile = tile0; tile * 16 < rows; tile += row_tiles) {
     const int r = tile * 16 + i16;
     const bool live = r < rows;
     const int t = min(r, rows - 1) / group;
@@ -189,8 +196,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int q = 0; q < NP; ++q) nan |= ks[x][q] > kScaleMax;
-          static_assert(kScaleMax == 252, "bytes from 253 on");
-          nan |= ((cur.vs[x] & 0x7f7f7f7fu) + 0x03030303u) & cur.vs[x] & 0x80808080u;
+          nan |= nan_bytes(cur.vs[x]);
         }
         const bool odd = j < all_lo || j + 32 > all_hi || !cur.have[0] || !cur.have[1] || __any(nan != 0);
         uint32_t poison = 0;  // this row's keys whose value is NaN
@@ -199,32 +205,26 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
           for (int x = 0; x < 2; ++x) {
             uint64_t kn = __ballot(ks[x][0] > kScaleMax);
             kn |= kn >> 32;
-            kn |= kn >> 16;
-            uint32_t w[4 * NP];
-#pragma unroll
-            for (int q = 0; q < NP; ++q) {
-              const uint4 y = cur.vw[x][q];
-              w[4 * q] = y.x, w[4 * q + 1] = y.y, w[4 * q + 2] = y.z, w[4 * q + 3] = y.w;
-            }
+            const uint32_t kn32 = (uint32_t)kn | (uint32_t)kn >> 16;
+            const int k = j + 16 * x + 4 * g;  // this lane's four keys
+            const uint32_t seen = cur.have[x] ? bits_between(sp.lo - k, sp.hi - k) : 0u;
+            const uint32_t bad = cur.have[x] ? nan_bytes(cur.vs[x]) : 0x80808080u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = j + 16 * x + 4 * g + e;
-              const bool seen = cur.have[x] && key >= sp.lo && key < sp.hi;
-              const uint32_t vb = (cur.vs[x] >> (8 * e)) & 255u;
-              float& pe = p[4 * x + e];
-              pe = !seen ? kNone : (kn >> (4 * g + e)) & 1 ? __builtin_nanf("") : pe;
+              const uint32_t keep = spread(seen, e), gone_v = spread(bad, 8 * e + 7);
+              p[4 * x + e] = __uint_as_float((__float_as_uint(p[4 * x + e]) & keep) | (kNoneBits & ~keep) |
+                                             (spread(kn32 >> (4 * g), e) & keep & kNanBits));
               // A NaN value must not reach the rows that do not see it (0 * NaN):
               // it goes out of V, and into the weight of those that do.
-              if (seen && vb > kScaleMax) poison |= 1u << (4 * x + e);
-              if (!cur.have[x] || vb > kScaleMax) {
-                cur.vs[x] = (cur.vs[x] & ~(255u << (8 * e))) | (127u << (8 * e));
+              poison |= (keep & gone_v & 1u) << (4 * x + e);
+              cur.vs[x] = (cur.vs[x] & ~(gone_v & 255u << (8 * e))) | (gone_v & 127u << (8 * e));
 #pragma unroll
-                for (int q = 0; q < NP; ++q) w[4 * q + e] = 0;
+              for (int q = 0; q < NP; ++q) {
+                uint4& y = cur.vw[x][q];
+                uint32_t& w = e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w;
+                w &= ~gone_v;
               }
             }
-#pragma unroll
-            for (int q = 0; q < NP; ++q)
-              cur.vw[x][q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
           }
         }
         // The maximum is only followed when a weight would pass 2^8: until
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
         if (__any(poison != 0)) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (poison >> e & 1) p[e] = __builtin_nanf("");
+            p[e] = __uint_as_float(__float_as_uint(p[e]) | (spread(poison, e) & kNanBits));
         }
         uint32_t pw[T][4];
 #pragma unroll
@@ -262,27 +262,28 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
         // O^T
         float vsc[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vsc[e] = scale_value((cur.vs[e >> 2] >> (8 * (e & 3))) & 255u);
+        for (int e = 0; e < 8; ++e) vsc[e] = scale_at(cur.vs[e >> 2], e & 3);
 #pragma unroll
         for (int c = 0; c < NP; ++c) {
-          uint32_t d[8][4];  // [key][value pair]
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 y = cur.vw[e >> 2][c];
-            uint32_t w = (e & 3) == 0 ? y.x : (e & 3) == 1 ? y.y : (e & 3) == 2 ? y.z : y.w;
-            if constexpr (D == 64) w >>= 16 * (i16 & 1);
-            decode8(w, vsc[e], d[e]);
-          }
+          for (int f = 0; f < (F < 8 ? F : 8); f += 2) {
+            uint32_t d[8];  // values f and f + 1 of each key
 #pragma unroll
-          for (int f = 0; f < (F < 8 ? F : 8); ++f) {
-            const uint32_t sel = f & 1 ? 0x07060302u : 0x05040100u;
-            const bf16x8_t vf = frag(__builtin_amdgcn_perm(d[1][f >> 1], d[0][f >> 1], sel),
-                                     __builtin_amdgcn_perm(d[3][f >> 1], d[2][f >> 1], sel),
-                                     __builtin_amdgcn_perm(d[5][f >> 1], d[4][f >> 1], sel),
-                                     __builtin_amdgcn_perm(d[7][f >> 1], d[6][f >> 1], sel));
+            for (int e = 0; e < 8; ++e) {
+              const uint4 y = cur.vw[e >> 2][c];
+              uint32_t w = (e & 3) == 0 ? y.x : (e & 3) == 1 ? y.y : (e & 3) == 2 ? y.z : y.w;
+              if constexpr (D == 64) w >>= 16 * (i16 & 1);
+              d[e] = decode2(w, vsc[e], f >> 1);
+            }
 #pragma unroll
-            for (int y = T - 1; y >= 0; --y)
-              o[8 * c + f] = mfma16(vf, frag(pw[y][0], pw[y][1], pw[y][2], pw[y][3]), o[8 * c + f]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t sel = h ? 0x07060302u : 0x05040100u;
+              const bf16x8_t vf = frag(__builtin_amdgcn_perm(d[1], d[0], sel), __builtin_amdgcn_perm(d[3], d[2], sel),
+                                       __builtin_amdgcn_perm(d[5], d[4], sel), __builtin_amdgcn_perm(d[7], d[6], sel));
+#pragma unroll
+              for (int y = T - 1; y >= 0; --y)
+                o[8 * c + f + h] = mfma16(vf, frag(pw[y][0], pw[y][1], pw[y][2], pw[y][3]), o[8 * c + f + h]);
+            }
           }
         }
       }
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
     }
     __syncthreads();
     if (wave == 0 && live) {
-#pragma unroll
+#pragma unroll 1  // all at once would need the most registers of the kernel
       for (int w = 0; w < kFewWaves - 1; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -452,11 +453,14 @@ int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, i
     *each = 0;
     return (int)(want < 1 ? 1 : want);
   }
-  // Stretches that give about 2048 workgroups of four waves (eight a CU, so
-  // that sequences shorter than max_kv leave enough of them), of 512 keys or
-  // more where there are many and 128 at least.
+  // Stretches that give 512 workgroups of four waves, or 1024 where some
+  // sequences may be shorter than max_kv; of 512 keys or more where there is
+  // much to do (each workgroup loads its rows and hands in its sums), and of
+  // 128 at least. 1 token over 128k keys: 512 take 35.4 us, 768 36.8, 1024
+  // 40.6, 2304 44.0; 32 ragged sequences: 1024 128.8 us, 2048 129.9, 6144 134.4.
   const int64_t tiles = (rows + 15) / 16 * kv_heads * batch;
-  int64_t e = keys * tiles / 2048;
+  const int64_t want = batch > 1 ? 1024 : 512;
+  int64_t e = (keys * tiles + want - 1) / want;
   const int64_t least = keys * tiles < 512 * 256 ? 128 : 512;
   if (e < least) e = least;
   if (e > (1 << 20)) e = 1 << 20;
@@ -471,8 +475,9 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int group = a.q.heads / a.pool.heads;
   if (attn_many((int64_t)a.max_new * group, a.f32, a.pool.dim)) return launch_attend_many(a, s);
   int64_t tiles = ((int64_t)a.max_new * group + 15) / 16;
-  if (tiles * a.pool.heads > 65535) tiles = 65535 / a.pool.heads;
-  const dim3 grid(a.splits, (uint32_t)(tiles * a.pool.heads), a.pool.batch);
+  const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads * a.pool.batch);
+  if (tiles > most) tiles = most < 1 ? 1 : most;  // a workgroup then takes several
+  const uint32_t grid = (uint32_t)(tiles * a.splits * a.pool.heads * a.pool.batch);
 #define TTT_CALL(D, T, F) attend_few_kernel<D, T, F><<<grid, 64 * kFewWaves, 0, s>>>(a, (int)tiles)
   switch (a.pool.dim) {
     case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;

@@ -31,6 +31,12 @@ __device__ __forceinline__ uint32_t scale_byte(float a) {
 
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// Byte e of a word as a scale for the conversions below, which read the
+// exponent field alone: the byte is shifted there, whatever comes with it.
+__device__ __forceinline__ float scale_at(uint32_t w, int e) {
+  return __uint_as_float(e == 0 ? w << 23 : e == 1 ? w << 15 : e == 2 ? w << 7 : w >> 1);
+}
+
 // Eight values divided by the scale, as codes, the first in the low bits:
 // nearest, ties to the even code, saturating (v_cvt_scalef32_pk_fp4_f32).
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float scale) {
@@ -46,6 +52,15 @@ __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float scale) {
 template <int SEL>
 __device__ __forceinline__ uint32_t decode2(uint32_t w, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+}
+
+__device__ __forceinline__ uint32_t decode2(uint32_t w, float scale, int sel) {
+  switch (sel) {  // folded where sel is known
+    case 0: return decode2<0>(w, scale);
+    case 1: return decode2<1>(w, scale);
+    case 2: return decode2<2>(w, scale);
+    default: return decode2<3>(w, scale);
+  }
 }
 
 __device__ __forceinline__ void decode8(uint32_t w, float scale, uint32_t (&v)[4]) {
