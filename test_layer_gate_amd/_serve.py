@@ -9,6 +9,7 @@ built positionally and tensors are passed as plain addresses.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -49,6 +50,7 @@ class Attn(ctypes.Structure):
 
 
 _lib = None
+_ref = ctypes.byref
 
 
 def _L():
@@ -73,52 +75,85 @@ def _L():
     return L
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# The current stream's handle without building a torch.cuda.Stream (2.9 us of
+# a call's 10) where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t, what, dtype=None, dim=None):
-    """The view [rows, heads, dim] (or [B, T, heads, dim] whose sequences
-    follow each other evenly) as the library takes it."""
+def _stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _empty(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _rows_of(t, what):
+    """(rows, heads, dim), (token stride, head stride) of the view [rows,
+    heads, dim], or [B, T, heads, dim] whose sequences follow each other
+    evenly."""
     if not t.is_cuda:
         raise ValueError("all tensors must be on the GPU")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     shape, st = t.shape, t.stride()
     if len(shape) == 4:
         if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
             raise ValueError(f"{what}: the sequences of a [B, T, heads, dim] tensor must follow "
                              "each other at T times the token stride")
         ts = st[1] if shape[1] > 1 else st[0]
-        shape, st = (shape[0] * shape[1],) + tuple(shape[2:]), (ts,) + tuple(st[2:])
-    if len(shape) != 3:
+        shape, st = (shape[0] * shape[1], shape[2], shape[3]), (ts, st[2], st[3])
+    elif len(shape) != 3:
         raise ValueError(f"{what} must be [rows, heads, dim] or [B, T, heads, dim]")
-    if shape[2] > 1 and st[2] != 1:
+    n, h, d = shape
+    if d > 1 and st[2] != 1:
         raise ValueError(f"{what}: the values of a head must be contiguous")
-    if dim is not None and shape[2] != dim:
-        raise ValueError(f"{what}: head dim {shape[2]}, expected {dim}")
     # the stride of an axis of length 1 means nothing: any aligned one will do
-    return Rows(t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2],
-                st[1] if shape[1] > 1 else shape[2], shape[1], 0), shape[0], shape[2]
+    return n, h, d, Rows(t.data_ptr(), st[0] if n > 1 else h * d, st[1] if h > 1 else d, h, 0)
+
+
+def _rows(t, what, n, dim, dtype):
+    """The view as the library takes it, of `n` rows of heads of `dim`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    m, _, d, r = _rows_of(t, what)
+    if m != n or d != dim:
+        raise ValueError(f"{what} must have {n} rows and heads of {dim}, got {m} and {d}")
+    return r
 
 
 def _ints(t, what, shape=None):
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor on the GPU")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
+def _positions(t, n):
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError("positions must have one entry a row")
+    return _ints(t, "positions")
+
+
+def _act(t, what):
+    d = t.dtype
+    return 0 if d is torch.bfloat16 else 1 if d is torch.float32 else _b._dtype_code(t, what)
+
+
 def _rope(table, interleaved):
-    if (table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32
+    shape = table.shape
+    if (len(shape) != 3 or shape[2] != 2 or table.dtype is not torch.float32
             or not table.is_cuda or not table.is_contiguous()):
         raise ValueError("the rope table must be a contiguous float32 [max_pos, rot_dim / 2, 2] "
                          "tensor on the GPU")
-    return Rope(table.data_ptr(), 2 * table.shape[1], table.shape[0],
-                ROPE_INTERLEAVED if interleaved else 0, 0)
+    return Rope(table.data_ptr(), 2 * shape[1], shape[0], ROPE_INTERLEAVED if interleaved else 0, 0)
 
 
 def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, original=None,
@@ -141,36 +176,25 @@ def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, orig
     sc = RopeScaling(ROPE_KINDS.get(scaling, 0), 0, float(factor), float(original or 1.0),
                      float(low), float(high), float(amplitude))
     _b._check(_L().ttt_rope_table(table.data_ptr(), int(max_pos), int(rot_dim), float(base),
-                                  ctypes.byref(sc), _stream(stream)))
+                                  ctypes.byref(sc), _stream(stream, table)))
     return table
 
 
 def _rope_call(fn, q, k, table, positions, interleaved, q_out, k_out, stream):
-    rq, n, dim = _rows(q, "q")
-    act = _b._dtype_code(q, "q")
-    seq = q.shape[1] if q.dim() == 4 else n
+    n, _, dim, rq = _rows_of(q, "q")
+    act, dtype = _act(q, "q"), q.dtype
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ro, no, _ = _rows(q_out, "q_out", q.dtype, dim)
-    rk = rko = None
+        q_out = _empty(q)
+    ro = _rows(q_out, "q_out", n, dim, dtype)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        rk, nk, _ = _rows(k, "k", q.dtype, dim)
-        rko, nko, _ = _rows(k_out, "k_out", q.dtype, dim)
-        if nk != n or nko != n:
-            raise ValueError("q, k and their outputs must have the same rows")
-    if no != n:
-        raise ValueError("q and q_out must have the same rows")
-    rope = _rope(table, interleaved)
-    pos = None
-    if positions is not None:
-        if positions.numel() != n:
-            raise ValueError("positions must have one entry a row")
-        pos = _ints(positions, "positions")
-    ref = ctypes.byref
-    st = fn(n, max(seq, 1), dim, act, ref(rope), pos, ref(rq), ref(rk) if rk is not None else None, ref(ro),
-            ref(rko) if rko is not None else None, _stream(stream))
+            k_out = _empty(k)
+        rk, rko = _ref(_rows(k, "k", n, dim, dtype)), _ref(_rows(k_out, "k_out", n, dim, dtype))
+    else:
+        rk = rko = None
+    st = fn(n, max(q.shape[1], 1) if q.dim() == 4 else max(n, 1), dim, act,
+            _ref(_rope(table, interleaved)), _positions(positions, n), _ref(rq), rk, _ref(ro), rko,
+            _stream(stream, q))
     if st:
         _b._check(st)
     return q_out, k_out
@@ -208,10 +232,10 @@ def kv_pages(n_pages, page_size, kv_heads, head_dim, device="cuda"):
 
 
 def _cache(pages, page_table, kv_lens, q_starts, dim):
-    if pages.dim() != 3 or pages.dtype != torch.uint8 or not pages.is_cuda:
+    shape, st = pages.shape, pages.stride()
+    if len(shape) != 3 or pages.dtype is not torch.uint8 or not pages.is_cuda:
         raise ValueError("pages must be a uint8 [n_pages, kv_heads, bytes] tensor on the GPU")
-    n_pages, heads, block = pages.shape
-    st = pages.stride()
+    n_pages, heads, block = shape
     if st[2] != 1 or (heads > 1 and st[1] != block):
         raise ValueError("a page's heads must be contiguous")
     page, rest = divmod(block * 16, dim * 17)
@@ -219,11 +243,11 @@ def _cache(pages, page_table, kv_lens, q_starts, dim):
         raise ValueError(f"{block} bytes a head are no whole number of tokens of dim {dim}")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch, max_pages]")
-    batch = page_table.shape[0]
+    batch, max_pages = page_table.shape
     return Cache(pages.data_ptr(), st[0] if n_pages > 1 else heads * block,
                  _ints(page_table, "page_table"), _ints(kv_lens, "kv_lens", (batch,)),
-                 _ints(q_starts, "q_starts", (batch + 1,)), batch, page_table.shape[1], n_pages,
-                 page, heads, dim, 0)
+                 _ints(q_starts, "q_starts", (batch + 1,)), batch, max_pages, n_pages, page, heads,
+                 dim, 0)
 
 
 def kv_append(pages, page_table, kv_lens, k, v, *, q=None, q_starts=None, rope_table=None,
@@ -233,32 +257,20 @@ def kv_append(pages, page_table, kv_lens, k, v, *, q=None, q_starts=None, rope_t
     [batch] with the new tokens counted, q_starts int32 [batch + 1] (None:
     the same number of rows each). With rope_table, k is rotated first, and
     q, if given, beside it. Returns the rotated q (or None)."""
-    rk, n, dim = _rows(k, "k")
-    act = _b._dtype_code(k, "k")
-    rv, nv, _ = _rows(v, "v", k.dtype, dim)
-    if nv != n:
-        raise ValueError("k and v must have the same rows")
+    n, _, dim, rk = _rows_of(k, "k")
+    act, dtype = _act(k, "k"), k.dtype
+    rv = _rows(v, "v", n, dim, dtype)
     cache = _cache(pages, page_table, kv_lens, q_starts, dim)
-    ref = ctypes.byref
     rq = ro = None
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        rq, nq, _ = _rows(q, "q", k.dtype, dim)
-        ro, no, _ = _rows(q_out, "q_out", k.dtype, dim)
-        if nq != n or no != n:
-            raise ValueError("q, q_out and k must have the same rows")
+            q_out = _empty(q)
+        rq, ro = _ref(_rows(q, "q", n, dim, dtype)), _ref(_rows(q_out, "q_out", n, dim, dtype))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rope = None if rope_table is None else _rope(rope_table, interleaved)
-    pos = None
-    if positions is not None:
-        if positions.numel() != n:
-            raise ValueError("positions must have one entry a row")
-        pos = _ints(positions, "positions")
-    st = _L().ttt_kv_append(ref(cache), n, act, ref(rk), ref(rv), None if rq is None else ref(rq),
-                            None if ro is None else ref(ro), None if rope is None else ref(rope),
-                            pos, _stream(stream))
+    st = _L().ttt_kv_append(_ref(cache), n, act, _ref(rk), _ref(rv), rq, ro,
+                            None if rope_table is None else _ref(_rope(rope_table, interleaved)),
+                            _positions(positions, n), _stream(stream, k))
     if st:
         _b._check(st)
     return q_out
@@ -275,30 +287,28 @@ def kv_read(pages, page_table, kv_lens, rows, head_dim, dtype=torch.bfloat16, *,
         k_out = torch.empty(shape, dtype=dtype, device=pages.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=pages.device)
-    rk, nk, _ = _rows(k_out, "k_out", dtype, head_dim)
-    rv, nv, _ = _rows(v_out, "v_out", dtype, head_dim)
-    if nk != rows or nv != rows:
-        raise ValueError("k_out and v_out must have `rows` rows")
-    st = _L().ttt_kv_read(ctypes.byref(cache), rows, _b._dtype_code(k_out, "k_out"),
-                          ctypes.byref(rk), ctypes.byref(rv), _stream(stream))
+    rk = _rows(k_out, "k_out", rows, head_dim, dtype)
+    rv = _rows(v_out, "v_out", rows, head_dim, dtype)
+    st = _L().ttt_kv_read(_ref(cache), rows, _act(k_out, "k_out"), _ref(rk), _ref(rv),
+                          _stream(stream, pages))
     if st:
         _b._check(st)
     return k_out, v_out
 
 
-def _attn(scale, window, max_new, max_kv, causal, dim):
-    return Attn(dim ** -0.5 if scale is None else scale, window, max_new, max_kv,
-                0 if causal else ATTN_ALL_KEYS, 0)
+@functools.lru_cache(maxsize=1024)  # of sizes alone
+def _workspace(batch, rows, act, kv_heads, q_heads, dim, max_new, max_kv, window):
+    n = ctypes.c_size_t(0)
+    a = Attn(1.0, window, max_new, max_kv, 0, 0)
+    _b._check(_L().ttt_kv_attention_workspace_size(_ref(a), batch, rows, act, kv_heads, q_heads, dim,
+                                                   _ref(n)))
+    return n.value
 
 
 def kv_attention_workspace_size(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bfloat16, *,
                                 max_new, max_kv, window=0) -> int:
-    n = ctypes.c_size_t(0)
-    a = _attn(None, window, max_new, max_kv, True, head_dim)
     act = _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16
-    _b._check(_L().ttt_kv_attention_workspace_size(ctypes.byref(a), batch, rows, act, kv_heads,
-                                                   q_heads, head_dim, ctypes.byref(n)))
-    return n.value
+    return _workspace(batch, rows, act, kv_heads, q_heads, head_dim, max_new, max_kv, window)
 
 
 def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, max_kv=None,
@@ -311,37 +321,31 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     the sequences' rows and lengths, where the caller knows better ones than
     `rows` and what the page table can hold. Returns o, or (o, lse) with
     with_lse (lse float32 [rows, q_heads])."""
-    rq, n, dim = _rows(q, "q")
-    act = _b._dtype_code(q, "q")
+    n, heads, dim, rq = _rows_of(q, "q")
+    act = _act(q, "q")
     cache = _cache(pages, page_table, kv_lens, q_starts, dim)
     if max_new is None:
         max_new = max(1, n if q_starts is not None else n // cache.batch)
     if max_kv is None:
         max_kv = cache.max_pages * cache.page_size
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ro, no, _ = _rows(out, "out", q.dtype, dim)
-    if no != n:
-        raise ValueError("q and out must have the same rows")
+        out = _empty(q)
+    ro = _rows(out, "out", n, dim, q.dtype)
     if lse is None:
         if with_lse:
-            lse = torch.empty((n, rq.heads), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != n * rq.heads:
+            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    elif lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != n * heads:
         raise ValueError("lse must be a contiguous float32 [rows, q_heads] tensor")
-    a = _attn(scale, window, max_new, max_kv, causal, dim)
-    L, ref = _L(), ctypes.byref
+    a = Attn(dim ** -0.5 if scale is None else scale, window, max_new, max_kv,
+             0 if causal else ATTN_ALL_KEYS, 0)
     if workspace is None:
-        need = ctypes.c_size_t(0)
-        st = L.ttt_kv_attention_workspace_size(ref(a), cache.batch, n, act, cache.kv_heads,
-                                               rq.heads, dim, ref(need))
-        if st:
-            _b._check(st)
-        if need.value:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    st = L.ttt_kv_attention(ref(cache), ref(a), n, act, ref(rq), ref(ro),
-                            None if lse is None else lse.data_ptr(),
-                            None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.numel(), _stream(stream))
+        need = _workspace(cache.batch, n, act, cache.kv_heads, heads, dim, max_new, max_kv, window)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = _L().ttt_kv_attention(_ref(cache), _ref(a), n, act, _ref(rq), _ref(ro),
+                               None if lse is None else lse.data_ptr(),
+                               None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel(), _stream(stream, q))
     if st:
         _b._check(st)
     return (out, lse) if with_lse or lse is not None else out
