@@ -28,8 +28,20 @@ namespace {
 // neighbouring values of key i; of the result it holds, for row i, keys 4g .. 4g + 3 of either 16. Those eight are what the second product
 // O^T = V^T P^T (16x16x32) asks of it: the order of the contraction is free as
 // long as V agrees, so P goes over without a move between lanes. Of V it
-// brings the same eight keys' values i D / 16 .. + D / 16 - 1.
-constexpr int kFewWaves = 4;
+// brings the same eight keys' values i D / 16 .. + D / 16 - 1. NW waves share
+// a workgroup's stretch of keys and join in LDS.
+
+// Loads of an address put together from integers, which has to be marked as
+// global memory's.
+typedef const __attribute__((address_space(1))) uint8_t* Global;
+__device__ __forceinline__ uint4 load16(Global p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 w = *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(p);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t load4(Global p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p);
+}
 
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
 template <int D>
@@ -40,13 +52,14 @@ struct FewTile {
   bool have[2];
 };
 
-template <int D, int T, bool F32>
-__global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void attend_few_kernel(AttnLaunch a, int row_tiles) {
+template <int D, int T, bool F32, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void attend_few_kernel(
+    AttnLaunch a, int row_tiles) {
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
-  __shared__ float red_o[kFewWaves - 1][16][D + 4];
-  __shared__ float red_ml[kFewWaves][16][2];
+  __shared__ float red_o[NW - 1][16][D + 4];
+  __shared__ float red_ml[NW][16][2];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -103,31 +116,34 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
     for (int f = 0; f < F; ++f) o[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     float m = kNone, ms = 0.f, l = 0.f;  // maximum (unscaled), its scaled value (0 for none), sum
 
-    const int k_lane = i16 * (D / 2) + (D == 64 ? g >> 1 : g * NP) * 16;
-    const int v_lane = page * (D / 2) + g * (2 * D) + (D == 64 ? (i16 >> 1) * 16 : i16 * (D / 8));
+    const uint32_t k_lane = i16 * (D / 2) + (D == 64 ? g >> 1 : g * NP) * 16;
+    const uint32_t v_lane = page * (D / 2) + g * (2 * D) + (D == 64 ? (i16 >> 1) * 16 : i16 * (D / 8));
     // K's scales are read as words (a byte load's widening would be waited for
     // at once) and cut to the lane's byte where they are used.
-    const int ks_lane = page * D + (D == 64 ? (i16 >> 1) * 4 : D == 128 ? i16 * 4 : i16 * 8 + (g >> 1) * 4);
+    const uint32_t ks_lane = page * D + (D == 64 ? (i16 >> 1) * 4 : D == 128 ? i16 * 4 : i16 * 8 + (g >> 1) * 4);
     const int ks_shift = D == 64 ? 16 * (i16 & 1) + 8 * (g >> 1) : D == 128 ? 8 * g : 16 * (g & 1);
-    const int vs_lane = page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + 4 * g;
+    const uint32_t vs_lane = page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + 4 * g;
 
     // This split's stretches of `each` keys, a quarter of each for every wave.
     for (int s0 = lo + split * a.each; s0 < hi; s0 += a.splits * a.each) {
-      const int per = a.each / kFewWaves;
+      const int per = a.each / NW;
       const int k0 = s0 + wave * per, k1 = min(hi, k0 + per);
-      int64_t my_block = 0;  // where 64 pieces of 16 keys lie: one a lane
-      int my_off = 0;
-      uint64_t gone = 0;     // those that have no page, or are past the end
+      // Where 64 pieces of 16 keys lie, one a lane: the address of the head's
+      // block and the first key's place in it. Loads take the address from
+      // scalar registers and a 32-bit offset of the lane's.
+      uint64_t my_block = (uint64_t)a.pool.pages;
+      uint32_t my_off = 0;
+      uint64_t gone = 0;  // pieces that have no page, or are past the end
       auto find = [&](int base) {
         const int piece = (base >> 4) + lane;
         const int pg = piece / gpp;
-        my_block = 0, my_off = 0;
+        my_block = (uint64_t)a.pool.pages, my_off = 0;
         bool ok = pg < a.pool.max_pages && piece * 16 < k1;
         if (ok) {
           const int id = a.pool.table[(int64_t)b * a.pool.max_pages + pg];
           ok = (uint32_t)id < (uint32_t)a.pool.n_pages;
           if (ok) {
-            my_block = id * a.pool.page_stride + hk * head_block_bytes(page, D);
+            my_block += id * a.pool.page_stride + hk * head_block_bytes(page, D);
             my_off = (piece - pg * gpp) * 16;
           }
         }
@@ -138,17 +154,16 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
         for (int u = 0; u < 2; ++u) {
           const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)my_block, src + u);
           const uint32_t hi32 = __builtin_amdgcn_readlane((int)(my_block >> 32), src + u);
-          const int off = __builtin_amdgcn_readlane(my_off, src + u);
+          const uint32_t off = __builtin_amdgcn_readlane((int)my_off, src + u);
           x.have[u] = (gone >> (src + u) & 1) == 0;
-          const uint8_t* bp = a.pool.pages + ((uint64_t)hi32 << 32 | lo32);
-          const uint8_t* cp = bp + off * (D / 2);
+          const Global bp = reinterpret_cast<Global>((uint64_t)hi32 << 32 | lo32);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            x.kw[u][p] = *reinterpret_cast<const uint4*>(cp + k_lane + 16 * p);
-            x.vw[u][p] = *reinterpret_cast<const uint4*>(cp + v_lane + 16 * p);
+            x.kw[u][p] = load16(bp + (k_lane + off * (D / 2)) + 16 * p);
+            x.vw[u][p] = load16(bp + (v_lane + off * (D / 2)) + 16 * p);
           }
-          x.ks[u] = *reinterpret_cast<const uint32_t*>(bp + off * (D / 32) + ks_lane);
-          x.vs[u] = *reinterpret_cast<const uint32_t*>(bp + off + vs_lane);
+          x.ks[u] = load4(bp + (ks_lane + off * (D / 32)));
+          x.vs[u] = load4(bp + (vs_lane + off));
         }
       };
       FewTile<D> cur, nxt;
@@ -194,9 +209,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
         uint32_t nan = 0;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-#pragma unroll
-          for (int q = 0; q < NP; ++q) nan |= ks[x][q] > kScaleMax;
-          nan |= nan_bytes(cur.vs[x]);
+          nan |= nan_bytes(cur.ks[x]) | nan_bytes(cur.vs[x]);
         }
         const bool odd = j < all_lo || j + 32 > all_hi || !cur.have[0] || !cur.have[1] || __any(nan != 0);
         uint32_t poison = 0;  // this row's keys whose value is NaN
@@ -298,11 +311,11 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
     __syncthreads();
     float mj = kNone;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) mj = fmaxf(mj, red_ml[w][i16][0]);
+    for (int w = 0; w < NW; ++w) mj = fmaxf(mj, red_ml[w][i16][0]);
     const float mj0 = mj == kNone ? 0.f : mj;
     float lj = 0.f;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w)
+    for (int w = 0; w < NW; ++w)
       lj += red_ml[w][i16][1] * __builtin_amdgcn_exp2f(red_ml[w][i16][0] - mj0);
     const float al = __builtin_amdgcn_exp2f(m - mj0);
 #pragma unroll
@@ -321,7 +334,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 && F32 ? 1 : 2) void atten
     __syncthreads();
     if (wave == 0 && live) {
 #pragma unroll 1  // all at once would need the most registers of the kernel
-      for (int w = 0; w < kFewWaves - 1; ++w)
+      for (int w = 0; w < NW - 1; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -436,6 +449,13 @@ namespace {
 
 // Rows of one sequence and key head from which the many-row kernel is taken.
 constexpr int kManyFrom = 64;
+// Keys up to which one workgroup of the few-row kernel takes a whole sequence,
+// without the join's launch and its workspace. On the GPU alone (32/8 heads)
+// one sequence of 512 keys takes 7.5 us so and 7.8 in parts, of 1024 9.6 and
+// 8.0, of 2048 14.2 and 8.4; 16 sequences of 1024 10.0 and 10.7. A launch and
+// an allocation saved are 4 us of the caller's time, which is what a call as
+// short as this waits for.
+constexpr int kOneGroup = 1024;
 
 }  // namespace
 
@@ -452,6 +472,11 @@ int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, i
     if (want > most) want = most;
     *each = 0;
     return (int)(want < 1 ? 1 : want);
+  }
+  // A short sequence is one workgroup of eight waves: no join, no workspace.
+  if (keys <= kOneGroup) {
+    *each = (int)((keys + 255) & ~(int64_t)255);
+    return 1;
   }
   // Stretches that give 512 workgroups of four waves, or 1024 where some
   // sequences may be shorter than max_kv; of 512 keys or more where there is
@@ -478,7 +503,13 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads * a.pool.batch);
   if (tiles > most) tiles = most < 1 ? 1 : most;  // a workgroup then takes several
   const uint32_t grid = (uint32_t)(tiles * a.splits * a.pool.heads * a.pool.batch);
-#define TTT_CALL(D, T, F) attend_few_kernel<D, T, F><<<grid, 64 * kFewWaves, 0, s>>>(a, (int)tiles)
+  // (wide fp32 heads need the registers that eight waves do not have)
+  const bool wide = a.splits == 1 && a.each <= kOneGroup && !(a.f32 && a.pool.dim == 256);
+#define TTT_CALL(D, T, F)                                             \
+  if (wide)                                                           \
+    attend_few_kernel<D, T, F, F && D == 256 ? 4 : 8><<<grid, 512, 0, s>>>(a, (int)tiles); \
+  else                                                                \
+    attend_few_kernel<D, T, F, 4><<<grid, 256, 0, s>>>(a, (int)tiles)
   switch (a.pool.dim) {
     case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
     case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
