@@ -29,10 +29,13 @@ namespace {
 // values both.
 constexpr int kManyKeys = 64;
 
-// Which of a tile's keys have no page, are NaN, or have a NaN value: one bit a
-// key, 32 keys a word.
-struct TileMarks {
-  uint32_t absent[2], knan[2], vnan[2];
+// Which of a tile's keys have no page or are NaN, and which have a NaN value:
+// one bit a key, 32 keys a word.
+struct KeyMarks {
+  uint32_t absent[2], nan[2];
+};
+struct ValueMarks {
+  uint32_t nan[2];
 };
 
 template <int D>
@@ -74,14 +77,14 @@ __device__ __forceinline__ void fetch(Raw<D>& r, const AttnLaunch& a, bool is_v,
 
 template <int D>
 __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t* kbuf, uint8_t* vbuf,
-                                       TileMarks* marks, int lane) {
+                                       KeyMarks* kmarks, ValueMarks* vmarks, int lane) {
   if (!r.have) {  // no such page, or past the end: zeros, which no row counts
 #pragma unroll
     for (int u = 0; u < Raw<D>::kUnits; ++u) {
       r.w[u] = make_uint4(0, 0, 0, 0);
       r.s[u] = 0x7f7f7f7fu;
     }
-    if (lane == 0 && !is_v) atomicOr(&marks->absent[piece >> 1], 0xffffu << (16 * (piece & 1)));
+    if (lane == 0 && !is_v) atomicOr(&kmarks->absent[piece >> 1], 0xffffu << (16 * (piece & 1)));
   }
 #pragma unroll
   for (int u = 0; u < Raw<D>::kUnits; ++u) {
@@ -95,7 +98,7 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (bad >> (8 * e + 7) & 1) {
-            atomicOr(&marks->vnan[piece >> 1], 1u << (16 * (piece & 1) + 4 * q + e));
+            atomicOr(&vmarks->nan[piece >> 1], 1u << (16 * (piece & 1) + 4 * q + e));
             w[e] = 0;
             r.s[u] = (r.s[u] & ~(255u << (8 * e))) | (127u << (8 * e));
           }
@@ -117,7 +120,7 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
       const bool live = unit_live<D>(lane);
       const int c = n >> 4, t = n & 15;
       if (__any(live && r.s[u] > kScaleMax) && live && r.s[u] > kScaleMax)
-        atomicOr(&marks->knan[piece >> 1], 1u << (16 * (piece & 1) + t));
+        atomicOr(&kmarks->nan[piece >> 1], 1u << (16 * (piece & 1) + t));
       if (!live) continue;
       const float sc = scale_at(r.s[u], 0);
       const uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
@@ -136,13 +139,13 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
 template <int D, int T, bool F32>
 __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(AttnLaunch a, int row_tiles) {
   constexpr int NW = many_waves(D, F32), kManyRows = 32 * NW;
-  constexpr int KINDS = 8 / NW;          // of keys and values, what one wave decodes
   constexpr int KS = D / 16;             // steps of the first product
   constexpr int NT = D / 32;             // fragments of V^T
-  constexpr int SUB = 2;                 // 32-key tiles whose scores are held at once
-  __shared__ __attribute__((aligned(16))) uint8_t kbuf[2][kManyKeys * D * 2];
+  constexpr int KB = D == 256 ? 2 : 3;   // tiles of keys in LDS
+  __shared__ __attribute__((aligned(16))) uint8_t kbuf[KB][kManyKeys * D * 2];
   __shared__ __attribute__((aligned(16))) uint8_t vbuf[2][kManyKeys * D * 2];
-  __shared__ TileMarks marks[3];
+  __shared__ KeyMarks kmarks[4];
+  __shared__ ValueMarks vmarks[3];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -201,144 +204,208 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       for (int e = 0; e < 16; ++e) o[f][e] = 0.f;
     float m = kNone, ms = 0.f, l = 0.f;  // maximum (unscaled), its scaled value (0 for none), sum
 
-    // This wave's 16 tokens of the tile at key j.
-    auto lookup = [&](int j, int* off) {
-      const int key = j + 16 * piece, pg = key / page;
-      *off = key - pg * page;
-      return key < s1 && pg < a.pool.max_pages ? a.pool.table[(int64_t)b * a.pool.max_pages + pg] : -1;
+    // Tile t holds the keys from s0 + 64 t. Where this wave's 16 of its tokens lie:
+    const int tiles = (max(s1 - s0, 0) + kManyKeys - 1) / kManyKeys;
+    struct Place {
+      int id, off;
+    };
+    auto lookup = [&](int t) {
+      const int key = s0 + t * kManyKeys + 16 * piece, pg = key / page;
+      Place p;
+      p.off = key - pg * page;
+      p.id = key < s1 && pg < a.pool.max_pages ? a.pool.table[(int64_t)b * a.pool.max_pages + pg] : -1;
+      return p;
+    };
+    auto fetch_tile = [&](Raw<D>& r, bool is_v, Place p) {
+      fetch<D>(r, a, is_v, hk, p.id, p.off, p.id >= 0, lane);
+    };
+    auto unpack_tile = [&](Raw<D>& r, bool is_v, int t) {
+      unpack<D>(r, is_v, piece, kbuf[t % KB], vbuf[t & 1], &kmarks[t & 3], &vmarks[t % 3], lane);
     };
 
-    __syncthreads();  // the last tile of rows is done with LDS
-    if (threadIdx.x < 3) marks[threadIdx.x] = TileMarks{};
-    __syncthreads();
-    Raw<D> raw[KINDS];
-    int off, next = lookup(s0, &off);
-    auto fetch_all = [&]() {
+    auto fragment = [&](const uint8_t* at, int i) { return *reinterpret_cast<const bf16x8_t*>(at + i * 1024); };
+    // S^T of half u of a tile: 32 keys.
+    auto scores = [&](f32x16_t& s, int t, int u) {
 #pragma unroll
-      for (int z = 0; z < KINDS; ++z)
-        fetch<D>(raw[z], a, KINDS == 2 ? z == 1 : wave >= 4, hk, next, off, next >= 0, lane);
-    };
-    auto unpack_all = [&](int buf, int mk) {
+      for (int e = 0; e < 16; ++e) s[e] = 0.f;
+      const uint8_t* at = kbuf[t % KB] + u * (KS * 1024) + lane * 16;
 #pragma unroll
-      for (int z = 0; z < KINDS; ++z)
-        unpack<D>(raw[z], KINDS == 2 ? z == 1 : wave >= 4, piece, kbuf[buf], vbuf[buf], &marks[mk], lane);
-    };
-    if (s0 < s1) {
-      fetch_all();
-      unpack_all(0, 0);
-      next = lookup(s0 + kManyKeys, &off);
-      fetch_all();
-      next = lookup(s0 + 2 * kManyKeys, &off);
-    }
-    int cur = 0, mk = 0;
-    for (int j = s0; j < s1; j += kManyKeys, cur ^= 1, mk = mk == 2 ? 0 : mk + 1) {
-      __syncthreads();  // tile j is in LDS; the buffers of the one before are free
-      const int mk1 = mk == 2 ? 0 : mk + 1, mk2 = mk1 == 2 ? 0 : mk1 + 1;
-      if (threadIdx.x == 0) marks[mk2] = TileMarks{};
-      if (j + kManyKeys < s1) {
-        unpack_all(cur ^ 1, mk1);
-        fetch_all();
-        next = lookup(j + 3 * kManyKeys, &off);
+      for (int q = 0; q < KS; ++q) {
+        const bf16x8_t kf = fragment(at, q);
+#pragma unroll
+        for (int y = T - 1; y >= 0; --y)
+          s = mfma32(kf, frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), s);
       }
-      if (j >= last.hi || j + kManyKeys <= first.lo) continue;
-      const TileMarks mark = marks[mk];
-      const bool odd = __builtin_amdgcn_readfirstlane(
-          (mark.absent[0] | mark.absent[1] | mark.knan[0] | mark.knan[1] | mark.vnan[0] | mark.vnan[1]) != 0 ||
-          j < last.lo || j + kManyKeys > first.hi);
+    };
+
+    // Half u of tile t: its scores `s` are there; `n` gets those of the half
+    // after it meanwhile.
+    auto step = [&](f32x16_t& s, f32x16_t& n, int t, int u, bool odd) {
+      const uint8_t* kat = kbuf[(u ? t + 1 : t) % KB] + (u ^ 1) * (KS * 1024) + lane * 16;
+      bf16x8_t ring[4];
 #pragma unroll
-      for (int sub = 0; sub < 2 / SUB; ++sub) {
-        f32x16_t s[SUB];
+      for (int q = 0; q < 4; ++q) ring[q] = fragment(kat, q);
+      uint32_t poison = 0;  // keys that this row sees whose value is NaN
+      if (odd) {
+        rare_path();
+        const int j = s0 + t * kManyKeys + 32 * u;
+        const uint32_t seen = (bits_between(sp.lo - j, sp.hi - j) & ~kmarks[t & 3].absent[u]) >> (4 * half);
+        const uint32_t nan = (kmarks[t & 3].nan[u] >> (4 * half)) & seen;
+        poison = (vmarks[t % 3].nan[u] >> (4 * half)) & seen;
 #pragma unroll
-        for (int x = 0; x < SUB; ++x) {
+        for (int e = 0; e < 16; ++e) {
+          const int k = 8 * (e >> 2) + (e & 3);
+          const uint32_t keep = spread(seen, k);
+          s[e] = __uint_as_float((__float_as_uint(s[e]) & keep) | (kNoneBits & ~keep) |
+                                 (spread(nan, k) & kNanBits));
+        }
+      }
+      float mx = kNone;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[x][e] = 0.f;
-          const uint8_t* at = kbuf[cur] + (sub * SUB + x) * (KS * 1024) + lane * 16;
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[e]);
+      // The maximum is only followed when a weight would pass 2^8: fp32 and
+      // bf16 hold weights up to there as well as up to 1, and until then the
+      // lanes need not agree on a new one and nothing is rescaled.
+      if (__any(mx > m + grown)) {
+        rare_path();
+        const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
+        const float n0 = mn == kNone ? 0.f : mn * sc;
+        const float al = m == kNone ? 0.f : __builtin_amdgcn_exp2f(ms - n0);
+        m = mn, ms = n0;
+        l *= al;
 #pragma unroll
-          for (int q = 0; q < KS; ++q) {
-            const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(at + q * 1024);
+        for (int f = 0; f < NT; ++f)
 #pragma unroll
-            for (int y = T - 1; y >= 0; --y)
-              s[x] = mfma32(kf, frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), s[x]);
+          for (int e = 0; e < 16; ++e) o[f][e] *= al;
+      }
+      // The next half's first product runs on the matrix unit while the vector
+      // unit takes this one's exponentials: a matrix instruction holds its
+      // unit for 32 clocks, in which a wave can issue up to seven others, so
+      // they are laid out in turns and kept there. Fragments are read from LDS
+      // four ahead, at last those of the second product. (Past the last tile
+      // the first product is of old keys, and unused.)
+      const uint8_t* vat = vbuf[t & 1] + 2 * u * (NT * 1024) + lane * 16;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t pw[T][8];  // the weights, two keys a word
+#pragma unroll
+      for (int e = 0; e < 16; ++e) n[e] = 0.f;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < KS; ++q) {
+#pragma unroll
+        for (int y = T - 1; y >= 0; --y)
+          n = mfma32(ring[q & 3], frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), n);
+        ring[q & 3] = q + 4 < KS ? fragment(kat, q + 4) : fragment(vat, q + 4 - KS);
+#pragma unroll
+        for (int e = q * 16 / KS; e < (q + 1) * 16 / KS; ++e) {
+          s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], sc, -ms));
+          sum[e & 3] += s[e];
+          if (e & 1) {
+            uint32_t w[T];
+            split2<T>(s[e - 1], s[e], w);
+#pragma unroll
+            for (int y = 0; y < T; ++y) pw[y][e >> 1] = w[y];
           }
         }
-        uint32_t poison[SUB] = {};  // keys that this row sees whose value is NaN
-        if (odd) {
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (odd) {
+        rare_path();
+        // A NaN value is out of V, where it would reach every row: it enters
+        // the weight of the rows that see it.
 #pragma unroll
-          for (int x = 0; x < SUB; ++x) {
-            const int y = sub * SUB + x, j0 = j + 32 * y;
-            const uint32_t seen =
-                (bits_between(sp.lo - j0, sp.hi - j0) & ~(y ? mark.absent[1] : mark.absent[0])) >> (4 * half);
-            const uint32_t nan = ((y ? mark.knan[1] : mark.knan[0]) >> (4 * half)) & seen;
-            poison[x] = ((y ? mark.vnan[1] : mark.vnan[0]) >> (4 * half)) & seen;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int k = 8 * (e >> 2) + (e & 3);
-              const uint32_t keep = spread(seen, k);
-              s[x][e] = __uint_as_float((__float_as_uint(s[x][e]) & keep) | (kNoneBits & ~keep) |
-                                        (spread(nan, k) & kNanBits));
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int k = 8 * (e >> 1) + 2 * (e & 1);
+          pw[0][e] |= (spread(poison, k) & 0x7fc0u) | (spread(poison, k + 1) & 0x7fc00000u);
         }
-        float mx = kNone;
+      }
 #pragma unroll
-        for (int x = 0; x < SUB; ++x)
+      for (int i = 0; i < 2 * NT; ++i) {
+        const int g = i / NT, f = i % NT;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[x][e]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        // The maximum is only followed when it has grown by more than a
-        // factor 2^8 of the weights: until then they stay below 2^8, which
-        // fp32 and bf16 hold as well as 1, and nothing has to be rescaled.
-        if (__any(mx > m + grown)) {
-          const float mn = fmaxf(m, mx);
-          const float n0 = mn == kNone ? 0.f : mn * sc;
-          const float al = m == kNone ? 0.f : __builtin_amdgcn_exp2f(ms - n0);
-          m = mn, ms = n0;
-          l *= al;
-#pragma unroll
-          for (int f = 0; f < NT; ++f)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[f][e] *= al;
+        for (int y = T - 1; y >= 0; --y)
+          o[f] = mfma32(ring[i & 3], frag(pw[y][4 * g], pw[y][4 * g + 1], pw[y][4 * g + 2], pw[y][4 * g + 3]), o[f]);
+        if (i + 4 < 2 * NT) ring[i & 3] = fragment(vat, i + 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto wanted = [&](int t) {
+      const int j = s0 + t * kManyKeys;
+      return t < tiles && j < last.hi && j + kManyKeys > first.lo;
+    };
+
+    // Tile t is computed from keys t and t + 1 and values t; keys t + 2 and
+    // values t + 1 are decoded meanwhile into the buffers that t - 1 has left,
+    // keys t + 3 and values t + 2 are on their way, and the pages of the ones
+    // after those are looked up. (Wide heads' LDS holds two tiles of keys: there
+    // keys t + 2 take the place of t's, behind a barrier in the tile's middle.) Waves that decode keys do it first and those that
+    // decode values last, so that the two of a SIMD are not at the same work.
+    constexpr bool kBoth = NW == 4;
+    const bool do_k = kBoth || wave < 4, do_v = kBoth || wave >= 4;
+    __syncthreads();  // the last tile of rows is done with LDS
+    if (threadIdx.x < 4) kmarks[threadIdx.x] = KeyMarks{};
+    if (threadIdx.x < 3) vmarks[threadIdx.x] = ValueMarks{};
+    __syncthreads();
+    Raw<D> rk, rv;
+    Place pk, pv;
+    f32x16_t sa, sb;
+    if (tiles > 0) {
+      if (do_k) {
+        fetch_tile(rk, false, lookup(0));
+        unpack_tile(rk, false, 0);
+        fetch_tile(rk, false, lookup(1));
+        unpack_tile(rk, false, 1);
+        fetch_tile(rk, false, lookup(2));
+        pk = lookup(3);
+      }
+      if (do_v) {
+        fetch_tile(rv, true, lookup(0));
+        unpack_tile(rv, true, 0);
+        fetch_tile(rv, true, lookup(1));
+        pv = lookup(2);
+      }
+      __syncthreads();
+      scores(sa, 0, 0);
+    }
+    for (int t = 0; t < tiles; ++t) {
+      __syncthreads();
+      if (threadIdx.x == 0) {  // of tiles t + 3 and t + 2: read before this barrier, written after the next
+        kmarks[(t + 3) & 3] = KeyMarks{};
+        vmarks[(t + 2) % 3] = ValueMarks{};
+      }
+      auto keys = [&]() {
+        if (do_k && t + 2 < tiles) {
+          unpack_tile(rk, false, t + 2);
+          fetch_tile(rk, false, pk);
+          pk = lookup(t + 4);
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < SUB; ++x)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            s[x][e] = __builtin_amdgcn_exp2f(fmaf(s[x][e], sc, -ms));
-            sum[e & 3] += s[x][e];
-          }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (odd) {
-          // A NaN value is out of V, where it would reach every row: it enters
-          // the weight of the rows that see it.
-#pragma unroll
-          for (int x = 0; x < SUB; ++x)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              s[x][e] = __uint_as_float(__float_as_uint(s[x][e]) |
-                                        (spread(poison[x], 8 * (e >> 2) + (e & 3)) & kNanBits));
+      };
+      if (KB == 3) keys();
+      if (wanted(t)) {
+        const KeyMarks km = kmarks[t & 3];
+        const ValueMarks vm = vmarks[t % 3];
+        const int j = s0 + t * kManyKeys;
+        const bool odd = __builtin_amdgcn_readfirstlane(
+            (km.absent[0] | km.absent[1] | km.nan[0] | km.nan[1] | vm.nan[0] | vm.nan[1]) != 0 ||
+            j < last.lo || j + kManyKeys > first.hi);
+        step(sa, sb, t, 0, odd);
+        if (KB == 2) {  // the second half of keys t is read: their buffer is free
+          __syncthreads();
+          keys();
         }
-#pragma unroll
-        for (int x = 0; x < SUB; ++x)
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t pw[T][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[T];
-              split2<T>(s[x][8 * g + 2 * e], s[x][8 * g + 2 * e + 1], w);
-#pragma unroll
-              for (int y = 0; y < T; ++y) pw[y][e] = w[y];
-            }
-            const uint8_t* at = vbuf[cur] + (2 * (sub * SUB + x) + g) * (NT * 1024) + lane * 16;
-#pragma unroll
-            for (int f = 0; f < NT; ++f) {
-              const bf16x8_t vf = *reinterpret_cast<const bf16x8_t*>(at + f * 1024);
-#pragma unroll
-              for (int y = T - 1; y >= 0; --y)
-                o[f] = mfma32(vf, frag(pw[y][0], pw[y][1], pw[y][2], pw[y][3]), o[f]);
-            }
-          }
+        step(sb, sa, t, 1, odd);
+      } else {
+        if (KB == 2) {
+          __syncthreads();
+          keys();
+        }
+        if (wanted(t + 1)) scores(sa, t + 1, 0);
+      }
+      if (do_v && t + 1 < tiles) {
+        unpack_tile(rv, true, t + 1);
+        fetch_tile(rv, true, pv);
+        pv = lookup(t + 3);
       }
     }
     l += __shfl_xor(l, 32);

@@ -56,6 +56,11 @@ __device__ __forceinline__ uint32_t spread(uint32_t w, int k) {
 }
 constexpr uint32_t kNanBits = 0x7fc00000u, kNoneBits = 0xff800000u;
 
+// In a block that few waves take: keeps the compiler from running its plain
+// arithmetic always and selecting the result, which it does to save a branch
+// (the masks of 64 keys were a third of the many-row kernel's vector work).
+__device__ __forceinline__ void rare_path() { asm volatile(""); }
+
 // The bytes of four scales that stand for NaN, each as its top bit.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   static_assert(kScaleMax == 252, "bytes from 253 on");

@@ -214,6 +214,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
         const bool odd = j < all_lo || j + 32 > all_hi || !cur.have[0] || !cur.have[1] || __any(nan != 0);
         uint32_t poison = 0;  // this row's keys whose value is NaN
         if (odd) {
+          rare_path();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             uint64_t kn = __ballot(ks[x][0] > kScaleMax);
@@ -260,6 +261,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
         for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], sc, -ms));
         l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
         if (__any(poison != 0)) {
+          rare_path();
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             p[e] = __uint_as_float(__float_as_uint(p[e]) | (spread(poison, e) & kNanBits));
