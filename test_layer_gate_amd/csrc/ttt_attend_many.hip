@@ -53,24 +53,23 @@ __device__ __forceinline__ bool unit_live(int lane) { return D >= 128 || lane < 
 // Keys: unit (block of 32 values c, token t), lane = 16 c + t (+ 64 a unit).
 // Values: unit (four tokens q, 8 values c), lane = (D / 8) q + c.
 template <int D>
-__device__ __forceinline__ void fetch(Raw<D>& r, const AttnLaunch& a, bool is_v, int hk, int id,
-                                      int off, bool have, int lane) {
-  r.have = have && (uint32_t)id < (uint32_t)a.pool.n_pages;
-  if (!r.have || !unit_live<D>(lane)) return;
-  const int page = a.pool.page;
-  const uint8_t* p = a.pool.pages + id * a.pool.page_stride + hk * head_block_bytes(page, D);
+__device__ __forceinline__ void fetch(Raw<D>& r, bool is_v, Global p, uint32_t off, bool have, int page,
+                                      int lane) {
+  r.have = have;
+  if (!unit_live<D>(lane)) return;
 #pragma unroll
   for (int u = 0; u < Raw<D>::kUnits; ++u) {
     const int n = lane + 64 * u;
     if (is_v) {
       const int q = n / (D / 8), c = n % (D / 8);
-      r.w[u] = *reinterpret_cast<const uint4*>(p + page * (D / 2) + off * (D / 2) + n * 16);
-      r.s[u] = *reinterpret_cast<const uint32_t*>(p + page * D + page * (D / 32) + (c >> 2) * page +
-                                                  off + 4 * q);
+      r.w[u] = load16(p + (uint32_t)(page * (D / 2) + n * 16 + off * (D / 2)));
+      r.s[u] = load4(p + (uint32_t)(page * D + page * (D / 32) + (c >> 2) * page + 4 * q + off));
     } else {
       const int c = n >> 4, t = n & 15;
-      r.w[u] = *reinterpret_cast<const uint4*>(p + (off + t) * (D / 2) + c * 16);
-      r.s[u] = p[page * D + (off + t) * (D / 32) + c];
+      // the token's scales are read as a word (a byte's widening would be
+      // waited for at once): D = 64's two bytes with a neighbour's
+      r.w[u] = load16(p + (uint32_t)(t * (D / 2) + c * 16 + off * (D / 2)));
+      r.s[u] = load4(p + (uint32_t)(page * D + (D == 64 ? (t >> 1) * 4 : t * (D / 32) + (c & ~3)) + off * (D / 32)));
     }
   }
 }
@@ -119,10 +118,14 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
     } else {
       const bool live = unit_live<D>(lane);
       const int c = n >> 4, t = n & 15;
-      if (__any(live && r.s[u] > kScaleMax) && live && r.s[u] > kScaleMax)
-        atomicOr(&kmarks->nan[piece >> 1], 1u << (16 * (piece & 1) + t));
+      const uint32_t byte = r.s[u] >> (D == 64 ? 16 * (t & 1) + 8 * c : 8 * (c & 3)) & 255u;
+      const bool bad = live && byte > kScaleMax;
+      if (__any(bad)) {
+        rare_path();
+        if (bad) atomicOr(&kmarks->nan[piece >> 1], 1u << (16 * (piece & 1) + t));
+      }
       if (!live) continue;
-      const float sc = scale_at(r.s[u], 0);
+      const float sc = scale_value(byte);
       const uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
       constexpr int S = D / 16;  // steps; values 32c + 8j .. are half j % 2 of step 2c + j / 2
       uint8_t* at = kbuf + ((piece >> 1) * S + 2 * c) * 1024 + ((piece & 1) * 16 + t) * 16;
@@ -204,20 +207,35 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       for (int e = 0; e < 16; ++e) o[f][e] = 0.f;
     float m = kNone, ms = 0.f, l = 0.f;  // maximum (unscaled), its scaled value (0 for none), sum
 
-    // Tile t holds the keys from s0 + 64 t. Where this wave's 16 of its tokens lie:
+    // Tile t holds the keys from s0 + 64 t. Where this wave's 16 tokens of the
+    // tiles t0 .. t0 + 63 lie: one tile a lane.
     const int tiles = (max(s1 - s0, 0) + kManyKeys - 1) / kManyKeys;
-    struct Place {
-      int id, off;
+    uint64_t my_block = (uint64_t)a.pool.pages;
+    uint32_t my_off = 0;
+    uint64_t gone = 0;  // tiles whose page is none, or that are past the end
+    int t0 = 0;
+    auto find = [&](int t) {
+      t0 = t;
+      const int key = s0 + (t + lane) * kManyKeys + 16 * piece, pg = key / page;
+      my_block = (uint64_t)a.pool.pages, my_off = 0;
+      bool ok = key < s1 && pg < a.pool.max_pages;
+      if (ok) {
+        const int id = a.pool.table[(int64_t)b * a.pool.max_pages + pg];
+        ok = (uint32_t)id < (uint32_t)a.pool.n_pages;
+        if (ok) {
+          my_block += id * a.pool.page_stride + hk * head_block_bytes(page, D);
+          my_off = key - pg * page;
+        }
+      }
+      gone = __ballot(!ok);
     };
-    auto lookup = [&](int t) {
-      const int key = s0 + t * kManyKeys + 16 * piece, pg = key / page;
-      Place p;
-      p.off = key - pg * page;
-      p.id = key < s1 && pg < a.pool.max_pages ? a.pool.table[(int64_t)b * a.pool.max_pages + pg] : -1;
-      return p;
-    };
-    auto fetch_tile = [&](Raw<D>& r, bool is_v, Place p) {
-      fetch<D>(r, a, is_v, hk, p.id, p.off, p.id >= 0, lane);
+    auto fetch_tile = [&](Raw<D>& r, bool is_v, int t) {
+      if (t - t0 >= 64) find(t - 1);  // keys are a tile ahead of values
+      const int i = t - t0;
+      const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)my_block, i);
+      const uint32_t hi32 = __builtin_amdgcn_readlane((int)(my_block >> 32), i);
+      fetch<D>(r, is_v, reinterpret_cast<Global>((uint64_t)hi32 << 32 | lo32),
+               __builtin_amdgcn_readlane((int)my_off, i), (gone >> i & 1) == 0, page, lane);
     };
     auto unpack_tile = [&](Raw<D>& r, bool is_v, int t) {
       unpack<D>(r, is_v, piece, kbuf[t % KB], vbuf[t & 1], &kmarks[t & 3], &vmarks[t % 3], lane);
@@ -238,8 +256,16 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       }
     };
 
-    // Half u of tile t: its scores `s` are there; `n` gets those of the half
-    // after it meanwhile.
+    auto largest = [&](const f32x16_t& s) {
+      float x = s[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) x = fmaxf(x, s[e]);
+      return x;
+    };
+
+    // Half u of tile t: its scores `s` are there and mx is their largest of
+    // this lane's; `n` gets those of the half after it meanwhile, and mx theirs.
+    float mx = kNone;
     auto step = [&](f32x16_t& s, f32x16_t& n, int t, int u, bool odd) {
       const uint8_t* kat = kbuf[(u ? t + 1 : t) % KB] + (u ^ 1) * (KS * 1024) + lane * 16;
       bf16x8_t ring[4];
@@ -259,10 +285,8 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
           s[e] = __uint_as_float((__float_as_uint(s[e]) & keep) | (kNoneBits & ~keep) |
                                  (spread(nan, k) & kNanBits));
         }
+        mx = largest(s);
       }
-      float mx = kNone;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[e]);
       // The maximum is only followed when a weight would pass 2^8: fp32 and
       // bf16 hold weights up to there as well as up to 1, and until then the
       // lanes need not agree on a new one and nothing is rescaled.
@@ -327,6 +351,9 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
         for (int y = T - 1; y >= 0; --y)
           o[f] = mfma32(ring[i & 3], frag(pw[y][4 * g], pw[y][4 * g + 1], pw[y][4 * g + 2], pw[y][4 * g + 3]), o[f]);
         if (i + 4 < 2 * NT) ring[i & 3] = fragment(vat, i + 4);
+        // the next half's maximum, beside the second product
+#pragma unroll
+        for (int e = i * 8 / NT; e < (i + 1) * 8 / NT; ++e) mx = e == 0 ? n[0] : fmaxf(mx, n[e]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -348,25 +375,24 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
     if (threadIdx.x < 3) vmarks[threadIdx.x] = ValueMarks{};
     __syncthreads();
     Raw<D> rk, rv;
-    Place pk, pv;
     f32x16_t sa, sb;
     if (tiles > 0) {
+      find(0);
       if (do_k) {
-        fetch_tile(rk, false, lookup(0));
+        fetch_tile(rk, false, 0);
         unpack_tile(rk, false, 0);
-        fetch_tile(rk, false, lookup(1));
+        fetch_tile(rk, false, 1);
         unpack_tile(rk, false, 1);
-        fetch_tile(rk, false, lookup(2));
-        pk = lookup(3);
+        fetch_tile(rk, false, 2);
       }
       if (do_v) {
-        fetch_tile(rv, true, lookup(0));
+        fetch_tile(rv, true, 0);
         unpack_tile(rv, true, 0);
-        fetch_tile(rv, true, lookup(1));
-        pv = lookup(2);
+        fetch_tile(rv, true, 1);
       }
       __syncthreads();
       scores(sa, 0, 0);
+      mx = largest(sa);
     }
     for (int t = 0; t < tiles; ++t) {
       __syncthreads();
@@ -377,8 +403,7 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       auto keys = [&]() {
         if (do_k && t + 2 < tiles) {
           unpack_tile(rk, false, t + 2);
-          fetch_tile(rk, false, pk);
-          pk = lookup(t + 4);
+          fetch_tile(rk, false, t + 3);
         }
       };
       if (KB == 3) keys();
@@ -400,12 +425,14 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
           __syncthreads();
           keys();
         }
-        if (wanted(t + 1)) scores(sa, t + 1, 0);
+        if (wanted(t + 1)) {
+          scores(sa, t + 1, 0);
+          mx = largest(sa);
+        }
       }
       if (do_v && t + 1 < tiles) {
         unpack_tile(rv, true, t + 1);
-        fetch_tile(rv, true, pv);
-        pv = lookup(t + 3);
+        fetch_tile(rv, true, t + 2);
       }
     }
     l += __shfl_xor(l, 32);

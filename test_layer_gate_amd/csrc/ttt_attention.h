@@ -79,18 +79,38 @@ __device__ __forceinline__ Span span_of(const AttnLaunch& a, int len, int news, 
   return s;
 }
 
+// A word at an address that is the same for the whole wave, of memory that
+// the kernel does not write: through the scalar cache, so that a page number
+// needed later is not waited for with the vector loads that are under way.
+__device__ __forceinline__ int uniform_load(const int32_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* Constant;
+  return reinterpret_cast<Constant>(reinterpret_cast<uint64_t>(p))[i];
+}
+
+// Loads of an address put together from integers, which has to be marked as
+// global memory's.
+typedef const __attribute__((address_space(1))) uint8_t* Global;
+__device__ __forceinline__ uint4 load16(Global p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 w = *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(p);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t load4(Global p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p);
+}
+
 // Sequence b's rows, and its keys.
 struct Seq {
   int row0, news, len;
 };
 __device__ __forceinline__ Seq seq_of(const Pool& p, int b) {
   const int each = p.tokens / p.batch;
-  const int r0 = p.starts ? p.starts[b] : b * each;
-  const int r1 = p.starts ? p.starts[b + 1] : r0 + each;
+  const int r0 = p.starts ? uniform_load(p.starts, b) : b * each;
+  const int r1 = p.starts ? uniform_load(p.starts, b + 1) : r0 + each;
   Seq s;
   s.row0 = r0;
   s.news = r0 < 0 ? 0 : min(r1, p.tokens) - r0;
-  s.len = min(p.lens[b], p.max_pages * p.page);
+  s.len = min(uniform_load(p.lens, b), p.max_pages * p.page);
   return s;
 }
 

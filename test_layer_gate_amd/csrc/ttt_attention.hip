@@ -31,18 +31,6 @@ namespace {
 // brings the same eight keys' values i D / 16 .. + D / 16 - 1. NW waves share
 // a workgroup's stretch of keys and join in LDS.
 
-// Loads of an address put together from integers, which has to be marked as
-// global memory's.
-typedef const __attribute__((address_space(1))) uint8_t* Global;
-__device__ __forceinline__ uint4 load16(Global p) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const u32x4 w = *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(p);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint32_t load4(Global p) {
-  return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p);
-}
-
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
 template <int D>
 struct FewTile {
