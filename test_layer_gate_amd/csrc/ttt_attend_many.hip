@@ -144,6 +144,8 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
   constexpr int NW = many_waves(D, F32), kManyRows = 32 * NW;
   constexpr int KS = D / 16;             // steps of the first product
   constexpr int NT = D / 32;             // fragments of V^T
+  constexpr int kFence = 0x406;          // lets vector, scalar and exponential instructions pass
+  constexpr int RD = D == 64 ? 4 : 8;    // fragments read ahead
   constexpr int KB = D == 256 ? 2 : 3;   // tiles of keys in LDS
   __shared__ __attribute__((aligned(16))) uint8_t kbuf[KB][kManyKeys * D * 2];
   __shared__ __attribute__((aligned(16))) uint8_t vbuf[2][kManyKeys * D * 2];
@@ -268,9 +270,9 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
     float mx = kNone;
     auto step = [&](f32x16_t& s, f32x16_t& n, int t, int u, bool odd) {
       const uint8_t* kat = kbuf[(u ? t + 1 : t) % KB] + (u ^ 1) * (KS * 1024) + lane * 16;
-      bf16x8_t ring[4];
+      bf16x8_t ring[RD];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) ring[q] = fragment(kat, q);
+      for (int q = 0; q < RD; ++q) ring[q] = fragment(kat, q);
       uint32_t poison = 0;  // keys that this row sees whose value is NaN
       if (odd) {
         rare_path();
@@ -304,10 +306,11 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       }
       // The next half's first product runs on the matrix unit while the vector
       // unit takes this one's exponentials: a matrix instruction holds its
-      // unit for 32 clocks, in which a wave can issue up to seven others, so
-      // they are laid out in turns and kept there. Fragments are read from LDS
-      // four ahead, at last those of the second product. (Past the last tile
-      // the first product is of old keys, and unused.)
+      // unit for 32 clocks, in which a wave can issue up to seven others. They
+      // are laid out in turns, and the fences keep matrix instructions and LDS
+      // reads in this order, the latter RD fragments ahead of their use (at
+      // last those of the second product); vector instructions may move.
+      // (Past the last tile the first product is of old keys, and unused.)
       const uint8_t* vat = vbuf[t & 1] + 2 * u * (NT * 1024) + lane * 16;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t pw[T][8];  // the weights, two keys a word
@@ -318,8 +321,8 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       for (int q = 0; q < KS; ++q) {
 #pragma unroll
         for (int y = T - 1; y >= 0; --y)
-          n = mfma32(ring[q & 3], frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), n);
-        ring[q & 3] = q + 4 < KS ? fragment(kat, q + 4) : fragment(vat, q + 4 - KS);
+          n = mfma32(ring[q % RD], frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), n);
+        ring[q % RD] = q + RD < KS ? fragment(kat, q + RD) : fragment(vat, q + RD - KS);
 #pragma unroll
         for (int e = q * 16 / KS; e < (q + 1) * 16 / KS; ++e) {
           s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], sc, -ms));
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
             for (int y = 0; y < T; ++y) pw[y][e >> 1] = w[y];
           }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(kFence);
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (odd) {
@@ -349,12 +352,12 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
         const int g = i / NT, f = i % NT;
 #pragma unroll
         for (int y = T - 1; y >= 0; --y)
-          o[f] = mfma32(ring[i & 3], frag(pw[y][4 * g], pw[y][4 * g + 1], pw[y][4 * g + 2], pw[y][4 * g + 3]), o[f]);
-        if (i + 4 < 2 * NT) ring[i & 3] = fragment(vat, i + 4);
+          o[f] = mfma32(ring[i % RD], frag(pw[y][4 * g], pw[y][4 * g + 1], pw[y][4 * g + 2], pw[y][4 * g + 3]), o[f]);
+        if (i + RD < 2 * NT) ring[i % RD] = fragment(vat, i + RD);
         // the next half's maximum, beside the second product
 #pragma unroll
         for (int e = i * 8 / NT; e < (i + 1) * 8 / NT; ++e) mx = e == 0 ? n[0] : fmaxf(mx, n[e]);
-        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(kFence);
       }
     };
     auto wanted = [&](int t) {
