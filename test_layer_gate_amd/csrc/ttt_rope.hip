@@ -11,14 +11,17 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-// A unit is 16 values of one head: 8 pairs of the rotated part (halves i and
-// i + rot / 2, or 16 neighbours), or 16 values of the part that is copied. A
-// thread takes one unit of a token and walks over heads with it, so that the
-// 8 cosines and sines (64 bytes) are loaded once for them. Bound by HBM: each
-// value is read once and written once, in 16-byte pieces.
+// A unit is two pieces of 16 bytes (W values) of one head: W values from i
+// and W from i + rot / 2, W pairs of the half layout and of the interleaved
+// one W / 2 pairs each; of the part that is copied, likewise. Neighbouring
+// lanes take neighbouring pieces, then neighbouring heads of the token, so
+// that a wave reads and writes whole lines; a lane then walks over the
+// remaining heads with the cosines and sines it has loaded. Bound by HBM:
+// 64k tokens of 32 + 8 heads of 128 in bf16 move at 6.3 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeLaunch a, int units, int lanes,
                                                             int64_t total) {
+  constexpr int W = kWide<F32>;
   const int64_t id = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
   if (id >= total) return;
   const int u = (int)(id % units);
@@ -26,38 +29,48 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeLaunch a, int un
   const int h0 = (int)(r % lanes);
   const int n = (int)(r / lanes);
   const RopeArgs& rope = a.rope;
-  const int rot_units = rope.rot >> 4;
+  const int rot_units = rope.rot / (2 * W);
   const bool turned = u < rot_units;
-  // first and second 8 values of the unit
-  const int i0 = !turned ? u * 16 : rope.interleaved ? u * 16 : u * 8;
-  const int i1 = !turned || rope.interleaved ? i0 + 8 : i0 + (rope.rot >> 1);
-  float c[8], s[8];
+  const int i0 = turned ? u * W : rope.rot + (u - rot_units) * W;
+  const int i1 = i0 + (turned ? rope.rot / 2 : (a.dim - rope.rot) / 2);
+  // the pieces' pairs: of the half layout the first W, of the other W / 2 each
+  float c[W], s[W];
   if (turned) {
     const int pos = a.positions ? a.positions[n] : n % a.seq_len;
-    load_cs8(rope, pos, u * 8, c, s);
+    if (rope.interleaved) {
+      float cc[W / 2], ss[W / 2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        load_cs<W / 2>(rope, pos, (x ? i1 : i0) / 2, cc, ss);
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) c[x * W / 2 + e] = cc[e], s[x * W / 2 + e] = ss[e];
+      }
+    } else {
+      load_cs<W>(rope, pos, i0, c, s);
+    }
   }
   const int heads = a.x[0].heads + a.x[1].heads;
   for (int h = h0; h < heads; h += lanes) {
     const int t = h >= a.x[0].heads;
     const int hh = t ? h - a.x[0].heads : h;
     const int64_t xi = n * a.x[t].ts + hh * a.x[t].hs, yi = n * a.y[t].ts + hh * a.y[t].hs;
-    float p[8], q[8];
-    load8<F32>(a.x[t].p, xi + i0, p);
-    load8<F32>(a.x[t].p, xi + i1, q);
+    float p[W], q[W];
+    stream_load<F32>(a.x[t].p, xi + i0, p);
+    stream_load<F32>(a.x[t].p, xi + i1, q);
     if (turned) {
       if (rope.interleaved) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < W / 2; ++e) {
           turn(p[2 * e], p[2 * e + 1], c[e], s[e], &p[2 * e], &p[2 * e + 1]);
-          turn(q[2 * e], q[2 * e + 1], c[4 + e], s[4 + e], &q[2 * e], &q[2 * e + 1]);
+          turn(q[2 * e], q[2 * e + 1], c[W / 2 + e], s[W / 2 + e], &q[2 * e], &q[2 * e + 1]);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn(p[e], q[e], c[e], s[e], &p[e], &q[e]);
+        for (int e = 0; e < W; ++e) turn(p[e], q[e], c[e], s[e], &p[e], &q[e]);
       }
     }
-    store8<F32>(a.y[t].p, yi + i0, p);
-    store8<F32>(a.y[t].p, yi + i1, q);
+    stream_store<F32>(a.y[t].p, yi + i0, p);
+    stream_store<F32>(a.y[t].p, yi + i1, q);
   }
 }
 
@@ -115,11 +128,14 @@ __global__ __launch_bounds__(kRopeThreads) void rope_table_kernel(
 }  // namespace
 
 hipError_t launch_rope(const RopeLaunch& a, hipStream_t s) {
-  const int units = a.dim / 16, heads = a.x[0].heads + a.x[1].heads;
-  // Heads that a thread walks over: as many as leave the chip full.
+  const int units = a.dim / (2 * (a.f32 ? kWide<true> : kWide<false>)), heads = a.x[0].heads + a.x[1].heads;
+  // Heads that are not walked over: enough for a wave or two to stay within
+  // a token (of 1: 304 us for the 64k tokens above, 8: 249, 16: 237, all:
+  // 267), and for the chip to be full.
   int lanes = heads;
   const int64_t one = (int64_t)a.tokens * units;
-  while (lanes > 1 && one * ((lanes + 1) / 2) >= (int64_t)256 * 2048) lanes = (lanes + 1) / 2;
+  while (lanes > 1 && units * ((lanes + 1) / 2) >= 128 && one * ((lanes + 1) / 2) >= (int64_t)256 * 2048)
+    lanes = (lanes + 1) / 2;
   const int64_t total = one * lanes;
   const int64_t grid = (total + kRopeThreads - 1) / kRopeThreads;
   if (a.f32)

@@ -39,20 +39,55 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
   }
 }
 
-// cos and sin of the 8 pairs i .. i + 7 of position `pos`; NaN for a position
-// that the table does not hold.
-__device__ __forceinline__ void load_cs8(const RopeArgs& r, int pos, int i, float (&c)[8],
-                                         float (&s)[8]) {
+// 16 bytes (W = 8 bf16 or 4 fp32 values) that are read or written once, past
+// the caches' replacement: 64k tokens of 40 rotated heads take 220 us so and
+// 237 with plain accesses. Only where a wave's accesses fill whole lines: half
+// lines written this way cost a read and a write each.
+template <bool F32>
+constexpr int kWide = F32 ? 4 : 8;
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+template <bool F32>
+__device__ __forceinline__ void stream_load(const void* p, int64_t i, float (&v)[kWide<F32>]) {
+  const u32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
+      static_cast<const char*>(p) + i * (F32 ? 4 : 2)));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (F32) {
+      v[e] = __uint_as_float(w[e]);
+    } else {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void stream_store(void* p, int64_t i, const float (&v)[kWide<F32>]) {
+  u32x4_t w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (F32)
+      w[e] = __float_as_uint(v[e]);
+    else
+      w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+  }
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(static_cast<char*>(p) + i * (F32 ? 4 : 2)));
+}
+
+// cos and sin of the N pairs i .. i + N - 1 (N even) of position `pos`; NaN
+// for a position that the table does not hold.
+template <int N>
+__device__ __forceinline__ void load_cs(const RopeArgs& r, int pos, int i, float (&c)[N],
+                                        float (&s)[N]) {
   if ((uint32_t)pos < (uint32_t)r.max_pos) {
     const float4* t = reinterpret_cast<const float4*>(r.table + ((int64_t)pos * (r.rot >> 1) + i) * 2);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < N / 2; ++e) {
       const float4 a = t[e];
       c[2 * e] = a.x, s[2 * e] = r.sign * a.y, c[2 * e + 1] = a.z, s[2 * e + 1] = r.sign * a.w;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = s[e] = __builtin_nanf("");
+    for (int e = 0; e < N; ++e) c[e] = s[e] = __builtin_nanf("");
   }
 }
 
@@ -64,6 +99,13 @@ __device__ __forceinline__ void turn(float a, float b, float c, float s, float* 
   const float ac = a * c, bs = b * s, bc = b * c, as = a * s;
   *ya = ac - bs;
   *yb = bc + as;
+}
+
+// One half of it, s with its sign: a c - b s is a c + b (-s) to the bit.
+__device__ __forceinline__ float turn_half(float x, float mate, float c, float s) {
+#pragma clang fp contract(off)
+  const float xc = x * c, ms = mate * s;
+  return xc + ms;
 }
 
 // Where new token n belongs: its sequence, and its index among the
