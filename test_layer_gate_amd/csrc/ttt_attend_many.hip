@@ -1,6 +1,6 @@
-// gfx950 kernel of attention over the paged 4-bit cache for many rows
-// (prompts and segments); the method and the few-row kernel are in
-// ttt_attention.hip.
+// gfx950 kernel of attention over the paged 4-bit cache for many bf16 rows
+// with heads of 64 and 128 (prompts and segments); the method, the few-row
+// kernel and the choice between them are in ttt_attention.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -23,11 +23,8 @@ namespace {
 // list the keys of 16 in the order 0-3, 8-11 | 4-7, 12-15, which is how they
 // are written. The rows of V^T are numbered so that a lane of O^T holds
 // neighbouring values: fragment t, row i is value i D / 32 + t.
-//
-// Wide heads and fp32 rows need more than the 256 registers that two waves a
-// SIMD have: they take 4 waves (128 rows), each of which decodes keys and
-// values both.
-constexpr int kManyKeys = 64;
+constexpr int kManyWaves = 8, kManyRows = 32 * kManyWaves, kManyKeys = 64;
+static_assert(kManyRows == kManyTile, "rows a workgroup");
 
 // Which of a tile's keys have no page or are NaN, and which have a NaN value:
 // one bit a key, 32 keys a word.
@@ -40,114 +37,101 @@ struct ValueMarks {
 
 template <int D>
 struct Raw {  // a lane's share of 16 tokens' codes, and their scales
-  static constexpr int kUnits = D == 256 ? 2 : 1;
-  uint4 w[kUnits];
-  uint32_t s[kUnits];
+  uint4 w;
+  uint32_t s;
   bool have;
 };
 
 // D = 64: half the lanes have no unit.
 template <int D>
-__device__ __forceinline__ bool unit_live(int lane) { return D >= 128 || lane < 32; }
+__device__ __forceinline__ bool unit_live(int lane) { return D == 128 || lane < 32; }
 
-// Keys: unit (block of 32 values c, token t), lane = 16 c + t (+ 64 a unit).
-// Values: unit (four tokens q, 8 values c), lane = (D / 8) q + c.
+// Keys: unit (block of 32 values c, token t), lane = 16 c + t. Values: unit
+// (four tokens q, 8 values c), lane = (D / 8) q + c. p: the head's block of
+// the page, off: the first token's place there.
 template <int D>
 __device__ __forceinline__ void fetch(Raw<D>& r, bool is_v, Global p, uint32_t off, bool have, int page,
                                       int lane) {
   r.have = have;
   if (!unit_live<D>(lane)) return;
+  if (is_v) {
+    const int q = lane / (D / 8), c = lane % (D / 8);
+    r.w = load16(p + (uint32_t)(page * (D / 2) + lane * 16 + off * (D / 2)));
+    r.s = load4(p + (uint32_t)(page * D + page * (D / 32) + (c >> 2) * page + 4 * q + off));
+  } else {
+    const int c = lane >> 4, t = lane & 15;
+    // the token's scales are read as a word (a byte's widening would be
+    // waited for at once): D = 64's two bytes with a neighbour's
+    r.w = load16(p + (uint32_t)(t * (D / 2) + c * 16 + off * (D / 2)));
+    r.s = load4(p + (uint32_t)(page * D + (D == 64 ? (t >> 1) * 4 : t * 4) + off * (D / 32)));
+  }
+}
+
+// 16 tokens' keys or values into LDS, as the fragments want them.
+template <int D>
+__device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t* kbuf, uint8_t* vbuf,
+                                       KeyMarks* kmarks, ValueMarks* vmarks, int lane) {
+  const bool live = unit_live<D>(lane);
+  const int shift = 16 * (piece & 1);  // of the piece in its word of marks
+  if (!r.have) {  // no such page, or past the end: zeros, which no row counts
+    r.w = make_uint4(0, 0, 0, 0);
+    r.s = 0x7f7f7f7fu;
+    if (lane == 0 && !is_v) atomicOr(&kmarks->absent[piece >> 1], 0xffffu << shift);
+  }
+  uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+  if (is_v) {
+    const uint32_t bad = live ? nan_bytes(r.s) : 0u;
+    const int q = lane / (D / 8), c = lane % (D / 8);
+    if (__any(bad != 0)) {
+      rare_path();
 #pragma unroll
-  for (int u = 0; u < Raw<D>::kUnits; ++u) {
-    const int n = lane + 64 * u;
-    if (is_v) {
-      const int q = n / (D / 8), c = n % (D / 8);
-      r.w[u] = load16(p + (uint32_t)(page * (D / 2) + n * 16 + off * (D / 2)));
-      r.s[u] = load4(p + (uint32_t)(page * D + page * (D / 32) + (c >> 2) * page + 4 * q + off));
-    } else {
-      const int c = n >> 4, t = n & 15;
-      // the token's scales are read as a word (a byte's widening would be
-      // waited for at once): D = 64's two bytes with a neighbour's
-      r.w[u] = load16(p + (uint32_t)(t * (D / 2) + c * 16 + off * (D / 2)));
-      r.s[u] = load4(p + (uint32_t)(page * D + (D == 64 ? (t >> 1) * 4 : t * (D / 32) + (c & ~3)) + off * (D / 32)));
+      for (int e = 0; e < 4; ++e)
+        if (bad >> (8 * e + 7) & 1) {
+          atomicOr(&vmarks->nan[piece >> 1], 1u << (shift + 4 * q + e));
+          w[e] = 0;
+          r.s = (r.s & ~(255u << (8 * e))) | (127u << (8 * e));
+        }
+    }
+    if (!live) return;
+    uint32_t d[4][4];  // [token][value pair]
+#pragma unroll
+    for (int e = 0; e < 4; ++e) decode8(w[e], scale_at(r.s, e), d[e]);
+    constexpr int NT = D / 32;  // fragments; value 8c + j is row (8c + j) / NT of fragment j % NT
+    uint8_t* at = vbuf + piece * (NT * 1024) + (q & 1) * 512 + (q >> 1) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+      const uint2 x = make_uint2(__builtin_amdgcn_perm(d[1][j >> 1], d[0][j >> 1], sel),
+                                 __builtin_amdgcn_perm(d[3][j >> 1], d[2][j >> 1], sel));
+      *reinterpret_cast<uint2*>(at + (j % NT) * 1024 + (8 * c / NT + j / NT) * 16) = x;
+    }
+  } else {
+    const int c = lane >> 4, t = lane & 15;
+    const uint32_t byte = r.s >> (D == 64 ? 16 * (t & 1) + 8 * c : 8 * c) & 255u;
+    const bool bad = live && byte > kScaleMax;
+    if (__any(bad)) {
+      rare_path();
+      if (bad) atomicOr(&kmarks->nan[piece >> 1], 1u << (shift + t));
+    }
+    if (!live) return;
+    constexpr int KS = D / 16;  // steps; values 32c + 8j .. are half j % 2 of step 2c + j / 2
+    uint8_t* at = kbuf + ((piece >> 1) * KS + 2 * c) * 1024 + ((piece & 1) * 16 + t) * 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t d[4];
+      decode8(w[j], scale_value(byte), d);
+      *reinterpret_cast<uint4*>(at + (j >> 1) * 1024 + (j & 1) * 512) = make_uint4(d[0], d[1], d[2], d[3]);
     }
   }
 }
 
 template <int D>
-__device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t* kbuf, uint8_t* vbuf,
-                                       KeyMarks* kmarks, ValueMarks* vmarks, int lane) {
-  if (!r.have) {  // no such page, or past the end: zeros, which no row counts
-#pragma unroll
-    for (int u = 0; u < Raw<D>::kUnits; ++u) {
-      r.w[u] = make_uint4(0, 0, 0, 0);
-      r.s[u] = 0x7f7f7f7fu;
-    }
-    if (lane == 0 && !is_v) atomicOr(&kmarks->absent[piece >> 1], 0xffffu << (16 * (piece & 1)));
-  }
-#pragma unroll
-  for (int u = 0; u < Raw<D>::kUnits; ++u) {
-    const int n = lane + 64 * u;
-    if (is_v) {
-      const bool live = unit_live<D>(lane);
-      const uint32_t bad = live ? nan_bytes(r.s[u]) : 0u;
-      const int q = n / (D / 8), c = n % (D / 8);
-      uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
-      if (__any(bad != 0)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (bad >> (8 * e + 7) & 1) {
-            atomicOr(&vmarks->nan[piece >> 1], 1u << (16 * (piece & 1) + 4 * q + e));
-            w[e] = 0;
-            r.s[u] = (r.s[u] & ~(255u << (8 * e))) | (127u << (8 * e));
-          }
-      }
-      if (!live) continue;
-      uint32_t d[4][4];  // [token][value pair]
-#pragma unroll
-      for (int e = 0; e < 4; ++e) decode8(w[e], scale_at(r.s[u], e), d[e]);
-      constexpr int T = D / 32;  // fragments; value 8c + j is row (8c + j) / T of fragment j % T
-      uint8_t* at = vbuf + piece * (T * 1024) + (q & 1) * 512 + (q >> 1) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
-        const uint2 x = make_uint2(__builtin_amdgcn_perm(d[1][j >> 1], d[0][j >> 1], sel),
-                                   __builtin_amdgcn_perm(d[3][j >> 1], d[2][j >> 1], sel));
-        *reinterpret_cast<uint2*>(at + (j % T) * 1024 + (8 * c / T + j / T) * 16) = x;
-      }
-    } else {
-      const bool live = unit_live<D>(lane);
-      const int c = n >> 4, t = n & 15;
-      const uint32_t byte = r.s[u] >> (D == 64 ? 16 * (t & 1) + 8 * c : 8 * (c & 3)) & 255u;
-      const bool bad = live && byte > kScaleMax;
-      if (__any(bad)) {
-        rare_path();
-        if (bad) atomicOr(&kmarks->nan[piece >> 1], 1u << (16 * (piece & 1) + t));
-      }
-      if (!live) continue;
-      const float sc = scale_value(byte);
-      const uint32_t w[4] = {r.w[u].x, r.w[u].y, r.w[u].z, r.w[u].w};
-      constexpr int S = D / 16;  // steps; values 32c + 8j .. are half j % 2 of step 2c + j / 2
-      uint8_t* at = kbuf + ((piece >> 1) * S + 2 * c) * 1024 + ((piece & 1) * 16 + t) * 16;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t d[4];
-        decode8(w[j], sc, d);
-        *reinterpret_cast<uint4*>(at + (j >> 1) * 1024 + (j & 1) * 512) = make_uint4(d[0], d[1], d[2], d[3]);
-      }
-    }
-  }
-}
-
-template <int D, int T, bool F32>
-__global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(AttnLaunch a, int row_tiles) {
-  constexpr int NW = many_waves(D, F32), kManyRows = 32 * NW;
-  constexpr int KS = D / 16;             // steps of the first product
-  constexpr int NT = D / 32;             // fragments of V^T
-  constexpr int kFence = 0x406;          // lets vector, scalar and exponential instructions pass
-  constexpr int RD = D == 64 ? 4 : 8;    // fragments read ahead
-  constexpr int KB = D == 256 ? 2 : 3;   // tiles of keys in LDS
-  __shared__ __attribute__((aligned(16))) uint8_t kbuf[KB][kManyKeys * D * 2];
+__global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(AttnLaunch a, int row_tiles) {
+  constexpr int KS = D / 16;           // steps of the first product
+  constexpr int NT = D / 32;           // fragments of V^T
+  constexpr int kFence = 0x406;        // lets vector, scalar and exponential instructions pass
+  constexpr int RD = D == 64 ? 4 : 8;  // fragments read ahead
+  __shared__ __attribute__((aligned(16))) uint8_t kbuf[3][kManyKeys * D * 2];
   __shared__ __attribute__((aligned(16))) uint8_t vbuf[2][kManyKeys * D * 2];
   __shared__ KeyMarks kmarks[4];
   __shared__ ValueMarks vmarks[3];
@@ -185,21 +169,15 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
     each = (each + kManyKeys - 1) & ~(kManyKeys - 1);
     const int s0 = lo + split * each, s1 = min(hi, s0 + each);
 
-    uint32_t qf[T][KS][4];
+    // Q as the first product's B operand; a negative scale turns its sign.
+    bf16x8_t qf[KS];
     {
-      const int64_t at = (int64_t)(seq.row0 + t) * a.q.ts + head * a.q.hs + half * 8;
+      const u16* at = static_cast<const u16*>(a.q.p) + (int64_t)(seq.row0 + t) * a.q.ts + head * a.q.hs + half * 8;
       const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        float v[8];
-        load8<F32>(a.q.p, at + 16 * s, v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[T];
-          split2<T>(v[2 * e], v[2 * e + 1], w);
-#pragma unroll
-          for (int x = 0; x < T; ++x) qf[x][s][e] = w[x] ^ flip;
-        }
+        const uint4 w = *reinterpret_cast<const uint4*>(at + 16 * s);
+        qf[s] = frag(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
       }
     }
     f32x16_t o[NT];
@@ -232,7 +210,7 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       gone = __ballot(!ok);
     };
     auto fetch_tile = [&](Raw<D>& r, bool is_v, int t) {
-      if (t - t0 >= 64) find(t - 1);  // keys are a tile ahead of values
+      if (t - t0 >= 64) find(t);
       const int i = t - t0;
       const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)my_block, i);
       const uint32_t hi32 = __builtin_amdgcn_readlane((int)(my_block >> 32), i);
@@ -240,7 +218,7 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
                __builtin_amdgcn_readlane((int)my_off, i), (gone >> i & 1) == 0, page, lane);
     };
     auto unpack_tile = [&](Raw<D>& r, bool is_v, int t) {
-      unpack<D>(r, is_v, piece, kbuf[t % KB], vbuf[t & 1], &kmarks[t & 3], &vmarks[t % 3], lane);
+      unpack<D>(r, is_v, piece, kbuf[t % 3], vbuf[t & 1], &kmarks[t & 3], &vmarks[t % 3], lane);
     };
 
     auto fragment = [&](const uint8_t* at, int i) { return *reinterpret_cast<const bf16x8_t*>(at + i * 1024); };
@@ -248,13 +226,11 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
     auto scores = [&](f32x16_t& s, int t, int u) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = 0.f;
-      const uint8_t* at = kbuf[t % KB] + u * (KS * 1024) + lane * 16;
+      const uint8_t* at = kbuf[t % 3] + u * (KS * 1024) + lane * 16;
 #pragma unroll
       for (int q = 0; q < KS; ++q) {
         const bf16x8_t kf = fragment(at, q);
-#pragma unroll
-        for (int y = T - 1; y >= 0; --y)
-          s = mfma32(kf, frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), s);
+        s = mfma32(kf, qf[q], s);
       }
     };
 
@@ -269,7 +245,7 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
     // this lane's; `n` gets those of the half after it meanwhile, and mx theirs.
     float mx = kNone;
     auto step = [&](f32x16_t& s, f32x16_t& n, int t, int u, bool odd) {
-      const uint8_t* kat = kbuf[(u ? t + 1 : t) % KB] + (u ^ 1) * (KS * 1024) + lane * 16;
+      const uint8_t* kat = kbuf[(u ? t + 1 : t) % 3] + (u ^ 1) * (KS * 1024) + lane * 16;
       bf16x8_t ring[RD];
 #pragma unroll
       for (int q = 0; q < RD; ++q) ring[q] = fragment(kat, q);
@@ -313,26 +289,19 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       // (Past the last tile the first product is of old keys, and unused.)
       const uint8_t* vat = vbuf[t & 1] + 2 * u * (NT * 1024) + lane * 16;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t pw[T][8];  // the weights, two keys a word
+      uint32_t pw[8];  // the weights, two keys a word
 #pragma unroll
       for (int e = 0; e < 16; ++e) n[e] = 0.f;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < KS; ++q) {
-#pragma unroll
-        for (int y = T - 1; y >= 0; --y)
-          n = mfma32(ring[q % RD], frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), n);
+        n = mfma32(ring[q % RD], qf[q], n);
         ring[q % RD] = q + RD < KS ? fragment(kat, q + RD) : fragment(vat, q + RD - KS);
 #pragma unroll
         for (int e = q * 16 / KS; e < (q + 1) * 16 / KS; ++e) {
           s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], sc, -ms));
           sum[e & 3] += s[e];
-          if (e & 1) {
-            uint32_t w[T];
-            split2<T>(s[e - 1], s[e], w);
-#pragma unroll
-            for (int y = 0; y < T; ++y) pw[y][e >> 1] = w[y];
-          }
+          if (e & 1) pw[e >> 1] = pack_bf16(s[e - 1], s[e]);
         }
         __builtin_amdgcn_sched_barrier(kFence);
       }
@@ -344,15 +313,13 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int k = 8 * (e >> 1) + 2 * (e & 1);
-          pw[0][e] |= (spread(poison, k) & 0x7fc0u) | (spread(poison, k + 1) & 0x7fc00000u);
+          pw[e] |= (spread(poison, k) & 0x7fc0u) | (spread(poison, k + 1) & 0x7fc00000u);
         }
       }
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i) {
         const int g = i / NT, f = i % NT;
-#pragma unroll
-        for (int y = T - 1; y >= 0; --y)
-          o[f] = mfma32(ring[i % RD], frag(pw[y][4 * g], pw[y][4 * g + 1], pw[y][4 * g + 2], pw[y][4 * g + 3]), o[f]);
+        o[f] = mfma32(ring[i % RD], frag(pw[4 * g], pw[4 * g + 1], pw[4 * g + 2], pw[4 * g + 3]), o[f]);
         if (i + RD < 2 * NT) ring[i % RD] = fragment(vat, i + RD);
         // the next half's maximum, beside the second product
 #pragma unroll
@@ -367,31 +334,24 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
 
     // Tile t is computed from keys t and t + 1 and values t; keys t + 2 and
     // values t + 1 are decoded meanwhile into the buffers that t - 1 has left,
-    // keys t + 3 and values t + 2 are on their way, and the pages of the ones
-    // after those are looked up. (Wide heads' LDS holds two tiles of keys: there
-    // keys t + 2 take the place of t's, behind a barrier in the tile's middle.) Waves that decode keys do it first and those that
-    // decode values last, so that the two of a SIMD are not at the same work.
-    constexpr bool kBoth = NW == 4;
-    const bool do_k = kBoth || wave < 4, do_v = kBoth || wave >= 4;
+    // and keys t + 3 and values t + 2 are on their way. Waves 0-3 decode keys,
+    // first of all, and waves 4-7 values, last of all, so that the two of a
+    // SIMD are not at the same work.
+    const bool is_v = wave >= 4;
     __syncthreads();  // the last tile of rows is done with LDS
     if (threadIdx.x < 4) kmarks[threadIdx.x] = KeyMarks{};
     if (threadIdx.x < 3) vmarks[threadIdx.x] = ValueMarks{};
     __syncthreads();
-    Raw<D> rk, rv;
+    Raw<D> raw;
     f32x16_t sa, sb;
     if (tiles > 0) {
       find(0);
-      if (do_k) {
-        fetch_tile(rk, false, 0);
-        unpack_tile(rk, false, 0);
-        fetch_tile(rk, false, 1);
-        unpack_tile(rk, false, 1);
-        fetch_tile(rk, false, 2);
-      }
-      if (do_v) {
-        fetch_tile(rv, true, 0);
-        unpack_tile(rv, true, 0);
-        fetch_tile(rv, true, 1);
+      fetch_tile(raw, is_v, 0);
+      unpack_tile(raw, is_v, 0);
+      fetch_tile(raw, is_v, 1);
+      if (!is_v) {
+        unpack_tile(raw, false, 1);
+        fetch_tile(raw, false, 2);
       }
       __syncthreads();
       scores(sa, 0, 0);
@@ -403,13 +363,10 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
         kmarks[(t + 3) & 3] = KeyMarks{};
         vmarks[(t + 2) % 3] = ValueMarks{};
       }
-      auto keys = [&]() {
-        if (do_k && t + 2 < tiles) {
-          unpack_tile(rk, false, t + 2);
-          fetch_tile(rk, false, t + 3);
-        }
-      };
-      if (KB == 3) keys();
+      if (!is_v && t + 2 < tiles) {
+        unpack_tile(raw, false, t + 2);
+        fetch_tile(raw, false, t + 3);
+      }
       if (wanted(t)) {
         const KeyMarks km = kmarks[t & 3];
         const ValueMarks vm = vmarks[t % 3];
@@ -418,24 +375,14 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
             (km.absent[0] | km.absent[1] | km.nan[0] | km.nan[1] | vm.nan[0] | vm.nan[1]) != 0 ||
             j < last.lo || j + kManyKeys > first.hi);
         step(sa, sb, t, 0, odd);
-        if (KB == 2) {  // the second half of keys t is read: their buffer is free
-          __syncthreads();
-          keys();
-        }
         step(sb, sa, t, 1, odd);
-      } else {
-        if (KB == 2) {
-          __syncthreads();
-          keys();
-        }
-        if (wanted(t + 1)) {
-          scores(sa, t + 1, 0);
-          mx = largest(sa);
-        }
+      } else if (wanted(t + 1)) {
+        scores(sa, t + 1, 0);
+        mx = largest(sa);
       }
-      if (do_v && t + 1 < tiles) {
-        unpack_tile(rv, true, t + 1);
-        fetch_tile(rv, true, t + 2);
+      if (is_v && t + 1 < tiles) {
+        unpack_tile(raw, true, t + 1);
+        fetch_tile(raw, true, t + 2);
       }
     }
     l += __shfl_xor(l, 32);
@@ -467,14 +414,9 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
       for (int e = 0; e < 16; ++e) {
         const int64_t x = at + NT * (8 * (e >> 2) + 4 * half + (e & 3));
 #pragma unroll
-        for (int f = 0; f < NT; f += 2) {
-          if constexpr (F32)
-            *reinterpret_cast<float2*>(static_cast<float*>(a.o.p) + x + f) =
-                make_float2(o[f][e] * inv, o[f + 1][e] * inv);
-          else
-            *reinterpret_cast<uint32_t*>(static_cast<u16*>(a.o.p) + x + f) =
-                pack_bf16(o[f][e] * inv, o[f + 1][e] * inv);
-        }
+        for (int f = 0; f < NT; f += 2)
+          *reinterpret_cast<uint32_t*>(static_cast<u16*>(a.o.p) + x + f) =
+              pack_bf16(o[f][e] * inv, o[f + 1][e] * inv);
       }
     }
   }
@@ -484,18 +426,14 @@ __global__ __launch_bounds__(64 * many_waves(D, F32)) void attend_many_kernel(At
 
 hipError_t launch_attend_many(const AttnLaunch& a, hipStream_t s) {
   const int group = a.q.heads / a.pool.heads;
-  const int waves = many_waves(a.pool.dim, a.f32);
-  int64_t tiles = ((int64_t)a.max_new * group + 32 * waves - 1) / (32 * waves);
+  int64_t tiles = ((int64_t)a.max_new * group + kManyRows - 1) / kManyRows;
   const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads);
   if (tiles > most) tiles = most;  // a workgroup then takes several
   const dim3 grid((uint32_t)(tiles * a.splits * a.pool.heads), a.pool.batch);
-#define TTT_CALL(D, T, F) attend_many_kernel<D, T, F><<<grid, 64 * waves, 0, s>>>(a, (int)tiles)
-  switch (a.pool.dim) {
-    case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
-    case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
-    default: if (a.f32) { TTT_CALL(256, 3, true); } else { TTT_CALL(256, 1, false); } break;
-  }
-#undef TTT_CALL
+  if (a.pool.dim == 64)
+    attend_many_kernel<64><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)tiles);
+  else
+    attend_many_kernel<128><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)tiles);
   return hipGetLastError();
 }
 

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
   int id = blockIdx.x;
   const int hk = id % a.pool.heads;
   id /= a.pool.heads;
-  const int tile0 = id % row_tiles;
+  const int tile0 = row_tiles - 1 - id % row_tiles;  // the last, which see most, first
   id /= row_tiles;
   const int b = id % a.pool.batch, split = id / a.pool.batch;
   const int group = a.q.heads / a.pool.heads;
@@ -113,8 +113,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
     const uint32_t vs_lane = page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + 4 * g;
 
     // This split's stretches of `each` keys, a quarter of each for every wave.
-    for (int s0 = lo + split * a.each; s0 < hi; s0 += a.splits * a.each) {
-      const int per = a.each / NW;
+    // (One part: all of the tile's keys, whatever the launch expected.)
+    const int per = a.splits == 1 ? (max(hi - lo, 1) + 32 * NW - 1) / (32 * NW) * 32 : a.each / NW;
+    for (int s0 = lo + split * per * NW; s0 < hi; s0 += a.splits * per * NW) {
       const int k0 = s0 + wave * per, k1 = min(hi, k0 + per);
       // Where 64 pieces of 16 keys lie, one a lane: the address of the head's
       // block and the first key's place in it. Loads take the address from
@@ -437,8 +438,23 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
 
 namespace {
 
-// Rows of one sequence and key head from which the many-row kernel is taken.
-constexpr int kManyFrom = 64;
+// Whether the many-row kernel is taken: for bf16 rows with heads of 64 or 128,
+// more than 128 of them a sequence and key head, and 2^25 pairs of a row and
+// a key in all. It decodes a tile of keys for 256 rows at once, and starts
+// slowly. In us, few-row kernel / many-row kernel (32/8 heads):
+//   128: 256 rows of 8k keys 32 / 41, of 16k 47 / 48; 512 of 16k 83 / 65; 4096
+//   of 8k 260 / 162, 16384 749 / 449; 4 sequences of 16k keys: 128 rows each
+//   82 / 89, 256 153 / 102.   64: 256 of 16k 39 / 36, 16384 of 8k 534 / 334.
+// fp32 rows keep the matrix unit three times as long, beside which decoding
+// for 16 rows alone costs little, and with wide heads a workgroup's sums leave
+// no registers for a second wave: built for them, it took 879 us for the
+// few-row kernel's 783 (fp32, 64), 1146 for 1162 (fp32, 128), 2148 for 1351
+// (fp32, 256) and 612 for 689 (bf16, 256) over 16384 rows and 8k keys, and
+// lost wherever there were fewer.
+bool take_many(int64_t rows, double pairs, bool f32, int dim) {
+  return !f32 && dim <= 128 && rows > 128 && pairs >= 0x1p25;
+}
+
 // Keys up to which one workgroup of the few-row kernel takes a whole sequence,
 // without the join's launch and its workspace. On the GPU alone (32/8 heads)
 // one sequence of 512 keys takes 7.5 us so and 7.8 in parts, of 1024 9.6 and
@@ -449,61 +465,52 @@ constexpr int kOneGroup = 1024;
 
 }  // namespace
 
-int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
-                int dim, int* each) {
+AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
+                   int dim) {
   const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
   int64_t keys = max_kv;
   if (window > 0) keys = keys < (int64_t)window + max_new ? keys : (int64_t)window + max_new;
-  if (attn_many(rows, f32, dim)) {
-    const int per = 32 * many_waves(dim, f32);
-    const int64_t groups = (rows + per - 1) / per * kv_heads * batch;
+  if (take_many(rows, (double)rows * keys * kv_heads * batch, f32, dim)) {
+    // Parts until there is a workgroup for every CU, of 512 keys at least.
+    const int64_t groups = (rows + kManyTile - 1) / kManyTile * kv_heads * batch;
     const int64_t most = (keys + 511) / 512;
     int64_t want = 256 / groups;
     if (want > most) want = most;
-    *each = 0;
-    return (int)(want < 1 ? 1 : want);
+    return {true, (int)(want < 1 ? 1 : want), 0};
   }
-  // A short sequence is one workgroup of eight waves: no join, no workspace.
-  if (keys <= kOneGroup) {
-    *each = (int)((keys + 255) & ~(int64_t)255);
-    return 1;
-  }
+  // A short sequence is one workgroup of eight waves.
+  if (keys <= kOneGroup) return {false, 1, kOneGroup};
   // Stretches that give 512 workgroups of four waves, or 1024 where some
   // sequences may be shorter than max_kv; of 512 keys or more where there is
   // much to do (each workgroup loads its rows and hands in its sums), and of
   // 128 at least. 1 token over 128k keys: 512 take 35.4 us, 768 36.8, 1024
   // 40.6, 2304 44.0; 32 ragged sequences: 1024 128.8 us, 2048 129.9, 6144 134.4.
-  const int64_t tiles = (rows + 15) / 16 * kv_heads * batch;
-  const int64_t want = batch > 1 ? 1024 : 512;
-  int64_t e = (keys * tiles + want - 1) / want;
-  const int64_t least = keys * tiles < 512 * 256 ? 128 : 512;
-  if (e < least) e = least;
-  if (e > (1 << 20)) e = 1 << 20;
-  e = (e + 127) & ~(int64_t)127;
-  *each = (int)e;
-  return (int)((keys + e - 1) / e);
+  const double work = (double)keys * ((rows + 15) / 16) * kv_heads * batch;
+  const double fair = work / (batch > 1 ? 1024 : 512), least = work < 512 * 256 ? 128 : 512;
+  const double most = 1 << 20, e = fair < least ? least : fair > most ? most : fair;
+  const int each = ((int)e + 127) / 128 * 128;
+  return {false, (int)((keys + each - 1) / each), each};
 }
 
-bool attn_many(int64_t rows, bool f32, int dim) { return rows >= kManyFrom && !(f32 && dim == 256); }
-
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
+  if (a.many) return launch_attend_many(a, s);
   const int group = a.q.heads / a.pool.heads;
-  if (attn_many((int64_t)a.max_new * group, a.f32, a.pool.dim)) return launch_attend_many(a, s);
   int64_t tiles = ((int64_t)a.max_new * group + 15) / 16;
   const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads * a.pool.batch);
   if (tiles > most) tiles = most < 1 ? 1 : most;  // a workgroup then takes several
   const uint32_t grid = (uint32_t)(tiles * a.splits * a.pool.heads * a.pool.batch);
-  // (wide fp32 heads need the registers that eight waves do not have)
-  const bool wide = a.splits == 1 && a.each <= kOneGroup && !(a.f32 && a.pool.dim == 256);
-#define TTT_CALL(D, T, F)                                             \
-  if (wide)                                                           \
-    attend_few_kernel<D, T, F, F && D == 256 ? 4 : 8><<<grid, 512, 0, s>>>(a, (int)tiles); \
-  else                                                                \
+  // Eight waves for short sequences; wide fp32 heads need the registers that
+  // eight do not have.
+  const bool wide = a.splits == 1 && a.each <= kOneGroup;
+#define TTT_CALL(D, T, F, W)                                                       \
+  if (wide)                                                                        \
+    attend_few_kernel<D, T, F, W><<<grid, 64 * W, 0, s>>>(a, (int)tiles);          \
+  else                                                                             \
     attend_few_kernel<D, T, F, 4><<<grid, 256, 0, s>>>(a, (int)tiles)
   switch (a.pool.dim) {
-    case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
-    case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
-    default: if (a.f32) { TTT_CALL(256, 3, true); } else { TTT_CALL(256, 1, false); } break;
+    case 64: if (a.f32) { TTT_CALL(64, 3, true, 8); } else { TTT_CALL(64, 1, false, 8); } break;
+    case 128: if (a.f32) { TTT_CALL(128, 3, true, 8); } else { TTT_CALL(128, 1, false, 8); } break;
+    default: if (a.f32) { TTT_CALL(256, 3, true, 4); } else { TTT_CALL(256, 1, false, 8); } break;
   }
 #undef TTT_CALL
   return hipGetLastError();

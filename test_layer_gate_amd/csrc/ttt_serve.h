@@ -69,7 +69,8 @@ struct AttnLaunch {
   float scale;
   int causal, window, max_new, max_kv;
   bool f32;
-  int splits, each;      // attn_splits()
+  bool many;             // attn_plan()
+  int splits, each;
   float* part;           // [splits][tokens * q heads][D] (splits > 1)
   float* part_ml;        // [splits][tokens * q heads][2]
 };
@@ -80,14 +81,16 @@ hipError_t launch_rope_table(float* table, int max_pos, int rot, double base, in
                              hipStream_t s);
 hipError_t launch_append(const AppendLaunch& a, hipStream_t s);
 hipError_t launch_read(const ReadLaunch& a, hipStream_t s);
-// How many parts each sequence's keys are cut into; for the few-row kernel
-// *each keys a stretch, part s taking every splits-th stretch from the s-th.
-int attn_splits(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
-                int dim, int* each);
-// Whether `rows` rows a sequence and key head go to the many-row kernel, and
-// how many waves of 32 rows its workgroups have.
-bool attn_many(int64_t rows, bool f32, int dim);
-constexpr int many_waves(int dim, bool f32) { return dim == 256 || f32 ? 4 : 8; }
+// How attention is launched: by which kernel, in how many parts of each
+// sequence's keys, and for the few-row kernel in stretches of how many keys
+// (part s takes every splits-th stretch from the s-th).
+struct AttnPlan {
+  bool many;
+  int splits, each;
+};
+AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
+                   int dim);
+constexpr int kManyTile = 256;  // rows of a workgroup of the many-row kernel
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s);
 hipError_t launch_attend_many(const AttnLaunch& a, hipStream_t s);
 hipError_t launch_attention_join(const AttnLaunch& a, hipStream_t s);

@@ -464,9 +464,9 @@ ttt_status ttt_kv_attention_workspace_size(const ttt_attn* attn, int32_t batch, 
   TTT_TRY(check_tokens(tokens, act_dtype));
   size_t page = 0;
   TTT_TRY(ttt_kv_page_bytes(16, kv_heads, head_dim, &page));
-  int each = 0;
-  const int n = tttk::attn_splits(batch, kv_heads, q_heads, attn->max_new, attn->max_kv, attn->window,
-                                  act_dtype == TTT_F32, head_dim, &each);
+  const int n = tttk::attn_plan(batch, kv_heads, q_heads, attn->max_new, attn->max_kv, attn->window,
+                                act_dtype == TTT_F32, head_dim)
+                    .splits;
   *bytes = part_bytes(n, tokens, q_heads, head_dim) + ml_bytes(n, tokens, q_heads);
   return TTT_OK;
   TTT_ENTRY_END
@@ -488,8 +488,9 @@ ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_
   TTT_TRY(check_attn(attn, a.pool.batch, a.pool.heads, q->heads));
   if (lse != nullptr) TTT_TRY(check_ptr(lse, "lse", 4));
   if (tokens == 0) return TTT_OK;
-  a.splits = tttk::attn_splits(a.pool.batch, a.pool.heads, q->heads, attn->max_new, attn->max_kv,
-                               attn->window, a.f32, dim, &a.each);
+  const tttk::AttnPlan plan = tttk::attn_plan(a.pool.batch, a.pool.heads, q->heads, attn->max_new,
+                                              attn->max_kv, attn->window, a.f32, dim);
+  a.many = plan.many, a.splits = plan.splits, a.each = plan.each;
   const size_t need_part = part_bytes(a.splits, tokens, q->heads, dim);
   const size_t need = need_part + ml_bytes(a.splits, tokens, q->heads);
   const int64_t size = a.f32 ? 4 : 2;

@@ -58,14 +58,28 @@ def pool_of(rng, lens, page, hk, dim, garbage=True):
     return pages, table
 
 
-def check(ttt, dtype, page, hk, hq, dim, news, lens, *, window=0, causal=True, seed=0, sharp=1.5,
-          pages=None, table=None, q=None, no_starts=False, **kw):
+# The bounds size the launch, and with it choose the kernel: under large ones
+# bf16 rows with heads of 64 and 128 go to the many-row kernel whatever there
+# is of them, the first in few parts, the second in many (some of them empty).
+MANY = [dict(max_new=4096, max_kv=1 << 16), dict(max_new=200, max_kv=1 << 22)]
+
+
+def check(ttt, dtype, page, hk, hq, dim, news, lens, *, q=None, seed=0, **kw):
     rng = np.random.default_rng(seed)
-    if pages is None:
-        pages, table = pool_of(rng, lens, page, hk, dim)
-    n = sum(news)
+    if kw.get("pages") is None:
+        kw["pages"], kw["table"] = pool_of(rng, lens, page, hk, dim)
     if q is None:
-        q = torch.from_numpy(sharp * rng.standard_normal((n, hq, dim))).to(dtype).cuda()
+        q = torch.from_numpy(kw.pop("sharp", 1.5) * rng.standard_normal((sum(news), hq, dim))).to(dtype).cuda()
+    refs = {}
+    o = check_one(ttt, dtype, page, hk, hq, dim, news, lens, q, refs, **kw)
+    if dtype == BF and dim <= 128 and "max_new" not in kw:
+        for bounds in MANY:
+            check_one(ttt, dtype, page, hk, hq, dim, news, lens, q, refs, **kw, **bounds)
+    return o
+
+
+def check_one(ttt, dtype, page, hk, hq, dim, news, lens, q, refs, *, window=0, causal=True,
+              pages=None, table=None, no_starts=False, **kw):
     starts = np.concatenate([[0], np.cumsum(news)])
     scale = dim ** -0.5
     o, lse = ttt.kv_attention(q, torch.from_numpy(pages).cuda(), ints(table), ints(lens),
@@ -76,8 +90,10 @@ def check(ttt, dtype, page, hk, hq, dim, news, lens, *, window=0, causal=True, s
     o, lse, qh = host(o), host(lse), host(q)
     for b, (m, length) in enumerate(zip(news, lens)):
         r = slice(starts[b], starts[b + 1])
-        k, v, have = so.gather(pages, table, b, int(length), dim)
-        ref, lref, w = so.attend(qh[r], k, v, have, int(length), scale, window, causal)
+        if b not in refs:
+            k, v, have = so.gather(pages, table, b, int(length), dim)
+            refs[b] = (k, *so.attend(qh[r], k, v, have, int(length), scale, window, causal))
+        k, ref, lref, w = refs[b]
         ks = np.abs(np.nan_to_num(k)).repeat(hq // hk, 1)
         terms = scale * np.einsum("thd,jhd->thj", np.abs(qh[r]), ks).max(-1) if length else 0.0
         rel = (4 * np.sqrt(dim) * 2 ** -24 * terms + 2 ** -21 + 4 * np.sqrt(max(length, 1)) * 2 ** -24)
@@ -176,8 +192,12 @@ def test_bounds_are_hints(ttt):
     """max_new and max_kv size the launch; wrong ones change no result."""
     rng = np.random.default_rng(6)
     pages, table = pool_of(rng, [3000, 40], 64, 2, 128)
-    for kw in (dict(max_new=1, max_kv=1), dict(max_new=64, max_kv=64), dict(max_new=9999, max_kv=10 ** 8)):
-        check(ttt, BF, 64, 2, 8, 128, [37, 5], [3000, 40], pages=pages, table=table, **kw)
+    for dtype in (BF, F32):
+        for kw in (dict(max_new=1, max_kv=1), dict(max_new=64, max_kv=64), dict(max_new=9999, max_kv=10 ** 8),
+                   dict(max_new=1, max_kv=10 ** 8)):
+            check(ttt, dtype, 64, 2, 8, 128, [37, 5], [3000, 40], pages=pages, table=table, **kw)
+    # one small workgroup of rows for all of them
+    check(ttt, BF, 64, 2, 8, 128, [300], [3000], max_new=33, max_kv=1 << 22)
 
 
 def test_strided_rows_other_streams_and_outputs(ttt):
@@ -239,3 +259,29 @@ def test_captured_step_follows_the_lengths(ttt):
         torch.cuda.synchronize()
         assert torch.equal(got, o), t
         assert torch.equal(pages, eager), t
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_rows_over_long_caches(ttt, dim):
+    """Rows and keys enough for the many-row kernel by themselves, whole and in
+    parts: page tables longer than the 64 tiles it looks up at once."""
+    check(ttt, BF, 16, 1, 2, dim, [66, 70], [4700, 9000], window=0, max_new=70, max_kv=1 << 22)
+    check(ttt, BF, 256, 1, 2, dim, [66], [9000], window=5000, max_new=4096, max_kv=1 << 13)
+
+
+def test_negative_and_zero_scales(ttt):
+    """A scale of either sign, and none: the maximum is followed unscaled."""
+    rng = np.random.default_rng(9)
+    pages, table = pool_of(rng, [300], 32, 2, 128)
+    q = torch.from_numpy(rng.standard_normal((20, 4, 128)))
+    k, v, have = so.gather(pages, table, 0, 300, 128)
+    for dtype in (BF, F32):
+        x = q.to(dtype).cuda()
+        for scale in (-0.1, 0.0, 1e-30):
+            ref, lref, w = so.attend(host(x), k, v, have, 300, scale)
+            for kw in ({}, *MANY):
+                o, lse = ttt.kv_attention(x, torch.from_numpy(pages).cuda(), ints(table), ints([300]),
+                                          scale=scale, with_lse=True, **kw)
+                u = 2 ** -7 if dtype == BF else 2 ** -17
+                assert (np.abs(host(o) - ref) <= u * (w + np.abs(ref))).all()
+                assert (np.abs(host(lse) - lref) <= 2 ** -17 * (1 + np.abs(lref))).all()
