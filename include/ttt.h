@@ -517,7 +517,7 @@ typedef struct ttt_cache {
   const int32_t* page_table;  /* [batch][max_pages] */
   const int32_t* kv_lens;     /* [batch] */
   const int32_t* q_starts;    /* [batch + 1], or NULL: tokens / batch each */
-  int32_t batch, max_pages, n_pages;
+  int32_t batch, max_pages, n_pages;  /* max_pages * page_size <= 2^30 */
   int32_t page_size;          /* a multiple of 16, at most 4096 */
   int32_t kv_heads;
   int32_t head_dim;           /* 64, 128 or 256 */

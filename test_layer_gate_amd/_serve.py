@@ -88,8 +88,17 @@ def _stream(stream, t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
-def _empty(t):
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _on(stream, make, *args, **kw):
+    """A tensor from the memory of the stream that the call runs on: torch may
+    give it away, when it is dropped, only behind the kernels there."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _empty(t, stream):
+    return _on(stream, torch.empty_like, t, memory_format=torch.contiguous_format)
 
 
 def _rows_of(t, what):
@@ -171,8 +180,8 @@ def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, orig
         amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 0 else 1.0
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
-    table = torch.empty((max(int(max_pos), 0), max(int(rot_dim), 0) // 2, 2), dtype=torch.float32,
-                        device=device)
+    table = _on(stream, torch.empty, (max(int(max_pos), 0), max(int(rot_dim), 0) // 2, 2),
+                dtype=torch.float32, device=device)
     sc = RopeScaling(ROPE_KINDS.get(scaling, 0), 0, float(factor), float(original or 1.0),
                      float(low), float(high), float(amplitude))
     _b._check(_L().ttt_rope_table(table.data_ptr(), int(max_pos), int(rot_dim), float(base),
@@ -184,11 +193,11 @@ def _rope_call(fn, q, k, table, positions, interleaved, q_out, k_out, stream):
     n, _, dim, rq = _rows_of(q, "q")
     act, dtype = _act(q, "q"), q.dtype
     if q_out is None:
-        q_out = _empty(q)
+        q_out = _empty(q, stream)
     ro = _rows(q_out, "q_out", n, dim, dtype)
     if k is not None:
         if k_out is None:
-            k_out = _empty(k)
+            k_out = _empty(k, stream)
         rk, rko = _ref(_rows(k, "k", n, dim, dtype)), _ref(_rows(k_out, "k_out", n, dim, dtype))
     else:
         rk = rko = None
@@ -264,7 +273,7 @@ def kv_append(pages, page_table, kv_lens, k, v, *, q=None, q_starts=None, rope_t
     rq = ro = None
     if q is not None:
         if q_out is None:
-            q_out = _empty(q)
+            q_out = _empty(q, stream)
         rq, ro = _ref(_rows(q, "q", n, dim, dtype)), _ref(_rows(q_out, "q_out", n, dim, dtype))
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -284,9 +293,9 @@ def kv_read(pages, page_table, kv_lens, rows, head_dim, dtype=torch.bfloat16, *,
     cache = _cache(pages, page_table, kv_lens, q_starts, head_dim)
     shape = (rows, pages.shape[1], head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=pages.device)
+        k_out = _on(stream, torch.empty, shape, dtype=dtype, device=pages.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=pages.device)
+        v_out = _on(stream, torch.empty, shape, dtype=dtype, device=pages.device)
     rk = _rows(k_out, "k_out", rows, head_dim, dtype)
     rv = _rows(v_out, "v_out", rows, head_dim, dtype)
     st = _L().ttt_kv_read(_ref(cache), rows, _act(k_out, "k_out"), _ref(rk), _ref(rv),
@@ -329,11 +338,11 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     if max_kv is None:
         max_kv = cache.max_pages * cache.page_size
     if out is None:
-        out = _empty(q)
+        out = _empty(q, stream)
     ro = _rows(out, "out", n, dim, q.dtype)
     if lse is None:
         if with_lse:
-            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+            lse = _on(stream, torch.empty, (n, heads), dtype=torch.float32, device=q.device)
     elif lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != n * heads:
         raise ValueError("lse must be a contiguous float32 [rows, q_heads] tensor")
     a = Attn(dim ** -0.5 if scale is None else scale, window, max_new, max_kv,
@@ -341,7 +350,7 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     if workspace is None:
         need = _workspace(cache.batch, n, act, cache.kv_heads, heads, dim, max_new, max_kv, window)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _on(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
     st = _L().ttt_kv_attention(_ref(cache), _ref(a), n, act, _ref(rq), _ref(ro),
                                None if lse is None else lse.data_ptr(),
                                None if workspace is None else workspace.data_ptr(),

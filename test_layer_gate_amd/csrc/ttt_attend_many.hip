@@ -14,8 +14,17 @@ namespace {
 // rows: waves 0-3 decode the tile's keys, waves 4-7 its values (each 16
 // tokens), and leave them in LDS in the order in which the matrix
 // instructions read them, 1 KB a fragment, so that a fragment is one
-// contiguous read. Two tiles' buffers alternate; raw codes are fetched two
-// tiles ahead and page numbers three.
+// contiguous read. Three tiles of keys and two of values are held: the keys of
+// the next tile are read by this one's work, those after it written meanwhile.
+// Raw codes are on their way one tile longer, and where a wave's pieces of 64
+// tiles lie is looked up at once, a tile a lane.
+//
+// Bound by the matrix unit and by what has to run beside it: of a matrix
+// instruction's 32 clocks a wave's exponentials, packing and fragment reads
+// take most, and decoding the rest. 1024 tokens of 32/8 heads of 128 at the end
+// of 64k keys take 1.0 ms, 1085 TFLOP/s (large library products reach 1211 to
+// 1361). Of 1.11 ms, an earlier step's, copies without decoding took 0.91,
+// without exponentials 0.95, with neither 0.79.
 //
 // S^T = K Q^T with 32x32x16: a lane holds, of one row, the keys 8 (i / 4) + 4
 // (lane / 32) + i % 4 of a 32-key tile. Taken eight at a time these are what
@@ -426,10 +435,9 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(AttnLaunch
 
 hipError_t launch_attend_many(const AttnLaunch& a, hipStream_t s) {
   const int group = a.q.heads / a.pool.heads;
-  int64_t tiles = ((int64_t)a.max_new * group + kManyRows - 1) / kManyRows;
-  const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads);
-  if (tiles > most) tiles = most;  // a workgroup then takes several
-  const dim3 grid((uint32_t)(tiles * a.splits * a.pool.heads), a.pool.batch);
+  const int64_t others = (int64_t)a.splits * a.pool.heads;
+  const int64_t tiles = tttk::row_tiles(a, group, kManyRows, others);
+  const dim3 grid((uint32_t)(tiles * others), a.pool.batch);
   if (a.pool.dim == 64)
     attend_many_kernel<64><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)tiles);
   else

@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u;
 }
 
-// The keys that row r of a tile sees: [lo, hi).
+// The keys that a sequence's new token t sees: [lo, hi).
 struct Span {
   int lo, hi;
 };
@@ -75,7 +75,7 @@ __device__ __forceinline__ Span span_of(const AttnLaunch& a, int len, int news, 
   const int p = len - news + t;
   Span s;
   s.hi = a.causal ? min(p + 1, len) : len;
-  s.lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  s.lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
   return s;
 }
 
@@ -97,6 +97,28 @@ __device__ __forceinline__ uint4 load16(Global p) {
 }
 __device__ __forceinline__ uint32_t load4(Global p) {
   return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p);
+}
+
+// Tiles of `each` rows that a sequence is launched with: as max_new and the
+// rows there are at all allow; not above 2^20 workgroups, `others` a tile (a
+// workgroup then takes several tiles).
+inline int64_t row_tiles(const AttnLaunch& a, int group, int each, int64_t others) {
+  const int64_t news = a.max_new < a.pool.tokens ? a.max_new : a.pool.tokens;
+  int64_t tiles = (news * group + each - 1) / each;
+  const int64_t most = ((int64_t)1 << 20) / others;
+  if (tiles > most) tiles = most;
+  return tiles < 1 ? 1 : tiles;
+}
+
+// n workgroups, numbered along x and then y: a dimension of a launch holds
+// less than 2^32 threads. The last of y may have workgroups too many.
+inline dim3 grid_of(int64_t n) {
+  constexpr int64_t kWidth = (int64_t)1 << 22;
+  if (n <= kWidth) return dim3((uint32_t)n);
+  return dim3((uint32_t)kWidth, (uint32_t)((n + kWidth - 1) / kWidth));
+}
+__device__ __forceinline__ int64_t block_of_grid() {
+  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
 }
 
 // Sequence b's rows, and its keys.

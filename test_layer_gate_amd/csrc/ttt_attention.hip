@@ -25,11 +25,17 @@ namespace {
 // Few rows. A wave takes 16 rows (query heads of one key head, times tokens)
 // and a stretch of the keys, 32 at a time, the next 32 on their way meanwhile.
 // S^T = K Q^T with 16x16x32: lane (i, g) = (lane % 16, lane / 16) brings D / 4
-// neighbouring values of key i; of the result it holds, for row i, keys 4g .. 4g + 3 of either 16. Those eight are what the second product
-// O^T = V^T P^T (16x16x32) asks of it: the order of the contraction is free as
-// long as V agrees, so P goes over without a move between lanes. Of V it
-// brings the same eight keys' values i D / 16 .. + D / 16 - 1. NW waves share
-// a workgroup's stretch of keys and join in LDS.
+// neighbouring values of key i; of the result it holds, for row i, keys 4g ..
+// 4g + 3 of either 16. Those eight are what the second product O^T = V^T P^T
+// (16x16x32) asks of it: the order of the contraction is free as long as V
+// agrees, so P goes over without a move between lanes. Of V it brings the same
+// eight keys' values i D / 16 .. + D / 16 - 1. NW waves share a workgroup's
+// stretch of keys and join in LDS.
+//
+// Bound by how many bytes are on their way: three waves a SIMD (bf16, 128) with
+// 32 keys each, 4.3 KB. One token of 40/8 heads of 128 over 128k keys (143 MB)
+// takes 27 us, 5.3 TB/s, and its join 4; 32 sequences of 4k to 32k keys, 32/8
+// heads (0.56 GB), 115 us and 5.
 
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
 template <int D>
@@ -55,12 +61,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
   // Key heads vary fastest, then rows, sequences and at last splits: workgroups
   // go round the XCDs in this order, and a split that short sequences do not
   // have must not be one XCD's.
-  int id = blockIdx.x;
+  int id = (int)block_of_grid();
   const int hk = id % a.pool.heads;
   id /= a.pool.heads;
   const int tile0 = row_tiles - 1 - id % row_tiles;  // the last, which see most, first
   id /= row_tiles;
   const int b = id % a.pool.batch, split = id / a.pool.batch;
+  if (split >= a.splits) return;
   const int group = a.q.heads / a.pool.heads;
   const int page = a.pool.page, gpp = page >> 4;  // 16-key pieces a page
 
@@ -112,11 +119,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
     const int ks_shift = D == 64 ? 16 * (i16 & 1) + 8 * (g >> 1) : D == 128 ? 8 * g : 16 * (g & 1);
     const uint32_t vs_lane = page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + 4 * g;
 
-    // This split's stretches of `each` keys, a quarter of each for every wave.
+    // This split's stretches of `each` keys, a wave's share of each.
     // (One part: all of the tile's keys, whatever the launch expected.)
     const int per = a.splits == 1 ? (max(hi - lo, 1) + 32 * NW - 1) / (32 * NW) * 32 : a.each / NW;
-    for (int s0 = lo + split * per * NW; s0 < hi; s0 += a.splits * per * NW) {
-      const int k0 = s0 + wave * per, k1 = min(hi, k0 + per);
+    for (int64_t s0 = lo + (int64_t)split * per * NW; s0 < hi; s0 += (int64_t)a.splits * per * NW) {
+      const int k0 = (int)s0 + wave * per, k1 = min(hi, k0 + per);
       // Where 64 pieces of 16 keys lie, one a lane: the address of the head's
       // block and the first key's place in it. Loads take the address from
       // scalar registers and a 32-bit offset of the lane's.
@@ -384,7 +391,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
   __shared__ float red_l[ROWS][LANES];
   const int rr = threadIdx.x / TPR, c = threadIdx.x % TPR % (D / 4), y = threadIdx.x % TPR / (D / 4);
   const int64_t rows = (int64_t)a.pool.tokens * a.q.heads;
-  const int64_t row = min((int64_t)blockIdx.x * ROWS + rr, rows - 1);
+  const int64_t row0 = block_of_grid() * ROWS;
+  if (row0 >= rows) return;
+  const int64_t row = min(row0 + rr, rows - 1);
   float m = kNone;
   if constexpr (LANES > 1) {
     // the maximum, one split a thread
@@ -420,7 +429,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
       l += red_l[rr][z];
     }
   }
-  if ((int64_t)blockIdx.x * ROWS + rr >= rows) return;
+  if (row0 + rr >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int n = (int)(row / a.q.heads), h = (int)(row % a.q.heads);
   if (a.lse != nullptr && c == 0)
@@ -468,7 +477,7 @@ constexpr int kOneGroup = 1024;
 AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
                    int dim) {
   const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
-  int64_t keys = max_kv;
+  int64_t keys = max_kv < kMaxKeys ? max_kv : kMaxKeys;
   if (window > 0) keys = keys < (int64_t)window + max_new ? keys : (int64_t)window + max_new;
   if (take_many(rows, (double)rows * keys * kv_heads * batch, f32, dim)) {
     // Parts until there is a workgroup for every CU, of 512 keys at least.
@@ -495,10 +504,9 @@ AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   if (a.many) return launch_attend_many(a, s);
   const int group = a.q.heads / a.pool.heads;
-  int64_t tiles = ((int64_t)a.max_new * group + 15) / 16;
-  const int64_t most = ((int64_t)1 << 30) / ((int64_t)a.splits * a.pool.heads * a.pool.batch);
-  if (tiles > most) tiles = most < 1 ? 1 : most;  // a workgroup then takes several
-  const uint32_t grid = (uint32_t)(tiles * a.splits * a.pool.heads * a.pool.batch);
+  const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
+  const int64_t tiles = tttk::row_tiles(a, group, 16, others);
+  const dim3 grid = grid_of(tiles * others);
   // Eight waves for short sequences; wide fp32 heads need the registers that
   // eight do not have.
   const bool wide = a.splits == 1 && a.each <= kOneGroup;
@@ -523,10 +531,10 @@ hipError_t launch_attention_join(const AttnLaunch& a, hipStream_t s) {
   const bool one = a.splits > 4 || rows < 512;
 #define TTT_CALL(D, F)                                                                        \
   if (one)                                                                                    \
-    attend_join_kernel<D, F, 1><<<(uint32_t)rows, 256, 0, s>>>(a);                            \
+    attend_join_kernel<D, F, 1><<<grid_of(rows), 256, 0, s>>>(a);                             \
   else                                                                                        \
     attend_join_kernel<D, F, 1024 / D>                                                        \
-        <<<(uint32_t)((rows + 1024 / D - 1) / (1024 / D)), 256, 0, s>>>(a)
+        <<<grid_of((rows + 1024 / D - 1) / (1024 / D)), 256, 0, s>>>(a)
   switch (a.pool.dim) {
     case 64: if (a.f32) { TTT_CALL(64, true); } else { TTT_CALL(64, false); } break;
     case 128: if (a.f32) { TTT_CALL(128, true); } else { TTT_CALL(128, false); } break;

@@ -81,6 +81,8 @@ hipError_t launch_rope_table(float* table, int max_pos, int rot, double base, in
                              hipStream_t s);
 hipError_t launch_append(const AppendLaunch& a, hipStream_t s);
 hipError_t launch_read(const ReadLaunch& a, hipStream_t s);
+// Tokens that a sequence may have: sums of two places among them stay in 32 bits.
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;
 // How attention is launched: by which kernel, in how many parts of each
 // sequence's keys, and for the few-row kernel in stretches of how many keys
 // (part s takes every splits-th stretch from the s-th).

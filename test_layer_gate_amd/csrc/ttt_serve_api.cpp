@@ -173,8 +173,8 @@ ttt_status check_cache(const ttt_cache* c, int64_t tokens, tttk::Pool* p) {
     return fail(TTT_ERR_INVALID_ARG, "n_pages and max_pages must be >= 1");
   size_t bytes = 0;
   TTT_TRY(ttt_kv_page_bytes(c->page_size, c->kv_heads, c->head_dim, &bytes));
-  if ((int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31)
-    return fail(TTT_ERR_UNSUPPORTED, "max_pages * page_size above 2^31");
+  if ((int64_t)c->max_pages * c->page_size > tttk::kMaxKeys)
+    return fail(TTT_ERR_UNSUPPORTED, "max_pages * page_size above 2^30");
   if (c->page_stride < (int64_t)bytes || c->page_stride % 16 != 0)
     return fail(TTT_ERR_INVALID_ARG,
                 "page_stride must be a multiple of 16, at least ttt_kv_page_bytes()");
@@ -316,6 +316,8 @@ ttt_status ttt_rope_table(float* table, int32_t max_pos, int32_t rot_dim, double
   if (rot_dim < 2) return fail(TTT_ERR_INVALID_ARG, "rot_dim must be >= 2");
   if (rot_dim % 16 != 0 || rot_dim > kMaxRopeDim)
     return fail(TTT_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16, at most 1024");
+  if ((int64_t)max_pos * rot_dim > (int64_t)1 << 32)
+    return fail(TTT_ERR_UNSUPPORTED, "max_pos * rot_dim above 2^32");
   if (!std::isfinite(base) || !(base > 1.0))
     return fail(TTT_ERR_INVALID_ARG, "base must be finite and > 1");
   TableArgs t = {table, max_pos, rot_dim, TTT_ROPE_PLAIN, base, 1.0, 1.0, 1.0, 1.0, 1.0};
@@ -486,6 +488,8 @@ ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_
   if (q->heads != o->heads)
     return fail(TTT_ERR_INVALID_ARG, "an output needs its input's heads");
   TTT_TRY(check_attn(attn, a.pool.batch, a.pool.heads, q->heads));
+  if ((int64_t)tokens * q->heads > (int64_t)1 << 30)
+    return fail(TTT_ERR_UNSUPPORTED, "tokens * q heads above 2^30");
   if (lse != nullptr) TTT_TRY(check_ptr(lse, "lse", 4));
   if (tokens == 0) return TTT_OK;
   const tttk::AttnPlan plan = tttk::attn_plan(a.pool.batch, a.pool.heads, q->heads, attn->max_new,

@@ -94,7 +94,7 @@ def test_rope_empty_and_aliases_that_are_fine(L):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(table=None), INVALID), (dict(max_pos=0), INVALID), (dict(rot=0), INVALID),
-    (dict(rot=20), UNSUPPORTED), (dict(base=1.0), INVALID), (dict(base=float("inf")), INVALID),
+    (dict(rot=20), UNSUPPORTED), (dict(max_pos=(1 << 26) + 1), UNSUPPORTED), (dict(base=1.0), INVALID), (dict(base=float("inf")), INVALID),
     (dict(kind=5), INVALID), (dict(kind=-1), INVALID), (dict(factor=0.5), INVALID),
     (dict(kind=3, original=0.0), INVALID), (dict(kind=3, low=0.0), INVALID),
     (dict(kind=4, low=4.0, high=4.0), INVALID), (dict(amplitude=0.0), INVALID),
@@ -128,7 +128,8 @@ BAD_CACHES = [
     (dict(page_stride=8 * 64 * 136 + 8), INVALID), (dict(pages=None), INVALID),
     (dict(pages=2000 * MB + 8), INVALID), (dict(page_table=None), INVALID), (dict(kv_lens=None), INVALID),
     (dict(kv_lens=3001 * MB + 1), INVALID), (dict(q_starts=3002 * MB + 2), INVALID),
-    (dict(q_starts=None, batch=3), INVALID), (dict(max_pages=1 << 26), UNSUPPORTED)]
+    (dict(q_starts=None, batch=3), INVALID), (dict(max_pages=1 << 26), UNSUPPORTED),
+    (dict(max_pages=(1 << 24) + 1), UNSUPPORTED)]
 
 
 def append_call(L, c=None, tokens=16, act=0, k=None, v=None, q=None, qo=None, r=None, pos=None, none=()):
@@ -170,7 +171,8 @@ BAD_ATTN = [
 
 @pytest.mark.parametrize("kw,code", [(dict(c=cache(**k)), code) for k, code in BAD_CACHES] +
                          [(dict(a=attn(**k)), code) for k, code in BAD_ATTN] + [
-    (dict(tokens=-4), INVALID), (dict(act=7), INVALID), (dict(q=rows(5 * MB, 12), o=rows(9 * MB, 12)), INVALID),
+    (dict(tokens=-4), INVALID), (dict(act=7), INVALID),
+    (dict(tokens=1 << 24, q=rows(5 * MB, 128), o=rows(9 * MB, 128)), UNSUPPORTED), (dict(q=rows(5 * MB, 12), o=rows(9 * MB, 12)), INVALID),
     (dict(o=rows(9 * MB, 16)), INVALID), (dict(o=rows(5 * MB, 32)), ALIAS), (dict(o=rows(2000 * MB, 32)), ALIAS),
     (dict(lse=5 * MB), ALIAS), (dict(lse=13 * MB + 2), INVALID), (dict(lse=9 * MB), ALIAS),
     (dict(ws=None), INVALID), (dict(ws=100 * MB + 16), INVALID), (dict(ws=5 * MB), ALIAS),

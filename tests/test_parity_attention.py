@@ -285,3 +285,74 @@ def test_negative_and_zero_scales(ttt):
                 u = 2 ** -7 if dtype == BF else 2 ** -17
                 assert (np.abs(host(o) - ref) <= u * (w + np.abs(ref))).all()
                 assert (np.abs(host(lse) - lref) <= 2 ** -17 * (1 + np.abs(lref))).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_before_the_first_token_under_the_widest_window(ttt, dtype):
+    """More rows than tokens: the first stand before the sequence and see
+    nothing, whatever the window; the others see all before them."""
+    for window in (2 ** 31 - 1, 2 ** 31 - 3):
+        check(ttt, dtype, 32, 2, 8, 128, [8, 300], [5, 200], window=window)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_longest_sequence(ttt, dtype):
+    """2^30 tokens: its last ones give what they give at the end of 8192."""
+    page, dim = 4096, 64
+    rng = np.random.default_rng(12)
+    longest = (1 << 30) // page
+    pool = ttt.kv_pages(3, page, 1, dim)
+    table = torch.full((2, longest), -1, dtype=torch.int32, device="cuda")
+    table[0, :2] = table[1, -2:] = ints([2, 1])
+    short, far = (ints([x]) for x in (8192, 1 << 30))
+    x = torch.from_numpy(rng.standard_normal((300, 3, dim))).to(dtype).cuda()
+    read = []
+    for t, lens in ((table[:1], short), (table[1:], far)):
+        pool.zero_()
+        ttt.kv_append(pool, t, lens, x[:, 1:2], x[:, 2:])
+        read.append((pool.clone(), *ttt.kv_read(pool, t, lens, 300, dim, dtype)))
+    assert all(torch.equal(a, b) for a, b in zip(*read)) and read[0][1].any()
+    for rows in (1, 300):
+        for kw in ({}, MANY[0], dict(max_new=1 << 20)):
+            got = [ttt.kv_attention(x[:rows, :1].expand(rows, 4, dim).contiguous(), pool, t, lens, window=100,
+                                    with_lse=True, **kw) for t, lens in ((table[:1], short), (table[1:], far))]
+            assert all(torch.equal(a, b) for a, b in zip(*got)), (rows, kw)
+            assert torch.isfinite(got[0][1]).all()
+
+
+def test_more_workgroups_than_a_dimension_holds(ttt):
+    """65535 sequences of 256 key heads, the last four of them with a row."""
+    rng = np.random.default_rng(13)
+    batch, heads, dim = 65535, 256, 64
+    pool = torch.from_numpy(pool_of(rng, [16], 16, heads, dim, garbage=False)[0]).cuda()
+    table = torch.full((batch, 1), -1, dtype=torch.int32, device="cuda")
+    table[-4:] = ints([[0], [2], [1], [0]])
+    lens, starts = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    lens[-4:], starts[-4:] = ints([3, 9, 16, 1]), ints([1, 2, 3, 4])
+    q = torch.from_numpy(rng.standard_normal((4, heads, dim))).to(BF).cuda()
+    last = (table[-4:].contiguous(), lens[-4:].contiguous(), starts[-5:].contiguous())
+    for max_new in (1, 1 << 24):     # either kernel
+        few = ttt.kv_attention(q, pool, *last[:2], q_starts=last[2], max_new=max_new, max_kv=16)
+        got = ttt.kv_attention(q, pool, table, lens, q_starts=starts, max_new=max_new, max_kv=16)
+        torch.cuda.synchronize()
+        assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(few)) and got.any()
+
+
+def test_outputs_live_on_the_stream_of_the_call(ttt):
+    """Memory taken for a call on another stream is that stream's, so that
+    nothing else is given it while the kernels there are under way."""
+    def owner(t):
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+    s = torch.cuda.Stream()
+    table, lens = ints([[0], [1]]), ints([9, 9])
+    pool, rope = ttt.kv_pages(2, 64, 2, 64), ttt.rope_table(64, 64)
+    x = torch.ones((18, 2, 64), dtype=BF, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    q = ttt.kv_append(pool, table, lens, x, x, q=x, rope_table=rope, stream=s)
+    o, lse = ttt.kv_attention(q, pool, table, lens, max_kv=1 << 16, with_lse=True, stream=s)
+    made = [q, o, lse, *ttt.kv_read(pool, table, lens, 18, 64, stream=s),
+            *ttt.rope_forward(x, x, rope, stream=s), ttt.rope_table(64, 64, stream=s)]
+    s.synchronize()
+    assert all(owner(t) == [s.cuda_stream] for t in made)
+    assert torch.equal(o[::9], x[::9])     # every row's values are ones, which the cache holds exactly
