@@ -13,13 +13,13 @@ namespace {
 constexpr int kCacheThreads = 256;
 constexpr int kCacheWaves = kCacheThreads / 64;
 
-// A wave holds TOK = 512 / D tokens of one head, 8 values a lane: lane t +
-// TOK * u has values 8u .. 8u + 7 of token t, so that the four lanes of a
-// block sit TOK apart and the lanes of neighbouring tokens next to each
-// other, as the V codes lie in the page.
+// A wave holds 512 / D tokens of one head, 8 values a lane: lane t * D / 8 + u
+// has values 8u .. 8u + 7 of token t, so that neighbouring lanes read and
+// write neighbouring pieces of 16 bytes (a token a lane, as V's codes lie in the page, took
+// twice the time).
 template <int D>
 struct WaveTile {
-  static constexpr int kTok = 512 / D;
+  static constexpr int kTok = 512 / D, kPieces = D / 8;
 };
 
 // A lane's place in its token's page: the page's address (null: the token has
@@ -49,22 +49,19 @@ __device__ __forceinline__ Place<D> place_of(const Pool& p, int seq, int idx, in
 template <int D>
 __device__ __forceinline__ void put8(const float (&x)[8], int t, int u, uint8_t* block, uint32_t code,
                                      uint32_t scale) {
-  constexpr int kTok = WaveTile<D>::kTok;
   float m = 0.f, z = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
 #pragma unroll
   for (int e = 0; e < 8; ++e) z += x[e] * 0.f;  // NaN where any is not finite (fmax drops a NaN)
-  m = fmaxf(m, __shfl_xor(m, kTok));
-  m = fmaxf(m, __shfl_xor(m, 2 * kTok));
+  m = fmaxf(m, __shfl_xor(m, 1));
+  m = fmaxf(m, __shfl_xor(m, 2));
   uint32_t sb = scale_byte(m);
   uint32_t w = encode8(x, scale_value(sb));
   const uint64_t odd = __ballot(!(z == 0.f));
   if (odd != 0) {
-    uint64_t lanes = 1;  // of a token
-#pragma unroll
-    for (int y = kTok; y < 64; y <<= 1) lanes |= lanes << y;
-    if (odd >> t & lanes) sb = kScaleNan, w = 0;
+    constexpr uint64_t kLanes = (1ull << WaveTile<D>::kPieces) - 1;  // of a token
+    if (odd >> (t * WaveTile<D>::kPieces) & kLanes) sb = kScaleNan, w = 0;
   }
   if (block == nullptr) return;
   *reinterpret_cast<uint32_t*>(block + code) = w;
@@ -82,7 +79,7 @@ __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, i
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * kCacheWaves + (threadIdx.x >> 6);
   int h = (int)(wave % lanes);
-  const int t = lane % kTok, u = lane / kTok;
+  const int t = lane / WaveTile<D>::kPieces, u = lane % WaveTile<D>::kPieces;
   const int64_t n64 = wave / lanes * kTok + t;
   const bool live = n64 < a.pool.tokens;
   const int n = live ? (int)n64 : a.pool.tokens - 1;
@@ -161,8 +158,8 @@ __global__ __launch_bounds__(kCacheThreads) void read_kernel(ReadLaunch a, int l
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * kCacheWaves + (threadIdx.x >> 6);
   const int h0 = (int)(wave % lanes);
-  const int64_t n64 = wave / lanes * kTok + (lane % kTok);
-  const int u = lane / kTok;
+  const int64_t n64 = wave / lanes * kTok + lane / WaveTile<D>::kPieces;
+  const int u = lane % WaveTile<D>::kPieces;
   if (n64 >= a.pool.tokens) return;
   const int n = (int)n64;
   int seq, idx;
