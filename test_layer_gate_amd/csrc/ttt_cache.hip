@@ -68,11 +68,43 @@ __device__ __forceinline__ void put8(const float (&x)[8], int t, int u, uint8_t*
   if ((u & 3) == 0) block[scale] = (uint8_t)sb;
 }
 
+// A lane's 8 values as they lie in memory. bf16 rows are read past the
+// caches' replacement (a lane's two halves of fp32 are half lines each).
+template <bool F32>
+struct Words {
+  uint32_t w[F32 ? 8 : 4];
+};
+
+template <bool F32>
+__device__ __forceinline__ Words<F32> load_words(const void* p, int64_t i) {
+  Words<F32> x;
+  if constexpr (F32) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    const uint4 a = q[0], b = q[1];
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w, x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
+  } else {
+    const u32x4_t a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(static_cast<const u16*>(p) + i));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.w[e] = a[e];
+  }
+  return x;
+}
+
+template <bool F32>
+__device__ __forceinline__ void values_of(const Words<F32>& x, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if constexpr (F32)
+      v[e] = __uint_as_float(x.w[e]);
+    else
+      v[e] = __uint_as_float(e & 1 ? x.w[e >> 1] & 0xffff0000u : x.w[e >> 1] << 16);
+}
+
 // Each wave walks over the heads of its tokens: queries (rotated, written in
-// their own type), keys (rotated, quantised) and values (quantised). Bound by
-// HBM for prompts, by latency for single tokens (there every wave has one
-// head). A lane of a rotated tensor reads its partner's 8 values too, which
-// the first level of cache holds from the partner's own read.
+// their own type), keys (rotated, quantised) and values (quantised), the next
+// head on its way meanwhile. Bound by HBM for prompts, by latency for single
+// tokens (there every wave has one head). Of the half layout a lane gets its
+// partners from the lane that holds them.
 template <int D, bool F32>
 __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, int lanes) {
   constexpr int kTok = WaveTile<D>::kTok;
@@ -83,16 +115,24 @@ __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, i
   const int64_t n64 = wave / lanes * kTok + t;
   const bool live = n64 < a.pool.tokens;
   const int n = live ? (int)n64 : a.pool.tokens - 1;
+  const int nq = a.q.heads, nk = a.k.heads, all = nq + 2 * nk;
+  const int i = u * 8;
+  auto load = [&](int h) {
+    if (h < nq) return load_words<F32>(a.q.p, n * a.q.ts + h * a.q.hs + i);
+    if (h < nq + nk) return load_words<F32>(a.k.p, n * a.k.ts + (h - nq) * a.k.hs + i);
+    return load_words<F32>(a.v.p, n * a.v.ts + (h - nq - nk) * a.v.hs + i);
+  };
+  if (h >= all) return;
+  Words<F32> next = load(h);
   int seq, idx;
   find_token(a.pool, n, &seq, &idx);
   const RopeArgs& rope = a.rope;
   const int half = rope.rot >> 1;
-  const int i = u * 8;
   const bool turned = i < rope.rot;
   const bool upper = !rope.interleaved && i >= half;
-  // From the lane's 8 values to those its pairs need: none where neighbours
-  // are paired.
-  const int mate = !turned || rope.interleaved ? 0 : upper ? -half : half;
+  // The lane of the 8 values that the lane's are paired with: itself where
+  // neighbours are.
+  const int mate = lane + (!turned || rope.interleaved ? 0 : upper ? -(half / 8) : half / 8);
   float c[8], s[8];
   if (turned) {
     const int pos = a.positions ? a.positions[n] : idx;
@@ -108,45 +148,44 @@ __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, i
       for (int e = 0; e < 8; ++e) s[e] = upper ? s[e] : -s[e];
     }
   }
-  auto rotated = [&](const void* p, int64_t at, float (&v)[8]) {
-    load8<F32>(p, at, v);
-    if (!turned) return;
-    if (rope.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) turn(v[2 * e], v[2 * e + 1], c[e], s[e], &v[2 * e], &v[2 * e + 1]);
-    } else {
-      float w[8];
-      load8<F32>(p, at + mate, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = turn_half(v[e], w[e], c[e], s[e]);
-    }
-  };
-  const int nq = a.q.heads, nk = a.k.heads;
-  float v[8];
-  int64_t at = n * a.q.ts + i;
-  for (; h < nq; h += lanes) {
-    rotated(a.q.p, at + h * a.q.hs, v);
-    if (live) {
-      const int64_t to = n * a.qo.ts + h * a.qo.hs + i;
-      if constexpr (F32)
-        store8<true>(a.qo.p, to, v);
-      else
-        stream_store<false>(a.qo.p, to, v);
-    }
-  }
   const Place<D> pl = place_of<D>(a.pool, seq, live ? idx : -1, u);
   const int64_t block = head_block_bytes(a.pool.page, D);
-  at = n * a.k.ts + i;
-  for (; h < nq + nk; h += lanes) {
-    const int hh = h - nq;
-    rotated(a.k.p, at + hh * a.k.hs, v);
-    put8<D>(v, t, u, pl.page ? pl.page + hh * block : nullptr, pl.k_code, pl.k_scale);
-  }
-  at = n * a.v.ts + i;
-  for (; h < nq + 2 * nk; h += lanes) {
-    const int hh = h - nq - nk;
-    load8<F32>(a.v.p, at + hh * a.v.hs, v);
-    put8<D>(v, t, u, pl.page ? pl.page + hh * block : nullptr, pl.v_code, pl.v_scale);
+  for (; h < all; h += lanes) {
+    const Words<F32> now = next;
+    if (h + lanes < all) next = load(h + lanes);
+    float v[8];
+    values_of<F32>(now, v);
+    if (h < nq + nk && rope.rot > 0) {
+      if (rope.interleaved) {
+        if (turned) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) turn(v[2 * e], v[2 * e + 1], c[e], s[e], &v[2 * e], &v[2 * e + 1]);
+        }
+      } else {
+        Words<F32> other;
+#pragma unroll
+        for (int e = 0; e < (F32 ? 8 : 4); ++e) other.w[e] = __shfl(now.w[e], mate);
+        if (turned) {
+          float w[8];
+          values_of<F32>(other, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = turn_half(v[e], w[e], c[e], s[e]);
+        }
+      }
+    }
+    if (h < nq) {
+      if (live) {
+        const int64_t to = n * a.qo.ts + h * a.qo.hs + i;
+        if constexpr (F32)
+          store8<true>(a.qo.p, to, v);
+        else
+          stream_store<false>(a.qo.p, to, v);
+      }
+    } else {
+      const bool is_v = h >= nq + nk;
+      put8<D>(v, t, u, pl.page ? pl.page + (h - nq - (is_v ? nk : 0)) * block : nullptr,
+              is_v ? pl.v_code : pl.k_code, is_v ? pl.v_scale : pl.k_scale);
+    }
   }
 }
 
