@@ -31,10 +31,11 @@ struct Place {
 };
 
 template <int D>
-__device__ __forceinline__ Place<D> place_of(const Pool& p, int seq, int idx, int u) {
-  Place<D> at = {};
-  int off = 0;
-  at.page = token_block(p, seq, idx, 0, &off);
+__device__ __forceinline__ Place<D> place_of(const Pool& p, Token tok, int u) {
+  const InPage in = page_of(p, tok);
+  const uint32_t off = in.off;
+  Place<D> at;
+  at.page = in.page;
   const uint32_t codes = p.page * (D / 2);
   at.k_code = off * (D / 2) + u * 4;
   at.v_code = codes + (off >> 2) * (2 * D) + u * 16 + (off & 3) * 4;
@@ -124,8 +125,7 @@ __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, i
   };
   if (h >= all) return;
   Words<F32> next = load(h);
-  int seq, idx;
-  find_token(a.pool, n, &seq, &idx);
+  const Token tok = find_token(a.pool, n);
   const RopeArgs& rope = a.rope;
   const int half = rope.rot >> 1;
   const bool turned = i < rope.rot;
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, i
   const int mate = lane + (!turned || rope.interleaved ? 0 : upper ? -(half / 8) : half / 8);
   float c[8], s[8];
   if (turned) {
-    const int pos = a.positions ? a.positions[n] : idx;
+    const int pos = a.positions ? a.positions[n] : tok.idx;
     if (rope.interleaved) {
       float cc[4], ss[4];
       load_cs<4>(rope, pos, i / 2, cc, ss);
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kCacheThreads) void append_kernel(AppendLaunch a, i
       for (int e = 0; e < 8; ++e) s[e] = upper ? s[e] : -s[e];
     }
   }
-  const Place<D> pl = place_of<D>(a.pool, seq, live ? idx : -1, u);
+  const Place<D> pl = place_of<D>(a.pool, live ? tok : Token{0, -1}, u);
   const int64_t block = head_block_bytes(a.pool.page, D);
   for (; h < all; h += lanes) {
     const Words<F32> now = next;
@@ -201,9 +201,8 @@ __global__ __launch_bounds__(kCacheThreads) void read_kernel(ReadLaunch a, int l
   const int u = lane % WaveTile<D>::kPieces;
   if (n64 >= a.pool.tokens) return;
   const int n = (int)n64;
-  int seq, idx;
-  find_token(a.pool, n, &seq, &idx);
-  const Place<D> pl = place_of<D>(a.pool, seq, idx, u);
+  const Token tok = find_token(a.pool, n);
+  const Place<D> pl = place_of<D>(a.pool, tok, u);
   const int64_t block = head_block_bytes(a.pool.page, D);
   const int nk = a.k.heads;
   for (int h = h0; h < 2 * nk; h += lanes) {

@@ -74,20 +74,18 @@ __device__ __forceinline__ void stream_store(void* p, int64_t i, const float (&v
 }
 
 // cos and sin of the N pairs i .. i + N - 1 (N even) of position `pos`; NaN
-// for a position that the table does not hold.
+// for a position that the table does not hold (selected after a read of its
+// first row: branches here kept the arrays from registers).
 template <int N>
 __device__ __forceinline__ void load_cs(const RopeArgs& r, int pos, int i, float (&c)[N],
                                         float (&s)[N]) {
-  if ((uint32_t)pos < (uint32_t)r.max_pos) {
-    const float4* t = reinterpret_cast<const float4*>(r.table + ((int64_t)pos * (r.rot >> 1) + i) * 2);
+  const bool in = (uint32_t)pos < (uint32_t)r.max_pos;
+  const float4* t = reinterpret_cast<const float4*>(r.table + ((int64_t)(in ? pos : 0) * (r.rot >> 1) + i) * 2);
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-      const float4 a = t[e];
-      c[2 * e] = a.x, s[2 * e] = r.sign * a.y, c[2 * e + 1] = a.z, s[2 * e + 1] = r.sign * a.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) c[e] = s[e] = __builtin_nanf("");
+  for (int e = 0; e < N / 2; ++e) {
+    const float4 a = t[e];
+    c[2 * e] = in ? a.x : __builtin_nanf(""), s[2 * e] = in ? r.sign * a.y : __builtin_nanf("");
+    c[2 * e + 1] = in ? a.z : __builtin_nanf(""), s[2 * e + 1] = in ? r.sign * a.w : __builtin_nanf("");
   }
 }
 
@@ -111,14 +109,14 @@ __device__ __forceinline__ float turn_half(float x, float mate, float c, float s
 // Where new token n belongs: its sequence, and its index among the
 // sequence's tokens. n is the same for the lanes that ask for it; every lane
 // of the wave must call it. A token that no sequence claims gets index -1.
-__device__ __forceinline__ void find_token(const Pool& p, int n, int* seq, int* idx) {
-  int b;
+struct Token {
+  int seq, idx;
+};
+__device__ __forceinline__ Token find_token(const Pool& p, int n) {
   if (p.starts == nullptr) {
     const int each = p.tokens / p.batch;
-    b = n / each;
-    *seq = b;
-    *idx = p.lens[b] - each + (n - b * each);
-    return;
+    const int b = n / each;
+    return {b, p.lens[b] - each + (n - b * each)};
   }
   // the last b with starts[b] <= n: found by halves
   int lo = 0, hi = p.batch;
@@ -126,25 +124,27 @@ __device__ __forceinline__ void find_token(const Pool& p, int n, int* seq, int* 
     const int mid = (lo + hi) >> 1;
     if (p.starts[mid] <= n) lo = mid; else hi = mid;
   }
-  *seq = lo;
   const int end = p.starts[lo + 1];
-  *idx = n >= p.starts[lo] && n < end ? p.lens[lo] - end + n : -1;
+  return {lo, n >= p.starts[lo] && n < end ? p.lens[lo] - end + n : -1};
 }
 
 __device__ __forceinline__ int64_t head_block_bytes(int page, int dim) {
   return (int64_t)page * (dim + dim / 16);
 }
 
-// The head's block of the page that holds token idx of sequence seq, and the
-// token's place in it; null where the sequence has no such page.
-__device__ __forceinline__ uint8_t* token_block(const Pool& p, int seq, int idx, int head, int* off) {
-  if (idx < 0) return nullptr;
-  const int pg = idx / p.page;
-  if (pg >= p.max_pages) return nullptr;
-  *off = idx - pg * p.page;
-  const int id = p.table[(int64_t)seq * p.max_pages + pg];
-  if ((uint32_t)id >= (uint32_t)p.n_pages) return nullptr;
-  return p.pages + id * p.page_stride + head * head_block_bytes(p.page, p.dim);
+// The page that holds token idx of sequence seq, and the token's place in it;
+// null where the sequence has no such page.
+struct InPage {
+  uint8_t* page;
+  int off;
+};
+__device__ __forceinline__ InPage page_of(const Pool& p, Token t) {
+  if (t.idx < 0) return {nullptr, 0};
+  const int pg = t.idx / p.page;
+  if (pg >= p.max_pages) return {nullptr, 0};
+  const int id = p.table[(int64_t)t.seq * p.max_pages + pg];
+  if ((uint32_t)id >= (uint32_t)p.n_pages) return {nullptr, 0};
+  return {p.pages + id * p.page_stride, t.idx - pg * p.page};
 }
 
 }  // namespace tttk
