@@ -47,12 +47,18 @@ struct FewTile {
 };
 
 template <int D, int T, bool F32, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void attend_few_kernel(
+__global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
-  __shared__ float red_o[NW - 1][16][D + 4];
+  // Three terms of the rows' queries would be the registers of a second wave:
+  // the waves, whose rows are the same, read them from LDS.
+  constexpr bool kShareQ = T > 1;
+  constexpr size_t kRed = sizeof(float) * (NW - 1) * 16 * (D + 4), kQ = kShareQ ? T * KS * 1024 : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t pool[kRed > kQ ? kRed : kQ];
+  float(*red_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(pool);
+  uint4(*shared_q)[KS][64] = reinterpret_cast<uint4(*)[KS][64]>(pool);
   __shared__ float red_ml[NW][16][2];
 
   const int lane = threadIdx.x & 63;
@@ -89,21 +95,29 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
     const int all_lo = last.lo, all_hi = first.hi;  // keys that every row sees
 
     // Q as the first product's B operand: step s, values (D / 4) g + 8 s ..
-    uint32_t qf[T][KS][4];
+    uint4 qf[kShareQ ? 1 : KS];
     {
+      if constexpr (kShareQ) __syncthreads();  // the last tile's readers are done
       const int64_t at = (int64_t)(row0 + t) * a.q.ts + head * a.q.hs + g * (D / 4);
+      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
+        if (kShareQ && s % NW != wave) continue;
         float v[8];
         load8<F32>(a.q.p, at + 8 * s, v);
+        uint32_t w[4][T];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[T];
-          split2<T>(v[2 * e], v[2 * e + 1], w);
+        for (int e = 0; e < 4; ++e) split2<T>(v[2 * e], v[2 * e + 1], w[e]);
 #pragma unroll
-          for (int x = 0; x < T; ++x) qf[x][s][e] = w[x] ^ (a.scale < 0.f ? 0x80008000u : 0u);
+        for (int x = 0; x < T; ++x) {
+          const uint4 y = make_uint4(w[0][x] ^ flip, w[1][x] ^ flip, w[2][x] ^ flip, w[3][x] ^ flip);
+          if constexpr (kShareQ)
+            shared_q[x][s][lane] = y;
+          else
+            qf[s] = y;
         }
       }
+      if constexpr (kShareQ) __syncthreads();
     }
     const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1.2e-38f), grown = fminf(8.f / sc, 1e38f);
     f32x4_t o[F];
@@ -180,22 +194,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 && F32 && NW == 4 ? 1 : 2) void a
 #pragma unroll
           for (int q = 0; q < NP; ++q) ks[x][q] = (cur.ks[x] >> (ks_shift + 8 * q)) & 255u;
         // S^T
+        if constexpr (kShareQ) asm volatile("" ::: "memory");  // not all at once, ahead of the loop
         f32x4_t s[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          s[x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < 2; ++x) s[x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = 0; q < KS; ++q) {
+        for (int q = 0; q < KS; ++q) {
+          bf16x8_t kf[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
             const uint4 w = cur.kw[x][q >> 2];
             uint32_t c = (q & 3) == 0 ? w.x : (q & 3) == 1 ? w.y : (q & 3) == 2 ? w.z : w.w;
             // D = 64: a lane's 16 values are half of a block
             if constexpr (D == 64) c = g & 1 ? (q == 0 ? w.z : w.w) : c;
             uint32_t d[4];
             decode8(c, scale_value(ks[x][q >> 2]), d);
-            const bf16x8_t kf = frag(d[0], d[1], d[2], d[3]);
+            kf[x] = frag(d[0], d[1], d[2], d[3]);
+          }
 #pragma unroll
-            for (int y = T - 1; y >= 0; --y)
-              s[x] = mfma16(kf, frag(qf[y][q][0], qf[y][q][1], qf[y][q][2], qf[y][q][3]), s[x]);
+          for (int y = T - 1; y >= 0; --y) {
+            const uint4 z = kShareQ ? shared_q[y][q][lane] : qf[kShareQ ? 0 : q];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) s[x] = mfma16(kf[x], frag(z.x, z.y, z.z, z.w), s[x]);
           }
         }
         float p[8];
@@ -507,8 +527,6 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
   const int64_t tiles = tttk::row_tiles(a, group, 16, others);
   const dim3 grid = grid_of(tiles * others);
-  // Eight waves for short sequences; wide fp32 heads need the registers that
-  // eight do not have.
   const bool wide = a.splits == 1 && a.each <= kOneGroup;
 #define TTT_CALL(D, T, F, W)                                                       \
   if (wide)                                                                        \
@@ -518,7 +536,7 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   switch (a.pool.dim) {
     case 64: if (a.f32) { TTT_CALL(64, 3, true, 8); } else { TTT_CALL(64, 1, false, 8); } break;
     case 128: if (a.f32) { TTT_CALL(128, 3, true, 8); } else { TTT_CALL(128, 1, false, 8); } break;
-    default: if (a.f32) { TTT_CALL(256, 3, true, 4); } else { TTT_CALL(256, 1, false, 8); } break;
+    default: if (a.f32) { TTT_CALL(256, 3, true, 8); } else { TTT_CALL(256, 1, false, 8); } break;
   }
 #undef TTT_CALL
   return hipGetLastError();
