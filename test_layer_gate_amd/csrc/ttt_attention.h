@@ -121,19 +121,77 @@ __device__ __forceinline__ int64_t block_of_grid() {
   return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
 }
 
-// Sequence b's rows, and its keys.
+// Sequence b's rows, and its keys. UNIFORM: b is the same for the whole wave.
 struct Seq {
   int row0, news, len;
 };
-__device__ __forceinline__ Seq seq_of(const Pool& p, int b) {
+template <bool UNIFORM>
+__device__ __forceinline__ Seq seq_at(const Pool& p, int b) {
+  auto word = [](const int32_t* w, int i) { return UNIFORM ? uniform_load(w, i) : w[i]; };
   const int each = p.tokens / p.batch;
-  const int r0 = p.starts ? uniform_load(p.starts, b) : b * each;
-  const int r1 = p.starts ? uniform_load(p.starts, b + 1) : r0 + each;
+  const int r0 = p.starts ? word(p.starts, b) : b * each;
+  const int r1 = p.starts ? word(p.starts, b + 1) : r0 + each;
   Seq s;
   s.row0 = r0;
   s.news = r0 < 0 ? 0 : min(r1, p.tokens) - r0;
-  s.len = min(uniform_load(p.lens, b), p.max_pages * p.page);
+  s.len = min(word(p.lens, b), p.max_pages * p.page);
   return s;
+}
+__device__ __forceinline__ Seq seq_of(const Pool& p, int b) { return seq_at<true>(p, b); }
+
+// Units of keys that a sequence's first 16 rows see; at least one, so that
+// rows that see nothing are written, and none without rows.
+__device__ __forceinline__ uint32_t units_of(const AttnLaunch& a, const Seq& s, int group, int unit) {
+  if (s.news <= 0) return 0;
+  const Span first = span_of(a, s.len, s.news, 0);
+  const Span last = span_of(a, s.len, s.news, (min(16, s.news * group) - 1) / group);
+  return (uint32_t)(max(last.hi - (first.lo & ~31), 1) + unit - 1) / unit;
+}
+
+// A slice of the units of all sequences, one after the other: [at, end), which
+// begins in sequence b, whose n units begin at `off`; slices are of `per`.
+struct Line {
+  uint32_t at, end, off, n, per;
+  int b;
+};
+constexpr int kSliceBatch = 256;  // sequences at most: four a lane
+__device__ __forceinline__ Line line_of(const AttnLaunch& a, int slice, int group, int unit, int lane) {
+  uint32_t n[kSliceBatch / 64], sum[kSliceBatch / 64], total = 0;
+#pragma unroll
+  for (int c = 0; c < kSliceBatch / 64; ++c) {
+    n[c] = sum[c] = 0;
+    if (c * 64 >= a.pool.batch) continue;
+    const int b = c * 64 + lane;
+    if (b < a.pool.batch) n[c] = units_of(a, seq_at<false>(a.pool, b), group, unit);
+    uint32_t x = n[c];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    sum[c] = total + x;
+    total += __builtin_amdgcn_readlane(x, 63);
+  }
+  Line l = {};
+  l.per = (total + a.slices - 1) / a.slices;
+  l.at = slice * l.per;
+  l.end = min(total, l.at + l.per);
+  if (l.at >= total) {
+    l.end = l.at;
+    return l;
+  }
+  bool found = false;
+#pragma unroll
+  for (int c = 0; c < kSliceBatch / 64; ++c) {
+    const uint64_t past = __ballot(sum[c] > l.at);
+    if (found || past == 0) continue;
+    found = true;
+    const int i = __builtin_ctzll(past);
+    l.b = c * 64 + i;
+    l.n = __builtin_amdgcn_readlane(n[c], i);
+    l.off = __builtin_amdgcn_readlane(sum[c], i) - l.n;
+  }
+  return l;
 }
 
 }  // namespace tttk

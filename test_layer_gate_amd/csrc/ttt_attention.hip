@@ -35,7 +35,7 @@ namespace {
 // Bound by how many bytes are on their way: three waves a SIMD (bf16, 128) with
 // 32 keys each, 4.3 KB. One token of 40/8 heads of 128 over 128k keys (143 MB)
 // takes 27 us, 5.3 TB/s, and its join 4; 32 sequences of 4k to 32k keys, 32/8
-// heads (0.56 GB), 115 us and 5.
+// heads (0.56 GB), 104 us and 6.
 
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
 template <int D>
@@ -46,7 +46,7 @@ struct FewTile {
   bool have[2];
 };
 
-template <int D, int T, bool F32, int NW>
+template <int D, int T, bool F32, int NW, bool SLICED>
 __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
@@ -64,25 +64,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  // Key heads vary fastest, then rows, sequences and at last splits: workgroups
-  // go round the XCDs in this order, and a split that short sequences do not
-  // have must not be one XCD's.
+  // Key heads vary fastest, then slices, or rows, sequences and at last splits:
+  // workgroups go round the XCDs in this order, and a split that short
+  // sequences do not have must not be one XCD's.
   int id = (int)block_of_grid();
   const int hk = id % a.pool.heads;
   id /= a.pool.heads;
-  const int tile0 = row_tiles - 1 - id % row_tiles;  // the last, which see most, first
-  id /= row_tiles;
-  const int b = id % a.pool.batch, split = id / a.pool.batch;
-  if (split >= a.splits) return;
   const int group = a.q.heads / a.pool.heads;
   const int page = a.pool.page, gpp = page >> 4;  // 16-key pieces a page
+  int b, tile, split = 0;
+  Line line = {};
+  if constexpr (SLICED) {
+    if (id >= a.slices) return;
+    line = line_of(a, id, group, 32 * NW, lane);
+    if (line.at >= line.end) return;
+    b = line.b, tile = 0;
+  } else {
+    tile = row_tiles - 1 - id % row_tiles;  // the last, which see most, first
+    id /= row_tiles;
+    b = id % a.pool.batch, split = id / a.pool.batch;
+    if (split >= a.splits) return;
+  }
 
-  const Seq seq = seq_of(a.pool, b);
-  if (seq.news <= 0) return;
-  const int row0 = seq.row0, news = seq.news, len = seq.len;
-  const int rows = news * group;
-
-  for (int tile = tile0; tile * 16 < rows; tile += row_tiles) {
+  for (;;) {
+    const Seq seq = seq_of(a.pool, b);
+    const int row0 = seq.row0, news = seq.news, len = seq.len;
+    const int rows = max(news, 0) * group;
+    if (tile * 16 >= rows) break;  // (of a slice's sequences, the first tile has rows)
     const int r = tile * 16 + i16;
     const bool live = r < rows;
     const int t = min(r, rows - 1) / group;
@@ -133,11 +141,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     const int ks_shift = D == 64 ? 16 * (i16 & 1) + 8 * (g >> 1) : D == 128 ? 8 * g : 16 * (g & 1);
     const uint32_t vs_lane = page * D + page * (D / 32) + (i16 * (D / 16) / 32) * page + 4 * g;
 
-    // This split's stretches of `each` keys, a wave's share of each.
-    // (One part: all of the tile's keys, whatever the launch expected.)
-    const int per = a.splits == 1 ? (max(hi - lo, 1) + 32 * NW - 1) / (32 * NW) * 32 : a.each / NW;
-    for (int64_t s0 = lo + (int64_t)split * per * NW; s0 < hi; s0 += (int64_t)a.splits * per * NW) {
-      const int k0 = (int)s0 + wave * per, k1 = min(hi, k0 + per);
+    // This part's stretches of keys, a wave's share of each: of a slice what it
+    // has of the sequence; of a split every splits-th; of one part all of the
+    // tile's keys, whatever the launch expected. What a slice has no part for,
+    // rows past the first 16 (more than max_new allowed for), are done whole
+    // by the workgroup that has the sequence's first keys.
+    const bool sliced = SLICED && tile == 0;
+    const uint32_t u0 = line.at - line.off, u1 = min(line.n, line.end - line.off);  // of a slice
+    const int per = sliced ? (int)(u1 - u0) * 32
+                    : SLICED || a.splits == 1 ? (max(hi - lo, 1) + 32 * NW - 1) / (32 * NW) * 32
+                                                    : a.each / NW;
+    const int64_t begin = lo + (sliced ? (int64_t)u0 * 32 * NW : (int64_t)split * per * NW);
+    const int64_t end = sliced ? min((int64_t)hi, lo + (int64_t)u1 * 32 * NW) : hi;
+    for (int64_t s0 = begin; s0 < end; s0 += (int64_t)(SLICED ? 1 : a.splits) * per * NW) {
+      const int k0 = (int)s0 + wave * per, k1 = min((int)end, k0 + per);
       // Where 64 pieces of 16 keys lie, one a lane: the address of the head's
       // block and the first key's place in it. Loads take the address from
       // scalar registers and a 32-bit offset of the lane's.
@@ -358,8 +375,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
 #pragma unroll
           for (int f = 0; f < F; ++f) o[f][e] += red_o[w][i16][F * (4 * g + e) + f];
       const int64_t row = (int64_t)(row0 + t) * a.q.heads + head;
-      if (a.splits > 1) {
-        const int64_t at = (int64_t)split * a.pool.tokens * a.q.heads + row;
+      if (sliced ? u0 > 0 || u1 < line.n : a.splits > 1) {
+        // slice + sequence: no two pairs that meet have the same sum
+        const int part = ((int)(line.at / line.per) + b) * a.pool.heads + hk;
+        const int64_t at = sliced ? (int64_t)part * 16 + i16 : (int64_t)split * a.pool.tokens * a.q.heads + row;
+        if (sliced && u0 == 0 && g == 0)
+          *reinterpret_cast<int2*>(a.part_of + 2 * row) = make_int2(
+              part * 16 + i16, (int)((line.off + line.n - 1) / line.per - line.at / line.per) + 1);
         if (g == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(mj, lj);
         float* dst = a.part + at * D;
 #pragma unroll
@@ -372,6 +394,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
         const float inv = lj == 0.f ? 0.f : 1.f / lj;
         if (a.lse != nullptr && g == 0)
           a.lse[row] = lj == 0.f ? kNone : (mj + __builtin_amdgcn_logf(lj)) * kLn2;
+        if (SLICED && g == 0) *reinterpret_cast<int2*>(a.part_of + 2 * row) = make_int2(0, 0);
         const int64_t at = (int64_t)(row0 + t) * a.o.ts + head * a.o.hs;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -396,10 +419,25 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
         }
       }
     }
+    if constexpr (!SLICED) {
+      tile += row_tiles;
+      continue;
+    }
+    if (u0 == 0 && (tile + 1) * 16 < rows) {
+      ++tile;
+      continue;
+    }
+    // the slice's next sequence that has rows
+    tile = 0;
+    line.at = line.off += line.n;
+    line.n = 0;
+    while (line.at < line.end && line.n == 0 && ++b < a.pool.batch)
+      line.n = units_of(a, seq_of(a.pool, b), group, 32 * NW);
+    if (line.n == 0) break;
   }
 }
 
-// Joins the splits of every row, in their order. ROWS rows a workgroup: each
+// Joins the parts of every row, in their order. ROWS rows a workgroup: each
 // has 256 / ROWS threads, D / 4 of which hold 4 values each of one split; the
 // others take every LANES-th split beside them and are added at the end. With
 // many splits there are few rows: one a workgroup.
@@ -414,25 +452,38 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
   const int64_t row0 = block_of_grid() * ROWS;
   if (row0 >= rows) return;
   const int64_t row = min(row0 + rr, rows - 1);
+  // The row's parts: `count` from `base`, `stride` apart. Rows that no sequence
+  // claims have nothing in part_of: whatever is there is kept in bounds.
+  int64_t base = row, stride = rows;
+  int count = a.splits;
+  if (a.slices > 0) {
+    stride = a.pool.heads * 16;
+    const int all = (a.slices + a.pool.batch - 1) * (int)stride;
+    const int2 d = *reinterpret_cast<const int2*>(a.part_of + 2 * row);
+    if (d.y <= 0 || (uint32_t)d.x >= (uint32_t)all) return;
+    base = d.x;
+    count = min(d.y, (all - 1 - d.x) / (int)stride + 1);
+  }
   float m = kNone;
   if constexpr (LANES > 1) {
-    // the maximum, one split a thread
-    for (int s = threadIdx.x; s < a.splits; s += 256) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+    // the maximum, one part a thread
+    for (int s = threadIdx.x; s < count; s += 256) m = fmaxf(m, a.part_ml[2 * (base + s * stride)]);
     m = wave_max(m);
     __shared__ float red_m[4];
     if ((threadIdx.x & 63) == 0) red_m[threadIdx.x >> 6] = m;
     __syncthreads();
     m = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
   } else {
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+    for (int s = 0; s < count; ++s) m = fmaxf(m, a.part_ml[2 * (base + s * stride)]);
   }
   const float m0 = m == kNone ? 0.f : m;
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = y; s < a.splits; s += LANES) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (s * rows + row));
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (s * rows + row) * D + 4 * c);
+  for (int s = y; s < count; s += LANES) {
+    const int64_t at = base + s * stride;
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+    const float4 v = *reinterpret_cast<const float4*>(a.part + at * D + 4 * c);
     const float w = __builtin_amdgcn_exp2f(ml.x - m0);
     l += ml.y * w;
     acc.x += v.x * w, acc.y += v.y * w, acc.z += v.z * w, acc.w += v.w * w;
@@ -505,20 +556,34 @@ AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv
     const int64_t most = (keys + 511) / 512;
     int64_t want = 256 / groups;
     if (want > most) want = most;
-    return {true, (int)(want < 1 ? 1 : want), 0};
+    return {true, (int)(want < 1 ? 1 : want), 0, 0};
   }
   // A short sequence is one workgroup of eight waves.
-  if (keys <= kOneGroup) return {false, 1, kOneGroup};
+  if (keys <= kOneGroup) return {false, 1, kOneGroup, 0};
+  // Several sequences with one tile of rows each: a slice for every workgroup
+  // that the card holds at once, whatever the lengths are, which only the GPU
+  // knows. Against parts of 8192 keys each (us, with the join, 32/8 heads of
+  // 128): 24 sequences of 16k keys 101 / 89, 32 of 4k to 32k 155 / 134, one of
+  // 128k and 31 of 1k 380 / 51, 128 of 1 to 8k 133 / 124; 2 of 1500 14.4 / 15.2,
+  // 200 of 1 to 4k (one part each then) 92 / 99. 512 slices 134 us for the 32,
+  // 1024 152, 1536 139.
+  if (rows <= 16 && batch > 1 && batch <= kSliceBatch) {
+    const int64_t units = (keys + 127) / 128 * batch;
+    const int64_t fit = dim == 256 ? 512 : dim == 64 && !f32 ? 1024 : 768;
+    int64_t slices = fit / kv_heads < 1 ? 1 : fit / kv_heads;
+    if (slices > units) slices = units;
+    return {false, 1, 0, (int)slices};
+  }
   // Stretches that give 512 workgroups of four waves, or 1024 where some
   // sequences may be shorter than max_kv; of 512 keys or more where there is
   // much to do (each workgroup loads its rows and hands in its sums), and of
   // 128 at least. 1 token over 128k keys: 512 take 35.4 us, 768 36.8, 1024
-  // 40.6, 2304 44.0; 32 ragged sequences: 1024 128.8 us, 2048 129.9, 6144 134.4.
+  // 40.6, 2304 44.0.
   const double work = (double)keys * ((rows + 15) / 16) * kv_heads * batch;
   const double fair = work / (batch > 1 ? 1024 : 512), least = work < 512 * 256 ? 128 : 512;
   const double most = 1 << 20, e = fair < least ? least : fair > most ? most : fair;
   const int each = ((int)e + 127) / 128 * 128;
-  return {false, (int)((keys + each - 1) / each), each};
+  return {false, (int)((keys + each - 1) / each), each, 0};
 }
 
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
@@ -526,17 +591,19 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int group = a.q.heads / a.pool.heads;
   const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
   const int64_t tiles = tttk::row_tiles(a, group, 16, others);
-  const dim3 grid = grid_of(tiles * others);
+  const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
   const bool wide = a.splits == 1 && a.each <= kOneGroup;
-#define TTT_CALL(D, T, F, W)                                                       \
-  if (wide)                                                                        \
-    attend_few_kernel<D, T, F, W><<<grid, 64 * W, 0, s>>>(a, (int)tiles);          \
+#define TTT_CALL(D, T, F)                                                          \
+  if (a.slices > 0)                                                                \
+    attend_few_kernel<D, T, F, 4, true><<<grid, 256, 0, s>>>(a, 1);                \
+  else if (wide)                                                                   \
+    attend_few_kernel<D, T, F, 8, false><<<grid, 512, 0, s>>>    (a, (int)tiles);   \
   else                                                                             \
-    attend_few_kernel<D, T, F, 4><<<grid, 256, 0, s>>>(a, (int)tiles)
+    attend_few_kernel<D, T, F, 4, false><<<grid, 256, 0, s>>>(a, (int)tiles)
   switch (a.pool.dim) {
-    case 64: if (a.f32) { TTT_CALL(64, 3, true, 8); } else { TTT_CALL(64, 1, false, 8); } break;
-    case 128: if (a.f32) { TTT_CALL(128, 3, true, 8); } else { TTT_CALL(128, 1, false, 8); } break;
-    default: if (a.f32) { TTT_CALL(256, 3, true, 8); } else { TTT_CALL(256, 1, false, 8); } break;
+    case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
+    case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
+    default: if (a.f32) { TTT_CALL(256, 3, true); } else { TTT_CALL(256, 1, false); } break;
   }
 #undef TTT_CALL
   return hipGetLastError();
@@ -544,9 +611,9 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
 
 hipError_t launch_attention_join(const AttnLaunch& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.pool.tokens * a.q.heads;
-  // One row a workgroup has up to 16 splits in flight at once; with fewer
-  // than that to join, as many rows as have threads for one each.
-  const bool one = a.splits > 4 || rows < 512;
+  // One row a workgroup has up to 16 parts in flight at once; with few of them
+  // to join, as many rows as have threads for one each.
+  const bool one = (a.slices > 0 ? a.slices > a.pool.batch : a.splits > 4) || rows < 512;
 #define TTT_CALL(D, F)                                                                        \
   if (one)                                                                                    \
     attend_join_kernel<D, F, 1><<<grid_of(rows), 256, 0, s>>>(a);                             \

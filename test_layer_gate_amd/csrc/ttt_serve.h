@@ -70,9 +70,11 @@ struct AttnLaunch {
   int causal, window, max_new, max_kv;
   bool f32;
   bool many;             // attn_plan()
-  int splits, each;
-  float* part;           // [splits][tokens * q heads][D] (splits > 1)
-  float* part_ml;        // [splits][tokens * q heads][2]
+  int splits, each, slices;
+  float* part;           // [splits][tokens * q heads][D] (splits > 1), or
+                         // [slices + batch - 1][kv heads][16][D] (slices > 0)
+  float* part_ml;        // likewise, [2] for [D]
+  int* part_of;          // [tokens * q heads][2]: a row's first part, and how many (slices > 0)
 };
 
 hipError_t launch_rope(const RopeLaunch& a, hipStream_t s);
@@ -85,10 +87,11 @@ hipError_t launch_read(const ReadLaunch& a, hipStream_t s);
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;
 // How attention is launched: by which kernel, in how many parts of each
 // sequence's keys, and for the few-row kernel in stretches of how many keys
-// (part s takes every splits-th stretch from the s-th).
+// (part s takes every splits-th stretch from the s-th). slices > 0: the keys of
+// all sequences, one after the other, are cut into that many even slices.
 struct AttnPlan {
   bool many;
-  int splits, each;
+  int splits, each, slices;
 };
 AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
                    int dim);

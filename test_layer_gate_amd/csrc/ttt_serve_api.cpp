@@ -296,12 +296,18 @@ ttt_status check_attn(const ttt_attn* at, int32_t batch, int32_t kv_heads, int32
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Bytes of the parts' weighted sums, then of their maxima and sums.
-size_t part_bytes(int splits, int64_t tokens, int64_t heads, int64_t dim) {
-  return splits > 1 ? align256((size_t)splits * tokens * heads * dim * 4) : 0;
-}
-size_t ml_bytes(int splits, int64_t tokens, int64_t heads) {
-  return splits > 1 ? align256((size_t)splits * tokens * heads * 8) : 0;
+// Bytes of the parts' weighted sums, of their maxima and sums, and of where
+// the parts of each row are.
+struct PartBytes {
+  size_t part, ml, of;
+  size_t all() const { return part + ml + of; }
+};
+PartBytes part_bytes(const tttk::AttnPlan& p, int64_t batch, int64_t tokens, int64_t kv_heads, int64_t q_heads,
+                     int64_t dim) {
+  const size_t rows = p.slices > 0   ? (size_t)(p.slices + batch - 1) * kv_heads * 16
+                      : p.splits > 1 ? (size_t)p.splits * tokens * q_heads
+                                     : 0;
+  return {align256(rows * dim * 4), align256(rows * 8), p.slices > 0 ? align256((size_t)tokens * q_heads * 8) : 0};
 }
 
 }  // namespace
@@ -466,10 +472,9 @@ ttt_status ttt_kv_attention_workspace_size(const ttt_attn* attn, int32_t batch, 
   TTT_TRY(check_tokens(tokens, act_dtype));
   size_t page = 0;
   TTT_TRY(ttt_kv_page_bytes(16, kv_heads, head_dim, &page));
-  const int n = tttk::attn_plan(batch, kv_heads, q_heads, attn->max_new, attn->max_kv, attn->window,
-                                act_dtype == TTT_F32, head_dim)
-                    .splits;
-  *bytes = part_bytes(n, tokens, q_heads, head_dim) + ml_bytes(n, tokens, q_heads);
+  const tttk::AttnPlan plan = tttk::attn_plan(batch, kv_heads, q_heads, attn->max_new, attn->max_kv,
+                                              attn->window, act_dtype == TTT_F32, head_dim);
+  *bytes = part_bytes(plan, batch, tokens, kv_heads, q_heads, head_dim).all();
   return TTT_OK;
   TTT_ENTRY_END
 }
@@ -494,9 +499,9 @@ ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_
   if (tokens == 0) return TTT_OK;
   const tttk::AttnPlan plan = tttk::attn_plan(a.pool.batch, a.pool.heads, q->heads, attn->max_new,
                                               attn->max_kv, attn->window, a.f32, dim);
-  a.many = plan.many, a.splits = plan.splits, a.each = plan.each;
-  const size_t need_part = part_bytes(a.splits, tokens, q->heads, dim);
-  const size_t need = need_part + ml_bytes(a.splits, tokens, q->heads);
+  a.many = plan.many, a.splits = plan.splits, a.each = plan.each, a.slices = plan.slices;
+  const PartBytes parts = part_bytes(plan, a.pool.batch, tokens, a.pool.heads, q->heads, dim);
+  const size_t need = parts.all();
   const int64_t size = a.f32 ? 4 : 2;
   const Reach pool = pool_reach(a.pool);
   const Reach qi = reach_of("q", *q, tokens, dim, size), oo = reach_of("o", *o, tokens, dim, size);
@@ -528,9 +533,10 @@ ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_
   a.causal = (attn->flags & TTT_ATTN_ALL_KEYS) == 0;
   a.window = attn->window, a.max_new = attn->max_new, a.max_kv = attn->max_kv;
   a.part = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + need_part);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.part);
+  a.part_of = reinterpret_cast<int*>(static_cast<char*>(workspace) + parts.part + parts.ml);
   TTT_TRY((launch<tttk::AttnLaunch, tttk::launch_attention>("kv_attention", a, stream)));
-  if (a.splits > 1)
+  if (need > 0)
     TTT_TRY((launch<tttk::AttnLaunch, tttk::launch_attention_join>("kv_attention_join", a, stream)));
   return TTT_OK;
   TTT_ENTRY_END

@@ -288,6 +288,28 @@ def test_negative_and_zero_scales(ttt):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 100])
+def test_slices_over_ragged_sequences(ttt, dtype, dim, window):
+    """Up to 16 rows a sequence and a long bound: even slices of all keys.
+    Slices of many sequences, some of them without rows or keys; slices of one
+    long one between short ones; and more rows than the bound said."""
+    rng = np.random.default_rng(14)
+    news, lens = rng.integers(0, 9, 120), rng.integers(0, 300, 120)
+    lens[::7], news[3:9], news[-2:] = 0, 0, 0
+    check(ttt, dtype, 16, 8, 16, dim, list(news), list(lens), window=window, max_new=8, max_kv=1 << 16, seed=1)
+    lens = [3, 0, 2500, 1, 129, 700, 0]
+    check(ttt, dtype, 64, 2, 6, dim, [1] * 7, lens, window=window, max_new=1, max_kv=8192, no_starts=True, seed=2)
+    check(ttt, dtype, 64, 2, 6, dim, [1, 0, 40, 1, 0, 7, 3], lens, window=window, max_new=1, max_kv=8192, seed=3)
+
+
+@pytest.mark.parametrize("batch", [64, 65, 256, 257])
+def test_slices_by_batch(ttt, batch):
+    lens = 1 + np.arange(batch) * 37 % 301
+    check(ttt, BF, 32, 1, 4, 128, [1] * batch, list(lens), max_new=1, max_kv=4096, no_starts=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_before_the_first_token_under_the_widest_window(ttt, dtype):
     """More rows than tokens: the first stand before the sequence and see
     nothing, whatever the window; the others see all before them."""
