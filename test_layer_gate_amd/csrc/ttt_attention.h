@@ -90,9 +90,15 @@ __device__ __forceinline__ int uniform_load(const int32_t* p, int64_t i) {
 // Loads of an address put together from integers, which has to be marked as
 // global memory's.
 typedef const __attribute__((address_space(1))) uint8_t* Global;
+// ONCE: past the caches' replacement, for what no other wave will read.
+template <bool ONCE = false>
 __device__ __forceinline__ uint4 load16(Global p) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const u32x4 w = *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(p);
+  const auto* q = reinterpret_cast<const __attribute__((address_space(1))) u32x4_t*>(p);
+  u32x4_t w;
+  if constexpr (ONCE)
+    w = __builtin_nontemporal_load(q);
+  else
+    w = *q;
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ uint32_t load4(Global p) {

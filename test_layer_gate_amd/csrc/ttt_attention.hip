@@ -32,10 +32,20 @@ namespace {
 // eight keys' values i D / 16 .. + D / 16 - 1. NW waves share a workgroup's
 // stretch of keys and join in LDS.
 //
-// Bound by how many bytes are on their way: three waves a SIMD (bf16, 128) with
-// 32 keys each, 4.3 KB. One token of 40/8 heads of 128 over 128k keys (143 MB)
-// takes 27 us, 5.3 TB/s, and its join 4; 32 sequences of 4k to 32k keys, 32/8
-// heads (0.56 GB), 104 us and 6.
+// Long caches are bound by HBM: a copy that only reads the same bytes is 5%
+// faster. Three waves a SIMD (bf16, 128) have 32 keys each under way, 4.3 KB.
+// One token of 40/8 heads of 128 over 128k keys (143 MB)
+// takes 24 us, 5.9 TB/s, and its join 4; 32 sequences of 4k to 32k keys, 32/8
+// heads (0.56 GB), 92 us, 6.1 TB/s, and 5. (Keys that came through LDS, two
+// tiles ahead, took 5% longer: it is not the bytes on their way that are few.)
+
+// Who else reads a workgroup's keys: those of the sequence's other rows; no
+// one, where 16 rows are all; no one, and the keys are a slice of all
+// sequences'. Codes that are read once are read past the caches' replacement:
+// one token over 128k keys 33.8 / 31.0 us a call, 32 ragged sequences 109 / 97.
+// Rows that share them are slower so (windowed fp32 rows 66 / 69), and so are
+// short sequences in one workgroup (12.1 / 12.6).
+enum Keys { kShared, kAlone, kSliced };
 
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
 template <int D>
@@ -46,9 +56,10 @@ struct FewTile {
   bool have[2];
 };
 
-template <int D, int T, bool F32, int NW, bool SLICED>
+template <int D, int T, bool F32, int NW, Keys KEYS>
 __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
+  constexpr bool SLICED = KEYS == kSliced, kOnce = KEYS != kShared;
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
@@ -186,8 +197,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
           const Global bp = reinterpret_cast<Global>((uint64_t)hi32 << 32 | lo32);
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            x.kw[u][p] = load16(bp + (k_lane + off * (D / 2)) + 16 * p);
-            x.vw[u][p] = load16(bp + (v_lane + off * (D / 2)) + 16 * p);
+            x.kw[u][p] = load16<kOnce>(bp + (k_lane + off * (D / 2)) + 16 * p);
+            x.vw[u][p] = load16<kOnce>(bp + (v_lane + off * (D / 2)) + 16 * p);
           }
           x.ks[u] = load4(bp + (ks_lane + off * (D / 32)));
           x.vs[u] = load4(bp + (vs_lane + off));
@@ -592,14 +603,17 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
   const int64_t tiles = tttk::row_tiles(a, group, 16, others);
   const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
-  const bool wide = a.splits == 1 && a.each <= kOneGroup;
-#define TTT_CALL(D, T, F)                                                          \
-  if (a.slices > 0)                                                                \
-    attend_few_kernel<D, T, F, 4, true><<<grid, 256, 0, s>>>(a, 1);                \
-  else if (wide)                                                                   \
-    attend_few_kernel<D, T, F, 8, false><<<grid, 512, 0, s>>>    (a, (int)tiles);   \
-  else                                                                             \
-    attend_few_kernel<D, T, F, 4, false><<<grid, 256, 0, s>>>(a, (int)tiles)
+  const bool wide = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
+  const bool alone = (int64_t)a.max_new * group <= 16;
+#define TTT_CALL(D, T, F)                                                                   \
+  if (wide)                                                                                 \
+    attend_few_kernel<D, T, F, 8, kShared><<<grid, 512, 0, s>>>(a, (int)tiles);             \
+  else if (a.slices > 0)                                                                    \
+    attend_few_kernel<D, T, F, 4, kSliced><<<grid, 256, 0, s>>>(a, 1);                      \
+  else if (alone)                                                                           \
+    attend_few_kernel<D, T, F, 4, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles);              \
+  else                                                                                      \
+    attend_few_kernel<D, T, F, 4, kShared><<<grid, 256, 0, s>>>(a, (int)tiles)
   switch (a.pool.dim) {
     case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
     case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
