@@ -44,7 +44,8 @@ namespace {
 // sequences'. Codes that are read once are read past the caches' replacement:
 // one token over 128k keys 33.8 / 31.0 us a call, 32 ragged sequences 109 / 97.
 // Rows that share them are slower so (windowed fp32 rows 66 / 69), and so are
-// short sequences in one workgroup (12.1 / 12.6).
+// short sequences in one workgroup (12.1 / 12.6) and heads of 256, of which a
+// read takes half of a lane's 32 bytes (32 sequences 138 / 141).
 enum Keys { kShared, kAlone, kSliced };
 
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
@@ -59,7 +60,7 @@ struct FewTile {
 template <int D, int T, bool F32, int NW, Keys KEYS>
 __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
-  constexpr bool SLICED = KEYS == kSliced, kOnce = KEYS != kShared;
+  constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && KEYS != kShared;
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
