@@ -145,12 +145,12 @@ __device__ __forceinline__ Seq seq_at(const Pool& p, int b) {
 }
 __device__ __forceinline__ Seq seq_of(const Pool& p, int b) { return seq_at<true>(p, b); }
 
-// Units of keys that a sequence's first 16 rows see; at least one, so that
+// Units of keys that a sequence's first `tile` rows see; at least one, so that
 // rows that see nothing are written, and none without rows.
-__device__ __forceinline__ uint32_t units_of(const AttnLaunch& a, const Seq& s, int group, int unit) {
+__device__ __forceinline__ uint32_t units_of(const AttnLaunch& a, const Seq& s, int tile, int group, int unit) {
   if (s.news <= 0) return 0;
   const Span first = span_of(a, s.len, s.news, 0);
-  const Span last = span_of(a, s.len, s.news, (min(16, s.news * group) - 1) / group);
+  const Span last = span_of(a, s.len, s.news, (min(tile, s.news * group) - 1) / group);
   return (uint32_t)(max(last.hi - (first.lo & ~31), 1) + unit - 1) / unit;
 }
 
@@ -161,14 +161,15 @@ struct Line {
   int b;
 };
 constexpr int kSliceBatch = 256;  // sequences at most: four a lane
-__device__ __forceinline__ Line line_of(const AttnLaunch& a, int slice, int group, int unit, int lane) {
+__device__ __forceinline__ Line line_of(const AttnLaunch& a, int slice, int tile, int group, int unit,
+                                     int lane) {
   uint32_t n[kSliceBatch / 64], sum[kSliceBatch / 64], total = 0;
 #pragma unroll
   for (int c = 0; c < kSliceBatch / 64; ++c) {
     n[c] = sum[c] = 0;
     if (c * 64 >= a.pool.batch) continue;
     const int b = c * 64 + lane;
-    if (b < a.pool.batch) n[c] = units_of(a, seq_at<false>(a.pool, b), group, unit);
+    if (b < a.pool.batch) n[c] = units_of(a, seq_at<false>(a.pool, b), tile, group, unit);
     uint32_t x = n[c];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {

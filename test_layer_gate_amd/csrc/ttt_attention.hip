@@ -14,6 +14,7 @@
 // time and without decoding; they keep about 17 bits of a sum of 8 products,
 // which left scores and lse off by 1e-4, and were not taken.)
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "ttt_attention.h"
@@ -22,22 +23,25 @@ namespace tttk {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Few rows. A wave takes 16 rows (query heads of one key head, times tokens)
-// and a stretch of the keys, 32 at a time, the next 32 on their way meanwhile.
-// S^T = K Q^T with 16x16x32: lane (i, g) = (lane % 16, lane / 16) brings D / 4
-// neighbouring values of key i; of the result it holds, for row i, keys 4g ..
-// 4g + 3 of either 16. Those eight are what the second product O^T = V^T P^T
-// (16x16x32) asks of it: the order of the contraction is free as long as V
-// agrees, so P goes over without a move between lanes. Of V it brings the same
-// eight keys' values i D / 16 .. + D / 16 - 1. NW waves share a workgroup's
-// stretch of keys and join in LDS.
+// Few rows. A wave takes 16 rows (query heads of one key head, times tokens),
+// or 32 that share the decoded keys, and a stretch of the keys, 32 at a time,
+// the next 32 on their way meanwhile. S^T = K Q^T with 16x16x32: lane (i, g) =
+// (lane % 16, lane / 16) brings D / 4 neighbouring values of key i; of the
+// result it holds, for row i, keys 4g .. 4g + 3 of either 16. Those eight are
+// what the second product O^T = V^T P^T (16x16x32) asks of it: the order of the
+// contraction is free as long as V agrees, so P goes over without a move
+// between lanes. Of V it brings the same eight keys' values i D / 16 .. + D /
+// 16 - 1. NW waves share a workgroup's stretch of keys and join in LDS.
 //
 // Long caches are bound by HBM: a copy that only reads the same bytes is 5%
 // faster. Three waves a SIMD (bf16, 128) have 32 keys each under way, 4.3 KB.
-// One token of 40/8 heads of 128 over 128k keys (143 MB)
-// takes 24 us, 5.9 TB/s, and its join 4; 32 sequences of 4k to 32k keys, 32/8
-// heads (0.56 GB), 92 us, 6.1 TB/s, and 5. (Keys that came through LDS, two
-// tiles ahead, took 5% longer: it is not the bytes on their way that are few.)
+// One token of 40/8 heads of 128 over 128k keys (143 MB) takes 24 us, 5.9 TB/s,
+// and its join 4; 32 sequences of 4k to 32k keys, 32/8 heads (0.56 GB), 92 us,
+// 6.1 TB/s, and 5. (Keys that came through LDS, two tiles ahead, took 5%
+// longer: it is not the bytes on their way that are few.) From 17 rows on
+// decoding is what bounds it, which 32 rows share where registers allow (bf16,
+// heads of 64 and 128): 4 tokens of 40/8 heads of 128 after 93k keys in 10
+// sequences 315 us for 16, 228 for 32.
 
 // Who else reads a workgroup's keys: those of the sequence's other rows; no
 // one, where 16 rows are all; no one, and the keys are a slice of all
@@ -57,21 +61,23 @@ struct FewTile {
   bool have[2];
 };
 
-template <int D, int T, bool F32, int NW, Keys KEYS>
-__global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
+template <int D, int T, bool F32, int NW, int RT, Keys KEYS>
+__global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
   constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && KEYS != kShared;
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
+  constexpr int kRows = 16 * RT;        // of a tile
   // Three terms of the rows' queries would be the registers of a second wave:
   // the waves, whose rows are the same, read them from LDS.
   constexpr bool kShareQ = T > 1;
-  constexpr size_t kRed = sizeof(float) * (NW - 1) * 16 * (D + 4), kQ = kShareQ ? T * KS * 1024 : 0;
+  static_assert(RT == 1 || !kShareQ, "shared queries are of one tile");
+  constexpr size_t kRed = sizeof(float) * (NW - 1) * kRows * (D + 4), kQ = kShareQ ? T * KS * 1024 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t pool[kRed > kQ ? kRed : kQ];
-  float(*red_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(pool);
+  float(*red_o)[kRows][D + 4] = reinterpret_cast<float(*)[kRows][D + 4]>(pool);
   uint4(*shared_q)[KS][64] = reinterpret_cast<uint4(*)[KS][64]>(pool);
-  __shared__ float red_ml[NW][16][2];
+  __shared__ float red_ml[NW][kRows][2];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -88,7 +94,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
   Line line = {};
   if constexpr (SLICED) {
     if (id >= a.slices) return;
-    line = line_of(a, id, group, 32 * NW, lane);
+    line = line_of(a, id, kRows, group, 32 * NW, lane);
     if (line.at >= line.end) return;
     b = line.b, tile = 0;
   } else {
@@ -102,48 +108,61 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     const Seq seq = seq_of(a.pool, b);
     const int row0 = seq.row0, news = seq.news, len = seq.len;
     const int rows = max(news, 0) * group;
-    if (tile * 16 >= rows) break;  // (of a slice's sequences, the first tile has rows)
-    const int r = tile * 16 + i16;
-    const bool live = r < rows;
-    const int t = min(r, rows - 1) / group;
-    const int head = hk * group + min(r, rows - 1) % group;
-    const Span sp = span_of(a, len, news, t);
+    if (tile * kRows >= rows) break;  // (of a slice's sequences, the first tile has rows)
+    bool live[RT];
+    int t[RT], head[RT];
+    Span sp[RT];
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      const int r = tile * kRows + 16 * x + i16;
+      live[x] = r < rows;
+      t[x] = min(r, rows - 1) / group;
+      head[x] = hk * group + min(r, rows - 1) % group;
+      sp[x] = span_of(a, len, news, t[x]);
+    }
     // the tile's keys
-    const Span first = span_of(a, len, news, tile * 16 / group);
-    const Span last = span_of(a, len, news, min(tile * 16 + 15, rows - 1) / group);
+    const Span first = span_of(a, len, news, tile * kRows / group);
+    const Span last = span_of(a, len, news, min(tile * kRows + kRows - 1, rows - 1) / group);
     const int lo = first.lo & ~31, hi = last.hi;
     const int all_lo = last.lo, all_hi = first.hi;  // keys that every row sees
 
     // Q as the first product's B operand: step s, values (D / 4) g + 8 s ..
-    uint4 qf[kShareQ ? 1 : KS];
+    uint4 qf[RT][kShareQ ? 1 : KS];
     {
       if constexpr (kShareQ) __syncthreads();  // the last tile's readers are done
-      const int64_t at = (int64_t)(row0 + t) * a.q.ts + head * a.q.hs + g * (D / 4);
       const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        if (kShareQ && s % NW != wave) continue;
-        float v[8];
-        load8<F32>(a.q.p, at + 8 * s, v);
-        uint32_t w[4][T];
+      for (int x = 0; x < RT; ++x) {
+        const int64_t at = (int64_t)(row0 + t[x]) * a.q.ts + head[x] * a.q.hs + g * (D / 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2<T>(v[2 * e], v[2 * e + 1], w[e]);
+        for (int s = 0; s < KS; ++s) {
+          if (kShareQ && s % NW != wave) continue;
+          float v[8];
+          load8<F32>(a.q.p, at + 8 * s, v);
+          uint32_t w[4][T];
 #pragma unroll
-        for (int x = 0; x < T; ++x) {
-          const uint4 y = make_uint4(w[0][x] ^ flip, w[1][x] ^ flip, w[2][x] ^ flip, w[3][x] ^ flip);
-          if constexpr (kShareQ)
-            shared_q[x][s][lane] = y;
-          else
-            qf[s] = y;
+          for (int e = 0; e < 4; ++e) split2<T>(v[2 * e], v[2 * e + 1], w[e]);
+#pragma unroll
+          for (int y = 0; y < T; ++y) {
+            const uint4 z = make_uint4(w[0][y] ^ flip, w[1][y] ^ flip, w[2][y] ^ flip, w[3][y] ^ flip);
+            if constexpr (kShareQ)
+              shared_q[y][s][lane] = z;
+            else
+              qf[x][s] = z;
+          }
         }
       }
       if constexpr (kShareQ) __syncthreads();
     }
     const float sc = fmaxf(fabsf(a.scale) * kLog2e, 1.2e-38f), grown = fminf(8.f / sc, 1e38f);
-    f32x4_t o[F];
+    f32x4_t o[RT][F];
+    float m[RT], ms[RT], l[RT];  // maximum (unscaled), its scaled value (0 for none), sum
 #pragma unroll
-    for (int f = 0; f < F; ++f) o[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float m = kNone, ms = 0.f, l = 0.f;  // maximum (unscaled), its scaled value (0 for none), sum
+    for (int x = 0; x < RT; ++x) {
+#pragma unroll
+      for (int f = 0; f < F; ++f) o[x][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      m[x] = kNone, ms[x] = 0.f, l[x] = 0.f;
+    }
 
     const uint32_t k_lane = i16 * (D / 2) + (D == 64 ? g >> 1 : g * NP) * 16;
     const uint32_t v_lane = page * (D / 2) + g * (2 * D) + (D == 64 ? (i16 >> 1) * 16 : i16 * (D / 8));
@@ -156,7 +175,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     // This part's stretches of keys, a wave's share of each: of a slice what it
     // has of the sequence; of a split every splits-th; of one part all of the
     // tile's keys, whatever the launch expected. What a slice has no part for,
-    // rows past the first 16 (more than max_new allowed for), are done whole
+    // rows past the first tile (more than max_new allowed for), are done whole
     // by the workgroup that has the sequence's first keys.
     const bool sliced = SLICED && tile == 0;
     const uint32_t u0 = line.at - line.off, u1 = min(line.n, line.end - line.off);  // of a slice
@@ -219,67 +238,75 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
         }
         uint32_t ks[2][NP];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int q = 0; q < NP; ++q) ks[x][q] = (cur.ks[x] >> (ks_shift + 8 * q)) & 255u;
+          for (int q = 0; q < NP; ++q) ks[u][q] = (cur.ks[u] >> (ks_shift + 8 * q)) & 255u;
         // S^T
         if constexpr (kShareQ) asm volatile("" ::: "memory");  // not all at once, ahead of the loop
-        f32x4_t s[2];
+        f32x4_t s[RT][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) s[x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < RT; ++x) s[x][0] = s[x][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < KS; ++q) {
           bf16x8_t kf[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint4 w = cur.kw[x][q >> 2];
+          for (int u = 0; u < 2; ++u) {
+            const uint4 w = cur.kw[u][q >> 2];
             uint32_t c = (q & 3) == 0 ? w.x : (q & 3) == 1 ? w.y : (q & 3) == 2 ? w.z : w.w;
             // D = 64: a lane's 16 values are half of a block
             if constexpr (D == 64) c = g & 1 ? (q == 0 ? w.z : w.w) : c;
             uint32_t d[4];
-            decode8(c, scale_value(ks[x][q >> 2]), d);
-            kf[x] = frag(d[0], d[1], d[2], d[3]);
+            decode8(c, scale_value(ks[u][q >> 2]), d);
+            kf[u] = frag(d[0], d[1], d[2], d[3]);
           }
 #pragma unroll
-          for (int y = T - 1; y >= 0; --y) {
-            const uint4 z = kShareQ ? shared_q[y][q][lane] : qf[kShareQ ? 0 : q];
+          for (int y = T - 1; y >= 0; --y)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) s[x] = mfma16(kf[x], frag(z.x, z.y, z.z, z.w), s[x]);
-          }
+            for (int x = 0; x < RT; ++x) {
+              const uint4 z = kShareQ ? shared_q[y][q][lane] : qf[x][kShareQ ? 0 : q];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) s[x][u] = mfma16(kf[u], frag(z.x, z.y, z.z, z.w), s[x][u]);
+            }
         }
-        float p[8];
+        float p[RT][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = s[e >> 2][e & 3];
+        for (int x = 0; x < RT; ++x)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[x][e] = s[x][e >> 2][e & 3];
         // Keys that some row does not see, that have no page, or that hold NaN
-        uint32_t nan = 0;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          nan |= nan_bytes(cur.ks[x]) | nan_bytes(cur.vs[x]);
-        }
+        const uint32_t nan = nan_bytes(cur.ks[0]) | nan_bytes(cur.vs[0]) | nan_bytes(cur.ks[1]) | nan_bytes(cur.vs[1]);
         const bool odd = j < all_lo || j + 32 > all_hi || !cur.have[0] || !cur.have[1] || __any(nan != 0);
-        uint32_t poison = 0;  // this row's keys whose value is NaN
+        uint32_t poison[RT] = {};  // the rows' keys whose value is NaN
         if (odd) {
           rare_path();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint64_t kn = __ballot(ks[x][0] > kScaleMax);
+          for (int u = 0; u < 2; ++u) {
+            uint64_t kn = __ballot(ks[u][0] > kScaleMax);
             kn |= kn >> 32;
             const uint32_t kn32 = (uint32_t)kn | (uint32_t)kn >> 16;
-            const int k = j + 16 * x + 4 * g;  // this lane's four keys
-            const uint32_t seen = cur.have[x] ? bits_between(sp.lo - k, sp.hi - k) : 0u;
-            const uint32_t bad = cur.have[x] ? nan_bytes(cur.vs[x]) : 0x80808080u;
+            const int k = j + 16 * u + 4 * g;  // this lane's four keys
+            const uint32_t bad = cur.have[u] ? nan_bytes(cur.vs[u]) : 0x80808080u;
+#pragma unroll
+            for (int x = 0; x < RT; ++x) {
+              const uint32_t seen = cur.have[u] ? bits_between(sp[x].lo - k, sp[x].hi - k) : 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t keep = spread(seen, e);
+                float& w = p[x][4 * u + e];
+                w = __uint_as_float((__float_as_uint(w) & keep) | (kNoneBits & ~keep) |
+                                    (spread(kn32 >> (4 * g), e) & keep & kNanBits));
+                poison[x] |= (keep & spread(bad, 8 * e + 7) & 1u) << (4 * u + e);
+              }
+            }
+            // A NaN value must not reach the rows that do not see it (0 * NaN):
+            // it goes out of V, and into the weight of those that do.
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t keep = spread(seen, e), gone_v = spread(bad, 8 * e + 7);
-              p[4 * x + e] = __uint_as_float((__float_as_uint(p[4 * x + e]) & keep) | (kNoneBits & ~keep) |
-                                             (spread(kn32 >> (4 * g), e) & keep & kNanBits));
-              // A NaN value must not reach the rows that do not see it (0 * NaN):
-              // it goes out of V, and into the weight of those that do.
-              poison |= (keep & gone_v & 1u) << (4 * x + e);
-              cur.vs[x] = (cur.vs[x] & ~(gone_v & 255u << (8 * e))) | (gone_v & 127u << (8 * e));
+              const uint32_t gone_v = spread(bad, 8 * e + 7);
+              cur.vs[u] = (cur.vs[u] & ~(gone_v & 255u << (8 * e))) | (gone_v & 127u << (8 * e));
 #pragma unroll
               for (int q = 0; q < NP; ++q) {
-                uint4& y = cur.vw[x][q];
+                uint4& y = cur.vw[u][q];
                 uint32_t& w = e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w;
                 w &= ~gone_v;
               }
@@ -288,36 +315,49 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
         }
         // The maximum is only followed when a weight would pass 2^8: until
         // then the lanes need not agree on a new one, and nothing is rescaled.
-        const float mx = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
-                               fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-        if (__any(mx > m + grown)) {
-          float mn = fmaxf(mx, __shfl_xor(mx, 16));
-          mn = fmaxf(fmaxf(mn, __shfl_xor(mn, 32)), m);
-          const float n0 = mn == kNone ? 0.f : mn * sc;
-          const float al = m == kNone ? 0.f : __builtin_amdgcn_exp2f(ms - n0);
-          m = mn, ms = n0;
-          l *= al;
+        float mx[RT];
+        bool up = false;
 #pragma unroll
-          for (int f = 0; f < F; ++f)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[f][e] *= al;
+        for (int x = 0; x < RT; ++x) {
+          mx[x] = fmaxf(fmaxf(fmaxf(p[x][0], p[x][1]), fmaxf(p[x][2], p[x][3])),
+                        fmaxf(fmaxf(p[x][4], p[x][5]), fmaxf(p[x][6], p[x][7])));
+          up |= mx[x] > m[x] + grown;
         }
+        if (__any(up)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], sc, -ms));
-        l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        if (__any(poison != 0)) {
-          rare_path();
+          for (int x = 0; x < RT; ++x) {
+            float mn = fmaxf(mx[x], __shfl_xor(mx[x], 16));
+            mn = fmaxf(fmaxf(mn, __shfl_xor(mn, 32)), m[x]);
+            const float n0 = mn == kNone ? 0.f : mn * sc;
+            const float al = m[x] == kNone ? 0.f : __builtin_amdgcn_exp2f(ms[x] - n0);
+            m[x] = mn, ms[x] = n0;
+            l[x] *= al;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            p[e] = __uint_as_float(__float_as_uint(p[e]) | (spread(poison, e) & kNanBits));
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[x][f][e] *= al;
+          }
         }
-        uint32_t pw[T][4];
+        uint32_t pw[RT][T][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[T];
-          split2<T>(p[2 * e], p[2 * e + 1], w);
+        for (int x = 0; x < RT; ++x) {
+          float(&w)[8] = p[x];
 #pragma unroll
-          for (int x = 0; x < T; ++x) pw[x][e] = w[x];
+          for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(fmaf(w[e], sc, -ms[x]));
+          l[x] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+          if (__any(poison[x] != 0)) {
+            rare_path();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = __uint_as_float(__float_as_uint(w[e]) | (spread(poison[x], e) & kNanBits));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t z[T];
+            split2<T>(w[2 * e], w[2 * e + 1], z);
+#pragma unroll
+            for (int y = 0; y < T; ++y) pw[x][y][e] = z[y];
+          }
         }
         // O^T
         float vsc[8];
@@ -342,72 +382,86 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
                                        __builtin_amdgcn_perm(d[5], d[4], sel), __builtin_amdgcn_perm(d[7], d[6], sel));
 #pragma unroll
               for (int y = T - 1; y >= 0; --y)
-                o[8 * c + f + h] = mfma16(vf, frag(pw[y][0], pw[y][1], pw[y][2], pw[y][3]), o[8 * c + f + h]);
+#pragma unroll
+                for (int x = 0; x < RT; ++x) {
+                  const auto& w = pw[x][y];
+                  o[x][8 * c + f + h] = mfma16(vf, frag(w[0], w[1], w[2], w[3]), o[x][8 * c + f + h]);
+                }
             }
           }
         }
       }
     }
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    m = m == kNone ? kNone : ms;
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      l[x] += __shfl_xor(l[x], 16);
+      l[x] += __shfl_xor(l[x], 32);
+      m[x] = m[x] == kNone ? kNone : ms[x];
+    }
 
     // Join the waves: all to the common maximum, then added in their order.
     __syncthreads();  // the last tile's readers are done
-    if (g == 0) red_ml[wave][i16][0] = m, red_ml[wave][i16][1] = l;
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
+      if (g == 0) red_ml[wave][16 * x + i16][0] = m[x], red_ml[wave][16 * x + i16][1] = l[x];
     __syncthreads();
-    float mj = kNone;
+    float mj[RT], lj[RT];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) mj = fmaxf(mj, red_ml[w][i16][0]);
-    const float mj0 = mj == kNone ? 0.f : mj;
-    float lj = 0.f;
+    for (int x = 0; x < RT; ++x) {
+      mj[x] = kNone, lj[x] = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-      lj += red_ml[w][i16][1] * __builtin_amdgcn_exp2f(red_ml[w][i16][0] - mj0);
-    const float al = __builtin_amdgcn_exp2f(m - mj0);
+      for (int w = 0; w < NW; ++w) mj[x] = fmaxf(mj[x], red_ml[w][16 * x + i16][0]);
+      const float mj0 = mj[x] == kNone ? 0.f : mj[x];
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+      for (int w = 0; w < NW; ++w)
+        lj[x] += red_ml[w][16 * x + i16][1] * __builtin_amdgcn_exp2f(red_ml[w][16 * x + i16][0] - mj0);
+      const float al = __builtin_amdgcn_exp2f(m[x] - mj0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[f][e] *= al;
-    // lane (i, g), o[f][e]: row i, value F (4g + e) + f
-    if (wave > 0) {
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) o[x][f][e] *= al;
+      // lane (i, g), o[f][e]: row i, value F (4g + e) + f
+      if (wave > 0) {
 #pragma unroll
-        for (int f = 0; f < F; f += 4)
-          *reinterpret_cast<float4*>(&red_o[wave - 1][i16][F * (4 * g + e) + f]) =
-              make_float4(o[f][e], o[f + 1][e], o[f + 2][e], o[f + 3][e]);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int f = 0; f < F; f += 4)
+            *reinterpret_cast<float4*>(&red_o[wave - 1][16 * x + i16][F * (4 * g + e) + f]) =
+                make_float4(o[x][f][e], o[x][f + 1][e], o[x][f + 2][e], o[x][f + 3][e]);
+      }
     }
     __syncthreads();
-    if (wave == 0 && live) {
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+      if (wave > 0 || !live[x]) continue;
 #pragma unroll 1  // all at once would need the most registers of the kernel
       for (int w = 0; w < NW - 1; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int f = 0; f < F; ++f) o[f][e] += red_o[w][i16][F * (4 * g + e) + f];
-      const int64_t row = (int64_t)(row0 + t) * a.q.heads + head;
+          for (int f = 0; f < F; ++f) o[x][f][e] += red_o[w][16 * x + i16][F * (4 * g + e) + f];
+      const int64_t row = (int64_t)(row0 + t[x]) * a.q.heads + head[x];
       if (sliced ? u0 > 0 || u1 < line.n : a.splits > 1) {
         // slice + sequence: no two pairs that meet have the same sum
-        const int part = ((int)(line.at / line.per) + b) * a.pool.heads + hk;
-        const int64_t at = sliced ? (int64_t)part * 16 + i16 : (int64_t)split * a.pool.tokens * a.q.heads + row;
+        const int part = (((int)(line.at / line.per) + b) * a.pool.heads + hk) * kRows + 16 * x + i16;
+        const int64_t at = sliced ? (int64_t)part : (int64_t)split * a.pool.tokens * a.q.heads + row;
         if (sliced && u0 == 0 && g == 0)
-          *reinterpret_cast<int2*>(a.part_of + 2 * row) = make_int2(
-              part * 16 + i16, (int)((line.off + line.n - 1) / line.per - line.at / line.per) + 1);
-        if (g == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(mj, lj);
+          *reinterpret_cast<int2*>(a.part_of + 2 * row) =
+              make_int2(part, (int)((line.off + line.n - 1) / line.per - line.at / line.per) + 1);
+        if (g == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(mj[x], lj[x]);
         float* dst = a.part + at * D;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int f = 0; f < F; f += 4)
             *reinterpret_cast<float4*>(dst + F * (4 * g + e) + f) =
-                make_float4(o[f][e], o[f + 1][e], o[f + 2][e], o[f + 3][e]);
+                make_float4(o[x][f][e], o[x][f + 1][e], o[x][f + 2][e], o[x][f + 3][e]);
       } else {
-        const float inv = lj == 0.f ? 0.f : 1.f / lj;
+        const float inv = lj[x] == 0.f ? 0.f : 1.f / lj[x];
         if (a.lse != nullptr && g == 0)
-          a.lse[row] = lj == 0.f ? kNone : (mj + __builtin_amdgcn_logf(lj)) * kLn2;
+          a.lse[row] = lj[x] == 0.f ? kNone : (mj[x] + __builtin_amdgcn_logf(lj[x])) * kLn2;
         if (SLICED && g == 0) *reinterpret_cast<int2*>(a.part_of + 2 * row) = make_int2(0, 0);
-        const int64_t at = (int64_t)(row0 + t) * a.o.ts + head * a.o.hs;
+        const int64_t at = (int64_t)(row0 + t[x]) * a.o.ts + head[x] * a.o.hs;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (F >= 8) {
@@ -415,18 +469,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
             for (int f = 0; f < F; f += 8) {
               float v[8];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] = o[f + x][e] * inv;
+              for (int y = 0; y < 8; ++y) v[y] = o[x][f + y][e] * inv;
               store8<F32>(a.o.p, at + F * (4 * g + e) + f, v);
             }
           } else {
-            const int64_t x = at + F * (4 * g + e);
+            const int64_t y = at + F * (4 * g + e);
             if constexpr (F32)
-              *reinterpret_cast<float4*>(static_cast<float*>(a.o.p) + x) =
-                  make_float4(o[0][e] * inv, o[1][e] * inv, o[2][e] * inv, o[3][e] * inv);
+              *reinterpret_cast<float4*>(static_cast<float*>(a.o.p) + y) =
+                  make_float4(o[x][0][e] * inv, o[x][1][e] * inv, o[x][2][e] * inv, o[x][3][e] * inv);
             else
-              *reinterpret_cast<uint2*>(static_cast<u16*>(a.o.p) + x) =
-                  make_uint2(pack_bf16(o[0][e] * inv, o[1][e] * inv),
-                             pack_bf16(o[2][e] * inv, o[3][e] * inv));
+              *reinterpret_cast<uint2*>(static_cast<u16*>(a.o.p) + y) =
+                  make_uint2(pack_bf16(o[x][0][e] * inv, o[x][1][e] * inv),
+                             pack_bf16(o[x][2][e] * inv, o[x][3][e] * inv));
           }
         }
       }
@@ -435,7 +489,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
       tile += row_tiles;
       continue;
     }
-    if (u0 == 0 && (tile + 1) * 16 < rows) {
+    if (u0 == 0 && (tile + 1) * kRows < rows) {
       ++tile;
       continue;
     }
@@ -444,7 +498,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_few_kernel(
     line.at = line.off += line.n;
     line.n = 0;
     while (line.at < line.end && line.n == 0 && ++b < a.pool.batch)
-      line.n = units_of(a, seq_of(a.pool, b), group, 32 * NW);
+      line.n = units_of(a, seq_of(a.pool, b), kRows, group, 32 * NW);
     if (line.n == 0) break;
   }
 }
@@ -469,7 +523,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
   int64_t base = row, stride = rows;
   int count = a.splits;
   if (a.slices > 0) {
-    stride = a.pool.heads * 16;
+    stride = a.pool.heads * a.tile;
     const int all = (a.slices + a.pool.batch - 1) * (int)stride;
     const int2 d = *reinterpret_cast<const int2*>(a.part_of + 2 * row);
     if (d.y <= 0 || (uint32_t)d.x >= (uint32_t)all) return;
@@ -530,23 +584,6 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
 
 namespace {
 
-// Whether the many-row kernel is taken: for bf16 rows with heads of 64 or 128,
-// more than 128 of them a sequence and key head, and 2^25 pairs of a row and
-// a key in all. It decodes a tile of keys for 256 rows at once, and starts
-// slowly. In us, few-row kernel / many-row kernel (32/8 heads):
-//   128: 256 rows of 8k keys 32 / 41, of 16k 47 / 48; 512 of 16k 83 / 65; 4096
-//   of 8k 260 / 162, 16384 749 / 449; 4 sequences of 16k keys: 128 rows each
-//   82 / 89, 256 153 / 102.   64: 256 of 16k 39 / 36, 16384 of 8k 534 / 334.
-// fp32 rows keep the matrix unit three times as long, beside which decoding
-// for 16 rows alone costs little, and with wide heads a workgroup's sums leave
-// no registers for a second wave: built for them, it took 879 us for the
-// few-row kernel's 783 (fp32, 64), 1146 for 1162 (fp32, 128), 2148 for 1351
-// (fp32, 256) and 612 for 689 (bf16, 256) over 16384 rows and 8k keys, and
-// lost wherever there were fewer.
-bool take_many(int64_t rows, double pairs, bool f32, int dim) {
-  return !f32 && dim <= 128 && rows > 128 && pairs >= 0x1p25;
-}
-
 // Keys up to which one workgroup of the few-row kernel takes a whole sequence,
 // without the join's launch and its workspace. On the GPU alone (32/8 heads)
 // one sequence of 512 keys takes 7.5 us so and 7.8 in parts, of 1024 9.6 and
@@ -555,23 +592,46 @@ bool take_many(int64_t rows, double pairs, bool f32, int dim) {
 // short as this waits for.
 constexpr int kOneGroup = 1024;
 
-}  // namespace
+// Eight waves take a short sequence faster than four while a workgroup has a
+// CU to itself (of 512 keys, 64 rows a workgroup 12.1 us / 12.3), and slower
+// when there are more (256 workgroups 14.7 / 12.6, 512 26.4 / 17.2).
+constexpr int kWideGroups = 128;
 
-AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
-                   int dim) {
-  const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
-  int64_t keys = max_kv < kMaxKeys ? max_kv : kMaxKeys;
-  if (window > 0) keys = keys < (int64_t)window + max_new ? keys : (int64_t)window + max_new;
-  if (take_many(rows, (double)rows * keys * kv_heads * batch, f32, dim)) {
-    // Parts until there is a workgroup for every CU, of 512 keys at least.
-    const int64_t groups = (rows + kManyTile - 1) / kManyTile * kv_heads * batch;
-    const int64_t most = (keys + 511) / 512;
-    int64_t want = 256 / groups;
-    if (want > most) want = most;
-    return {true, (int)(want < 1 ? 1 : want), 0, 0};
+// Whether the many-row kernel is taken, for bf16 rows with heads of 64 or 128:
+// by what either kernel takes, in us, of heads of 128 (of 64 both take 3/4).
+// A workgroup of the many-row kernel takes 2 us for 64 keys of its 256 rows,
+// one CU each, after 12 us of start; the rounds after the first start in 20.
+// The few-row kernel takes 0.8 us for 2^20 pairs of a row and a key, and 7 us
+// to start each round of 512 workgroups. Parts cost a join and their way
+// through memory. keys: of a tile of rows; seen: of them, on average.
+//   many / few, measured (32/8 heads; sequences x rows a key head over keys):
+//   1 x 256 over 1k 33 / 20, 16k 52 / 45, 64k 100 / 117; 1 x 64 over 64k 84 / 44,
+//   1 x 128 92 / 68; 8 x 128 over 8k 90 / 74; 4 x 512 over 4k 66 / 73; prompts of
+//   1 x 256 tokens 18 / 13, 4 x 256 19 / 24, 1 x 1k 47 / 31, 4 x 1k 77 / 98,
+//   8 x 512 53 / 80, 1 x 2k 75 / 73.
+// fp32 rows keep the matrix unit three times as long, beside which decoding
+// for 16 rows alone costs little, and with wide heads a workgroup's sums leave
+// no registers for a second wave: built for them, it took 879 us for the
+// few-row kernel's 783 (fp32, 64), 1146 for 1162 (fp32, 128), 2148 for 1351
+// (fp32, 256) and 612 for 689 (bf16, 256) over 16384 rows and 8k keys, and
+// lost wherever there were fewer.
+struct Costs {
+  double rows, heads;  // rows a key head; key heads of all sequences
+  static double parts(double rows, double n) { return n > 1 ? 5 + rows * n * 2.6e-4 : 0; }
+  double many(double keys, double seen, double splits) const {
+    const double groups = ceil(rows / kManyTile) * heads;
+    const double longest = ceil(keys / 64 / splits), mean = groups * seen / 64 / 256;
+    return 12 + 20 * fmax(groups * splits / 256 - 1, 0) + 2 * fmax(longest, mean) + parts(rows * heads, splits);
   }
-  // A short sequence is one workgroup of eight waves.
-  if (keys <= kOneGroup) return {false, 1, kOneGroup, 0};
+  double few(double tile, double seen, double splits) const {
+    const double groups = ceil(rows / tile) * heads * splits;
+    return 7 * fmax(groups / 512, 1) + 0.8 * rows * heads * seen / (1 << 20) + parts(rows * heads, splits);
+  }
+};
+
+AttnPlan few_plan(int batch, int kv_heads, int64_t rows, int64_t keys, int tile, bool f32, int dim) {
+  // A short sequence is one workgroup.
+  if (keys <= kOneGroup) return {false, 1, kOneGroup, 0, tile};
   // Several sequences with one tile of rows each: a slice for every workgroup
   // that the card holds at once, whatever the lengths are, which only the GPU
   // knows. Against parts of 8192 keys each (us, with the join, 32/8 heads of
@@ -579,46 +639,78 @@ AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv
   // 128k and 31 of 1k 380 / 51, 128 of 1 to 8k 133 / 124; 2 of 1500 14.4 / 15.2,
   // 200 of 1 to 4k (one part each then) 92 / 99. 512 slices 134 us for the 32,
   // 1024 152, 1536 139.
-  if (rows <= 16 && batch > 1 && batch <= kSliceBatch) {
+  if (rows <= tile && batch > 1 && batch <= kSliceBatch) {
     const int64_t units = (keys + 127) / 128 * batch;
-    const int64_t fit = dim == 256 ? 512 : dim == 64 && !f32 ? 1024 : 768;
+    const int64_t fit = dim == 256 || tile == 32 ? 512 : dim == 64 && !f32 ? 1024 : 768;
     int64_t slices = fit / kv_heads < 1 ? 1 : fit / kv_heads;
     if (slices > units) slices = units;
-    return {false, 1, 0, (int)slices};
+    return {false, 1, 0, (int)slices, tile};
   }
   // Stretches that give 512 workgroups of four waves, or 1024 where some
   // sequences may be shorter than max_kv; of 512 keys or more where there is
   // much to do (each workgroup loads its rows and hands in its sums), and of
   // 128 at least. 1 token over 128k keys: 512 take 35.4 us, 768 36.8, 1024
   // 40.6, 2304 44.0.
-  const double work = (double)keys * ((rows + 15) / 16) * kv_heads * batch;
+  const double work = (double)keys * ((rows + tile - 1) / tile) * kv_heads * batch;
   const double fair = work / (batch > 1 ? 1024 : 512), least = work < 512 * 256 ? 128 : 512;
   const double most = 1 << 20, e = fair < least ? least : fair > most ? most : fair;
   const int each = ((int)e + 127) / 128 * 128;
-  return {false, (int)((keys + each - 1) / each), each, 0};
+  return {false, (int)((keys + each - 1) / each), each, 0, tile};
+}
+
+}  // namespace
+
+AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
+                   int dim) {
+  const int group = q_heads / kv_heads;
+  const int64_t rows = (int64_t)max_new * group, all = max_kv < kMaxKeys ? max_kv : kMaxKeys;
+  // The keys of so many rows in a row.
+  auto span = [&](int tile) {
+    const int64_t near = (int64_t)window + (tile + group - 1) / group;
+    return window > 0 && near < all ? near : all;
+  };
+  const int tile = !f32 && dim <= 128 && rows > 16 ? 32 : 16;
+  const AttnPlan few = few_plan(batch, kv_heads, rows, span(tile), tile, f32, dim);
+  if (f32 || dim > 128 || rows <= 32) return few;
+  // Parts until there is a workgroup for every CU, of 512 keys at least.
+  const double heads = (double)kv_heads * batch, groups = ceil((double)rows / kManyTile) * heads;
+  const int64_t keys = span(kManyTile), most = (keys + 511) / 512;
+  int64_t want = (int64_t)(256 / groups);
+  if (want > most) want = most;
+  if (want < 1) want = 1;
+  const double before = 0.5 * (max_new < all ? max_new : all);  // keys that causal rows miss
+  const Costs c = {(double)rows, heads};
+  const double many = c.many((double)keys, fmin((double)keys, all - before), (double)want);
+  return many < c.few(tile, fmin((double)span(tile), all - before), few.splits)
+             ? AttnPlan{true, (int)want, 0, 0, 0} : few;
 }
 
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   if (a.many) return launch_attend_many(a, s);
   const int group = a.q.heads / a.pool.heads;
   const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
-  const int64_t tiles = tttk::row_tiles(a, group, 16, others);
+  const int64_t tiles = tttk::row_tiles(a, group, a.tile, others);
   const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
-  const bool wide = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
-  const bool alone = (int64_t)a.max_new * group <= 16;
-#define TTT_CALL(D, T, F)                                                                   \
+  const bool wide = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup && tiles * others <= kWideGroups;
+  const bool alone = (int64_t)a.max_new * group <= a.tile;
+#define TTT_CALL(D, T, F, RT)                                                               \
   if (wide)                                                                                 \
-    attend_few_kernel<D, T, F, 8, kShared><<<grid, 512, 0, s>>>(a, (int)tiles);             \
+    attend_few_kernel<D, T, F, 8, RT, kShared><<<grid, 512, 0, s>>>(a, (int)tiles);         \
   else if (a.slices > 0)                                                                    \
-    attend_few_kernel<D, T, F, 4, kSliced><<<grid, 256, 0, s>>>(a, 1);                      \
+    attend_few_kernel<D, T, F, 4, RT, kSliced><<<grid, 256, 0, s>>>(a, 1);                  \
   else if (alone)                                                                           \
-    attend_few_kernel<D, T, F, 4, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles);              \
+    attend_few_kernel<D, T, F, 4, RT, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles);          \
   else                                                                                      \
-    attend_few_kernel<D, T, F, 4, kShared><<<grid, 256, 0, s>>>(a, (int)tiles)
+    attend_few_kernel<D, T, F, 4, RT, kShared><<<grid, 256, 0, s>>>(a, (int)tiles)
+  const bool two = a.tile == 32;
   switch (a.pool.dim) {
-    case 64: if (a.f32) { TTT_CALL(64, 3, true); } else { TTT_CALL(64, 1, false); } break;
-    case 128: if (a.f32) { TTT_CALL(128, 3, true); } else { TTT_CALL(128, 1, false); } break;
-    default: if (a.f32) { TTT_CALL(256, 3, true); } else { TTT_CALL(256, 1, false); } break;
+    case 64:
+      if (a.f32) { TTT_CALL(64, 3, true, 1); } else if (two) { TTT_CALL(64, 1, false, 2); } else { TTT_CALL(64, 1, false, 1); }
+      break;
+    case 128:
+      if (a.f32) { TTT_CALL(128, 3, true, 1); } else if (two) { TTT_CALL(128, 1, false, 2); } else { TTT_CALL(128, 1, false, 1); }
+      break;
+    default: if (a.f32) { TTT_CALL(256, 3, true, 1); } else { TTT_CALL(256, 1, false, 1); } break;
   }
 #undef TTT_CALL
   return hipGetLastError();

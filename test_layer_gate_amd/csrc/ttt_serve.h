@@ -70,9 +70,9 @@ struct AttnLaunch {
   int causal, window, max_new, max_kv;
   bool f32;
   bool many;             // attn_plan()
-  int splits, each, slices;
+  int splits, each, slices, tile;
   float* part;           // [splits][tokens * q heads][D] (splits > 1), or
-                         // [slices + batch - 1][kv heads][16][D] (slices > 0)
+                         // [slices + batch - 1][kv heads][tile][D] (slices > 0)
   float* part_ml;        // likewise, [2] for [D]
   int* part_of;          // [tokens * q heads][2]: a row's first part, and how many (slices > 0)
 };
@@ -92,6 +92,7 @@ constexpr int64_t kMaxKeys = (int64_t)1 << 30;
 struct AttnPlan {
   bool many;
   int splits, each, slices;
+  int tile;  // rows a wave of the few-row kernel takes
 };
 AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
                    int dim);

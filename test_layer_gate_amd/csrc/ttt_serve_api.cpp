@@ -304,7 +304,7 @@ struct PartBytes {
 };
 PartBytes part_bytes(const tttk::AttnPlan& p, int64_t batch, int64_t tokens, int64_t kv_heads, int64_t q_heads,
                      int64_t dim) {
-  const size_t rows = p.slices > 0   ? (size_t)(p.slices + batch - 1) * kv_heads * 16
+  const size_t rows = p.slices > 0   ? (size_t)(p.slices + batch - 1) * kv_heads * p.tile
                       : p.splits > 1 ? (size_t)p.splits * tokens * q_heads
                                      : 0;
   return {align256(rows * dim * 4), align256(rows * 8), p.slices > 0 ? align256((size_t)tokens * q_heads * 8) : 0};
@@ -499,7 +499,7 @@ ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_
   if (tokens == 0) return TTT_OK;
   const tttk::AttnPlan plan = tttk::attn_plan(a.pool.batch, a.pool.heads, q->heads, attn->max_new,
                                               attn->max_kv, attn->window, a.f32, dim);
-  a.many = plan.many, a.splits = plan.splits, a.each = plan.each, a.slices = plan.slices;
+  a.many = plan.many, a.splits = plan.splits, a.each = plan.each, a.slices = plan.slices, a.tile = plan.tile;
   const PartBytes parts = part_bytes(plan, a.pool.batch, tokens, a.pool.heads, q->heads, dim);
   const size_t need = parts.all();
   const int64_t size = a.f32 ? 4 : 2;

@@ -60,8 +60,10 @@ def pool_of(rng, lens, page, hk, dim, garbage=True):
 
 # The bounds size the launch, and with it choose the kernel: under large ones
 # bf16 rows with heads of 64 and 128 go to the many-row kernel whatever there
-# is of them, the first in few parts, the second in many (some of them empty).
-MANY = [dict(max_new=4096, max_kv=1 << 16), dict(max_new=200, max_kv=1 << 22)]
+# is of them, the first in few parts, the second in many (some of them empty),
+# the third under a window too.
+MANY = [dict(max_new=4096, max_kv=1 << 16), dict(max_new=200, max_kv=1 << 22),
+        dict(max_new=1 << 20, max_kv=1 << 16)]
 
 
 def check(ttt, dtype, page, hk, hq, dim, news, lens, *, q=None, seed=0, **kw):
