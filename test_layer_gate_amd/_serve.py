@@ -4,13 +4,15 @@ attention over it.
 
 Only argument checking and marshalling live here, as in _binding.py. These
 calls come once a token, so they keep to a few microseconds: descriptors are
-built positionally and tensors are passed as plain addresses.
+packed as bytes in the layout of the header's structs (a third of the time that
+filling a ctypes structure takes) and tensors are passed as plain addresses.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 import math
+import struct
 
 import torch
 
@@ -49,6 +51,12 @@ class Attn(ctypes.Structure):
                 ("flags", _U), ("reserved", _U)]
 
 
+# The same layouts, packed; bytes are passed where the library takes a pointer.
+_pack_rows = struct.Struct("PqqiI").pack
+_pack_rope = struct.Struct("PiiII").pack
+_pack_cache = struct.Struct("PqPPPiiiiiii4x").pack
+_pack_attn = struct.Struct("fiiiII").pack
+
 _lib = None
 _ref = ctypes.byref
 
@@ -58,8 +66,8 @@ def _L():
     if _lib is not None:
         return _lib
     L = _b.lib()
-    R, C, A, Z = (ctypes.POINTER(t) for t in (Rows, Cache, Attn, ctypes.c_size_t))
-    T = ctypes.POINTER(Rope)
+    R = C = A = T = _P  # packed bytes, or a structure's address
+    Z = ctypes.POINTER(ctypes.c_size_t)
     L.ttt_rope_table.argtypes = [_P, _I, _I, ctypes.c_double, ctypes.POINTER(RopeScaling), _P]
     for fn in (L.ttt_rope_forward, L.ttt_rope_backward):
         fn.argtypes = [_I, _I, _I, _I, T, _P, R, R, R, R, _P]
@@ -98,6 +106,8 @@ def _on(stream, make, *args, **kw):
 
 
 def _empty(t, stream):
+    if stream is None:  # (torch.empty with a dtype and device takes twice as long)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     return _on(stream, torch.empty_like, t, memory_format=torch.contiguous_format)
 
 
@@ -107,20 +117,29 @@ def _rows_of(t, what):
     evenly."""
     if not t.is_cuda:
         raise ValueError("all tensors must be on the GPU")
-    shape, st = t.shape, t.stride()
-    if len(shape) == 4:
-        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+    st = t.stride()
+    if len(st) == 3:
+        n, h, d = t.shape
+        ts, hs, vs = st
+    elif len(st) == 4:
+        b, n, h, d = t.shape
+        bs, ts, hs, vs = st
+        if b > 1 and n > 1 and bs != n * ts:
             raise ValueError(f"{what}: the sequences of a [B, T, heads, dim] tensor must follow "
                              "each other at T times the token stride")
-        ts = st[1] if shape[1] > 1 else st[0]
-        shape, st = (shape[0] * shape[1], shape[2], shape[3]), (ts, st[2], st[3])
-    elif len(shape) != 3:
+        ts = ts if n > 1 else bs
+        n *= b
+    else:
         raise ValueError(f"{what} must be [rows, heads, dim] or [B, T, heads, dim]")
-    n, h, d = shape
-    if d > 1 and st[2] != 1:
+    if vs != 1 and d > 1:
         raise ValueError(f"{what}: the values of a head must be contiguous")
     # the stride of an axis of length 1 means nothing: any aligned one will do
-    return n, h, d, Rows(t.data_ptr(), st[0] if n > 1 else h * d, st[1] if h > 1 else d, h, 0)
+    return n, h, d, _pack_rows(t.data_ptr(), ts if n > 1 else h * d, hs if h > 1 else d, h, 0)
+
+
+def _dense(t, h, d):
+    """The same of a contiguous tensor made here."""
+    return _pack_rows(t.data_ptr(), h * d, d, h, 0)
 
 
 def _rows(t, what, n, dim, dtype):
@@ -162,7 +181,7 @@ def _rope(table, interleaved):
             or not table.is_cuda or not table.is_contiguous()):
         raise ValueError("the rope table must be a contiguous float32 [max_pos, rot_dim / 2, 2] "
                          "tensor on the GPU")
-    return Rope(table.data_ptr(), 2 * shape[1], shape[0], ROPE_INTERLEAVED if interleaved else 0, 0)
+    return _pack_rope(table.data_ptr(), 2 * shape[1], shape[0], ROPE_INTERLEAVED if interleaved else 0, 0)
 
 
 def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, original=None,
@@ -190,19 +209,23 @@ def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, orig
 
 
 def _rope_call(fn, q, k, table, positions, interleaved, q_out, k_out, stream):
-    n, _, dim, rq = _rows_of(q, "q")
+    n, h, dim, rq = _rows_of(q, "q")
     act, dtype = _act(q, "q"), q.dtype
     if q_out is None:
         q_out = _empty(q, stream)
-    ro = _rows(q_out, "q_out", n, dim, dtype)
+        ro = _dense(q_out, h, dim)
+    else:
+        ro = _rows(q_out, "q_out", n, dim, dtype)
+    rk = rko = None
     if k is not None:
+        rk = _rows(k, "k", n, dim, dtype)
         if k_out is None:
             k_out = _empty(k, stream)
-        rk, rko = _ref(_rows(k, "k", n, dim, dtype)), _ref(_rows(k_out, "k_out", n, dim, dtype))
-    else:
-        rk = rko = None
+            rko = _dense(k_out, k.shape[-2], dim)
+        else:
+            rko = _rows(k_out, "k_out", n, dim, dtype)
     st = fn(n, max(q.shape[1], 1) if q.dim() == 4 else max(n, 1), dim, act,
-            _ref(_rope(table, interleaved)), _positions(positions, n), _ref(rq), rk, _ref(ro), rko,
+            _rope(table, interleaved), _positions(positions, n), rq, rk, ro, rko,
             _stream(stream, q))
     if st:
         _b._check(st)
@@ -253,10 +276,10 @@ def _cache(pages, page_table, kv_lens, q_starts, dim):
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch, max_pages]")
     batch, max_pages = page_table.shape
-    return Cache(pages.data_ptr(), st[0] if n_pages > 1 else heads * block,
-                 _ints(page_table, "page_table"), _ints(kv_lens, "kv_lens", (batch,)),
-                 _ints(q_starts, "q_starts", (batch + 1,)), batch, max_pages, n_pages, page, heads,
-                 dim, 0)
+    return _pack_cache(pages.data_ptr(), st[0] if n_pages > 1 else heads * block,
+                       _ints(page_table, "page_table"), _ints(kv_lens, "kv_lens", (batch,)) or 0,
+                       _ints(q_starts, "q_starts", (batch + 1,)) or 0, batch, max_pages, n_pages, page,
+                       heads, dim, 0)
 
 
 def kv_append(pages, page_table, kv_lens, k, v, *, q=None, q_starts=None, rope_table=None,
@@ -272,13 +295,16 @@ def kv_append(pages, page_table, kv_lens, k, v, *, q=None, q_starts=None, rope_t
     cache = _cache(pages, page_table, kv_lens, q_starts, dim)
     rq = ro = None
     if q is not None:
+        rq = _rows(q, "q", n, dim, dtype)
         if q_out is None:
             q_out = _empty(q, stream)
-        rq, ro = _ref(_rows(q, "q", n, dim, dtype)), _ref(_rows(q_out, "q_out", n, dim, dtype))
+            ro = _dense(q_out, q.shape[-2], dim)
+        else:
+            ro = _rows(q_out, "q_out", n, dim, dtype)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    st = _L().ttt_kv_append(_ref(cache), n, act, _ref(rk), _ref(rv), rq, ro,
-                            None if rope_table is None else _ref(_rope(rope_table, interleaved)),
+    st = _L().ttt_kv_append(cache, n, act, rk, rv, rq, ro,
+                            None if rope_table is None else _rope(rope_table, interleaved),
                             _positions(positions, n), _stream(stream, k))
     if st:
         _b._check(st)
@@ -291,14 +317,19 @@ def kv_read(pages, page_table, kv_lens, rows, head_dim, dtype=torch.bfloat16, *,
     the order kv_append takes them (ttt_kv_read): k, v [rows, kv_heads,
     head_dim]."""
     cache = _cache(pages, page_table, kv_lens, q_starts, head_dim)
-    shape = (rows, pages.shape[1], head_dim)
+    heads = pages.shape[1]
+    shape = (rows, heads, head_dim)
     if k_out is None:
         k_out = _on(stream, torch.empty, shape, dtype=dtype, device=pages.device)
+        rk = _dense(k_out, heads, head_dim)
+    else:
+        rk = _rows(k_out, "k_out", rows, head_dim, dtype)
     if v_out is None:
-        v_out = _on(stream, torch.empty, shape, dtype=dtype, device=pages.device)
-    rk = _rows(k_out, "k_out", rows, head_dim, dtype)
-    rv = _rows(v_out, "v_out", rows, head_dim, dtype)
-    st = _L().ttt_kv_read(_ref(cache), rows, _act(k_out, "k_out"), _ref(rk), _ref(rv),
+        v_out = _empty(k_out, stream)
+        rv = _dense(v_out, heads, head_dim)
+    else:
+        rv = _rows(v_out, "v_out", rows, head_dim, dtype)
+    st = _L().ttt_kv_read(cache, rows, _act(k_out, "k_out"), rk, rv,
                           _stream(stream, pages))
     if st:
         _b._check(st)
@@ -308,8 +339,8 @@ def kv_read(pages, page_table, kv_lens, rows, head_dim, dtype=torch.bfloat16, *,
 @functools.lru_cache(maxsize=1024)  # of sizes alone
 def _workspace(batch, rows, act, kv_heads, q_heads, dim, max_new, max_kv, window):
     n = ctypes.c_size_t(0)
-    a = Attn(1.0, window, max_new, max_kv, 0, 0)
-    _b._check(_L().ttt_kv_attention_workspace_size(_ref(a), batch, rows, act, kv_heads, q_heads, dim,
+    a = _pack_attn(1.0, window, max_new, max_kv, 0, 0)
+    _b._check(_L().ttt_kv_attention_workspace_size(a, batch, rows, act, kv_heads, q_heads, dim,
                                                    _ref(n)))
     return n.value
 
@@ -333,25 +364,28 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     n, heads, dim, rq = _rows_of(q, "q")
     act = _act(q, "q")
     cache = _cache(pages, page_table, kv_lens, q_starts, dim)
+    batch, kv_heads = page_table.shape[0], pages.shape[1]
     if max_new is None:
-        max_new = max(1, n if q_starts is not None else n // cache.batch)
+        max_new = max(1, n if q_starts is not None else n // max(batch, 1))
     if max_kv is None:
-        max_kv = cache.max_pages * cache.page_size
+        max_kv = min(max(1, page_table.shape[1] * (pages.shape[2] * 16 // (dim * 17))), 1 << 30)
     if out is None:
         out = _empty(q, stream)
-    ro = _rows(out, "out", n, dim, q.dtype)
+        ro = _dense(out, heads, dim)
+    else:
+        ro = _rows(out, "out", n, dim, q.dtype)
     if lse is None:
         if with_lse:
             lse = _on(stream, torch.empty, (n, heads), dtype=torch.float32, device=q.device)
     elif lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != n * heads:
         raise ValueError("lse must be a contiguous float32 [rows, q_heads] tensor")
-    a = Attn(dim ** -0.5 if scale is None else scale, window, max_new, max_kv,
-             0 if causal else ATTN_ALL_KEYS, 0)
+    a = _pack_attn(dim ** -0.5 if scale is None else scale, window, max_new, max_kv,
+                   0 if causal else ATTN_ALL_KEYS, 0)
     if workspace is None:
-        need = _workspace(cache.batch, n, act, cache.kv_heads, heads, dim, max_new, max_kv, window)
+        need = _workspace(batch, n, act, kv_heads, heads, dim, max_new, max_kv, window)
         if need:
             workspace = _on(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
-    st = _L().ttt_kv_attention(_ref(cache), _ref(a), n, act, _ref(rq), _ref(ro),
+    st = _L().ttt_kv_attention(cache, a, n, act, rq, ro,
                                None if lse is None else lse.data_ptr(),
                                None if workspace is None else workspace.data_ptr(),
                                0 if workspace is None else workspace.numel(), _stream(stream, q))
