@@ -557,7 +557,8 @@ ttt_status ttt_kv_read(const ttt_cache* cache, int32_t tokens, int32_t act_dtype
  *            be NULL where that is 0)
  * Arithmetic: products of bf16 operands accumulated in fp32 (the cache's
  * values are exact in bf16). For bf16 rows the weights are rounded to bf16
- * before they meet the values; for fp32 rows queries and weights enter as
+ * before they meet the values (up to 16 rows of up to 1024 keys: two bf16
+ * terms); for fp32 rows queries and weights enter as
  * three bf16 terms each (24 bits). Maxima, sums and joins are fp32, in a fixed
  * order. */
 enum { TTT_ATTN_ALL_KEYS = 1u << 0 };

@@ -44,13 +44,13 @@ namespace {
 // sequences 315 us for 16, 228 for 32.
 
 // Who else reads a workgroup's keys: those of the sequence's other rows; no
-// one, where 16 rows are all; no one, and the keys are a slice of all
-// sequences'. Codes that are read once are read past the caches' replacement:
+// one, where one tile of rows is all; no one, and the keys are a slice of all
+// sequences'; no one, and the sequences are short. Codes that are read once are read past the caches' replacement:
 // one token over 128k keys 33.8 / 31.0 us a call, 32 ragged sequences 109 / 97.
 // Rows that share them are slower so (windowed fp32 rows 66 / 69), and so are
 // short sequences in one workgroup (12.1 / 12.6) and heads of 256, of which a
 // read takes half of a lane's 32 bytes (32 sequences 138 / 141).
-enum Keys { kShared, kAlone, kSliced };
+enum Keys { kShared, kAlone, kSliced, kShort };
 
 // One lane's share of 32 keys (two pieces of 16): raw codes and scales.
 template <int D>
@@ -64,11 +64,17 @@ struct FewTile {
 template <int D, int T, bool F32, int NW, int RT, Keys KEYS>
 __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
-  constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && KEYS != kShared;
+  constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && (KEYS == kAlone || KEYS == kSliced);
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
   constexpr int kRows = 16 * RT;        // of a tile
+  // Terms of the weights. For bf16 rows one term's error is about that of
+  // rounding the output (0.0013 rms beside 0.0016), and more where one key has
+  // nearly all of the weight, which the few rows of a short call do not average
+  // out: those take two terms (0.7 us of 10). In long sequences a second
+  // costs 8 to 13%.
+  constexpr int TP = F32 ? 3 : KEYS == kShort ? 2 : 1;
   // Three terms of the rows' queries would be the registers of a second wave:
   // the waves, whose rows are the same, read them from LDS.
   constexpr bool kShareQ = T > 1;
@@ -338,7 +344,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
               for (int e = 0; e < 4; ++e) o[x][f][e] *= al;
           }
         }
-        uint32_t pw[RT][T][4];
+        uint32_t pw[RT][TP][4];
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
           float(&w)[8] = p[x];
@@ -353,10 +359,10 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t z[T];
-            split2<T>(w[2 * e], w[2 * e + 1], z);
+            uint32_t z[TP];
+            split2<TP>(w[2 * e], w[2 * e + 1], z);
 #pragma unroll
-            for (int y = 0; y < T; ++y) pw[x][y][e] = z[y];
+            for (int y = 0; y < TP; ++y) pw[x][y][e] = z[y];
           }
         }
         // O^T
@@ -381,7 +387,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
               const bf16x8_t vf = frag(__builtin_amdgcn_perm(d[1], d[0], sel), __builtin_amdgcn_perm(d[3], d[2], sel),
                                        __builtin_amdgcn_perm(d[5], d[4], sel), __builtin_amdgcn_perm(d[7], d[6], sel));
 #pragma unroll
-              for (int y = T - 1; y >= 0; --y)
+              for (int y = TP - 1; y >= 0; --y)
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                   const auto& w = pw[x][y];
@@ -691,17 +697,25 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
   const int64_t tiles = tttk::row_tiles(a, group, a.tile, others);
   const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
-  const bool wide = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup && tiles * others <= kWideGroups;
+  const bool brief = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
+  const bool wide = brief && tiles * others <= kWideGroups;
   const bool alone = (int64_t)a.max_new * group <= a.tile;
 #define TTT_CALL(D, T, F, RT)                                                               \
-  if (wide)                                                                                 \
+  constexpr Keys kBrief = F || RT > 1 ? kShared : kShort;                                   \
+  if (brief && alone) {                                                                     \
+    if (wide)                                                                               \
+      attend_few_kernel<D, T, F, 8, RT, kBrief><<<grid, 512, 0, s>>>(a, (int)tiles);        \
+    else                                                                                    \
+      attend_few_kernel<D, T, F, 4, RT, kBrief><<<grid, 256, 0, s>>>(a, (int)tiles);        \
+  } else if (wide) {                                                                        \
     attend_few_kernel<D, T, F, 8, RT, kShared><<<grid, 512, 0, s>>>(a, (int)tiles);         \
-  else if (a.slices > 0)                                                                    \
+  } else if (a.slices > 0) {                                                                \
     attend_few_kernel<D, T, F, 4, RT, kSliced><<<grid, 256, 0, s>>>(a, 1);                  \
-  else if (alone)                                                                           \
+  } else if (alone) {                                                                       \
     attend_few_kernel<D, T, F, 4, RT, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles);          \
-  else                                                                                      \
-    attend_few_kernel<D, T, F, 4, RT, kShared><<<grid, 256, 0, s>>>(a, (int)tiles)
+  } else {                                                                                  \
+    attend_few_kernel<D, T, F, 4, RT, kShared><<<grid, 256, 0, s>>>(a, (int)tiles);         \
+  }
   const bool two = a.tile == 32;
   switch (a.pool.dim) {
     case 64:
