@@ -31,7 +31,7 @@ namespace {
 // what the second product O^T = V^T P^T (16x16x32) asks of it: the order of the
 // contraction is free as long as V agrees, so P goes over without a move
 // between lanes. Of V it brings the same eight keys' values i D / 16 .. + D /
-// 16 - 1. NW waves share a workgroup's stretch of keys and join in LDS.
+// 16 - 1. Four waves share a workgroup's stretch of keys and join in LDS.
 //
 // Long caches are bound by HBM: a copy that only reads the same bytes is 5%
 // faster. Three waves a SIMD (bf16, 128) have 32 keys each under way, 4.3 KB.
@@ -61,7 +61,9 @@ struct FewTile {
   bool have[2];
 };
 
-template <int D, int T, bool F32, int NW, int RT, Keys KEYS>
+constexpr int NW = 4;  // waves of a workgroup
+
+template <int D, int T, bool F32, int RT, Keys KEYS>
 __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
   constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && (KEYS == kAlone || KEYS == kSliced);
@@ -591,23 +593,19 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnLaunch a) {
 namespace {
 
 // Keys up to which one workgroup of the few-row kernel takes a whole sequence,
-// without the join's launch and its workspace. On the GPU alone (32/8 heads)
-// one sequence of 512 keys takes 7.5 us so and 7.8 in parts, of 1024 9.6 and
-// 8.0, of 2048 14.2 and 8.4; 16 sequences of 1024 10.0 and 10.7. A launch and
-// an allocation saved are 4 us of the caller's time, which is what a call as
-// short as this waits for.
+// without the join's launch and its workspace. On the GPU alone (one token,
+// 32/8 heads of 128) one sequence of 512 keys takes 7.4 us so and 8.2 in parts,
+// of 777 9.6 and 8.2, of 1024 10.5 and 8.3; 16 sequences of 1024 11.1 and 12.6.
+// A launch and an allocation saved are 4 us of the caller's time, which is what
+// a call as short as this waits for. (Eight waves a workgroup instead of four:
+// 10.1 us for 777 keys, 10.4 for 1024, 12.6 for 32 sequences of 1024 either way.)
 constexpr int kOneGroup = 1024;
-
-// Eight waves take a short sequence faster than four while a workgroup has a
-// CU to itself (of 512 keys, 64 rows a workgroup 12.1 us / 12.3), and slower
-// when there are more (256 workgroups 14.7 / 12.6, 512 26.4 / 17.2).
-constexpr int kWideGroups = 128;
 
 // Whether the many-row kernel is taken, for bf16 rows with heads of 64 or 128:
 // by what either kernel takes, in us, of heads of 128 (of 64 both take 3/4).
 // A workgroup of the many-row kernel takes 2 us for 64 keys of its 256 rows,
 // one CU each, after 12 us of start; the rounds after the first start in 20.
-// The few-row kernel takes 0.8 us for 2^20 pairs of a row and a key, and 7 us
+// The few-row kernel takes 0.8 us for 2^20 pairs of a row and a key, and 9 us
 // to start each round of 512 workgroups. Parts cost a join and their way
 // through memory. keys: of a tile of rows; seen: of them, on average.
 //   many / few, measured (32/8 heads; sequences x rows a key head over keys):
@@ -631,7 +629,7 @@ struct Costs {
   }
   double few(double tile, double seen, double splits) const {
     const double groups = ceil(rows / tile) * heads * splits;
-    return 7 * fmax(groups / 512, 1) + 0.8 * rows * heads * seen / (1 << 20) + parts(rows * heads, splits);
+    return 9 * fmax(groups / 512, 1) + 0.8 * rows * heads * seen / (1 << 20) + parts(rows * heads, splits);
   }
 };
 
@@ -698,24 +696,17 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const int64_t tiles = tttk::row_tiles(a, group, a.tile, others);
   const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
   const bool brief = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
-  const bool wide = brief && tiles * others <= kWideGroups;
   const bool alone = (int64_t)a.max_new * group <= a.tile;
 #define TTT_CALL(D, T, F, RT)                                                               \
   constexpr Keys kBrief = F || RT > 1 ? kShared : kShort;                                   \
-  if (brief && alone) {                                                                     \
-    if (wide)                                                                               \
-      attend_few_kernel<D, T, F, 8, RT, kBrief><<<grid, 512, 0, s>>>(a, (int)tiles);        \
-    else                                                                                    \
-      attend_few_kernel<D, T, F, 4, RT, kBrief><<<grid, 256, 0, s>>>(a, (int)tiles);        \
-  } else if (wide) {                                                                        \
-    attend_few_kernel<D, T, F, 8, RT, kShared><<<grid, 512, 0, s>>>(a, (int)tiles);         \
-  } else if (a.slices > 0) {                                                                \
-    attend_few_kernel<D, T, F, 4, RT, kSliced><<<grid, 256, 0, s>>>(a, 1);                  \
-  } else if (alone) {                                                                       \
-    attend_few_kernel<D, T, F, 4, RT, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles);          \
-  } else {                                                                                  \
-    attend_few_kernel<D, T, F, 4, RT, kShared><<<grid, 256, 0, s>>>(a, (int)tiles);         \
-  }
+  if (a.slices > 0)                                                                         \
+    attend_few_kernel<D, T, F, RT, kSliced><<<grid, 64 * NW, 0, s>>>(a, 1);                 \
+  else if (!alone)                                                                          \
+    attend_few_kernel<D, T, F, RT, kShared><<<grid, 64 * NW, 0, s>>>(a, (int)tiles);        \
+  else if (brief)                                                                           \
+    attend_few_kernel<D, T, F, RT, kBrief><<<grid, 64 * NW, 0, s>>>(a, (int)tiles);         \
+  else                                                                                      \
+    attend_few_kernel<D, T, F, RT, kAlone><<<grid, 64 * NW, 0, s>>>(a, (int)tiles)
   const bool two = a.tile == 32;
   switch (a.pool.dim) {
     case 64:
