@@ -17,7 +17,7 @@ constexpr int kRopeThreads = 256;
 // lanes take neighbouring pieces, then neighbouring heads of the token, so
 // that a wave reads and writes whole lines; a lane then walks over the
 // remaining heads with the cosines and sines it has loaded. Bound by HBM:
-// 64k tokens of 32 + 8 heads of 128 in bf16 move at 6.3 TB/s.
+// 64k tokens of 32 + 8 heads of 128 in bf16 take 216 us, 6.4 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeLaunch a, int units, int lanes,
                                                             int64_t total) {
@@ -130,8 +130,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_table_kernel(
 hipError_t launch_rope(const RopeLaunch& a, hipStream_t s) {
   const int units = a.dim / (2 * (a.f32 ? kWide<true> : kWide<false>)), heads = a.x[0].heads + a.x[1].heads;
   // Heads that are not walked over: enough for a wave or two to stay within
-  // a token (of 1: 304 us for the 64k tokens above, 8: 249, 16: 237, all:
-  // 267), and for the chip to be full.
+  // a token (with plain accesses, of 1: 304 us for the 64k tokens above, 8: 249,
+  // 16: 237, all: 267), and for the chip to be full.
   int lanes = heads;
   const int64_t one = (int64_t)a.tokens * units;
   while (lanes > 1 && units * ((lanes + 1) / 2) >= 128 && one * ((lanes + 1) / 2) >= (int64_t)256 * 2048)

@@ -40,7 +40,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
 }
 
 // 16 bytes (W = 8 bf16 or 4 fp32 values) that are read or written once, past
-// the caches' replacement: 64k tokens of 40 rotated heads take 220 us so and
+// the caches' replacement: 64k tokens of 40 rotated heads took 220 us so and
 // 237 with plain accesses. Only where a wave's accesses fill whole lines: half
 // lines written this way cost a read and a write each.
 template <bool F32>
