@@ -31,7 +31,8 @@ namespace {
 // what the second product O^T = V^T P^T (16x16x32) asks of it: the order of the
 // contraction is free as long as V agrees, so P goes over without a move
 // between lanes. Of V it brings the same eight keys' values i D / 16 .. + D /
-// 16 - 1. Four waves share a workgroup's stretch of keys and join in LDS.
+// 16 - 1. Four waves share a workgroup's stretch of keys and join in LDS, or,
+// where there are tiles enough for all, each has its own.
 //
 // Long caches are bound by HBM: a copy that only reads the same bytes is 5%
 // faster. Three waves a SIMD (bf16, 128) have 32 keys each under way, 4.3 KB.
@@ -61,9 +62,7 @@ struct FewTile {
   bool have[2];
 };
 
-constexpr int NW = 4;  // waves of a workgroup
-
-template <int D, int T, bool F32, int RT, Keys KEYS>
+template <int D, int T, bool F32, int RT, Keys KEYS, int NW = 4>
 __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
   constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && (KEYS == kAlone || KEYS == kSliced);
@@ -81,7 +80,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
   // the waves, whose rows are the same, read them from LDS.
   constexpr bool kShareQ = T > 1;
   static_assert(RT == 1 || !kShareQ, "shared queries are of one tile");
-  constexpr size_t kRed = sizeof(float) * (NW - 1) * kRows * (D + 4), kQ = kShareQ ? T * KS * 1024 : 0;
+  constexpr size_t kRed = NW == 1 ? 16 : sizeof(float) * (NW - 1) * kRows * (D + 4), kQ = kShareQ ? T * KS * 1024 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t pool[kRed > kQ ? kRed : kQ];
   float(*red_o)[kRows][D + 4] = reinterpret_cast<float(*)[kRows][D + 4]>(pool);
   uint4(*shared_q)[KS][64] = reinterpret_cast<uint4(*)[KS][64]>(pool);
@@ -601,6 +600,16 @@ namespace {
 // 10.1 us for 777 keys, 10.4 for 1024, 12.6 for 32 sequences of 1024 either way.)
 constexpr int kOneGroup = 1024;
 
+// Tiles of rows from which on every wave takes one of its own, all of its keys,
+// and none are joined: four waves a SIMD. fp32 prompts of 4 x 1738 tokens, 64/8
+// heads of 128, 696 us with four waves a tile and 620 so; of 6 x 603, 64/8 heads
+// of 64, 95 / 71; bf16 of 2 x 1976, 128/8 heads of 256, 519 / 399; fp32 rows that
+// see 6 keys (6 x 1234, 40/8 heads of 256) 179 / 97. With 2048 tiles it loses:
+// fp32 of 2048 tokens, 16/4 heads of 64, 47 / 65.
+constexpr int kOwnTile = 4096;
+template <int D, bool F32>
+constexpr bool kOwn = F32 || D == 256;  // the others' many tiles are the many-row kernel's
+
 // Whether the many-row kernel is taken, for bf16 rows with heads of 64 or 128:
 // by what either kernel takes, in us, of heads of 128 (of 64 both take 3/4).
 // A workgroup of the many-row kernel takes 2 us for 64 keys of its 256 rows,
@@ -700,16 +709,20 @@ hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
   const bool brief = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
   const bool alone = (int64_t)a.max_new * group <= a.tile;
-#define TTT_CALL(D, T, F, RT)                                                               \
-  constexpr Keys kBrief = F || RT > 1 ? kShared : kShort;                                   \
-  if (a.slices > 0)                                                                         \
-    attend_few_kernel<D, T, F, RT, kSliced><<<grid, 64 * NW, 0, s>>>(a, 1);                 \
-  else if (!alone)                                                                          \
-    attend_few_kernel<D, T, F, RT, kShared><<<grid, 64 * NW, 0, s>>>(a, (int)tiles);        \
-  else if (brief)                                                                           \
-    attend_few_kernel<D, T, F, RT, kBrief><<<grid, 64 * NW, 0, s>>>(a, (int)tiles);         \
-  else                                                                                      \
-    attend_few_kernel<D, T, F, RT, kAlone><<<grid, 64 * NW, 0, s>>>(a, (int)tiles)
+  const bool own = a.tile == 16 && !alone && a.splits == 1 && tiles * others >= kOwnTile;
+#define TTT_CALL(D, T, F, RT)                                                          \
+  constexpr Keys kBrief = F || RT > 1 ? kShared : kShort;                              \
+  if (a.slices > 0)                                                                    \
+    attend_few_kernel<D, T, F, RT, kSliced><<<grid, 256, 0, s>>>(a, 1);                \
+  else if (own && kOwn<D, F>)                                                          \
+    attend_few_kernel<D, T, F, RT, kShared, kOwn<D, F> ? 1 : 4>                        \
+        <<<grid, 64, 0, s>>>(a, (int)tiles);                                           \
+  else if (!alone)                                                                     \
+    attend_few_kernel<D, T, F, RT, kShared><<<grid, 256, 0, s>>>(a, (int)tiles);       \
+  else if (brief)                                                                      \
+    attend_few_kernel<D, T, F, RT, kBrief><<<grid, 256, 0, s>>>(a, (int)tiles);        \
+  else                                                                                 \
+    attend_few_kernel<D, T, F, RT, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles)
   const bool two = a.tile == 32;
   switch (a.pool.dim) {
     case 64:

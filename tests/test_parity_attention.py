@@ -380,3 +380,17 @@ def test_outputs_live_on_the_stream_of_the_call(ttt):
     s.synchronize()
     assert all(owner(t) == [s.cuda_stream] for t in made)
     assert torch.equal(o[::9], x[::9])     # every row's values are ones, which the cache holds exactly
+
+
+@pytest.mark.parametrize("dtype,hk,hq,dim", [(BF, 1, 3, 256), (F32, 2, 4, 64), (F32, 1, 2, 128), (F32, 1, 2, 256)])
+def test_tiles_enough_for_every_wave(ttt, dtype, hk, hq, dim):
+    """So many sequences that each wave has rows of its own (short keys, so
+    that they are not split): prompts, a window, rows without keys."""
+    rng = np.random.default_rng(15)
+    batch, new = 70, 40
+    news = rng.integers(0, new + 1, batch)
+    lens = news + rng.integers(-2, 30, batch).clip(-news, None)
+    lens[5] = 0
+    # max_new is a bound: tiles of rows that are not there make up the number
+    for window in (0, 7):
+        check(ttt, dtype, 16, hk, hq, dim, list(news), list(lens), window=window, max_new=1 << 12, max_kv=128, seed=4)
