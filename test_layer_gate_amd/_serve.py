@@ -377,18 +377,21 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     if lse is None:
         if with_lse:
             lse = _on(stream, torch.empty, (n, heads), dtype=torch.float32, device=q.device)
-    elif lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() != n * heads:
-        raise ValueError("lse must be a contiguous float32 [rows, q_heads] tensor")
+    elif (lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous()
+          or lse.numel() != n * heads):
+        raise ValueError("lse must be a contiguous float32 [rows, q_heads] tensor on the GPU")
     a = _pack_attn(dim ** -0.5 if scale is None else scale, window, max_new, max_kv,
                    0 if causal else ATTN_ALL_KEYS, 0)
     if workspace is None:
         need = _workspace(batch, n, act, kv_heads, heads, dim, max_new, max_kv, window)
         if need:
             workspace = _on(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the GPU")
     st = _L().ttt_kv_attention(cache, a, n, act, rq, ro,
                                None if lse is None else lse.data_ptr(),
                                None if workspace is None else workspace.data_ptr(),
-                               0 if workspace is None else workspace.numel(), _stream(stream, q))
+                               0 if workspace is None else workspace.nbytes, _stream(stream, q))
     if st:
         _b._check(st)
     return (out, lse) if with_lse or lse is not None else out

@@ -1,0 +1,67 @@
+"""CPU-only: what the Python entry points of the attention half of a block
+refuse by themselves, before the library is asked. Nothing is launched: the
+tensors say that they are on the GPU, and the library's functions only count
+their calls."""
+import pytest
+import torch
+
+from test_layer_gate_amd import _serve as sv
+
+BF, F32, U8, I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+
+
+class OnGpu(torch.Tensor):
+    is_cuda = True
+
+
+def gpu(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+
+class Library:
+    """Every function succeeds, and is counted."""
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    L = Library()
+    monkeypatch.setattr(sv, "_L", lambda: L)
+    monkeypatch.setattr(sv, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(sv, "_workspace", lambda *a: 0)
+    return L
+
+
+def attention(**kw):
+    q, pages = gpu(6, 4, 64), gpu(3, 2, 16 * 68, dtype=U8)
+    return sv.kv_attention(q, pages, gpu(2, 1, dtype=I32), gpu(2, dtype=I32), **kw)
+
+
+def test_attention_takes_the_callers_buffers(lib):
+    lse, ws = gpu(6, 4, dtype=F32), gpu(512, dtype=U8)
+    o, got = attention(lse=lse, workspace=ws)
+    assert got is lse and o.shape == (6, 4, 64) and lib.calls == ["ttt_kv_attention"]
+    attention(workspace=gpu(64, dtype=F32))      # any type: its bytes count
+    assert len(lib.calls) == 2
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lse=torch.zeros(6, 4)),                               # in host memory
+    dict(lse=gpu(6, 4)),                                       # bf16
+    dict(lse=gpu(6, 8, dtype=F32)[:, :4]),                     # rows apart
+    dict(lse=gpu(6, 3, dtype=F32)),
+    dict(workspace=torch.zeros(512, dtype=U8)),                # in host memory
+    dict(workspace=gpu(512, dtype=U8)[::2]),
+    dict(workspace=gpu(1, dtype=U8).expand(4096)),             # more elements than bytes
+])
+def test_attention_refuses_buffers_that_the_kernels_cannot_write(lib, kw):
+    with pytest.raises(ValueError):
+        attention(**kw)
+    assert not lib.calls
