@@ -201,6 +201,8 @@ def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, orig
         high = 32.0 if scaling == "yarn" else 4.0
     table = _on(stream, torch.empty, (max(int(max_pos), 0), max(int(rot_dim), 0) // 2, 2),
                 dtype=torch.float32, device=device)
+    if not table.is_cuda:
+        raise ValueError("the rope table is made on the GPU")
     sc = RopeScaling(ROPE_KINDS.get(scaling, 0), 0, float(factor), float(original or 1.0),
                      float(low), float(high), float(amplitude))
     _b._check(_L().ttt_rope_table(table.data_ptr(), int(max_pos), int(rot_dim), float(base),

@@ -65,3 +65,9 @@ def test_attention_refuses_buffers_that_the_kernels_cannot_write(lib, kw):
     with pytest.raises(ValueError):
         attention(**kw)
     assert not lib.calls
+
+
+def test_rope_table_is_made_on_the_gpu(lib):
+    with pytest.raises(ValueError):
+        sv.rope_table(64, 32, device="cpu")
+    assert not lib.calls
