@@ -133,6 +133,8 @@ def _rows_of(t, what):
         raise ValueError(f"{what} must be [rows, heads, dim] or [B, T, heads, dim]")
     if vs != 1 and d > 1:
         raise ValueError(f"{what}: the values of a head must be contiguous")
+    if n >> 31:  # ctypes would cut it to 32 bits
+        raise ValueError(f"{what} has {n} rows; the library counts them in 32 bits")
     # the stride of an axis of length 1 means nothing: any aligned one will do
     return n, h, d, _pack_rows(t.data_ptr(), ts if n > 1 else h * d, hs if h > 1 else d, h, 0)
 
@@ -191,21 +193,24 @@ def rope_table(max_pos, rot_dim, base=10000.0, *, scaling=None, factor=1.0, orig
     "bands", with its factor and, for the last two, the trained context
     `original` and the turns low and high (high: 32 for "yarn", 4 for
     "bands"). amplitude: None is 1, for "yarn" 0.1 log(factor) + 1."""
+    max_pos, rot_dim = int(max_pos), int(rot_dim)
     if scaling is not None and scaling not in ROPE_KINDS:
         raise ValueError(f"scaling must be None or one of {sorted(ROPE_KINDS)}, got {scaling!r}")
+    if max(abs(max_pos), abs(rot_dim)) >> 31:  # ctypes would cut them to 32 bits
+        raise ValueError("max_pos and rot_dim must lie below 2^31")
     if scaling in ("yarn", "bands") and original is None:
         raise ValueError(f"{scaling!r} needs the trained context `original`")
     if amplitude is None:
         amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 0 else 1.0
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
-    table = _on(stream, torch.empty, (max(int(max_pos), 0), max(int(rot_dim), 0) // 2, 2),
+    table = _on(stream, torch.empty, (max(max_pos, 0), max(rot_dim, 0) // 2, 2),
                 dtype=torch.float32, device=device)
     if not table.is_cuda:
         raise ValueError("the rope table is made on the GPU")
     sc = RopeScaling(ROPE_KINDS.get(scaling, 0), 0, float(factor), float(original or 1.0),
                      float(low), float(high), float(amplitude))
-    _b._check(_L().ttt_rope_table(table.data_ptr(), int(max_pos), int(rot_dim), float(base),
+    _b._check(_L().ttt_rope_table(table.data_ptr(), max_pos, rot_dim, float(base),
                                   ctypes.byref(sc), _stream(stream, table)))
     return table
 

@@ -71,3 +71,28 @@ def test_rope_table_is_made_on_the_gpu(lib):
     with pytest.raises(ValueError):
         sv.rope_table(64, 32, device="cpu")
     assert not lib.calls
+
+
+MANY = 2 ** 32 + 1       # 1 in 32 bits
+
+
+@pytest.mark.parametrize("call", [
+    lambda x: sv.kv_append(gpu(3, 2, 16 * 68, dtype=U8), gpu(1, 1, dtype=I32), gpu(1, dtype=I32), x, x),
+    lambda x: sv.rope_forward(x, None, gpu(8, 16, 2, dtype=F32), positions=gpu(1, dtype=I32).expand(MANY), q_out=x),
+    lambda x: sv.kv_attention(x, gpu(3, 2, 16 * 68, dtype=U8), gpu(1, 1, dtype=I32), gpu(1, dtype=I32), out=x,
+                              max_new=1, workspace=gpu(512, dtype=U8)),
+    lambda x: sv.kv_read(gpu(3, 2, 16 * 68, dtype=U8), gpu(1, 1, dtype=I32), gpu(1, dtype=I32), MANY, 64, k_out=x,
+                         v_out=x),
+], ids=["append", "rope", "attention", "read"])
+def test_rows_past_32_bits_are_refused(lib, call):
+    """The library counts rows in 32 bits: 2^32 + 1 of them would be one."""
+    with pytest.raises(ValueError, match="rows"):
+        call(gpu(1, 2, 64).expand(MANY, 2, 64))
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("kw", [dict(max_pos=MANY, rot_dim=0), dict(max_pos=0, rot_dim=MANY)])
+def test_rope_tables_past_32_bits_are_refused(lib, kw):
+    with pytest.raises(ValueError, match="2\\^31"):
+        sv.rope_table(**kw, device="meta")
+    assert not lib.calls
