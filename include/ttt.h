@@ -577,6 +577,19 @@ ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_
                             int32_t act_dtype, const ttt_rows* q, const ttt_rows* o, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* How ttt_kv_attention would take such a call (for tuning and for tests; the
+ * arguments are those of the workspace's size). */
+typedef struct ttt_attn_plan {
+  int32_t many;          /* 1: the kernel for many rows, 0: the one for few */
+  int32_t tile;          /* rows of a key head that a workgroup takes at once */
+  int32_t parts;         /* a sequence's keys are cut into so many parts */
+  int32_t slices;        /* > 0: the keys of all sequences together instead */
+  int64_t workgroups;
+} ttt_attn_plan;
+ttt_status ttt_kv_attention_plan(const ttt_attn* attn, int32_t batch, int32_t tokens,
+                                 int32_t act_dtype, int32_t kv_heads, int32_t q_heads,
+                                 int32_t head_dim, ttt_attn_plan* plan);
+
 /* The name of a status code ("TTT_OK", "TTT_ERR_INVALID_ARG", ...; codes
  * outside ttt_status give "TTT_ERR_UNKNOWN"). The string is static. */
 const char* ttt_status_string(int32_t status);

@@ -47,6 +47,7 @@ from ._binding import (  # noqa: F401
 from ._serve import (  # noqa: F401
     kv_append,
     kv_attention,
+    kv_attention_plan,
     kv_attention_workspace_size,
     kv_page_bytes,
     kv_pages,
@@ -64,7 +65,7 @@ __all__ = ["layer_forward", "layer_forward_packed", "packed_workspace_size", "pa
            "train_workspace_size", "backward_saved_workspace_size",
            "rope_table", "rope_forward", "rope_backward",
            "kv_pages", "kv_page_bytes", "kv_append", "kv_read",
-           "kv_attention", "kv_attention_workspace_size",
+           "kv_attention", "kv_attention_workspace_size", "kv_attention_plan",
            "copy_calibration",
            "make_desc", "profile_enable", "profile_read", "TTTError", "lib",
            "LIB_PATH"]

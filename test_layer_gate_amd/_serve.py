@@ -51,6 +51,10 @@ class Attn(ctypes.Structure):
                 ("flags", _U), ("reserved", _U)]
 
 
+class AttnPlan(ctypes.Structure):
+    _fields_ = [("many", _I), ("tile", _I), ("parts", _I), ("slices", _I), ("workgroups", _I64)]
+
+
 # The same layouts, packed; bytes are passed where the library takes a pointer.
 _pack_rows = struct.Struct("PqqiI").pack
 _pack_rope = struct.Struct("PiiII").pack
@@ -75,9 +79,11 @@ def _L():
     L.ttt_kv_append.argtypes = [C, _I, _I, R, R, R, R, T, _P, _P]
     L.ttt_kv_read.argtypes = [C, _I, _I, R, R, _P]
     L.ttt_kv_attention_workspace_size.argtypes = [A, _I, _I, _I, _I, _I, _I, Z]
+    L.ttt_kv_attention_plan.argtypes = [A, _I, _I, _I, _I, _I, _I, ctypes.POINTER(AttnPlan)]
     L.ttt_kv_attention.argtypes = [C, A, _I, _I, R, R, _P, _P, ctypes.c_size_t, _P]
     for fn in ("rope_table", "rope_forward", "rope_backward", "kv_page_bytes", "kv_append",
-               "kv_read", "kv_attention_workspace_size", "kv_attention"):
+               "kv_read", "kv_attention_workspace_size", "kv_attention_plan",
+               "kv_attention"):
         getattr(L, "ttt_" + fn).restype = ctypes.c_int
     _lib = L
     return L
@@ -356,6 +362,18 @@ def kv_attention_workspace_size(batch, rows, kv_heads, q_heads, head_dim, dtype=
                                 max_new, max_kv, window=0) -> int:
     act = _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16
     return _workspace(batch, rows, act, kv_heads, q_heads, head_dim, max_new, max_kv, window)
+
+
+def kv_attention_plan(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bfloat16, *,
+                      max_new, max_kv, window=0) -> dict:
+    """How kv_attention takes such a call (ttt_kv_attention_plan): its kernel
+    (many: True or False), rows of a tile, parts of a sequence's keys or slices
+    of all, and workgroups."""
+    p = AttnPlan()
+    _b._check(_L().ttt_kv_attention_plan(
+        _pack_attn(1.0, window, max_new, max_kv, 0, 0), batch, rows,
+        _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16, kv_heads, q_heads, head_dim, _ref(p)))
+    return dict(many=bool(p.many), tile=p.tile, parts=p.parts, slices=p.slices, workgroups=p.workgroups)
 
 
 def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, max_kv=None,

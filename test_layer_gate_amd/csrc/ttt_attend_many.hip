@@ -434,14 +434,12 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(AttnLaunch
 }  // namespace
 
 hipError_t launch_attend_many(const AttnLaunch& a, hipStream_t s) {
-  const int group = a.q.heads / a.pool.heads;
-  const int64_t others = (int64_t)a.splits * a.pool.heads;
-  const int64_t tiles = tttk::row_tiles(a, group, kManyRows, others);
-  const dim3 grid((uint32_t)(tiles * others), a.pool.batch);
+  const AttnGrid g = attn_grid(a);
+  const dim3 grid((uint32_t)(g.groups / a.pool.batch), a.pool.batch);
   if (a.pool.dim == 64)
-    attend_many_kernel<64><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)tiles);
+    attend_many_kernel<64><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)g.tiles);
   else
-    attend_many_kernel<128><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)tiles);
+    attend_many_kernel<128><<<grid, 64 * kManyWaves, 0, s>>>(a, (int)g.tiles);
   return hipGetLastError();
 }
 

@@ -105,17 +105,6 @@ __device__ __forceinline__ uint32_t load4(Global p) {
   return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p);
 }
 
-// Tiles of `each` rows that a sequence is launched with: as max_new and the
-// rows there are at all allow; not above 2^20 workgroups, `others` a tile (a
-// workgroup then takes several tiles).
-inline int64_t row_tiles(const AttnLaunch& a, int group, int each, int64_t others) {
-  const int64_t news = a.max_new < a.pool.tokens ? a.max_new : a.pool.tokens;
-  int64_t tiles = (news * group + each - 1) / each;
-  const int64_t most = ((int64_t)1 << 20) / others;
-  if (tiles > most) tiles = most;
-  return tiles < 1 ? 1 : tiles;
-}
-
 // n workgroups, numbered along x and then y: a dimension of a launch holds
 // less than 2^32 threads. The last of y may have workgroups too many.
 inline dim3 grid_of(int64_t n) {

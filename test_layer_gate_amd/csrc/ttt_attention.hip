@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
   // Key heads vary fastest, then slices, or rows, sequences and at last splits:
   // workgroups go round the XCDs in this order, and a split that short
   // sequences do not have must not be one XCD's.
-  int id = (int)block_of_grid();
+  int id = (int)block_of_grid();  // kMostGroups keeps it in 32 bits
   const int hk = id % a.pool.heads;
   id /= a.pool.heads;
   const int group = a.q.heads / a.pool.heads;
@@ -642,6 +642,11 @@ struct Costs {
   }
 };
 
+// Workgroups that parts and tiles of rows may make of a launch (of a sequence's
+// tiles, in the many-row kernel). Beyond them there is one a sequence and key
+// head, so that their number fits the kernels' 32 bits (2^26 at most).
+constexpr int64_t kMostGroups = (int64_t)1 << 20;
+
 AttnPlan few_plan(int batch, int kv_heads, int64_t rows, int64_t keys, int tile, bool f32, int dim) {
   // A short sequence is one workgroup.
   if (keys <= kOneGroup) return {false, 1, kOneGroup, 0, tile};
@@ -668,7 +673,12 @@ AttnPlan few_plan(int batch, int kv_heads, int64_t rows, int64_t keys, int tile,
   const double fair = work / (batch > 1 ? 1024 : 512), least = work < 512 * 256 ? 128 : 512;
   const double most = 1 << 20, e = fair < least ? least : fair > most ? most : fair;
   const int each = ((int)e + 127) / 128 * 128;
-  return {false, (int)((keys + each - 1) / each), each, 0, tile};
+  // max_kv is a bound: with many sequences and heads, parts of what it allows
+  // for would be more workgroups than 32 bits count (and the chip is full
+  // without them). A part walks over all keys, whatever their number.
+  const int64_t parts = (keys + each - 1) / each, most_parts = kMostGroups / ((int64_t)kv_heads * batch);
+  if (most_parts <= 1) return {false, 1, (int)keys, 0, tile};
+  return {false, (int)(parts < most_parts ? parts : most_parts), each, 0, tile};
 }
 
 }  // namespace
@@ -701,15 +711,29 @@ AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv
              ? AttnPlan{true, (int)want, 0, 0, 0} : few;
 }
 
+// Tiles of rows as max_new and the rows there are at all allow, within
+// kMostGroups: a workgroup then takes several.
+AttnGrid attn_grid(const AttnLaunch& a) {
+  if (a.slices > 0) return {(int64_t)a.slices * a.pool.heads, 1};
+  const int64_t each = a.many ? kManyTile : a.tile, batch = a.pool.batch;
+  const int64_t news = a.max_new < a.pool.tokens ? a.max_new : a.pool.tokens;
+  const int64_t others = (int64_t)a.splits * a.pool.heads * (a.many ? 1 : batch);
+  int64_t tiles = (news * (a.q.heads / a.pool.heads) + each - 1) / each;
+  const int64_t most = kMostGroups / others;
+  if (tiles > most) tiles = most;
+  if (tiles < 1) tiles = 1;
+  return {tiles * others * (a.many ? batch : 1), tiles};
+}
+
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   if (a.many) return launch_attend_many(a, s);
   const int group = a.q.heads / a.pool.heads;
-  const int64_t others = (int64_t)a.splits * a.pool.heads * a.pool.batch;
-  const int64_t tiles = tttk::row_tiles(a, group, a.tile, others);
-  const dim3 grid = grid_of(a.slices > 0 ? (int64_t)a.slices * a.pool.heads : tiles * others);
+  const AttnGrid g = attn_grid(a);
+  const int64_t tiles = g.tiles;
+  const dim3 grid = grid_of(g.groups);
   const bool brief = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
   const bool alone = (int64_t)a.max_new * group <= a.tile;
-  const bool own = a.tile == 16 && !alone && a.splits == 1 && tiles * others >= kOwnTile;
+  const bool own = a.tile == 16 && !alone && a.splits == 1 && g.groups >= kOwnTile;
 #define TTT_CALL(D, T, F, RT)                                                          \
   constexpr Keys kBrief = F || RT > 1 ? kShared : kShort;                              \
   if (a.slices > 0)                                                                    \

@@ -479,6 +479,25 @@ ttt_status ttt_kv_attention_workspace_size(const ttt_attn* attn, int32_t batch, 
   TTT_ENTRY_END
 }
 
+ttt_status ttt_kv_attention_plan(const ttt_attn* attn, int32_t batch, int32_t tokens,
+                                 int32_t act_dtype, int32_t kv_heads, int32_t q_heads,
+                                 int32_t head_dim, ttt_attn_plan* plan) {
+  TTT_ENTRY_BEGIN
+  if (plan == nullptr) return fail(TTT_ERR_INVALID_ARG, "plan is NULL");
+  size_t bytes = 0;
+  TTT_TRY(ttt_kv_attention_workspace_size(attn, batch, tokens, act_dtype, kv_heads, q_heads, head_dim,
+                                          &bytes));
+  const tttk::AttnPlan p = tttk::attn_plan(batch, kv_heads, q_heads, attn->max_new, attn->max_kv,
+                                           attn->window, act_dtype == TTT_F32, head_dim);
+  tttk::AttnLaunch a = {};
+  a.pool.batch = batch, a.pool.heads = kv_heads, a.pool.tokens = tokens, a.q.heads = q_heads;
+  a.max_new = attn->max_new;
+  a.many = p.many, a.splits = p.splits, a.slices = p.slices, a.tile = p.tile;
+  *plan = {p.many, p.many ? tttk::kManyTile : p.tile, p.splits, p.slices, tttk::attn_grid(a).groups};
+  return TTT_OK;
+  TTT_ENTRY_END
+}
+
 ttt_status ttt_kv_attention(const ttt_cache* cache, const ttt_attn* attn, int32_t tokens,
                             int32_t act_dtype, const ttt_rows* q, const ttt_rows* o, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream) {
