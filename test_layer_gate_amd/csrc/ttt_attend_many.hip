@@ -167,12 +167,12 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(AttnLaunch
     const bool live = r < rows;
     const int t = min(r, rows - 1) / group;
     const int head = hk * group + min(r, rows - 1) % group;
-    const Span sp = span_of(a, seq.len, seq.news, t);
-    const Span tile_first = span_of(a, seq.len, seq.news, tile * kManyRows / group);
-    const Span tile_last = span_of(a, seq.len, seq.news, min(tile * kManyRows + kManyRows - 1, rows - 1) / group);
+    const Span sp = span_of(a, seq, t);
+    const Span tile_first = span_of(a, seq, tile * kManyRows / group);
+    const Span tile_last = span_of(a, seq, min(tile * kManyRows + kManyRows - 1, rows - 1) / group);
     const int w0 = min(tile * kManyRows + wave * 32, rows - 1), w1 = min(w0 + 31, rows - 1);
-    const Span first = span_of(a, seq.len, seq.news, w0 / group);
-    const Span last = span_of(a, seq.len, seq.news, w1 / group);
+    const Span first = span_of(a, seq, w0 / group);
+    const Span last = span_of(a, seq, w1 / group);
     const int lo = tile_first.lo & ~(kManyKeys - 1), hi = tile_last.hi;
     int each = (max(hi - lo, 0) + a.splits - 1) / a.splits;
     each = (each + kManyKeys - 1) & ~(kManyKeys - 1);

@@ -67,18 +67,6 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u;
 }
 
-// The keys that a sequence's new token t sees: [lo, hi).
-struct Span {
-  int lo, hi;
-};
-__device__ __forceinline__ Span span_of(const AttnLaunch& a, int len, int news, int t) {
-  const int p = len - news + t;
-  Span s;
-  s.hi = a.causal ? min(p + 1, len) : len;
-  s.lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
-  return s;
-}
-
 // A word at an address that is the same for the whole wave, of memory that
 // the kernel does not write: through the scalar cache, so that a page number
 // needed later is not waited for with the vector loads that are under way.
@@ -116,9 +104,10 @@ __device__ __forceinline__ int64_t block_of_grid() {
   return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
 }
 
-// Sequence b's rows, and its keys. UNIFORM: b is the same for the whole wave.
+// Sequence b's rows, its length, and how many of its keys the page table has
+// entries for. UNIFORM: b is the same for the whole wave.
 struct Seq {
-  int row0, news, len;
+  int row0, news, len, held;
 };
 template <bool UNIFORM>
 __device__ __forceinline__ Seq seq_at(const Pool& p, int b) {
@@ -129,17 +118,32 @@ __device__ __forceinline__ Seq seq_at(const Pool& p, int b) {
   Seq s;
   s.row0 = r0;
   s.news = r0 < 0 ? 0 : min(r1, p.tokens) - r0;
-  s.len = min(word(p.lens, b), p.max_pages * p.page);
+  s.len = max(word(p.lens, b), 0);
+  s.held = min(s.len, p.max_pages * p.page);
   return s;
 }
 __device__ __forceinline__ Seq seq_of(const Pool& p, int b) { return seq_at<true>(p, b); }
+
+// The keys that a sequence's new token t sees and that the table has entries
+// for: [lo, hi). The token stands where the length puts it, whatever the table
+// holds.
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span span_of(const AttnLaunch& a, const Seq& q, int t) {
+  const int p = q.len - q.news + t;
+  Span s;
+  s.hi = a.causal ? min(p + 1, q.held) : q.held;
+  s.lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+  return s;
+}
 
 // Units of keys that a sequence's first `tile` rows see; at least one, so that
 // rows that see nothing are written, and none without rows.
 __device__ __forceinline__ uint32_t units_of(const AttnLaunch& a, const Seq& s, int tile, int group, int unit) {
   if (s.news <= 0) return 0;
-  const Span first = span_of(a, s.len, s.news, 0);
-  const Span last = span_of(a, s.len, s.news, (min(tile, s.news * group) - 1) / group);
+  const Span first = span_of(a, s, 0);
+  const Span last = span_of(a, s, (min(tile, s.news * group) - 1) / group);
   return (uint32_t)(max(last.hi - (first.lo & ~31), 1) + unit - 1) / unit;
 }
 

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
 
   for (;;) {
     const Seq seq = seq_of(a.pool, b);
-    const int row0 = seq.row0, news = seq.news, len = seq.len;
+    const int row0 = seq.row0, news = seq.news;
     const int rows = max(news, 0) * group;
     if (tile * kRows >= rows) break;  // (of a slice's sequences, the first tile has rows)
     bool live[RT];
@@ -125,11 +125,11 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
       live[x] = r < rows;
       t[x] = min(r, rows - 1) / group;
       head[x] = hk * group + min(r, rows - 1) % group;
-      sp[x] = span_of(a, len, news, t[x]);
+      sp[x] = span_of(a, seq, t[x]);
     }
     // the tile's keys
-    const Span first = span_of(a, len, news, tile * kRows / group);
-    const Span last = span_of(a, len, news, min(tile * kRows + kRows - 1, rows - 1) / group);
+    const Span first = span_of(a, seq, tile * kRows / group);
+    const Span last = span_of(a, seq, min(tile * kRows + kRows - 1, rows - 1) / group);
     const int lo = first.lo & ~31, hi = last.hi;
     const int all_lo = last.lo, all_hi = first.hi;  // keys that every row sees
 

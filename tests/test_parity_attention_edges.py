@@ -1,0 +1,42 @@
+"""GPU parity of attention over the paged 4-bit cache where sequences, pages
+and launches end: the checks and tolerances of test_parity_attention."""
+import numpy as np
+import pytest
+import torch
+
+from test_parity_attention import check, host, ints, pool_of, ttt  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+SLICES = dict(max_new=1, max_kv=1 << 16)     # several sequences: cut into slices of all their keys
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kw", [dict(), dict(window=20), dict(causal=False)], ids=["causal", "window", "all"])
+def test_sequences_longer_than_their_page_table(ttt, dtype, dim, kw):
+    """Rows stand where kv_lens says, as they do for append; what the table
+    has no entry for is seen by none of them."""
+    rng = np.random.default_rng(21)
+    lens = [200, 70, 45, 51]
+    pages, table = pool_of(rng, lens, 16, 2, dim)
+    table = table[:, :3]      # 48 tokens each
+    for news in ([170, 30, 5, 6], [1, 1, 1, 1], [3, 23, 1, 4]):
+        check(ttt, dtype, 16, 2, 4, dim, news, lens, pages=pages, table=table, **kw)
+        check(ttt, dtype, 16, 2, 4, dim, news, lens, pages=pages, table=table, **kw, **SLICES)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lengths_at_the_ends_of_32_bits(ttt, dtype):
+    rng = np.random.default_rng(22)
+    pages, table = pool_of(rng, [48], 16, 2, 128)
+    p, t = torch.from_numpy(pages).cuda(), ints(table)
+    q = torch.from_numpy(rng.standard_normal((20, 4, 128))).to(dtype).cuda()
+    for kw in (dict(), dict(max_new=4096, max_kv=1 << 16), dict(max_new=200, max_kv=1 << 22)):
+        ref = ttt.kv_attention(q, p, t, ints([48]), causal=False, with_lse=True, **kw)
+        got = ttt.kv_attention(q, p, t, ints([2 ** 31 - 1]), with_lse=True, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got)) and torch.isfinite(got[1]).all()
+        for length, opt in ((2 ** 31 - 1, dict(window=9)), (-1, dict()), (-2 ** 31, dict()), (-2 ** 31, dict(window=9)),
+                            (-2 ** 31, dict(causal=False))):
+            o, lse = ttt.kv_attention(q, p, t, ints([length]), with_lse=True, **opt, **kw)
+            assert not o.any() and torch.isneginf(lse).all(), (length, opt, kw)
