@@ -548,8 +548,9 @@ ttt_status ttt_kv_read(const ttt_cache* cache, int32_t tokens, int32_t act_dtype
  * Query head h reads kv head h / (q heads / kv heads).
  *   o    softmax(scale q k^T) v, act_dtype
  *   lse  [tokens][q heads] fp32, or NULL: log of the sum of exponentials
- * A row that sees nothing gives o = 0 and lse = -inf. A NaN or infinity that a
- * row does not see does not reach it.
+ * A row that sees nothing gives o = 0 and lse = -inf. A NaN that a row does not
+ * see does not reach it. A row that sees a token with a NaN block of K is NaN in
+ * o and lse, one with a NaN block of V in the block's 32 values of o.
  *   max_new  an upper bound of the sequences' new tokens, and
  *   max_kv   of their kv_lens: they size the launch; wrong ones cost time,
  *            not results

@@ -35,13 +35,13 @@ namespace {
 constexpr int kManyWaves = 8, kManyRows = 32 * kManyWaves, kManyKeys = 64;
 static_assert(kManyRows == kManyTile, "rows a workgroup");
 
-// Which of a tile's keys have no page or are NaN, and which have a NaN value:
-// one bit a key, 32 keys a word.
+// Which of a tile's keys have no page or are NaN, and which have a NaN value in
+// any block of 32, and in which: one bit a key, 32 keys a word.
 struct KeyMarks {
   uint32_t absent[2], nan[2];
 };
 struct ValueMarks {
-  uint32_t nan[2];
+  uint32_t nan[2], of[4][2];
 };
 
 template <int D>
@@ -96,7 +96,9 @@ __device__ __forceinline__ void unpack(Raw<D>& r, bool is_v, int piece, uint8_t*
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (bad >> (8 * e + 7) & 1) {
-          atomicOr(&vmarks->nan[piece >> 1], 1u << (shift + 4 * q + e));
+          const uint32_t bit = 1u << (shift + 4 * q + e);
+          atomicOr(&vmarks->nan[piece >> 1], bit);
+          atomicOr(&vmarks->of[c >> 2][piece >> 1], bit);
           w[e] = 0;
           r.s = (r.s & ~(255u << (8 * e))) | (127u << (8 * e));
         }
@@ -258,13 +260,22 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(AttnLaunch
       bf16x8_t ring[RD];
 #pragma unroll
       for (int q = 0; q < RD; ++q) ring[q] = fragment(kat, q);
-      uint32_t poison = 0;  // keys that this row sees whose value is NaN
       if (odd) {
         rare_path();
         const int j = s0 + t * kManyKeys + 32 * u;
-        const uint32_t seen = (bits_between(sp.lo - j, sp.hi - j) & ~kmarks[t & 3].absent[u]) >> (4 * half);
+        const uint32_t all = bits_between(sp.lo - j, sp.hi - j) & ~kmarks[t & 3].absent[u];
+        const uint32_t seen = all >> (4 * half);
         const uint32_t nan = (kmarks[t & 3].nan[u] >> (4 * half)) & seen;
-        poison = (vmarks[t % 3].nan[u] >> (4 * half)) & seen;
+        // A NaN value is out of V, where it would reach every row: it enters
+        // the sums of the rows that see it. Register e is of block e D / 512.
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          if (vmarks[t % 3].of[c][u] & all) {
+#pragma unroll
+            for (int f = 0; f < NT; ++f)
+#pragma unroll
+              for (int e = c * 512 / D; e < (c + 1) * 512 / D; ++e) o[f][e] = __builtin_nanf("");
+          }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int k = 8 * (e >> 2) + (e & 3);
@@ -315,16 +326,6 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(AttnLaunch
         __builtin_amdgcn_sched_barrier(kFence);
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (odd) {
-        rare_path();
-        // A NaN value is out of V, where it would reach every row: it enters
-        // the weight of the rows that see it.
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = 8 * (e >> 1) + 2 * (e & 1);
-          pw[e] |= (spread(poison, k) & 0x7fc0u) | (spread(poison, k + 1) & 0x7fc00000u);
-        }
-      }
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i) {
         const int g = i / NT, f = i % NT;

@@ -283,33 +283,50 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
         // Keys that some row does not see, that have no page, or that hold NaN
         const uint32_t nan = nan_bytes(cur.ks[0]) | nan_bytes(cur.vs[0]) | nan_bytes(cur.ks[1]) | nan_bytes(cur.vs[1]);
         const bool odd = j < all_lo || j + 32 > all_hi || !cur.have[0] || !cur.have[1] || __any(nan != 0);
-        uint32_t poison[RT] = {};  // the rows' keys whose value is NaN
         if (odd) {
           rare_path();
+          const uint32_t there = (cur.have[0] ? 0xffffu : 0u) | (cur.have[1] ? 0xffff0000u : 0u);
+          uint32_t seen[RT];
+#pragma unroll
+          for (int x = 0; x < RT; ++x) seen[x] = bits_between(sp[x].lo - j, sp[x].hi - j) & there;
+          uint32_t nan_v[NP] = {};  // keys that are NaN in the blocks of V whose sums the lane holds
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            uint64_t kn = __ballot(ks[u][0] > kScaleMax);
+            uint64_t kn = __ballot(ks[u][0] > kScaleMax || ks[u][NP - 1] > kScaleMax);
             kn |= kn >> 32;
             const uint32_t kn32 = (uint32_t)kn | (uint32_t)kn >> 16;
-            const int k = j + 16 * u + 4 * g;  // this lane's four keys
-            const uint32_t bad = cur.have[u] ? nan_bytes(cur.vs[u]) : 0x80808080u;
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
-              const uint32_t seen = cur.have[u] ? bits_between(sp[x].lo - k, sp[x].hi - k) : 0u;
+              const uint32_t mine = seen[x] >> (16 * u + 4 * g);  // of this lane's four keys
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t keep = spread(seen, e);
+                const uint32_t keep = spread(mine, e);
                 float& w = p[x][4 * u + e];
                 w = __uint_as_float((__float_as_uint(w) & keep) | (kNoneBits & ~keep) |
                                     (spread(kn32 >> (4 * g), e) & keep & kNanBits));
-                poison[x] |= (keep & spread(bad, 8 * e + 7) & 1u) << (4 * u + e);
               }
             }
             // A NaN value must not reach the rows that do not see it (0 * NaN):
-            // it goes out of V, and into the weight of those that do.
+            // it goes out of V, and into the sums of those that do. Lane (i, g)
+            // has the scales of block i D / 512 of V, and sums of block g D /
+            // 128 (of 256: and the next).
+            const uint32_t bad = cur.have[u] ? nan_bytes(cur.vs[u]) : 0u;
+            if (__any(bad != 0)) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint64_t all = __ballot(bad >> (8 * e + 7) & 1);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                  const uint64_t at = all >> ((g * D / 128 + q) * (512 / D));
+                  const uint32_t a0 = (uint32_t)at, a1 = (uint32_t)(at >> 32);
+                  nan_v[q] |= ((a0 & 1) | (a0 >> 16 & 1) << 4 | (a1 & 1) << 8 | (a1 >> 16 & 1) << 12) << (16 * u + e);
+                }
+              }
+            }
+            const uint32_t out = cur.have[u] ? bad : 0x80808080u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t gone_v = spread(bad, 8 * e + 7);
+              const uint32_t gone_v = spread(out, 8 * e + 7);
               cur.vs[u] = (cur.vs[u] & ~(gone_v & 255u << (8 * e))) | (gone_v & 127u << (8 * e));
 #pragma unroll
               for (int q = 0; q < NP; ++q) {
@@ -319,6 +336,14 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
               }
             }
           }
+#pragma unroll
+          for (int x = 0; x < RT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (nan_v[NP * e / 4] & seen[x]) {
+#pragma unroll
+                for (int f = 0; f < F; ++f) o[x][f][e] = __builtin_nanf("");
+              }
         }
         // The maximum is only followed when a weight would pass 2^8: until
         // then the lanes need not agree on a new one, and nothing is rescaled.
@@ -352,12 +377,6 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(fmaf(w[e], sc, -ms[x]));
           l[x] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-          if (__any(poison[x] != 0)) {
-            rare_path();
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[e] = __uint_as_float(__float_as_uint(w[e]) | (spread(poison[x], e) & kNanBits));
-          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t z[TP];

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.serve_oracle as so
 from test_parity_attention import check, host, ints, pool_of, ttt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +41,38 @@ def test_lengths_at_the_ends_of_32_bits(ttt, dtype):
                             (-2 ** 31, dict(causal=False))):
             o, lse = ttt.kv_attention(q, p, t, ints([length]), with_lse=True, **opt, **kw)
             assert not o.any() and torch.isneginf(lse).all(), (length, opt, kw)
+
+
+def spoil(pages, table, page, dim, part, where):
+    """NaN scales at (token, key head, block): only there."""
+    pages = pages.copy()
+    for n, (j, h, c) in enumerate(where):
+        at = so.page_offsets(page, dim, j % page)[2 if part == "k" else 3][c]
+        pages[table[0, j // page], h, at] = 253 + n % 3
+    return pages
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [1, 30, 200])
+def test_nan_scales_of_single_blocks(ttt, dtype, dim, news):
+    """A scale above 252 is its block's: of K the rows that see it are NaN, of
+    V those values of theirs, whichever kernel takes them."""
+    length, page = 200, 16
+    pages, table = pool_of(np.random.default_rng(23), [length], page, 2, dim)
+    first = max(length - news, 0)
+    q = torch.from_numpy(1.5 * np.random.default_rng(24).standard_normal((news, 8, dim))).to(dtype).cuda()
+    for part in ("k", "v"):
+        for c in range(dim // 32):
+            where = [(first + news // 2, 0, c), (3, 1, c), (length - 1, 1, (c + 1) % (dim // 32))]
+            bad = spoil(pages, table, page, dim, part, where)
+            o = check(ttt, dtype, page, 2, 8, dim, [news], [length], q=q, pages=bad, table=table)
+            _, lse = ttt.kv_attention(q, torch.from_numpy(bad).cuda(), ints(table), ints([length]), with_lse=True)
+            nan = np.isnan(o)
+            if part == "k":      # whole rows
+                assert (nan.any(-1) == nan.all(-1)).all() and np.array_equal(np.isnan(host(lse)), nan.any(-1))
+            else:                # the block of every row from there on, of the head's four
+                want = np.zeros_like(nan)
+                for j, h, b in where:
+                    want[max(0, j - first):, 4 * h:4 * h + 4, 32 * b:32 * b + 32] = True
+                assert np.array_equal(nan, want) and torch.isfinite(lse).all()
