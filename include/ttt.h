@@ -552,16 +552,16 @@ ttt_status ttt_kv_read(const ttt_cache* cache, int32_t tokens, int32_t act_dtype
  * see does not reach it. A row that sees a token with a NaN block of K is NaN in
  * o and lse, one with a NaN block of V in the block's 32 values of o.
  *   max_new  an upper bound of the sequences' new tokens, and
- *   max_kv   of their kv_lens: they size the launch; wrong ones cost time,
- *            not results
+ *   max_kv   of their kv_lens: they size the launch, and max_new decides on the
+ *            weights' terms below; otherwise wrong ones cost time, not results
  *   workspace  ttt_kv_attention_workspace_size() bytes, 256-byte aligned (may
  *            be NULL where that is 0)
  * Arithmetic: products of bf16 operands accumulated in fp32 (the cache's
- * values are exact in bf16). For bf16 rows the weights are rounded to bf16
- * before they meet the values (up to 16 rows of up to 1024 keys: two bf16
- * terms); for fp32 rows queries and weights enter as
- * three bf16 terms each (24 bits). Maxima, sums and joins are fp32, in a fixed
- * order. */
+ * values are exact in bf16). For bf16 rows the weights enter the second product
+ * as two bf16 terms (16 bits) where max_new allows for up to 16 rows a key head
+ * (max_new * q heads / kv heads), else rounded to one; for fp32 rows queries and
+ * weights enter as three bf16 terms each (24 bits). Maxima, sums and joins are
+ * fp32, in a fixed order. */
 enum { TTT_ATTN_ALL_KEYS = 1u << 0 };
 typedef struct ttt_attn {
   float scale;

@@ -384,7 +384,8 @@ def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, 
     how many keys (its own included) a row sees. causal=False: every key of
     the sequence. scale: None is dim ** -0.5. max_new, max_kv: upper bounds of
     the sequences' rows and lengths, where the caller knows better ones than
-    `rows` and what the page table can hold. Returns o, or (o, lse) with
+    `rows` and what the page table can hold; up to 16 rows a key head, which
+    max_new tells, keep 16 bits of bf16 rows' weights, more rows 8. Returns o, or (o, lse) with
     with_lse (lse float32 [rows, q_heads])."""
     n, heads, dim, rq = _rows_of(q, "q")
     act = _act(q, "q")

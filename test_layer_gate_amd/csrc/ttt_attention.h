@@ -22,6 +22,11 @@ __device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// c + a0 b0 + a1 b1 of pairs of bf16.
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, a), __builtin_bit_cast(bf16x2_t, b), c, false);
+}
+
 struct U4 {
   uint32_t v[4];
 };
@@ -40,6 +45,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&w)[T]) {
     y -= __uint_as_float(w[t - 1] & 0xffff0000u);
     w[t] = pack_bf16(x, y);
   }
+}
+
+// The value of lane i + 8 of the same 16 (a rotation, row_ror:8).
+__device__ __forceinline__ float eight_lanes_on(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xf, 0xf, true));
 }
 
 // Bits [a, b) of a word.

@@ -8,8 +8,9 @@
 //
 // Codes times their power-of-two scale are exact in bf16, so keys and values
 // enter the matrix instructions without a rounding; what is rounded is the
-// weights p (to bf16), and, for fp32 rows, nothing: q and p are then three
-// bf16 terms each. Everything accumulates in fp32. (The scaled matrix
+// weights p (to two bf16 terms where a sequence has up to 16 rows a key head,
+// to one where it has more), and, for fp32 rows, nothing: q and p are then
+// three bf16 terms each. Everything accumulates in fp32. (The scaled matrix
 // instructions would take keys as codes against 8-bit terms of q, in the same
 // time and without decoding; they keep about 17 bits of a sum of 8 products,
 // which left scores and lse off by 1e-4, and were not taken.)
@@ -24,7 +25,7 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Few rows. A wave takes 16 rows (query heads of one key head, times tokens),
-// or 32 that share the decoded keys, and a stretch of the keys, 32 at a time,
+// or 8, each twice, or 32 that share the decoded keys, and a stretch of the keys, 32 at a time,
 // the next 32 on their way meanwhile. S^T = K Q^T with 16x16x32: lane (i, g) =
 // (lane % 16, lane / 16) brings D / 4 neighbouring values of key i; of the
 // result it holds, for row i, keys 4g .. 4g + 3 of either 16. Those eight are
@@ -62,20 +63,27 @@ struct FewTile {
   bool have[2];
 };
 
-template <int D, int T, bool F32, int RT, Keys KEYS, int NW = 4>
-__global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_few_kernel(
+template <int D, int T, bool F32, int ROWS, Keys KEYS, int NW = 4>
+__global__ __launch_bounds__(64 * NW, D == 64 && ROWS <= 16 ? 4 : 2) void attend_few_kernel(
     AttnLaunch a, int row_tiles) {
   constexpr bool SLICED = KEYS == kSliced, kOnce = D < 256 && (KEYS == kAlone || KEYS == kSliced);
   constexpr int NP = D == 256 ? 2 : 1;  // 16-byte pieces a lane takes of a key
   constexpr int KS = D / 32;            // steps of the first product
   constexpr int F = D / 16;             // V fragments = values per lane
-  constexpr int kRows = 16 * RT;        // of a tile
-  // Terms of the weights. For bf16 rows one term's error is about that of
-  // rounding the output (0.0013 rms beside 0.0016), and more where one key has
-  // nearly all of the weight, which the few rows of a short call do not average
-  // out: those take two terms (0.7 us of 10). In long sequences a second
-  // costs 8 to 13%.
-  constexpr int TP = F32 ? 3 : KEYS == kShort ? 2 : 1;
+  constexpr int kRows = ROWS;           // of a tile
+  constexpr int RT = ROWS == 32 ? 2 : 1;
+  constexpr bool kPairs = ROWS == 8;
+  // Terms of the weights of bf16 rows. One term is off by about what rounding
+  // the output costs (0.0013 rms beside 0.0016), and by more where one key has
+  // nearly all of the weight, which few rows do not average out (one token over
+  // 777 keys 0.0021 to 0.0027 against 64 bits). Up to 8 rows fill half of the
+  // matrix instructions' columns: row i's second terms are column i + 8, at the
+  // cost of the split alone (0.0016 in all; 32 sequences of 4k to 32k keys, 32/8
+  // heads of 128, 97.9 us for 95.9 with one term, of 64 72.7 for 69.9). Up to 16
+  // rows get them by a second product (32/2 heads 39.2 us for 38.0). More rows
+  // have one term: there the matrix unit is what the call waits for. The choice
+  // is by max_new alone, so that a bound of the lengths changes no result.
+  constexpr int TP = F32 ? 3 : kPairs || ROWS == 32 || KEYS == kShared ? 1 : 2;
   // Three terms of the rows' queries would be the registers of a second wave:
   // the waves, whose rows are the same, read them from LDS.
   constexpr bool kShareQ = T > 1;
@@ -89,6 +97,9 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
+  const int i_row = kPairs ? i16 & 7 : i16;
+  const bool first_term = !kPairs || i16 < 8;
+  const uint32_t less = first_term ? 0u : 0xbf80u;  // -1 in bf16: a second term lacks the first
   // Key heads vary fastest, then slices, or rows, sequences and at last splits:
   // workgroups go round the XCDs in this order, and a split that short
   // sequences do not have must not be one XCD's.
@@ -121,8 +132,8 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
     Span sp[RT];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
-      const int r = tile * kRows + 16 * x + i16;
-      live[x] = r < rows;
+      const int r = tile * kRows + 16 * x + i_row;
+      live[x] = first_term && r < rows;
       t[x] = min(r, rows - 1) / group;
       head[x] = hk * group + min(r, rows - 1) % group;
       sp[x] = span_of(a, seq, t[x]);
@@ -379,6 +390,11 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
           l[x] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            if constexpr (kPairs) {
+              const uint32_t z = pack_bf16(w[2 * e], w[2 * e + 1]);
+              pw[x][0][e] = pack_bf16(dot2(z, less, w[2 * e]), dot2(z, less << 16, w[2 * e + 1]));
+              continue;
+            }
             uint32_t z[TP];
             split2<TP>(w[2 * e], w[2 * e + 1], z);
 #pragma unroll
@@ -423,36 +439,42 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
       l[x] += __shfl_xor(l[x], 16);
       l[x] += __shfl_xor(l[x], 32);
       m[x] = m[x] == kNone ? kNone : ms[x];
+      if constexpr (kPairs) {  // both terms' sums
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[x][f][e] += eight_lanes_on(o[x][f][e]);
+      }
     }
 
     // Join the waves: all to the common maximum, then added in their order.
     __syncthreads();  // the last tile's readers are done
 #pragma unroll
     for (int x = 0; x < RT; ++x)
-      if (g == 0) red_ml[wave][16 * x + i16][0] = m[x], red_ml[wave][16 * x + i16][1] = l[x];
+      if (g == 0 && first_term) red_ml[wave][16 * x + i_row][0] = m[x], red_ml[wave][16 * x + i_row][1] = l[x];
     __syncthreads();
     float mj[RT], lj[RT];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       mj[x] = kNone, lj[x] = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) mj[x] = fmaxf(mj[x], red_ml[w][16 * x + i16][0]);
+      for (int w = 0; w < NW; ++w) mj[x] = fmaxf(mj[x], red_ml[w][16 * x + i_row][0]);
       const float mj0 = mj[x] == kNone ? 0.f : mj[x];
 #pragma unroll
       for (int w = 0; w < NW; ++w)
-        lj[x] += red_ml[w][16 * x + i16][1] * __builtin_amdgcn_exp2f(red_ml[w][16 * x + i16][0] - mj0);
+        lj[x] += red_ml[w][16 * x + i_row][1] * __builtin_amdgcn_exp2f(red_ml[w][16 * x + i_row][0] - mj0);
       const float al = __builtin_amdgcn_exp2f(m[x] - mj0);
 #pragma unroll
       for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[x][f][e] *= al;
       // lane (i, g), o[f][e]: row i, value F (4g + e) + f
-      if (wave > 0) {
+      if (wave > 0 && first_term) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int f = 0; f < F; f += 4)
-            *reinterpret_cast<float4*>(&red_o[wave - 1][16 * x + i16][F * (4 * g + e) + f]) =
+            *reinterpret_cast<float4*>(&red_o[wave - 1][16 * x + i_row][F * (4 * g + e) + f]) =
                 make_float4(o[x][f][e], o[x][f + 1][e], o[x][f + 2][e], o[x][f + 3][e]);
       }
     }
@@ -465,11 +487,11 @@ __global__ __launch_bounds__(64 * NW, D == 64 && RT == 1 ? 4 : 2) void attend_fe
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int f = 0; f < F; ++f) o[x][f][e] += red_o[w][16 * x + i16][F * (4 * g + e) + f];
+          for (int f = 0; f < F; ++f) o[x][f][e] += red_o[w][16 * x + i_row][F * (4 * g + e) + f];
       const int64_t row = (int64_t)(row0 + t[x]) * a.q.heads + head[x];
       if (sliced ? u0 > 0 || u1 < line.n : a.splits > 1) {
         // slice + sequence: no two pairs that meet have the same sum
-        const int part = (((int)(line.at / line.per) + b) * a.pool.heads + hk) * kRows + 16 * x + i16;
+        const int part = (((int)(line.at / line.per) + b) * a.pool.heads + hk) * kRows + 16 * x + i_row;
         const int64_t at = sliced ? (int64_t)part : (int64_t)split * a.pool.tokens * a.q.heads + row;
         if (sliced && u0 == 0 && g == 0)
           *reinterpret_cast<int2*>(a.part_of + 2 * row) =
@@ -711,7 +733,7 @@ AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv
     const int64_t near = (int64_t)window + (tile + group - 1) / group;
     return window > 0 && near < all ? near : all;
   };
-  const int tile = !f32 && dim <= 128 && rows > 16 ? 32 : 16;
+  const int tile = f32 ? 16 : rows <= 8 ? 8 : dim <= 128 && rows > 16 ? 32 : 16;
   const AttnPlan few = few_plan(batch, kv_heads, rows, span(tile), tile, f32, dim);
   if (f32 || dim > 128 || rows <= 32) return few;
   // Parts until there is a workgroup for every CU, of 512 keys at least: 1024
@@ -744,39 +766,61 @@ AttnGrid attn_grid(const AttnLaunch& a) {
   return {tiles * others * (a.many ? batch : 1), tiles};
 }
 
+namespace {
+
+template <int D, bool F32, int ROWS>
+void launch_few(const AttnLaunch& a, hipStream_t s) {
+  constexpr int T = F32 ? 3 : 1;
+  const AttnGrid g = attn_grid(a);
+  const dim3 grid = grid_of(g.groups);
+  const int tiles = (int)g.tiles;
+  const bool alone = (int64_t)a.max_new * (a.q.heads / a.pool.heads) <= ROWS;
+  if (a.slices > 0) {
+    attend_few_kernel<D, T, F32, ROWS, kSliced><<<grid, 256, 0, s>>>(a, 1);
+    return;
+  }
+  // bf16 rows in tiles that more rows would not fit are alone.
+  if constexpr (F32 || (D == 256 && ROWS == 16) || ROWS == 32) {
+    if (!alone) {
+      if constexpr (kOwn<D, F32> && ROWS == 16) {
+        if (a.splits == 1 && g.groups >= kOwnTile) {
+          attend_few_kernel<D, T, F32, ROWS, kShared, 1><<<grid, 64, 0, s>>>(a, tiles);
+          return;
+        }
+      }
+      attend_few_kernel<D, T, F32, ROWS, kShared><<<grid, 256, 0, s>>>(a, tiles);
+      return;
+    }
+  }
+  // (of the others' a short launch is no different)
+  constexpr Keys kBrief = !F32 && ROWS == 16 ? kShort : kShared;
+  if (a.splits == 1 && a.each <= kOneGroup)
+    attend_few_kernel<D, T, F32, ROWS, kBrief><<<grid, 256, 0, s>>>(a, tiles);
+  else
+    attend_few_kernel<D, T, F32, ROWS, kAlone><<<grid, 256, 0, s>>>(a, tiles);
+}
+
+template <int D>
+void launch_few(const AttnLaunch& a, hipStream_t s) {
+  if (a.f32)
+    launch_few<D, true, 16>(a, s);
+  else if (a.tile == 8)
+    launch_few<D, false, 8>(a, s);
+  else if (a.tile == 16)
+    launch_few<D, false, 16>(a, s);
+  else if constexpr (D < 256)
+    launch_few<D, false, 32>(a, s);
+}
+
+}  // namespace
+
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s) {
   if (a.many) return launch_attend_many(a, s);
-  const int group = a.q.heads / a.pool.heads;
-  const AttnGrid g = attn_grid(a);
-  const int64_t tiles = g.tiles;
-  const dim3 grid = grid_of(g.groups);
-  const bool brief = a.slices == 0 && a.splits == 1 && a.each <= kOneGroup;
-  const bool alone = (int64_t)a.max_new * group <= a.tile;
-  const bool own = a.tile == 16 && !alone && a.splits == 1 && g.groups >= kOwnTile;
-#define TTT_CALL(D, T, F, RT)                                                          \
-  constexpr Keys kBrief = F || RT > 1 ? kShared : kShort;                              \
-  if (a.slices > 0)                                                                    \
-    attend_few_kernel<D, T, F, RT, kSliced><<<grid, 256, 0, s>>>(a, 1);                \
-  else if (own && kOwn<D, F>)                                                          \
-    attend_few_kernel<D, T, F, RT, kShared, kOwn<D, F> ? 1 : 4>                        \
-        <<<grid, 64, 0, s>>>(a, (int)tiles);                                           \
-  else if (!alone)                                                                     \
-    attend_few_kernel<D, T, F, RT, kShared><<<grid, 256, 0, s>>>(a, (int)tiles);       \
-  else if (brief)                                                                      \
-    attend_few_kernel<D, T, F, RT, kBrief><<<grid, 256, 0, s>>>(a, (int)tiles);        \
-  else                                                                                 \
-    attend_few_kernel<D, T, F, RT, kAlone><<<grid, 256, 0, s>>>(a, (int)tiles)
-  const bool two = a.tile == 32;
   switch (a.pool.dim) {
-    case 64:
-      if (a.f32) { TTT_CALL(64, 3, true, 1); } else if (two) { TTT_CALL(64, 1, false, 2); } else { TTT_CALL(64, 1, false, 1); }
-      break;
-    case 128:
-      if (a.f32) { TTT_CALL(128, 3, true, 1); } else if (two) { TTT_CALL(128, 1, false, 2); } else { TTT_CALL(128, 1, false, 1); }
-      break;
-    default: if (a.f32) { TTT_CALL(256, 3, true, 1); } else { TTT_CALL(256, 1, false, 1); } break;
+    case 64: launch_few<64>(a, s); break;
+    case 128: launch_few<128>(a, s); break;
+    default: launch_few<256>(a, s); break;
   }
-#undef TTT_CALL
   return hipGetLastError();
 }
 

@@ -76,3 +76,28 @@ def test_nan_scales_of_single_blocks(ttt, dtype, dim, news):
                 for j, h, b in where:
                     want[max(0, j - first):, 4 * h:4 * h + 4, 32 * b:32 * b + 32] = True
                 assert np.array_equal(nan, want) and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hk,hq,new", [(1, 1, 1), (2, 8, 1), (1, 4, 2), (1, 9, 1), (2, 10, 3), (1, 16, 1)])
+@pytest.mark.parametrize("lens", [[777], [1024], [1025], [60, 300, 1500]])
+def test_up_to_16_rows_keep_16_bits_of_the_weights(ttt, dim, hk, hq, new, lens):
+    """Under any max_kv. Two bf16 terms leave 2^-16 of a weight; the rest is the
+    tolerance of test_parity_attention, without one term's 2^-8."""
+    rng = np.random.default_rng(25)
+    page, scale = 64, dim ** -0.5
+    pages, table = pool_of(rng, lens, page, hk, dim)
+    q = torch.from_numpy(1.5 * rng.standard_normal((new * len(lens), hq, dim))).to(BF).cuda()
+    refs = []
+    for b, n in enumerate(lens):
+        k, v, have = so.gather(pages, table, b, n, dim)
+        qh = host(q[b * new:(b + 1) * new])
+        ref, _, w = so.attend(qh, k, v, have, n, scale)
+        terms = scale * np.einsum("thd,jhd->thj", np.abs(qh), np.abs(k).repeat(hq // hk, 1)).max(-1)
+        rel = 4 * np.sqrt(dim) * 2 ** -24 * terms + 2 ** -21 + 4 * np.sqrt(n) * 2 ** -24 + 2 ** -16
+        refs.append((ref, rel[..., None] * w + 2 ** -8 * np.abs(ref)))
+    ref, tol = (np.concatenate(x) for x in zip(*refs))
+    for max_kv in (max(lens), 1024, 1025, 1 << 17):
+        o = ttt.kv_attention(q, torch.from_numpy(pages).cuda(), ints(table), ints(lens), max_kv=max_kv)
+        err = np.abs(host(o) - ref)
+        assert (err <= tol).all(), (max_kv, float((err / tol).max()), int((err > tol).sum()))
