@@ -101,3 +101,26 @@ def test_up_to_16_rows_keep_16_bits_of_the_weights(ttt, dim, hk, hq, new, lens):
         o = ttt.kv_attention(q, torch.from_numpy(pages).cuda(), ints(table), ints(lens), max_kv=max_kv)
         err = np.abs(host(o) - ref)
         assert (err <= tol).all(), (max_kv, float((err / tol).max()), int((err > tol).sum()))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page,new,length,kw", [
+    (16, 200, 9000, dict()), (48, 131, 9001, dict(window=5000)), (16, 70, 13000, dict(window=8500)),
+    (112, 130, 8500, dict(causal=False)), (64, 300, 700, dict(window=65))])
+def test_many_rows_in_parts(ttt, dim, page, new, length, kw):
+    """The many-row kernel with each sequence's keys in two parts: of more than
+    the 64 tiles whose pages it looks up at once, of fewer, and of windows that
+    begin within a tile; rows for more than one wave."""
+    kw = dict(kw, max_new=1 << 14, max_kv=1 << 16)
+    plan = ttt.kv_attention_plan(1, new, 1, 2, dim, max_new=1 << 14, max_kv=1 << 16, window=kw.get("window", 0))
+    assert plan["many"] and (plan["parts"] == 2 or kw.get("window") == 65), plan
+    check(ttt, BF, page, 1, 2, dim, [new], [length], seed=length, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_rows_whole_and_ragged(ttt, dim):
+    """The same kernel over one part, several sequences and key heads."""
+    plan = ttt.kv_attention_plan(3, 340, 2, 8, dim, max_new=1 << 14, max_kv=1 << 16)
+    assert plan["many"] and plan["parts"] == 1, plan
+    for kw in (dict(), dict(window=100), dict(causal=False)):
+        check(ttt, BF, 48, 2, 8, dim, [150, 1, 189], [4700, 300, 189], seed=31, max_new=1 << 14, max_kv=1 << 16, **kw)
