@@ -585,6 +585,8 @@ typedef struct ttt_attn_plan {
   int32_t tile;          /* rows of a key head that a workgroup takes at once */
   int32_t parts;         /* a sequence's keys are cut into so many parts */
   int32_t slices;        /* > 0: the keys of all sequences together instead */
+  int32_t waves;         /* of a workgroup: where few rows are taken, 1: each has a tile */
+  int32_t reserved;
   int64_t workgroups;
 } ttt_attn_plan;
 ttt_status ttt_kv_attention_plan(const ttt_attn* attn, int32_t batch, int32_t tokens,

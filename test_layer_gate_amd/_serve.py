@@ -52,7 +52,8 @@ class Attn(ctypes.Structure):
 
 
 class AttnPlan(ctypes.Structure):
-    _fields_ = [("many", _I), ("tile", _I), ("parts", _I), ("slices", _I), ("workgroups", _I64)]
+    _fields_ = [("many", _I), ("tile", _I), ("parts", _I), ("slices", _I), ("waves", _I),
+                ("reserved", _I), ("workgroups", _I64)]
 
 
 # The same layouts, packed; bytes are passed where the library takes a pointer.
@@ -368,12 +369,13 @@ def kv_attention_plan(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bflo
                       max_new, max_kv, window=0) -> dict:
     """How kv_attention takes such a call (ttt_kv_attention_plan): its kernel
     (many: True or False), rows of a tile, parts of a sequence's keys or slices
-    of all, and workgroups."""
+    of all, workgroups and their waves."""
     p = AttnPlan()
     _b._check(_L().ttt_kv_attention_plan(
         _pack_attn(1.0, window, max_new, max_kv, 0, 0), batch, rows,
         _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16, kv_heads, q_heads, head_dim, _ref(p)))
-    return dict(many=bool(p.many), tile=p.tile, parts=p.parts, slices=p.slices, workgroups=p.workgroups)
+    return dict(many=bool(p.many), tile=p.tile, parts=p.parts, slices=p.slices, waves=p.waves,
+                workgroups=p.workgroups)
 
 
 def kv_attention(q, pages, page_table, kv_lens, *, q_starts=None, max_new=None, max_kv=None,

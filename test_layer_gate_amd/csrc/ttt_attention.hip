@@ -642,14 +642,20 @@ namespace {
 constexpr int kOneGroup = 1024;
 
 // Tiles of rows from which on every wave takes one of its own, all of its keys,
-// and none are joined: four waves a SIMD. fp32 prompts of 4 x 1738 tokens, 64/8
-// heads of 128, 696 us with four waves a tile and 620 so; of 6 x 603, 64/8 heads
-// of 64, 95 / 71; bf16 of 2 x 1976, 128/8 heads of 256, 519 / 399; fp32 rows that
-// see 6 keys (6 x 1234, 40/8 heads of 256) 179 / 97. With 2048 tiles it loses:
-// fp32 of 2048 tokens, 16/4 heads of 64, 47 / 65.
+// and none are joined, instead of sharing its keys with three others: fp32 rows,
+// and bf16 rows with heads of 256 (the others' many tiles are the many-row
+// kernel's). us, four waves a tile / one, causal prompts, sequences x tokens:
+//   fp32, 64/8 heads of 128, 4 x 1738 650 / 573; 32/8, 4 x 512 53 / 49, 1 x 8k 1447 / 1403
+//   fp32, 64/8 heads of 64, 6 x 603 124 / 98; 32/8, 4 x 1k 94 / 88, 2 x 2k 151 / 170
+//   bf16, 128/8 heads of 256, 2 x 1976 1091 / 887; 32/8, 4 x 512 77 / 51, 1 x 8k 1832 / 1737
+//   fp32, 32/8 heads of 256, 4 x 512 106 / 91, 4 x 1k 288 / 263, 2 x 2k 436 / 445,
+//   1 x 8k 2830 / 3145; 128/8, 1k tokens after 15k 5273 / 6612; 64/8, 2k tokens under
+//   a window of 64 160 / 109
+// With 2048 tiles it is even (fp32, 2048 tokens, 16/4 heads of 64: 46 / 45). fp32
+// queries of 256 take 24 KB of LDS, which leaves such waves 1.5 a SIMD: theirs
+// is for up to kOneGroup keys alone. (Of 64, 4 waves a SIMD, of 128, 3; bf16 of
+// 256, 2.)
 constexpr int kOwnTile = 4096;
-template <int D, bool F32>
-constexpr bool kOwn = F32 || D == 256;  // the others' many tiles are the many-row kernel's
 
 // Whether the many-row kernel is taken, for bf16 rows with heads of 64 or 128:
 // by what either kernel takes, in us, of heads of 128 (of 64 both take 3/4).
@@ -755,7 +761,7 @@ AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv
 // Tiles of rows as max_new and the rows there are at all allow, within
 // kMostGroups: a workgroup then takes several.
 AttnGrid attn_grid(const AttnLaunch& a) {
-  if (a.slices > 0) return {(int64_t)a.slices * a.pool.heads, 1};
+  if (a.slices > 0) return {(int64_t)a.slices * a.pool.heads, 1, 4};
   const int64_t each = a.many ? kManyTile : a.tile, batch = a.pool.batch;
   const int64_t news = a.max_new < a.pool.tokens ? a.max_new : a.pool.tokens;
   const int64_t others = (int64_t)a.splits * a.pool.heads * (a.many ? 1 : batch);
@@ -763,7 +769,12 @@ AttnGrid attn_grid(const AttnLaunch& a) {
   const int64_t most = kMostGroups / others;
   if (tiles > most) tiles = most;
   if (tiles < 1) tiles = 1;
-  return {tiles * others * (a.many ? batch : 1), tiles};
+  const int64_t groups = tiles * others * (a.many ? batch : 1);
+  if (a.many) return {groups, tiles, kManyTile / 32};
+  const bool alone = (int64_t)a.max_new * (a.q.heads / a.pool.heads) <= a.tile;
+  const bool may = a.tile == 16 && !alone && a.splits == 1 && (a.f32 || a.pool.dim == 256) &&
+                   !(a.f32 && a.pool.dim == 256 && a.each > kOneGroup);
+  return {groups, tiles, may && groups >= kOwnTile ? 1 : 4};
 }
 
 namespace {
@@ -782,8 +793,8 @@ void launch_few(const AttnLaunch& a, hipStream_t s) {
   // bf16 rows in tiles that more rows would not fit are alone.
   if constexpr (F32 || (D == 256 && ROWS == 16) || ROWS == 32) {
     if (!alone) {
-      if constexpr (kOwn<D, F32> && ROWS == 16) {
-        if (a.splits == 1 && g.groups >= kOwnTile) {
+      if constexpr (ROWS == 16) {
+        if (g.waves == 1) {
           attend_few_kernel<D, T, F32, ROWS, kShared, 1><<<grid, 64, 0, s>>>(a, tiles);
           return;
         }

@@ -97,10 +97,12 @@ struct AttnPlan {
 AttnPlan attn_plan(int batch, int kv_heads, int q_heads, int max_new, int max_kv, int window, bool f32,
                    int dim);
 constexpr int kManyTile = 256;  // rows of a workgroup of the many-row kernel
-// The workgroups of the launch (its pool's batch, heads and tokens, the query
-// heads, max_new and the plan), and how many tiles of rows a sequence gets.
+// The workgroups of the launch (from its pool's sizes, the query heads, max_new
+// and the plan), how many tiles of rows a sequence gets, and the waves of a
+// workgroup.
 struct AttnGrid {
   int64_t groups, tiles;
+  int waves;
 };
 AttnGrid attn_grid(const AttnLaunch& a);
 hipError_t launch_attention(const AttnLaunch& a, hipStream_t s);

@@ -492,8 +492,10 @@ ttt_status ttt_kv_attention_plan(const ttt_attn* attn, int32_t batch, int32_t to
   tttk::AttnLaunch a = {};
   a.pool.batch = batch, a.pool.heads = kv_heads, a.pool.tokens = tokens, a.q.heads = q_heads;
   a.max_new = attn->max_new;
-  a.many = p.many, a.splits = p.splits, a.slices = p.slices, a.tile = p.tile;
-  *plan = {p.many, p.many ? tttk::kManyTile : p.tile, p.splits, p.slices, tttk::attn_grid(a).groups};
+  a.many = p.many, a.splits = p.splits, a.each = p.each, a.slices = p.slices, a.tile = p.tile;
+  a.pool.dim = head_dim, a.f32 = act_dtype == TTT_F32;
+  const tttk::AttnGrid g = tttk::attn_grid(a);
+  *plan = {p.many, p.many ? tttk::kManyTile : p.tile, p.splits, p.slices, g.waves, 0, g.groups};
   return TTT_OK;
   TTT_ENTRY_END
 }

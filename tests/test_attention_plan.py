@@ -54,4 +54,16 @@ def test_plan_refusals():
     assert L.ttt_kv_attention_plan(None, 1, 1, 0, 8, 32, 128, ctypes.byref(p)) == -1
     assert L.ttt_kv_attention_plan(ctypes.byref(a), 0, 1, 0, 8, 32, 128, ctypes.byref(p)) == -1
     assert L.ttt_kv_attention_plan(ctypes.byref(a), 1, 1, 0, 8, 32, 96, ctypes.byref(p)) == -2
-    assert ctypes.sizeof(sv.AttnPlan) == 24
+    assert ctypes.sizeof(sv.AttnPlan) == 32
+
+
+def test_fp32_rows_of_wide_heads_share_long_keys():
+    """A wave with a tile of its own pays where tiles are many; of fp32 rows with
+    heads of 256, whose queries fill LDS, over short keys alone."""
+    def waves(dim, dtype, batch, new, keys, window=0):
+        return ttt.kv_attention_plan(batch, batch * new, 8, 32, dim, dtype, max_new=new, max_kv=keys, window=window)["waves"]
+    for n in (2048, 8192):
+        assert waves(256, F32, 2, n, n) == 4
+        assert waves(256, BF, 2, n, n) == 1 and waves(128, F32, 2, n, n) == 1 and waves(64, F32, 2, n, n) == 1
+    assert waves(256, F32, 4, 1024, 1024) == 1 and waves(256, F32, 2, 2048, 2048, window=64) == 1
+    assert waves(256, F32, 1, 1024, 1024) == 4      # too few tiles
