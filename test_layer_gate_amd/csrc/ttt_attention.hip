@@ -35,19 +35,21 @@ namespace {
 // 16 - 1. Four waves share a workgroup's stretch of keys and join in LDS, or,
 // where there are tiles enough for all, each has its own.
 //
-// Long caches are bound by HBM: a copy that only reads the same bytes is 5%
-// faster. Three waves a SIMD (bf16, 128) have 32 keys each under way, 4.3 KB.
-// One token of 40/8 heads of 128 over 128k keys (143 MB) takes 24 us, 5.9 TB/s,
-// and its join 4; 32 sequences of 4k to 32k keys, 32/8 heads (0.56 GB), 92 us,
-// 6.1 TB/s, and 5. (Keys that came through LDS, two tiles ahead, took 5%
-// longer: it is not the bytes on their way that are few.) From 17 rows on
-// decoding is what bounds it, which 32 rows share where registers allow (bf16,
-// heads of 64 and 128): 4 tokens of 40/8 heads of 128 after 93k keys in 10
-// sequences 315 us for 16, 228 for 32.
+// Long caches are bound by HBM: three waves a SIMD (bf16, 128) have 32 keys each
+// under way, 4.3 KB. One token of 40/8 heads of 128 over 128k keys (143 MB) takes
+// 27 us, 5.3 TB/s, and its join 4; 32 sequences of 4k to 32k keys, 32/8 heads
+// (0.56 GB), 91 to 94 us, 6.0 to 6.2 TB/s, and 5. A stream that only reads reaches
+// 6.6 TB/s. (Keys that came through LDS, two tiles ahead, took 5% longer: it is
+// not the bytes on their way that are few.) From 17 rows on decoding is what
+// bounds it, which 32 rows share where registers allow (bf16, heads of 64 and
+// 128): 4 tokens of 40/8 heads of 128 after 93k keys in 10 sequences 315 us for
+// 16 and 228 for 32 when that was chosen, 205 now.
 
 // Who else reads a workgroup's keys: those of the sequence's other rows; no
 // one, where one tile of rows is all; no one, and the keys are a slice of all
-// sequences'; no one, and the sequences are short. Codes that are read once are read past the caches' replacement:
+// sequences'; no one, and the sequences are short (of 9 to 16 bf16 rows; else as
+// where they are shared). Codes that are read once are read past the caches'
+// replacement:
 // one token over 128k keys 33.8 / 31.0 us a call, 32 ragged sequences 109 / 97.
 // Rows that share them are slower so (windowed fp32 rows 66 / 69), and so are
 // short sequences in one workgroup (12.1 / 12.6) and heads of 256, of which a
@@ -658,17 +660,17 @@ constexpr int kOneGroup = 1024;
 constexpr int kOwnTile = 4096;
 
 // Whether the many-row kernel is taken, for bf16 rows with heads of 64 or 128:
-// by what either kernel takes, in us, of heads of 128 (of 64 both take 3/4).
+// by what either kernel takes, in us, of heads of 128 (of 64 both take about 4/5).
 // A workgroup of the many-row kernel takes 2 us for 64 keys of its 256 rows,
 // one CU each, after 12 us of start; the rounds after the first start in 20.
 // The few-row kernel takes 0.8 us for 2^20 pairs of a row and a key, and 9 us
 // to start each round of 512 workgroups. Parts cost a join and their way
 // through memory. keys: of a tile of rows; seen: of them, on average.
-//   many / few, measured (32/8 heads; sequences x rows a key head over keys):
-//   1 x 256 over 1k 33 / 20, 16k 52 / 45, 64k 100 / 117; 1 x 64 over 64k 84 / 44,
-//   1 x 128 92 / 68; 8 x 128 over 8k 90 / 74; 4 x 512 over 4k 66 / 73; prompts of
-//   1 x 256 tokens 18 / 13, 4 x 256 19 / 24, 1 x 1k 47 / 31, 4 x 1k 77 / 98,
-//   8 x 512 53 / 80, 1 x 2k 75 / 73.
+//   many / few, measured (32/8 heads of 128 and, in brackets, 64; sequences x
+//   tokens): 1 x 256 after 16k 93 / 99 (80 / 82), 1 x 128 after 64k 153 / 182 (115 /
+//   145), 4 x 512 over 4k 135 / 171 (104 / 136); prompts of 1 x 1k tokens 43 / 26
+//   (32 / 21), 4 x 1k 69 / 88 (55 / 70), 1 x 2k 69 / 65 (55 / 51); of 64 also 1 x 256
+//   12.8 / 12.2, 4 x 256 13.4 / 15.6, 1 x 8k 415 / 544.
 // fp32 rows keep the matrix unit three times as long, beside which decoding
 // for 16 rows alone costs little, and with wide heads a workgroup's sums leave
 // no registers for a second wave: built for them, it took 879 us for the

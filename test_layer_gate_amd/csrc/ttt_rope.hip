@@ -74,7 +74,10 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeLaunch a, int un
   }
 }
 
-// The angle step of pair i: w = base^(-2i / rot), changed for long contexts.
+// The angle step of pair i: w = base^(-2i / rot), changed for long contexts by
+// published methods: position interpolation (1; Chen et al., 2023), the changed
+// base known as NTK-aware (2), YaRN (3; Peng et al., 2023), and the banded scaling
+// published with LLaMA 3.1 (4).
 //   1 linear: w / factor
 //   2 by base: base * factor^(rot / (rot - 2)), which leaves the fastest pair
 //     alone and divides the slowest one's step by factor
@@ -96,7 +99,7 @@ __device__ double angle_step(int i, int rot, double base, int kind, double facto
     double last = ceil(rot * log(orig / (lo * two_pi)) / (2 * lg));
     first = fmax(first, 0.0);
     last = fmin(last, rot - 1.0);
-    if (first == last) last += 0.001;
+    if (first == last) last += 0.001;  // a step: no ramp, and no 0 / 0
     const double ramp = fmin(fmax((i - first) / (last - first), 0.0), 1.0);
     return w * (1.0 - ramp) + w / factor * ramp;
   }

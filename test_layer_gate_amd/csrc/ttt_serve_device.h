@@ -107,8 +107,8 @@ __device__ __forceinline__ float turn_half(float x, float mate, float c, float s
 }
 
 // Where new token n belongs: its sequence, and its index among the
-// sequence's tokens. n is the same for the lanes that ask for it; every lane
-// of the wave must call it. A token that no sequence claims gets index -1.
+// sequence's tokens. Lanes may ask for different tokens. One that no sequence
+// claims gets index -1.
 struct Token {
   int seq, idx;
 };
