@@ -184,6 +184,12 @@ def _act(t, what):
     return 0 if d is torch.bfloat16 else 1 if d is torch.float32 else _b._dtype_code(t, what)
 
 
+def _act_of(dtype):
+    if dtype is torch.bfloat16 or dtype is torch.float32:
+        return _b.TTT_F32 if dtype is torch.float32 else _b.TTT_BF16
+    raise TypeError(f"rows must be bfloat16 or float32, got {dtype}")
+
+
 def _rope(table, interleaved):
     shape = table.shape
     if (len(shape) != 3 or shape[2] != 2 or table.dtype is not torch.float32
@@ -361,8 +367,7 @@ def _workspace(batch, rows, act, kv_heads, q_heads, dim, max_new, max_kv, window
 
 def kv_attention_workspace_size(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bfloat16, *,
                                 max_new, max_kv, window=0) -> int:
-    act = _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16
-    return _workspace(batch, rows, act, kv_heads, q_heads, head_dim, max_new, max_kv, window)
+    return _workspace(batch, rows, _act_of(dtype), kv_heads, q_heads, head_dim, max_new, max_kv, window)
 
 
 def kv_attention_plan(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bfloat16, *,
@@ -372,8 +377,8 @@ def kv_attention_plan(batch, rows, kv_heads, q_heads, head_dim, dtype=torch.bflo
     of all, workgroups and their waves."""
     p = AttnPlan()
     _b._check(_L().ttt_kv_attention_plan(
-        _pack_attn(1.0, window, max_new, max_kv, 0, 0), batch, rows,
-        _b.TTT_F32 if dtype == torch.float32 else _b.TTT_BF16, kv_heads, q_heads, head_dim, _ref(p)))
+        _pack_attn(1.0, window, max_new, max_kv, 0, 0), batch, rows, _act_of(dtype),
+        kv_heads, q_heads, head_dim, _ref(p)))
     return dict(many=bool(p.many), tile=p.tile, parts=p.parts, slices=p.slices, waves=p.waves,
                 workgroups=p.workgroups)
 

@@ -96,3 +96,12 @@ def test_rope_tables_past_32_bits_are_refused(lib, kw):
     with pytest.raises(ValueError, match="2\\^31"):
         sv.rope_table(**kw, device="meta")
     assert not lib.calls
+
+
+@pytest.mark.parametrize("size", [sv.kv_attention_workspace_size, sv.kv_attention_plan])
+def test_sizes_of_other_types_are_refused(size):
+    """As the call itself refuses them."""
+    for dtype in (torch.float16, torch.float64, None):
+        with pytest.raises(TypeError):
+            size(1, 1, 8, 32, 128, dtype, max_new=1, max_kv=1 << 17)
+    assert size(1, 1, 8, 32, 128, F32, max_new=1, max_kv=1 << 17)
