@@ -7,10 +7,12 @@ with the source tree; nothing is installed elsewhere.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -32,26 +34,41 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libttt_layer)")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           # packed-fp32 VALU forms stay off: hipcc would otherwise emit them
-           # from ordinary float code.
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-Wno-unused-command-line-argument",
-           "-I", INCLUDE, "-I", CSRC, "-o", tmp]
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
+FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+         # packed-fp32 VALU forms stay off: hipcc would otherwise emit them
+         # from ordinary float code.
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         "-Wno-unused-command-line-argument",
+         "-I", INCLUDE, "-I", CSRC]
+
+
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        if os.path.exists(tmp):
-            os.unlink(tmp)
         raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
     if verbose and res.stderr.strip():
         sys.stderr.write(res.stderr)
-    os.replace(tmp, LIB_PATH)
+
+
+def build(verbose: bool = False) -> str:
+    cc = hipcc()
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        jobs = min(len(SOURCES), len(os.sched_getaffinity(0)), 8)
+        with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
+            for f in [pool.submit(_run, [cc, *FLAGS, "-c", os.path.join(CSRC, s), "-o", o], verbose)
+                      for s, o in zip(SOURCES, objs)]:
+                f.result()
+        lib = LIB_PATH + ".tmp%d" % os.getpid()
+        try:
+            _run([cc, *FLAGS, "-shared", "-o", lib, *objs], verbose)
+            os.replace(lib, LIB_PATH)
+        finally:
+            if os.path.exists(lib):
+                os.unlink(lib)
     return LIB_PATH
 
 
