@@ -593,6 +593,166 @@ ttt_status ttt_kv_attention_plan(const ttt_attn* attn, int32_t batch, int32_t to
                                  int32_t act_dtype, int32_t kv_heads, int32_t q_heads,
                                  int32_t head_dim, ttt_attn_plan* plan);
 
+/* ------------------------------------------------------------------------
+ * Around and beside a block: the norms of its residual stream, linear
+ * attention, and the AdamW step on its weights. Conventions (validation before
+ * any launch, asynchrony, no allocation, errors, aliasing) as above.
+ *
+ * The norms before and after a block, fused with its gate and residual scale:
+ *   n = f, or with TTT_NORM_POST  f / sqrt(mean f^2 + eps) * post
+ *   r = x + scale * gate * n                           (res_dtype)
+ *   h = r / sqrt(mean r^2 + eps) * pre                 with TTT_NORM_PRE
+ * x is the residual stream, f what the block added to it, r the new stream and
+ * h what the next block reads; h is of r as it is stored.
+ *   x, r      [rows, d] res_dtype; r may be x
+ *   f, h      [rows, d] act_dtype; without f, r is NULL and h is of x
+ *   post, pre [d] weight_dtype, or NULL: ones
+ *   gate      [gates, d] act_dtype, rows a multiple of gates: row n has gate
+ *             n / (rows / gates) (one vector, one a sequence, one a row); NULL
+ *             with gates = 0
+ * Views are ttt_rows of one head (rows apart by token_stride). Sums and
+ * products are fp32, each result is rounded once. */
+enum { TTT_NORM_POST = 1u << 0, TTT_NORM_PRE = 1u << 1 };
+typedef struct ttt_norm {
+  int32_t rows;          /* 0 .. 2^24; 0: nothing to do (sums are zero) */
+  int32_t d;             /* a multiple of 8, at most 16384 */
+  int32_t gates;
+  int32_t act_dtype;     /* ttt_dtype */
+  int32_t res_dtype;     /* act_dtype, or TTT_F32 */
+  int32_t weight_dtype;
+  float scale;           /* finite */
+  float eps;             /* finite, >= 0 */
+  uint32_t flags;        /* TTT_NORM_* */
+  uint32_t reserved;     /* must be 0 */
+} ttt_norm;
+ttt_status ttt_block_norm(const ttt_norm* norm, const ttt_rows* x, const ttt_rows* f,
+                          const void* post, const void* pre, const ttt_rows* gate,
+                          const ttt_rows* r, const ttt_rows* h, void* stream);
+
+/* Its gradients, given those of r and h. The norms' factors are computed
+ * again from f and the stored r.
+ *   dr      [rows, d] res_dtype, or NULL: zero
+ *   dh      [rows, d] act_dtype, with TTT_NORM_PRE
+ *   r       [rows, d] res_dtype, with TTT_NORM_PRE: the forward's r (x where
+ *           there is no f)
+ *   dx      [rows, d] res_dtype out; may be dr
+ *   df      [rows, d] act_dtype out, with f
+ *   dgate   out, with gate: [rows, d] act_dtype where gates = rows, else the
+ *           sums over rows, [gates, d] fp32
+ *   dpost, dpre  [d] fp32 out, sums over rows: each with its weight
+ * Sums over rows are fp32 in a fixed order. */
+ttt_status ttt_block_norm_backward_workspace_size(const ttt_norm* norm, size_t* bytes);
+ttt_status ttt_block_norm_backward(const ttt_norm* norm, const ttt_rows* dr, const ttt_rows* dh,
+                                   const ttt_rows* r, const ttt_rows* f, const void* post,
+                                   const void* pre, const ttt_rows* gate, const ttt_rows* dx,
+                                   const ttt_rows* df, const ttt_rows* dgate, float* dpost,
+                                   float* dpre, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Linear attention with a decay for each head: a fast weight that decays and
+ * takes one outer product a token. For every sequence and kv head
+ *   S_t = exp(log_decay) S_{t-1} + k_t v_t^T,    o_t = scale S_t^T q_t
+ * for every query head of the kv head (query head h has kv head h / (q heads /
+ * kv heads)). Tokens are the rows of q_starts, as in the cache.
+ *   q  [tokens, q heads, dim_k], k [tokens, kv heads, dim_k],
+ *   v  [tokens, kv heads, dim_v], o [tokens, q heads, dim_v]: act_dtype; rows
+ *      of o that no sequence claims are not written
+ *   state  [batch, kv heads, dim_k, dim_v] fp32, in/out: S before the first
+ *      token, then after the last (a prompt may come in segments, and go on in
+ *      single tokens). NULL: zero before, and not returned. A sequence without
+ *      rows keeps its state
+ *   workspace  ttt_linear_attention_workspace_size() bytes, 256-byte aligned
+ *      (may be NULL where that is 0)
+ * A NaN or an infinity in a token reaches the tokens from it on, of its
+ * sequence, and no others. Arithmetic: states and sums are fp32. bf16 rows
+ * (more than 8 a sequence): products of bf16 operands; q k^T times its decays
+ * is rounded to bf16, the state enters o as two bf16 terms (16 bits), v times
+ * its decay enters the state as three (24 bits). fp32 rows, and up to 8 rows a
+ * sequence: fp32 throughout. */
+typedef struct ttt_linear {
+  const float* log_decay;     /* [kv heads] device memory, <= 0 (-inf: nothing is kept) */
+  const int32_t* q_starts;    /* [batch + 1] device memory, or NULL: tokens / batch each */
+  int32_t batch, tokens;
+  int32_t max_new;            /* an upper bound of a sequence's tokens: it sizes the launch;
+                                 a wrong one costs time, not results */
+  int32_t act_dtype;
+  int32_t kv_heads, q_heads;
+  int32_t dim_k, dim_v;       /* 64, 128 or 256 */
+  float scale;                /* finite */
+  uint32_t reserved;          /* must be 0 */
+} ttt_linear;
+ttt_status ttt_linear_attention_workspace_size(const ttt_linear* linear, size_t* bytes);
+ttt_status ttt_linear_attention(const ttt_linear* linear, const ttt_rows* q, const ttt_rows* k,
+                                const ttt_rows* v, const ttt_rows* o, float* state,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients.
+ *   d_o      [tokens, q heads, dim_v], the gradient of o
+ *   state    S before the first token, or NULL: zero
+ *   d_state  the gradient of S after the last token, or NULL: zero
+ *   dq, dk, dv  out, in act_dtype (dk and dv are sums over a kv head's query heads)
+ *   d_state0 out, fp32: the gradient of S before the first token, or NULL; may
+ *            be d_state
+ * log_decay and scale get no gradient. Arithmetic as in the forward, for any
+ * number of rows; a NaN or an infinity in d_o reaches only its own row of dq. */
+ttt_status ttt_linear_attention_backward_workspace_size(const ttt_linear* linear, size_t* bytes);
+ttt_status ttt_linear_attention_backward(const ttt_linear* linear, const ttt_rows* d_o,
+                                         const ttt_rows* q, const ttt_rows* k, const ttt_rows* v,
+                                         const float* state, const float* d_state,
+                                         const ttt_rows* dq, const ttt_rows* dk, const ttt_rows* dv,
+                                         float* d_state0, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/* AdamW over many tensors at once. For every value, with step t from 1:
+ *   g' = g * min(1, max_norm / *norm)                  where norm is given
+ *   m = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2
+ *   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * in fp32, rounded once to p's type. Where *norm is infinite or NaN, nothing is
+ * changed. p is updated in place; with a master, the master is p's fp32 value
+ * and p its rounding.
+ *
+ * The states of n tensors of n_i values are N = sum of n_i, each rounded up to
+ * a multiple of 256, values of m and v, in one buffer that zeroes make fresh:
+ *   32 bits  m [N], v [N] fp32
+ *   8 bits   m codes [N], r codes [N], m scales [N / 256], r scales [N / 256]
+ *            (fp32): m and r = sqrt(v) are code times scale. m's codes are E4M3
+ *            (to nearest, ties to even), the scale max|m| / 448 of the block;
+ *            r's have 4 exponent and 4 fraction bits and no sign (c < 16:
+ *            c 2^-10; else (16 + c % 16) 2^(c / 16 - 11)), the scale max r /
+ *            496; an r above 0 gets a code above 0. Scales are at least 2^-126.
+ *            A block with a NaN or an infinity is NaN.
+ * Tensor i starts at the sum of those before it, rounded likewise. The step
+ * itself uses m and v before they are rounded to 8 bits. */
+typedef struct ttt_param {
+  void* p;               /* [n] param_dtype, in place */
+  float* master;         /* [n], or NULL (for all tensors or for none; TTT_BF16 only) */
+  const void* g;         /* [n] grad_dtype */
+  int64_t n;             /* 0 .. 2^40; pointers of an empty tensor are not read */
+} ttt_param;
+typedef struct ttt_adamw {
+  int32_t param_dtype, grad_dtype;  /* TTT_F32 weights have TTT_F32 gradients or TTT_BF16 */
+  int32_t bits;          /* of the states: 8 or 32 */
+  int32_t step;          /* t >= 1 */
+  double lr, beta1, beta2, eps, weight_decay;
+  double max_norm;       /* > 0 with norm */
+  const float* norm;     /* device memory (ttt_grad_norm), or NULL */
+  const float* lr_device;      /* device memory, in lr's place, or NULL */
+  const int32_t* step_device;  /* likewise for step (a captured call's replays read them) */
+} ttt_adamw;
+ttt_status ttt_adamw_state_size(const int64_t* sizes, int32_t n, int32_t bits, size_t* bytes);
+ttt_status ttt_adamw_step(const ttt_adamw* adamw, const ttt_param* params, int32_t n, void* state,
+                          size_t state_bytes, void* stream);
+/* What an 8-bit state buffer of N values (a multiple of 256) stands for: m and
+ * v [N] in out_dtype, rounded once. */
+ttt_status ttt_adamw_read(const void* state, int64_t N, int32_t out_dtype, void* m, void* v,
+                          void* stream);
+/* The 2-norm of n tensors' values together, summed in 64 bits in a fixed order:
+ * *norm, device memory. */
+ttt_status ttt_grad_norm_workspace_size(int32_t n, size_t* bytes);
+ttt_status ttt_grad_norm(const void* const* grads, const int64_t* sizes, int32_t n,
+                         int32_t grad_dtype, float* norm, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
 /* The name of a status code ("TTT_OK", "TTT_ERR_INVALID_ARG", ...; codes
  * outside ttt_status give "TTT_ERR_UNKNOWN"). The string is static. */
 const char* ttt_status_string(int32_t status);

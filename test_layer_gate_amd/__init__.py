@@ -16,7 +16,25 @@ key/value cache held in 4 bits, and attention over it.
     table = rope_table(max_pos, rot_dim)
     q = kv_append(pages, page_table, kv_lens, k, v, q=q, rope_table=table)
     o = kv_attention(q, pages, page_table, kv_lens)
+
+Around and beside a block: the norms of its residual stream with gate and
+residual scale, linear attention with a decay for each head, and AdamW.
+
+    r, h = block_norm(x, f, post=w1, pre=w2, gate=g, scale=s)
+    o = linear_attention(q, k, v, log_decay, state=S)
+    adamw_step(params, grads, state, lr=3e-4, step=t, bits=8)
 """
+from ._block import (  # noqa: F401
+    adamw_read,
+    adamw_state,
+    adamw_state_size,
+    adamw_step,
+    block_norm,
+    block_norm_backward,
+    grad_norm,
+    linear_attention,
+    linear_attention_backward,
+)
 from ._binding import (  # noqa: F401
     LIB_PATH,
     TTTError,
@@ -66,6 +84,9 @@ __all__ = ["layer_forward", "layer_forward_packed", "packed_workspace_size", "pa
            "rope_table", "rope_forward", "rope_backward",
            "kv_pages", "kv_page_bytes", "kv_append", "kv_read",
            "kv_attention", "kv_attention_workspace_size", "kv_attention_plan",
+           "block_norm", "block_norm_backward",
+           "linear_attention", "linear_attention_backward",
+           "adamw_state_size", "adamw_state", "adamw_step", "adamw_read", "grad_norm",
            "copy_calibration",
            "make_desc", "profile_enable", "profile_read", "TTTError", "lib",
            "LIB_PATH"]

@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["ttt_kernels.hip", "ttt_decode.hip", "ttt_backward.hip", "ttt_noalloc.hip",
            "ttt_rope.hip", "ttt_cache.hip", "ttt_attention.hip",
            "ttt_attend_many.hip",
-           "ttt_api.cpp", "ttt_serve_api.cpp"]
+           "ttt_norm.hip", "ttt_linear.hip", "ttt_adamw.hip",
+           "ttt_api.cpp", "ttt_serve_api.cpp", "ttt_block_api.cpp"]
 ARCH = "gfx950"
 
 

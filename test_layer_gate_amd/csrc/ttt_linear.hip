@@ -1,0 +1,758 @@
+// gfx950 kernels of linear attention with a decay for each head:
+//   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+// in chunks on the matrix cores, and token by token.
+//
+// One chunked kernel serves the forward and, with the arguments in other
+// roles, all three gradients. For rows of q, k (A values a head) and v (B):
+//   o_i = s_in sum_{j <= i} g^(i - j) (q_i k_j) v_j + s_out g^(i + lead) E^T q_i
+//   E'  = g^C E + s_up sum_j g^(C - lead - j) k_j v_j^T         (C rows on)
+//   forward  (q, k, v),  lead 1, s = (scale, scale, 1),  E = S
+//   dq       (do, v, k), the same with E = S^T
+//   dk       (v, do, q), rows backwards, lead 0, s = (scale, 1, scale)
+//   dv       (k, q, do), likewise; E: the gradient of the state behind a row,
+//            times the rows' decays, from d_last on; its end is d_first
+// Where query heads share a state (q for the forward and dq; k and v for dk
+// and dv), the kernel goes over them within a chunk.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ttt_attention.h"
+#include "ttt_block.h"
+
+namespace tttk {
+namespace {
+
+// What one launch of the chunked kernel takes.
+struct Chunks {
+  Rows q, k, v, o;
+  const float* log_decay;
+  const int32_t* starts;
+  const float* state;           // E before a part's first row, or null: zeros
+  float* out;                   // E after the last (or, for sums alone, the part's own)
+  int64_t state_part, state_head, state_seq;  // strides of `state`, values; a part of 0: parts share one
+  int64_t out_part, out_head, out_seq;
+  int state_turned;             // state is [B][A]
+  int batch, tokens, heads, parts, part_rows, slices;
+  int lead, back;
+  float s_in, s_out, s_up;
+};
+
+// Tiles of rows in LDS, swizzled by 16-byte pieces so that a read of 8
+// consecutive rows at one piece, and a read of 4 rows of 4 neighbouring pieces
+// (the transposing read), each fall on different banks.
+template <bool F32>
+struct Elem {
+  static constexpr int size = F32 ? 4 : 2;
+  static constexpr int per16 = 16 / size;
+  static constexpr int kb = F32 ? 8 : 16;       // contraction of one mma()
+  static constexpr int rows = F32 ? 32 : 64;    // of a chunk
+};
+
+template <bool F32, int W>  // W values a row
+struct Tile {
+  static constexpr int pieces = W * Elem<F32>::size / 16;
+  static __device__ __forceinline__ int swz(int row) {
+    if constexpr (pieces >= 16)
+      return ((row & 1) << 2) | ((row >> 1) & 3) | (((row >> 1) & 1) << 3);
+    else
+      return (((row >> 1) & 1) << 2) | (row & 1) | (((row >> 2) & 1) << 1);
+  }
+  static __device__ __forceinline__ uint32_t at(int row, int piece) {
+    return (uint32_t)(row * pieces + (piece ^ swz(row))) * 16;
+  }
+};
+
+// c + a b over kb values of the contraction: one 32x32x16 product of bf16, or
+// four 32x32x2 of fp32. Lane l holds row (column) l % 32 and, of the
+// contraction's values, those at 4 (l / 32) + e, for bf16 the further ones 8
+// on (e = 0 .. 3): the order in which a product's result holds its rows, so
+// that states and weights go from one product to the next in registers.
+template <bool F32>
+__device__ __forceinline__ f32x16_t mma(const uint4& a, const uint4& b, f32x16_t c) {
+  if constexpr (F32) {
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  } else {
+    return mfma32(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c);
+  }
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+// Where a lane reads a tile: byte offsets that further rows add to and further
+// pieces are xored into (a row's pieces are a power of two, so a swizzled piece
+// is the row's start xor the swizzle xor the piece). They are kept from being
+// known across chunks: the compiler would hold an address for every read.
+template <bool F32, int W>
+struct Reader {
+  static constexpr int row_bytes = W * Elem<F32>::size;
+  uint32_t r, c[F32 ? 4 : 1];
+  __device__ __forceinline__ Reader() {
+    const int lane = threadIdx.x & 63, hf = lane >> 5;
+    if constexpr (F32) {
+      r = Tile<true, W>::at(lane & 31, hf);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = Tile<true, W>::at(4 * hf + e, (lane & 31) >> 2) + (lane & 3) * 4;
+    } else {
+      r = Tile<false, W>::at(lane & 31, 0) + 8 * hf;
+      // a transposing read: lane 4e + j of 16 addresses row e, columns 4j .. +
+      // 3, and lane i gets column i of the four rows
+      const int e = (lane >> 2) & 3, j = lane & 3;
+      c[0] = Tile<false, W>::at(4 * hf + e, 2 * ((lane >> 4) & 1) + (j >> 1)) + (j & 1) * 8;
+    }
+  }
+  __device__ __forceinline__ void forget() {
+    asm volatile("" : "+v"(r));
+#pragma unroll
+    for (int e = 0; e < (F32 ? 4 : 1); ++e) asm volatile("" : "+v"(c[e]));
+  }
+  // The lane's row 32 rt + l % 32, contraction block kb of the row's values.
+  __device__ __forceinline__ uint4 row(const char* tile, int rt, int kb) const {
+    const char* p = tile + 32 * rt * row_bytes;
+    if constexpr (F32) {
+      return *reinterpret_cast<const uint4*>(p + (r ^ (uint32_t)(kb * 32)));
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p + (r ^ (uint32_t)(kb * 32)));
+      const uint2 y = *reinterpret_cast<const uint2*>(p + (r ^ (uint32_t)(kb * 32 + 16)));
+      return make_uint4(x.x, x.y, y.x, y.y);
+    }
+  }
+  // The lane's column 32 cb + l % 32 of the rows of block kb.
+  __device__ __forceinline__ uint4 col(const char* tile, int kb, int cb) const {
+    const char* p = tile + Elem<F32>::kb * kb * row_bytes;
+    if constexpr (F32) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(p + (c[e] ^ (uint32_t)(cb * 128)));
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      const uint32_t at = c[0] ^ (uint32_t)(cb * 64);
+      const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + at));
+      const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + at + 8 * row_bytes));
+      const uint2 u = __builtin_bit_cast(uint2, x), w = __builtin_bit_cast(uint2, y);
+      return make_uint4(u.x, u.y, w.x, w.y);
+    }
+  }
+};
+
+// Values of a product's result (kb of its rows) as an operand: fp32 as they
+// are; as T terms of bf16.
+template <bool F32, int T>
+__device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4 (&f)[T]) {
+  if constexpr (F32) {
+    f[0] = make_uint4(__float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]), __float_as_uint(x[4 * u + 2]),
+                      __float_as_uint(x[4 * u + 3]));
+  } else {
+    uint32_t w[4][T];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2<T>(x[8 * u + 2 * e], x[8 * u + 2 * e + 1], w[e]);
+#pragma unroll
+    for (int t = 0; t < T; ++t) f[t] = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
+  }
+}
+
+// g^n for a whole n >= 0; 1 for n = 0 whatever g is.
+__device__ __forceinline__ float power(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
+
+// Rows [first, first + count) of a sequence that starts at row `base`, counted
+// from its end if back, into a tile; rows from count on are zero. Returns
+// whether any value is infinite or NaN (only asked of v).
+template <bool F32, int W, int NT, bool CHECK>
+__device__ __forceinline__ bool load_tile(char* tile, const Rows& x, int head, int col, int64_t row0, int dir, int count) {
+  constexpr int P = W * Elem<F32>::size / 16, N = Elem<F32>::rows * P / NT, R = NT / P;  // R rows at a time
+  static_assert(NT % P == 0 && Elem<F32>::rows % R == 0, "whole passes");
+  const int r = threadIdx.x / P, c = threadIdx.x % P;
+  const int64_t stride = x.ts * Elem<F32>::size * dir;
+  const char* p = static_cast<const char*>(x.p) + (head * x.hs + col + row0 * x.ts) * Elem<F32>::size + r * stride + c * 16;
+  uint4 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r + i * R < count) v[i] = *reinterpret_cast<const uint4*>(p);
+    p += R * stride;
+  }
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (CHECK) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (F32)
+          odd |= (w[e] & 0x7f800000u) == 0x7f800000u;
+        else
+          odd |= (w[e] & 0x7f800000u) == 0x7f800000u || (w[e] & 0x7f80u) == 0x7f80u;
+      }
+    }
+    *reinterpret_cast<uint4*>(tile + Tile<F32, W>::at(r + i * R, c)) = v[i];
+  }
+  return odd;
+}
+
+constexpr int kStoreRow = 40;  // values of a row of a wave's outputs in LDS, 32 and some against bank conflicts
+
+// One part of a sequence's rows for one state head and a slice of NW * 32 of
+// the B columns; wave w has columns 32 w .. of the slice, with its part of the
+// state in registers (fp32, 16 values a lane for each 32 of A).
+//
+// MANY: heads of k and v share the state (else heads of q do). SUMS: the
+// part's own sum alone, from zero.
+//
+// bf16: weights (q k) enter the product with v rounded to bf16 (they carry the
+// 2^-9 of a value that is rounded to bf16 once more at the end); states as two
+// bf16 terms (16 bits: each row reads every state again); in the update, whose
+// sums stay, v times its decay as three (24 bits). fp32: the matrix cores' fp32
+// products throughout.
+template <bool F32, int A, int NW, bool MANY, bool SUMS>
+__global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks a) {
+  constexpr int C = Elem<F32>::rows, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
+  constexpr int TS = F32 ? 1 : 2, TU = F32 ? 1 : 3;  // terms of states, of updates
+  constexpr int RT = C / 32, AT = A / 32, PER = 32 / KB;
+  constexpr int kBytesA = C * A * Elem<F32>::size, kBytesB = C * B * Elem<F32>::size;
+  __shared__ __attribute__((aligned(16))) char kt[kBytesA];
+  __shared__ __attribute__((aligned(16))) char vt[kBytesB];
+  __shared__ __attribute__((aligned(16))) char qt[SUMS ? 16 : kBytesA];
+  __shared__ __attribute__((aligned(16))) char ot[SUMS || F32 ? 16 : NW * C * kStoreRow * 2];
+  __shared__ __attribute__((aligned(16))) float row_f[C], up_f[C], off_f[32];
+  Reader<F32, A> ra;
+  Reader<F32, B> rb;
+
+  int id = blockIdx.x;
+  const int slice = id % a.slices;
+  id /= a.slices;
+  const int part = id % a.parts;
+  id /= a.parts;
+  const int head = id % a.heads, seq = id / a.heads;
+  int64_t base, len;
+  if (a.starts) {
+    const int lo = min(max(a.starts[seq], 0), a.tokens), hi = min(max(a.starts[seq + 1], 0), a.tokens);
+    base = lo, len = max(hi - lo, 0);
+  } else {
+    len = a.tokens / a.batch, base = seq * len;
+  }
+  // the last part takes what the others leave
+  const int64_t mine = (int64_t)part * a.part_rows;
+  const bool last = part == a.parts - 1 || mine + a.part_rows >= len;
+  if (part > 0 && mine >= len) return;
+  if (SUMS && last) return;  // (nobody reads it)
+  const int64_t end = last ? len : mine + a.part_rows;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hf = lane >> 5, col = lane & 31;
+  const int b0 = slice * B + wave * 32 + col;  // the lane's column
+  const int b_all = a.slices * B;
+  const float lg = a.log_decay[head] * kLog2e;
+
+  for (int i = threadIdx.x; i < C; i += NT) row_f[i] = a.s_out * power(lg, i + a.lead);
+  for (int i = threadIdx.x; i < 32; i += NT) off_f[i] = a.s_in * power(lg, 32 - i);
+  auto set_up = [&](int count) {
+    for (int i = threadIdx.x; i < C; i += NT) up_f[i] = a.s_up * power(lg, max(count - a.lead - i, 0));
+  };
+  set_up(C);
+  int up_for = C;
+  float diag[16];  // s_in g^(i - j) of a 32 x 32 block on the diagonal
+  float far = 0.f;
+  if constexpr (!SUMS) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) diag[r] = a.s_in * power(lg, max(col - (8 * (r >> 2) + 4 * hf + (r & 3)), 0));
+    far = power(lg, col);
+  }
+
+  f32x16_t st[AT];
+  if (!SUMS && a.state != nullptr) {
+    const float* e = a.state + seq * a.state_seq + head * a.state_head + part * a.state_part;
+    e += a.state_turned ? (int64_t)b0 * A + 4 * hf : (int64_t)(4 * hf) * b_all + b0;
+    const int step = a.state_turned ? 1 : b_all;
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st[t][r] = e[(32 * t + 8 * (r >> 2) + (r & 3)) * step];
+  } else {
+#pragma unroll
+    for (int t = 0; t < AT; ++t) st[t] = f32x16_t{};
+  }
+
+  const int q_heads = MANY ? 1 : a.q.heads / a.heads, k_heads = MANY ? a.k.heads / a.heads : 1;
+  for (int64_t t0 = mine; t0 < end;) {
+    int take = (int)min((int64_t)C, end - t0);
+    const int dir = a.back ? -1 : 1;
+    const int64_t row0 = a.back ? base + len - 1 - t0 : base + t0;
+    ra.forget();
+    rb.forget();
+
+    // x = the product of the rows (in qt) with the state before them
+    auto with_state = [&](f32x16_t(&x)[RT]) {
+      // (so that its conversion stays inside the loop over heads: it would take
+      // as many registers again)
+#pragma unroll
+      for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
+#pragma unroll
+      for (int it = 0; it < RT; ++it) x[it] = f32x16_t{};
+#pragma unroll
+      for (int kb = 0; kb < A / KB; ++kb) {
+        uint4 sf[TS];
+        as_operand<F32, TS>(st[kb / PER], kb % PER, sf);
+#pragma unroll
+        for (int it = 0; it < RT; ++it) {
+          const uint4 qf = ra.row(qt, it, kb);
+#pragma unroll
+          for (int t = 0; t < TS; ++t) x[it] = mma<F32>(qf, sf[t], x[it]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < RT; ++it)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 f = *reinterpret_cast<const float4*>(&row_f[32 * it + 8 * u + 4 * hf]);
+          x[it][4 * u] *= f.x, x[it][4 * u + 1] *= f.y, x[it][4 * u + 2] *= f.z, x[it][4 * u + 3] *= f.w;
+        }
+    };
+    // x += what the chunk's own rows up to each give
+    auto with_rows = [&](const uint4(&vf)[C / KB], f32x16_t(&x)[RT]) {
+#pragma unroll
+      for (int it = 0; it < RT; ++it) {
+        f32x16_t p[RT];  // rows j of tile jt, column i
+#pragma unroll
+        for (int jt = 0; jt <= it; ++jt) p[jt] = f32x16_t{};
+#pragma unroll
+        for (int kb = 0; kb < A / KB; ++kb) {
+          const uint4 qf = ra.row(qt, it, kb);
+#pragma unroll
+          for (int jt = 0; jt <= it; ++jt) p[jt] = mma<F32>(ra.row(kt, jt, kb), qf, p[jt]);
+        }
+#pragma unroll
+        for (int jt = 0; jt <= it; ++jt) {
+          if (jt == it) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p[jt][r] = 8 * (r >> 2) + 4 * hf + (r & 3) > col ? 0.f : p[jt][r] * diag[r];
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float4 f = *reinterpret_cast<const float4*>(&off_f[8 * u + 4 * hf]);
+              p[jt][4 * u] *= f.x * far, p[jt][4 * u + 1] *= f.y * far;
+              p[jt][4 * u + 2] *= f.z * far, p[jt][4 * u + 3] *= f.w * far;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < PER; ++u) {
+            uint4 w[1];
+            as_operand<F32, 1>(p[jt], u, w);
+            x[it] = mma<F32>(w[0], vf[jt * PER + u], x[it]);
+          }
+        }
+      }
+    };
+    auto load_v = [&](uint4(&vf)[C / KB]) {
+#pragma unroll
+      for (int kb = 0; kb < C / KB; ++kb) vf[kb] = rb.col(vt, kb, wave);
+    };
+    // bf16 values go through the wave's own LDS, so that rows leave in pieces
+    // of 16 bytes
+    auto store = [&](int q_head, const f32x16_t(&x)[RT]) {
+      if constexpr (F32) {
+        const int64_t ts = a.o.ts * dir;
+        float* to = static_cast<float*>(a.o.p) + row0 * a.o.ts + q_head * a.o.hs + b0 + 4 * hf * ts;
+#pragma unroll
+        for (int it = 0; it < RT; ++it)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e, to += ts)
+              if (32 * it + 8 * u + 4 * hf + e < take) *to = x[it][4 * u + e];
+            to += 4 * ts;
+          }
+      } else {
+        u16* mine = reinterpret_cast<u16*>(ot) + wave * C * kStoreRow;
+#pragma unroll
+        for (int it = 0; it < RT; ++it)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            mine[(32 * it + 8 * (r >> 2) + 4 * hf + (r & 3)) * kStoreRow + col] = bf16_rne(x[it][r]);
+        const int64_t ts = a.o.ts * dir;
+        u16* to = static_cast<u16*>(a.o.p) + row0 * a.o.ts + q_head * a.o.hs + slice * B + wave * 32 + (lane & 3) * 8 +
+                  (lane >> 2) * ts;
+#pragma unroll
+        for (int n = 0; n < C / 16; ++n, to += 16 * ts) {
+          const int i = 16 * n + (lane >> 2);
+          const uint4 w = *reinterpret_cast<const uint4*>(mine + i * kStoreRow + (lane & 3) * 8);
+          if (i < take) *reinterpret_cast<uint4*>(to) = w;
+        }
+      }
+    };
+    // st += (k decayed)^T v of the chunk in LDS
+    auto update = [&](const uint4(&vf)[C / KB]) {
+#pragma unroll
+      for (int kb = 0; kb < C / KB; ++kb) {
+        uint4 u[TU];
+        if constexpr (F32) {
+          const float4 f = *reinterpret_cast<const float4*>(&up_f[8 * kb + 4 * hf]);
+          u[0] = make_uint4(__float_as_uint(__uint_as_float(vf[kb].x) * f.x), __float_as_uint(__uint_as_float(vf[kb].y) * f.y),
+                            __float_as_uint(__uint_as_float(vf[kb].z) * f.z), __float_as_uint(__uint_as_float(vf[kb].w) * f.w));
+        } else {
+          const float4 f = *reinterpret_cast<const float4*>(&up_f[16 * kb + 4 * hf]);
+          const float4 g = *reinterpret_cast<const float4*>(&up_f[16 * kb + 8 + 4 * hf]);
+          const uint32_t w[4] = {vf[kb].x, vf[kb].y, vf[kb].z, vf[kb].w};
+          const float m[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
+          uint32_t z[4][TU];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            split2<TU>(__uint_as_float(w[e] << 16) * m[2 * e], __uint_as_float(w[e] & 0xffff0000u) * m[2 * e + 1], z[e]);
+#pragma unroll
+          for (int t = 0; t < TU; ++t) u[t] = make_uint4(z[0][t], z[1][t], z[2][t], z[3][t]);
+        }
+#pragma unroll
+        for (int t = 0; t < AT; ++t) {
+          const uint4 kf = ra.col(kt, kb, t);
+#pragma unroll
+          for (int x = 0; x < TU; ++x) st[t] = mma<F32>(kf, u[x], st[t]);
+        }
+      }
+    };
+
+    if constexpr (!MANY) {
+      // k and v once, heads of q in turn
+      __syncthreads();  // (the tiles' last readers are done)
+      load_tile<F32, A, NT, false>(kt, a.k, head, 0, row0, dir, take);
+      bool odd = load_tile<F32, B, NT, true>(vt, a.v, head, slice * B, row0, dir, take);
+      if constexpr (!SUMS) load_tile<F32, A, NT, false>(qt, a.q, head * q_heads, 0, row0, dir, take);
+      if (__syncthreads_or(!SUMS && odd && take > 1)) {
+        // an infinity or a NaN times a later row's weight of 0 would be NaN:
+        // such a chunk is taken a row at a time
+        take = 1;
+        load_tile<F32, A, NT, false>(kt, a.k, head, 0, row0, dir, take);
+        load_tile<F32, B, NT, false>(vt, a.v, head, slice * B, row0, dir, take);
+        __syncthreads();
+      }
+      if (take != up_for) {
+        set_up(take);
+        up_for = take;
+        __syncthreads();
+      }
+      uint4 vf[C / KB];
+      load_v(vf);
+      if constexpr (!SUMS) {
+        for (int h = 0; h < q_heads; ++h) {
+          if (h > 0) {
+            __syncthreads();
+            load_tile<F32, A, NT, false>(qt, a.q, head * q_heads + h, 0, row0, dir, take);
+            __syncthreads();
+          }
+          f32x16_t x[RT];
+          with_state(x);
+          with_rows(vf, x);
+          store(head * q_heads + h, x);
+        }
+      }
+      const float g = power(lg, take);
+#pragma unroll
+      for (int t = 0; t < AT; ++t) st[t] *= g;
+      update(vf);
+    } else {
+      // q once, heads of k and v in turn
+      __syncthreads();
+      if constexpr (!SUMS) {
+        load_tile<F32, A, NT, false>(qt, a.q, head, 0, row0, dir, take);
+      }
+      if constexpr (!SUMS) {
+        bool odd = false;
+        for (int h = 0; h < k_heads; ++h) {  // (as above, for any of the heads)
+          if (h > 0) __syncthreads();
+          odd |= load_tile<F32, B, NT, true>(vt, a.v, head * k_heads + h, slice * B, row0, dir, take);
+        }
+        if (__syncthreads_or(odd && take > 1)) take = 1;
+      }
+      if (take != up_for) {
+        set_up(take);
+        up_for = take;
+      }
+      f32x16_t x[RT];
+      if constexpr (!SUMS) with_state(x);
+      const float g = power(lg, take);
+#pragma unroll
+      for (int t = 0; t < AT; ++t) st[t] *= g;
+      for (int h = 0; h < k_heads; ++h) {
+        __syncthreads();
+        load_tile<F32, A, NT, false>(kt, a.k, head * k_heads + h, 0, row0, dir, take);
+        load_tile<F32, B, NT, false>(vt, a.v, head * k_heads + h, slice * B, row0, dir, take);
+        __syncthreads();
+        uint4 vf[C / KB];
+        load_v(vf);
+        if constexpr (!SUMS) with_rows(vf, x);
+        update(vf);
+      }
+      if constexpr (!SUMS) store(head, x);
+    }
+    t0 += take;
+  }
+
+  if (a.out != nullptr && (SUMS || last)) {
+    float* e = a.out + seq * a.out_seq + head * a.out_head + part * a.out_part;
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        e[(int64_t)(32 * t + 8 * (r >> 2) + 4 * hf + (r & 3)) * b_all + b0] = st[t][r];
+  }
+}
+
+// The states before every part from the parts' own sums, in their place: E_0
+// is the state before the sequence (or zero), E_{p+1} = g^rows E_p + U_p.
+constexpr int kScanThreads = 256;
+__global__ __launch_bounds__(kScanThreads) void scan_kernel(float* sums, const float* first, const float* log_decay,
+                                                            const int32_t* starts, int batch, int tokens, int heads,
+                                                            int parts, int part_rows, int size) {
+  const int blocks = size / (4 * kScanThreads);
+  const int64_t sh = blockIdx.x / blocks;
+  const int i = ((blockIdx.x % blocks) * kScanThreads + threadIdx.x) * 4;
+  const int seq = (int)(sh / heads), head = (int)(sh % heads);
+  int64_t len = tokens / batch;
+  if (starts) {
+    const int lo = min(max(starts[seq], 0), tokens), hi = min(max(starts[seq + 1], 0), tokens);
+    len = max(hi - lo, 0);
+  }
+  const float g = power(log_decay[head] * kLog2e, part_rows);
+  float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (first) e = *reinterpret_cast<const float4*>(first + sh * size + i);
+  float* p = sums + sh * parts * size + i;
+  for (int n = 0; n < parts; ++n, p += size) {
+    const bool more = n < parts - 1 && (int64_t)(n + 1) * part_rows < len;
+    float4 u;
+    if (more) u = *reinterpret_cast<const float4*>(p);
+    *reinterpret_cast<float4*>(p) = e;
+    if (!more) break;
+    e = make_float4(g * e.x + u.x, g * e.y + u.y, g * e.z + u.z, g * e.w + u.w);
+  }
+}
+
+// A few tokens a sequence: the state's slice of SB columns is read once, kept
+// in registers over the tokens, and written once: bound by HBM. Eight lanes
+// hold 32 neighbouring columns of a row of the state; 32 rows at a time.
+constexpr int kStepGroup = 8;   // heads of q at a time
+template <bool F32, int A, int G>
+__global__ __launch_bounds__(256) void token_kernel(LinearLaunch a) {
+  constexpr int SB = 32, R = A / 32;
+  __shared__ float kq[(1 + G) * A], vv[SB];
+  __shared__ float4 red[4][G][8];
+  const int slices = a.dv / SB;
+  int id = blockIdx.x;
+  const int slice = id % slices;
+  id /= slices;
+  const int head = id % a.kv_heads, seq = id / a.kv_heads;
+  int64_t base, len;
+  if (a.starts) {
+    const int lo = min(max(a.starts[seq], 0), a.tokens), hi = min(max(a.starts[seq + 1], 0), a.tokens);
+    base = lo, len = max(hi - lo, 0);
+  } else {
+    len = a.tokens / a.batch, base = seq * len;
+  }
+  const int group = a.q.heads / a.kv_heads;
+  const int c4 = threadIdx.x & 7, row = threadIdx.x >> 3;
+  const int64_t at = ((int64_t)(seq * a.kv_heads + head) * A + row) * a.dv + slice * SB + c4 * 4;
+  float4 st[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    st[r] = a.first ? *reinterpret_cast<const float4*>(a.first + at + (int64_t)r * 32 * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float g = power(a.log_decay[head] * kLog2e, 1);
+  auto value = [](const Rows& x, int64_t i) {
+    return F32 ? static_cast<const float*>(x.p)[i] : bf16_f32(static_cast<const u16*>(x.p)[i]);
+  };
+  for (int64_t t = 0; t < len; ++t) {
+    const int64_t n = base + t;
+    for (int h0 = 0; h0 < group; h0 += G) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < A; i += 256) {
+        if (h0 == 0) kq[i] = value(a.k, n * a.k.ts + head * a.k.hs + i);
+#pragma unroll
+        for (int x = 0; x < G; ++x)
+          if (h0 + x < group) kq[(1 + x) * A + i] = value(a.q, n * a.q.ts + (head * group + h0 + x) * a.q.hs + i);
+      }
+      if (h0 == 0 && threadIdx.x < SB) vv[threadIdx.x] = value(a.v, n * a.v.ts + head * a.v.hs + slice * SB + threadIdx.x);
+      __syncthreads();
+      if (h0 == 0) {
+        const float4 v = *reinterpret_cast<const float4*>(&vv[c4 * 4]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float k = kq[row + 32 * r];
+          st[r] = make_float4(g * st[r].x + k * v.x, g * st[r].y + k * v.y, g * st[r].z + k * v.z, g * st[r].w + k * v.w);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        if (h0 + x >= group) break;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float q = kq[(1 + x) * A + row + 32 * r];
+          o.x += q * st[r].x, o.y += q * st[r].y, o.z += q * st[r].z, o.w += q * st[r].w;
+        }
+#pragma unroll
+        for (int m = 8; m < 64; m <<= 1)
+          o.x += __shfl_xor(o.x, m), o.y += __shfl_xor(o.y, m), o.z += __shfl_xor(o.z, m), o.w += __shfl_xor(o.w, m);
+        if ((threadIdx.x & 63) < 8) red[threadIdx.x >> 6][x][c4] = o;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < G * SB; i += 256) {
+        const int x = i / SB, c = i % SB;
+        if (h0 + x < group) {
+          float o = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) o += reinterpret_cast<const float*>(&red[w][x][0])[c];
+          o *= a.scale;
+          const int64_t to = n * a.o.ts + (head * group + h0 + x) * a.o.hs + slice * SB + c;
+          if constexpr (F32)
+            static_cast<float*>(a.o.p)[to] = o;
+          else
+            static_cast<u16*>(a.o.p)[to] = bf16_rne(o);
+        }
+      }
+    }
+  }
+  if (a.last) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) *reinterpret_cast<float4*>(a.last + at + (int64_t)r * 32 * a.dv) = st[r];
+  }
+}
+
+__global__ __launch_bounds__(256) void through_kernel(const float* from, float* to, int64_t n4) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256)
+    reinterpret_cast<float4*>(to)[i] = from ? reinterpret_cast<const float4*>(from)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <bool F32, bool MANY, bool SUMS>
+hipError_t chunks_of(const Chunks& a, int A, int B, hipStream_t s) {
+  const dim3 g((uint32_t)((int64_t)a.batch * a.heads * a.parts * a.slices));
+  if (B == 64) {
+    if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS><<<g, 128, 0, s>>>(a);
+    else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS><<<g, 128, 0, s>>>(a);
+    else chunk_kernel<F32, 256, 2, MANY, SUMS><<<g, 128, 0, s>>>(a);
+  } else {
+    if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS><<<g, 256, 0, s>>>(a);
+    else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS><<<g, 256, 0, s>>>(a);
+    else chunk_kernel<F32, 256, 4, MANY, SUMS><<<g, 256, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <bool MANY, bool SUMS>
+hipError_t chunks(const Chunks& a, int A, int B, bool f32, hipStream_t s) {
+  return f32 ? chunks_of<true, MANY, SUMS>(a, A, B, s) : chunks_of<false, MANY, SUMS>(a, A, B, s);
+}
+
+int slices_of(int B) { return B == 256 ? 2 : 1; }
+
+Chunks base_of(const LinearLaunch& a, int B) {
+  Chunks c = {};
+  c.log_decay = a.log_decay, c.starts = a.starts;
+  c.batch = a.batch, c.tokens = a.tokens, c.heads = a.kv_heads, c.parts = a.parts, c.part_rows = a.part_rows;
+  c.slices = slices_of(B);
+  const int64_t size = (int64_t)a.dk * a.dv;
+  c.state_head = c.out_head = size, c.state_seq = c.out_seq = size * a.kv_heads;
+  return c;
+}
+
+// The parts' sums in `sums`, then what stands before each part.
+template <bool MANY>
+hipError_t before_parts(Chunks c, const LinearLaunch& a, const float* first, float* sums, hipStream_t s) {
+  const int size = a.dk * a.dv;
+  c.out = sums, c.out_part = size, c.out_head = (int64_t)size * a.parts, c.out_seq = c.out_head * a.kv_heads;
+  hipError_t e = chunks<MANY, true>(c, a.dk, a.dv, a.f32, s);
+  if (e != hipSuccess) return e;
+  scan_kernel<<<(uint32_t)((int64_t)a.batch * a.kv_heads * (size / (4 * kScanThreads))), kScanThreads, 0, s>>>(
+      sums, first, a.log_decay, a.starts, a.batch, a.tokens, a.kv_heads, a.parts, a.part_rows, size);
+  return hipGetLastError();
+}
+
+// Where the states before a part are: in `sums`, or with one part the first.
+void states_from(Chunks* c, const LinearLaunch& a, const float* first, const float* sums) {
+  if (a.parts == 1) {
+    c->state = first;
+    return;
+  }
+  const int64_t size = (int64_t)a.dk * a.dv;
+  c->state = sums, c->state_part = size, c->state_head = size * a.parts, c->state_seq = c->state_head * a.kv_heads;
+}
+
+template <bool F32, int G>
+hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
+  const dim3 g((uint32_t)((int64_t)a.batch * a.kv_heads * (a.dv / 32)));
+  if (a.dk == 64) token_kernel<F32, 64, G><<<g, 256, 0, s>>>(a);
+  else if (a.dk == 128) token_kernel<F32, 128, G><<<g, 256, 0, s>>>(a);
+  else token_kernel<F32, 256, G><<<g, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool linear_few(int max_new) { return max_new <= 8; }
+
+void linear_parts(LinearLaunch* a) {
+  const int rows = a->f32 ? 32 : 64;
+  const int64_t states = (int64_t)a->batch * a->kv_heads * slices_of(a->dv);
+  const int64_t want = std::max<int64_t>(1, 512 / states);
+  const int64_t most = std::max<int64_t>(1, a->max_new / (4 * rows));
+  const int64_t parts = std::min(want, most);
+  a->part_rows = (int)((((int64_t)a->max_new + parts - 1) / parts + rows - 1) / rows * rows);
+  a->parts = (int)(((int64_t)a->max_new + a->part_rows - 1) / a->part_rows);
+}
+
+hipError_t launch_linear(const LinearLaunch& a, hipStream_t s) {
+  if (linear_few(a.max_new)) {
+    const int group = a.q.heads / a.kv_heads;
+    if (group == 1) return a.f32 ? tokens_of<true, 1>(a, s) : tokens_of<false, 1>(a, s);
+    return a.f32 ? tokens_of<true, 4>(a, s) : tokens_of<false, 4>(a, s);
+  }
+  Chunks c = base_of(a, a.dv);
+  c.q = a.q, c.k = a.k, c.v = a.v, c.o = a.o;
+  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f;
+  if (a.parts > 1) {
+    const hipError_t e = before_parts<false>(c, a, a.first, a.sums, s);
+    if (e != hipSuccess) return e;
+  }
+  states_from(&c, a, a.first, a.sums);
+  c.out = a.last;
+  return chunks<false, false>(c, a.dk, a.dv, a.f32, s);
+}
+
+hipError_t launch_linear_backward(const LinearBackLaunch& b, hipStream_t s) {
+  const LinearLaunch& a = b.f;
+  hipError_t e;
+  // dq, from the states before each part
+  Chunks c = base_of(a, a.dv);
+  c.k = a.k, c.v = a.v;
+  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f;
+  if (a.parts > 1 && (e = before_parts<false>(c, a, a.first, a.sums, s)) != hipSuccess) return e;
+  states_from(&c, a, a.first, a.sums);
+  c.slices = slices_of(a.dk);
+  c.q = b.d_o, c.k = a.v, c.v = a.k, c.o = b.dq, c.state_turned = 1;
+  if ((e = chunks<false, false>(c, a.dv, a.dk, a.f32, s)) != hipSuccess) return e;
+  // dk and dv, from the gradients of the states behind each part
+  c = base_of(a, a.dv);
+  c.k = a.q, c.v = b.d_o;
+  c.lead = 0, c.back = 1, c.s_in = a.scale, c.s_out = 1.f, c.s_up = a.scale;
+  const bool many = a.q.heads > a.kv_heads;
+  if (a.parts > 1) {
+    e = many ? before_parts<true>(c, a, b.d_last, b.back_sums, s) : before_parts<false>(c, a, b.d_last, b.back_sums, s);
+    if (e != hipSuccess) return e;
+  }
+  states_from(&c, a, b.d_last, b.back_sums);
+  Chunks d = c;
+  d.slices = slices_of(a.dk);
+  d.q = a.v, d.k = b.d_o, d.v = a.q, d.o = b.dk, d.state_turned = 1;
+  e = many ? chunks<true, false>(d, a.dv, a.dk, a.f32, s) : chunks<false, false>(d, a.dv, a.dk, a.f32, s);
+  if (e != hipSuccess) return e;
+  c.q = a.k, c.o = b.dv, c.out = b.d_first;
+  return many ? chunks<true, false>(c, a.dk, a.dv, a.f32, s) : chunks<false, false>(c, a.dk, a.dv, a.f32, s);
+}
+
+hipError_t launch_linear_through(const LinearBackLaunch& b, hipStream_t s) {
+  const int64_t n4 = (int64_t)b.f.batch * b.f.kv_heads * b.f.dk * b.f.dv / 4;
+  if (b.d_first == b.d_last) return hipSuccess;
+  through_kernel<<<(uint32_t)std::min<int64_t>((n4 + 255) / 256, 4096), 256, 0, s>>>(b.d_last, b.d_first, n4);
+  return hipGetLastError();
+}
+
+}  // namespace tttk
