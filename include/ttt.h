@@ -694,7 +694,9 @@ ttt_status ttt_linear_attention(const ttt_linear* linear, const ttt_rows* q, con
  *   d_state0 out, fp32: the gradient of S before the first token, or NULL; may
  *            be d_state
  * log_decay and scale get no gradient. Arithmetic as in the forward, for any
- * number of rows; a NaN or an infinity in d_o reaches only its own row of dq. */
+ * number of rows. A NaN or an infinity reaches the rows whose gradients depend
+ * on it, and where query heads share a state up to 63 rows of dk and dv behind
+ * it. */
 ttt_status ttt_linear_attention_backward_workspace_size(const ttt_linear* linear, size_t* bytes);
 ttt_status ttt_linear_attention_backward(const ttt_linear* linear, const ttt_rows* d_o,
                                          const ttt_rows* q, const ttt_rows* k, const ttt_rows* v,

@@ -39,9 +39,11 @@ struct Chunks {
   float s_in, s_out, s_up;
 };
 
-// Tiles of rows in LDS, swizzled by 16-byte pieces so that a read of 8
-// consecutive rows at one piece, and a read of 4 rows of 4 neighbouring pieces
-// (the transposing read), each fall on different banks.
+// Tiles of rows in LDS, swizzled by 16-byte pieces. LDS takes a wave's 16-byte
+// reads 16 lanes at a time, lanes 0-3, 12-15 and 20-27 first, then the other
+// half of 32: in each of these groups one piece of every lane's row has to fall
+// on another 16 bytes of the 256 of all banks. So do, for a transposing read,
+// four neighbouring pieces of each of four neighbouring rows.
 template <bool F32>
 struct Elem {
   static constexpr int size = F32 ? 4 : 2;
@@ -53,11 +55,11 @@ struct Elem {
 template <bool F32, int W>  // W values a row
 struct Tile {
   static constexpr int pieces = W * Elem<F32>::size / 16;
-  static __device__ __forceinline__ int swz(int row) {
+  static constexpr __device__ __forceinline__ int swz(int row) {
     if constexpr (pieces >= 16)
-      return ((row & 1) << 2) | ((row >> 1) & 3) | (((row >> 1) & 1) << 3);
+      return ((row & 3) << 2) | ((row >> 2) & 3);
     else
-      return (((row >> 1) & 1) << 2) | (row & 1) | (((row >> 2) & 1) << 1);
+      return ((row >> 1) & 3) | (((row >> 1) ^ (row >> 3)) & 1) << 2;
   }
   static __device__ __forceinline__ uint32_t at(int row, int piece) {
     return (uint32_t)(row * pieces + (piece ^ swz(row))) * 16;
@@ -65,10 +67,11 @@ struct Tile {
 };
 
 // c + a b over kb values of the contraction: one 32x32x16 product of bf16, or
-// four 32x32x2 of fp32. Lane l holds row (column) l % 32 and, of the
-// contraction's values, those at 4 (l / 32) + e, for bf16 the further ones 8
-// on (e = 0 .. 3): the order in which a product's result holds its rows, so
-// that states and weights go from one product to the next in registers.
+// four 32x32x2 of fp32. A lane holds row (column) l % 32 and half of the
+// contraction's values; which ones does not matter as long as both operands
+// agree. They are chosen so that a product's result, whose lanes hold rows 8a +
+// 4 (l / 32) + e, can be an operand of the next one from its registers: states
+// and weights never leave them.
 template <bool F32>
 __device__ __forceinline__ f32x16_t mma(const uint4& a, const uint4& b, f32x16_t c) {
   if constexpr (F32) {
@@ -88,9 +91,19 @@ typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 // pieces are xored into (a row's pieces are a power of two, so a swizzled piece
 // is the row's start xor the swizzle xor the piece). They are kept from being
 // known across chunks: the compiler would hold an address for every read.
+//
+// For bf16, columns come turned: lane l has column l with bits 2 and 3
+// exchanged. A product's rows, in such an order, are held with a lane's eight of
+// every 16 as neighbours: what it meets next is one piece of 16 bytes, and so is
+// what it stores.
+template <bool F32>
+__device__ __forceinline__ int column_of(int l) {
+  return F32 ? l : (l & ~12) | (l & 4) << 1 | (l & 8) >> 1;
+}
 template <bool F32, int W>
 struct Reader {
   static constexpr int row_bytes = W * Elem<F32>::size;
+  static constexpr uint32_t eight = 16 * Tile<F32, W>::swz(8);  // what eight rows change in a piece's place
   uint32_t r, c[F32 ? 4 : 1];
   __device__ __forceinline__ Reader() {
     const int lane = threadIdx.x & 63, hf = lane >> 5;
@@ -99,11 +112,11 @@ struct Reader {
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[e] = Tile<true, W>::at(4 * hf + e, (lane & 31) >> 2) + (lane & 3) * 4;
     } else {
-      r = Tile<false, W>::at(lane & 31, 0) + 8 * hf;
-      // a transposing read: lane 4e + j of 16 addresses row e, columns 4j .. +
-      // 3, and lane i gets column i of the four rows
-      const int e = (lane >> 2) & 3, j = lane & 3;
-      c[0] = Tile<false, W>::at(4 * hf + e, 2 * ((lane >> 4) & 1) + (j >> 1)) + (j & 1) * 8;
+      r = Tile<false, W>::at(lane & 31, hf);
+      // a transposing read: lane 4e + j of 16 addresses four values of row e,
+      // and lane i gets value i % 4 of lane i / 4's of the four rows
+      const int e = (lane >> 2) & 3, j = lane & 3, k = (j >> 1) | (j & 1) << 1;
+      c[0] = Tile<false, W>::at(4 * hf + e, 2 * ((lane >> 4) & 1) + (k >> 1)) + (k & 1) * 8;
     }
   }
   __device__ __forceinline__ void forget() {
@@ -111,29 +124,24 @@ struct Reader {
 #pragma unroll
     for (int e = 0; e < (F32 ? 4 : 1); ++e) asm volatile("" : "+v"(c[e]));
   }
-  // The lane's row 32 rt + l % 32, contraction block kb of the row's values.
+  // The lane's row 32 rt + l % 32 and of its values those of piece 2 kb + l / 32.
   __device__ __forceinline__ uint4 row(const char* tile, int rt, int kb) const {
-    const char* p = tile + 32 * rt * row_bytes;
-    if constexpr (F32) {
-      return *reinterpret_cast<const uint4*>(p + (r ^ (uint32_t)(kb * 32)));
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(p + (r ^ (uint32_t)(kb * 32)));
-      const uint2 y = *reinterpret_cast<const uint2*>(p + (r ^ (uint32_t)(kb * 32 + 16)));
-      return make_uint4(x.x, x.y, y.x, y.y);
-    }
+    return *reinterpret_cast<const uint4*>(tile + 32 * rt * row_bytes + (r ^ (uint32_t)(kb * 32)));
   }
-  // The lane's column 32 cb + l % 32 of the rows of block kb.
+  // The lane's column of 32 from 32 cb (column_of(l % 32) of them) of the rows of
+  // block kb.
   __device__ __forceinline__ uint4 col(const char* tile, int kb, int cb) const {
     const char* p = tile + Elem<F32>::kb * kb * row_bytes;
     if constexpr (F32) {
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(p + (c[e] ^ (uint32_t)(cb * 128)));
+      for (int e = 0; e < 4; ++e)
+        w[e] = *reinterpret_cast<const uint32_t*>(p + (c[e] ^ (uint32_t)(cb * 128 ^ (kb & 1) * eight)));
       return make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       const uint32_t at = c[0] ^ (uint32_t)(cb * 64);
       const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + at));
-      const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + at + 8 * row_bytes));
+      const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + (at ^ eight) + 8 * row_bytes));
       const uint2 u = __builtin_bit_cast(uint2, x), w = __builtin_bit_cast(uint2, y);
       return make_uint4(u.x, u.y, w.x, w.y);
     }
@@ -159,42 +167,49 @@ __device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4 (&f)[
 // g^n for a whole n >= 0; 1 for n = 0 whatever g is.
 __device__ __forceinline__ float power(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
 
-// Rows [first, first + count) of a sequence that starts at row `base`, counted
-// from its end if back, into a tile; rows from count on are zero. Returns
-// whether any value is infinite or NaN (only asked of v).
-template <bool F32, int W, int NT, bool CHECK>
-__device__ __forceinline__ bool load_tile(char* tile, const Rows& x, int head, int col, int64_t row0, int dir, int count) {
-  constexpr int P = W * Elem<F32>::size / 16, N = Elem<F32>::rows * P / NT, R = NT / P;  // R rows at a time
+// A tile on its way: its rows are loaded to registers (get) while the kernel
+// works on others, and written to LDS (put) when their place is free. Rows
+// from `count` on are zero; dir -1 goes backwards from row0. put() tells, if
+// asked, whether a value is infinite or NaN.
+template <bool F32, int W, int NT>
+struct Fetch {
+  static constexpr int P = W * Elem<F32>::size / 16, R = NT / P;  // R rows at a time
+  static constexpr int N = Elem<F32>::rows / R;
   static_assert(NT % P == 0 && Elem<F32>::rows % R == 0, "whole passes");
-  const int r = threadIdx.x / P, c = threadIdx.x % P;
-  const int64_t stride = x.ts * Elem<F32>::size * dir;
-  const char* p = static_cast<const char*>(x.p) + (head * x.hs + col + row0 * x.ts) * Elem<F32>::size + r * stride + c * 16;
   uint4 v[N];
+  __device__ __forceinline__ void get(const Rows& x, int head, int col, int64_t row0, int dir, int count) {
+    const int r = threadIdx.x / P, c = threadIdx.x % P;
+    const int64_t stride = x.ts * Elem<F32>::size * dir;
+    const char* p = static_cast<const char*>(x.p) + (head * x.hs + col + row0 * x.ts) * Elem<F32>::size + r * stride + c * 16;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (r + i * R < count) v[i] = *reinterpret_cast<const uint4*>(p);
-    p += R * stride;
-  }
-  bool odd = false;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (CHECK) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (F32)
-          odd |= (w[e] & 0x7f800000u) == 0x7f800000u;
-        else
-          odd |= (w[e] & 0x7f800000u) == 0x7f800000u || (w[e] & 0x7f80u) == 0x7f80u;
-      }
+    for (int i = 0; i < N; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r + i * R < count) v[i] = *reinterpret_cast<const uint4*>(p);
+      p += R * stride;
     }
-    *reinterpret_cast<uint4*>(tile + Tile<F32, W>::at(r + i * R, c)) = v[i];
   }
-  return odd;
-}
-
-constexpr int kStoreRow = 40;  // values of a row of a wave's outputs in LDS, 32 and some against bank conflicts
+  template <bool CHECK>
+  __device__ __forceinline__ bool put(char* tile) const {
+    const int r = threadIdx.x / P, c = threadIdx.x % P;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (CHECK) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // an exponent of all ones carries into the sign's place
+          if constexpr (F32)
+            bits |= (w[e] & 0x7f800000u) + 0x00800000u;
+          else
+            bits |= (w[e] & 0x7f807f80u) + 0x00800080u;
+        }
+      }
+      *reinterpret_cast<uint4*>(tile + Tile<F32, W>::at(r + i * R, c)) = v[i];
+    }
+    return (bits & (F32 ? 0x80000000u : 0x80008000u)) != 0;
+  }
+};
 
 // One part of a sequence's rows for one state head and a slice of NW * 32 of
 // the B columns; wave w has columns 32 w .. of the slice, with its part of the
@@ -217,8 +232,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
   __shared__ __attribute__((aligned(16))) char kt[kBytesA];
   __shared__ __attribute__((aligned(16))) char vt[kBytesB];
   __shared__ __attribute__((aligned(16))) char qt[SUMS ? 16 : kBytesA];
-  __shared__ __attribute__((aligned(16))) char ot[SUMS || F32 ? 16 : NW * C * kStoreRow * 2];
-  __shared__ __attribute__((aligned(16))) float row_f[C], up_f[C], off_f[32];
+  __shared__ __attribute__((aligned(16))) float up_f[C], off_f[32];
   Reader<F32, A> ra;
   Reader<F32, B> rb;
 
@@ -243,106 +257,134 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
   const int64_t end = last ? len : mine + a.part_rows;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hf = lane >> 5, col = lane & 31;
-  const int b0 = slice * B + wave * 32 + col;  // the lane's column
+  const int b0 = slice * B + wave * 32 + column_of<F32>(col);  // the lane's column of the state
   const int b_all = a.slices * B;
   const float lg = a.log_decay[head] * kLog2e;
 
-  for (int i = threadIdx.x; i < C; i += NT) row_f[i] = a.s_out * power(lg, i + a.lead);
+  float row_f[RT];  // of the lane's row of x
+#pragma unroll
+  for (int it = 0; it < RT; ++it) row_f[it] = a.s_out * power(lg, 32 * it + col + a.lead);
   for (int i = threadIdx.x; i < 32; i += NT) off_f[i] = a.s_in * power(lg, 32 - i);
   auto set_up = [&](int count) {
     for (int i = threadIdx.x; i < C; i += NT) up_f[i] = a.s_up * power(lg, max(count - a.lead - i, 0));
   };
   set_up(C);
   int up_for = C;
-  float diag[16];  // s_in g^(i - j) of a 32 x 32 block on the diagonal
-  float far = 0.f;
-  if constexpr (!SUMS) {
+  // s_in g^(i - j) of a 32 x 32 block on the diagonal, as the lanes hold it
+  __shared__ float4 diag[SUMS ? 1 : 4][64];
+  const float far = power(lg, col);
+  if (!SUMS && wave == 0) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) diag[r] = a.s_in * power(lg, max(col - (8 * (r >> 2) + 4 * hf + (r & 3)), 0));
-    far = power(lg, col);
+    for (int u = 0; u < 4; ++u) {
+      const int n = col - 8 * u - 4 * hf;
+      diag[SUMS ? 0 : u][lane] = make_float4(a.s_in * power(lg, max(n, 0)), a.s_in * power(lg, max(n - 1, 0)),
+                                             a.s_in * power(lg, max(n - 2, 0)), a.s_in * power(lg, max(n - 3, 0)));
+    }
   }
 
+  // value r of a lane's 16 of a state is row state_row(r) + state_hf of the 32
+  auto state_row = [](int r) { return F32 ? 8 * (r >> 2) + (r & 3) : 16 * (r >> 3) + (r & 7); };
+  const int state_hf = (F32 ? 4 : 8) * hf;
   f32x16_t st[AT];
   if (!SUMS && a.state != nullptr) {
     const float* e = a.state + seq * a.state_seq + head * a.state_head + part * a.state_part;
-    e += a.state_turned ? (int64_t)b0 * A + 4 * hf : (int64_t)(4 * hf) * b_all + b0;
+    e += a.state_turned ? (int64_t)b0 * A + state_hf : (int64_t)state_hf * b_all + b0;
     const int step = a.state_turned ? 1 : b_all;
 #pragma unroll
     for (int t = 0; t < AT; ++t)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) st[t][r] = e[(32 * t + 8 * (r >> 2) + (r & 3)) * step];
+      for (int r = 0; r < 16; ++r) st[t][r] = e[(32 * t + state_row(r)) * step];
   } else {
 #pragma unroll
     for (int t = 0; t < AT; ++t) st[t] = f32x16_t{};
   }
 
   const int q_heads = MANY ? 1 : a.q.heads / a.heads, k_heads = MANY ? a.k.heads / a.heads : 1;
-  for (int64_t t0 = mine; t0 < end;) {
-    int take = (int)min((int64_t)C, end - t0);
-    const int dir = a.back ? -1 : 1;
-    const int64_t row0 = a.back ? base + len - 1 - t0 : base + t0;
+  const int dir = a.back ? -1 : 1;
+  int64_t t0 = mine, row0 = a.back ? base + len - 1 - t0 : base + t0;
+  int take = (int)min((int64_t)C, end - t0);
+  Fetch<F32, A, NT> fk, fq;
+  Fetch<F32, B, NT> fv;
+  fk.get(a.k, head * k_heads, 0, row0, dir, take);
+  fv.get(a.v, head * k_heads, slice * B, row0, dir, take);
+  if constexpr (!SUMS) fq.get(a.q, head * q_heads, 0, row0, dir, take);
+  while (t0 < end) {
     ra.forget();
     rb.forget();
 
-    // x = the product of the rows (in qt) with the state before them
-    auto with_state = [&](f32x16_t(&x)[RT]) {
-      // (so that its conversion stays inside the loop over heads: it would take
-      // as many registers again)
-#pragma unroll
-      for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
-#pragma unroll
-      for (int it = 0; it < RT; ++it) x[it] = f32x16_t{};
-#pragma unroll
-      for (int kb = 0; kb < A / KB; ++kb) {
-        uint4 sf[TS];
-        as_operand<F32, TS>(st[kb / PER], kb % PER, sf);
-#pragma unroll
-        for (int it = 0; it < RT; ++it) {
-          const uint4 qf = ra.row(qt, it, kb);
-#pragma unroll
-          for (int t = 0; t < TS; ++t) x[it] = mma<F32>(qf, sf[t], x[it]);
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < RT; ++it)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 f = *reinterpret_cast<const float4*>(&row_f[32 * it + 8 * u + 4 * hf]);
-          x[it][4 * u] *= f.x, x[it][4 * u + 1] *= f.y, x[it][4 * u + 2] *= f.z, x[it][4 * u + 3] *= f.w;
-        }
-    };
-    // x += what the chunk's own rows up to each give
-    auto with_rows = [&](const uint4(&vf)[C / KB], f32x16_t(&x)[RT]) {
+    // x of every row tile (column i: its row) = its product with the state before
+    // the chunk, and p (rows j of tile jt <= it, column i) = that with k, side by
+    // side: what is read of the next values of A has the time of seven products
+    auto products = [&](bool state, bool rows, f32x16_t(&x)[RT], f32x16_t(&p)[RT * (RT + 1) / 2]) {
+      uint4 qn[RT], kn[RT];
 #pragma unroll
       for (int it = 0; it < RT; ++it) {
-        f32x16_t p[RT];  // rows j of tile jt, column i
+        qn[it] = ra.row(qt, it, 0);
+        if (rows) kn[it] = ra.row(kt, it, 0);
+        if (state) x[it] = f32x16_t{};
 #pragma unroll
-        for (int jt = 0; jt <= it; ++jt) p[jt] = f32x16_t{};
+        for (int jt = 0; jt <= it; ++jt)
+          if (rows) p[it * (it + 1) / 2 + jt] = f32x16_t{};
+      }
 #pragma unroll
-        for (int kb = 0; kb < A / KB; ++kb) {
-          const uint4 qf = ra.row(qt, it, kb);
+      for (int kb = 0; kb < A / KB; ++kb) {
+        uint4 qf[RT], kf[RT], sf[TS];
 #pragma unroll
-          for (int jt = 0; jt <= it; ++jt) p[jt] = mma<F32>(ra.row(kt, jt, kb), qf, p[jt]);
+        for (int it = 0; it < RT; ++it) {
+          qf[it] = qn[it], kf[it] = kn[it];
+          if (kb + 1 < A / KB) {
+            qn[it] = ra.row(qt, it, kb + 1);
+            if (rows) kn[it] = ra.row(kt, it, kb + 1);
+          }
+        }
+        if (rows) {
+#pragma unroll
+          for (int it = 0; it < RT; ++it)
+#pragma unroll
+            for (int jt = 0; jt <= it; ++jt)
+              p[it * (it + 1) / 2 + jt] = mma<F32>(kf[jt], qf[it], p[it * (it + 1) / 2 + jt]);
+        }
+        if (state) {
+          as_operand<F32, TS>(st[kb / PER], kb % PER, sf);
+#pragma unroll
+          for (int t = 0; t < TS; ++t)
+#pragma unroll
+            for (int it = 0; it < RT; ++it) x[it] = mma<F32>(sf[t], qf[it], x[it]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (state) {
+#pragma unroll
+        for (int it = 0; it < RT; ++it)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[it][r] *= row_f[it];
+      }
+    };
+    // x += the weights p times their decays, times v
+    auto weigh = [&](int it, const uint4(&vf)[C / KB], f32x16_t* p, f32x16_t& x) {
+#pragma unroll
+      for (int jt = 0; jt <= it; ++jt) {
+        if (jt == it) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float4 f = diag[SUMS ? 0 : u][lane];
+            const int n = col - 8 * u - 4 * hf;  // (a weight that is not taken may be a NaN)
+            p[jt][4 * u] = n < 0 ? 0.f : p[jt][4 * u] * f.x, p[jt][4 * u + 1] = n < 1 ? 0.f : p[jt][4 * u + 1] * f.y;
+            p[jt][4 * u + 2] = n < 2 ? 0.f : p[jt][4 * u + 2] * f.z, p[jt][4 * u + 3] = n < 3 ? 0.f : p[jt][4 * u + 3] * f.w;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float4 f = *reinterpret_cast<const float4*>(&off_f[8 * u + 4 * hf]);
+            p[jt][4 * u] *= f.x * far, p[jt][4 * u + 1] *= f.y * far;
+            p[jt][4 * u + 2] *= f.z * far, p[jt][4 * u + 3] *= f.w * far;
+          }
         }
 #pragma unroll
-        for (int jt = 0; jt <= it; ++jt) {
-          if (jt == it) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) p[jt][r] = 8 * (r >> 2) + 4 * hf + (r & 3) > col ? 0.f : p[jt][r] * diag[r];
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float4 f = *reinterpret_cast<const float4*>(&off_f[8 * u + 4 * hf]);
-              p[jt][4 * u] *= f.x * far, p[jt][4 * u + 1] *= f.y * far;
-              p[jt][4 * u + 2] *= f.z * far, p[jt][4 * u + 3] *= f.w * far;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < PER; ++u) {
-            uint4 w[1];
-            as_operand<F32, 1>(p[jt], u, w);
-            x[it] = mma<F32>(w[0], vf[jt * PER + u], x[it]);
-          }
+        for (int u = 0; u < PER; ++u) {
+          uint4 w[1];
+          as_operand<F32, 1>(p[jt], u, w);
+          x = mma<F32>(vf[jt * PER + u], w[0], x);
         }
       }
     };
@@ -350,37 +392,21 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
 #pragma unroll
       for (int kb = 0; kb < C / KB; ++kb) vf[kb] = rb.col(vt, kb, wave);
     };
-    // bf16 values go through the wave's own LDS, so that rows leave in pieces
-    // of 16 bytes
-    auto store = [&](int q_head, const f32x16_t(&x)[RT]) {
+    // Row tile `it` of a head's outputs.
+    auto store = [&](int it, int q_head, const f32x16_t& x, int64_t row0, int take) {
+      if (32 * it + col >= take) return;
+      const int64_t to = (row0 + (int64_t)((32 * it + col) * dir)) * a.o.ts + q_head * a.o.hs + slice * B + wave * 32;
       if constexpr (F32) {
-        const int64_t ts = a.o.ts * dir;
-        float* to = static_cast<float*>(a.o.p) + row0 * a.o.ts + q_head * a.o.hs + b0 + 4 * hf * ts;
 #pragma unroll
-        for (int it = 0; it < RT; ++it)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e, to += ts)
-              if (32 * it + 8 * u + 4 * hf + e < take) *to = x[it][4 * u + e];
-            to += 4 * ts;
-          }
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.o.p) + to + 8 * u + 4 * hf) =
+              make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
       } else {
-        u16* mine = reinterpret_cast<u16*>(ot) + wave * C * kStoreRow;
 #pragma unroll
-        for (int it = 0; it < RT; ++it)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            mine[(32 * it + 8 * (r >> 2) + 4 * hf + (r & 3)) * kStoreRow + col] = bf16_rne(x[it][r]);
-        const int64_t ts = a.o.ts * dir;
-        u16* to = static_cast<u16*>(a.o.p) + row0 * a.o.ts + q_head * a.o.hs + slice * B + wave * 32 + (lane & 3) * 8 +
-                  (lane >> 2) * ts;
-#pragma unroll
-        for (int n = 0; n < C / 16; ++n, to += 16 * ts) {
-          const int i = 16 * n + (lane >> 2);
-          const uint4 w = *reinterpret_cast<const uint4*>(mine + i * kStoreRow + (lane & 3) * 8);
-          if (i < take) *reinterpret_cast<uint4*>(to) = w;
-        }
+        for (int u = 0; u < 2; ++u)
+          *reinterpret_cast<uint4*>(static_cast<u16*>(a.o.p) + to + 16 * u + 8 * hf) =
+              make_uint4(pack_bf16(x[8 * u], x[8 * u + 1]), pack_bf16(x[8 * u + 2], x[8 * u + 3]),
+                         pack_bf16(x[8 * u + 4], x[8 * u + 5]), pack_bf16(x[8 * u + 6], x[8 * u + 7]));
       }
     };
     // st += (k decayed)^T v of the chunk in LDS
@@ -410,92 +436,124 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
 #pragma unroll
           for (int x = 0; x < TU; ++x) st[t] = mma<F32>(kf, u[x], st[t]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    if constexpr (!MANY) {
-      // k and v once, heads of q in turn
-      __syncthreads();  // (the tiles' last readers are done)
-      load_tile<F32, A, NT, false>(kt, a.k, head, 0, row0, dir, take);
-      bool odd = load_tile<F32, B, NT, true>(vt, a.v, head, slice * B, row0, dir, take);
-      if constexpr (!SUMS) load_tile<F32, A, NT, false>(qt, a.q, head * q_heads, 0, row0, dir, take);
-      if (__syncthreads_or(!SUMS && odd && take > 1)) {
+    // the next chunk's tiles, behind this one's `take` rows
+    const int64_t row_now = row0;
+    auto next = [&](int now) {
+      t0 += now, row0 += now * dir;
+      // (a count of 0 behind the end: without a value of their own here, the
+      // registers would be taken through the whole loop)
+      take = (int)min((int64_t)C, end - t0);
+      fk.get(a.k, head * k_heads, 0, row0, dir, take);
+      fv.get(a.v, head * k_heads, slice * B, row0, dir, take);
+      if constexpr (!SUMS) fq.get(a.q, head * q_heads, 0, row0, dir, take);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int now = take;
+    uint4 vf[C / KB];
+    __syncthreads();  // (the tiles' last readers are done)
+    fk.template put<false>(kt);
+    bool odd = fv.template put<!SUMS && !MANY>(vt);
+    if constexpr (!SUMS) fq.template put<false>(qt);
+    if constexpr (!SUMS && !MANY) {
+      if (__syncthreads_or(odd && now > 1)) {
         // an infinity or a NaN times a later row's weight of 0 would be NaN:
         // such a chunk is taken a row at a time
-        take = 1;
-        load_tile<F32, A, NT, false>(kt, a.k, head, 0, row0, dir, take);
-        load_tile<F32, B, NT, false>(vt, a.v, head, slice * B, row0, dir, take);
+        now = 1;
+        fk.get(a.k, head, 0, row0, dir, now);
+        fv.get(a.v, head, slice * B, row0, dir, now);
+        fk.template put<false>(kt);
+        fv.template put<false>(vt);
         __syncthreads();
       }
-      if (take != up_for) {
-        set_up(take);
-        up_for = take;
-        __syncthreads();
-      }
-      uint4 vf[C / KB];
+    } else {
+      __syncthreads();
+    }
+    if (now != up_for) {
+      set_up(now);
+      up_for = now;
+      __syncthreads();
+    }
+    const float g = power(lg, now);
+    if constexpr (!MANY) {
+      // k and v once, heads of q in turn
       load_v(vf);
       if constexpr (!SUMS) {
         for (int h = 0; h < q_heads; ++h) {
-          if (h > 0) {
+          fq.get(a.q, head * q_heads + h + 1, 0, row0, dir, h + 1 < q_heads ? now : 0);
+          __builtin_amdgcn_sched_barrier(0);
+          // (so that the state's conversion stays inside the loop: kept over the
+          // heads it would take as many registers again)
+#pragma unroll
+          for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
+          f32x16_t x[RT], p[RT * (RT + 1) / 2];
+          products(true, true, x, p);
+#pragma unroll
+          for (int it = 0; it < RT; ++it) {
+            weigh(it, vf, p + it * (it + 1) / 2, x[it]);
+            store(it, head * q_heads + h, x[it], row_now, now);
+          }
+          if (h + 1 < q_heads) {
             __syncthreads();
-            load_tile<F32, A, NT, false>(qt, a.q, head * q_heads + h, 0, row0, dir, take);
+            fq.template put<false>(qt);
             __syncthreads();
           }
-          f32x16_t x[RT];
-          with_state(x);
-          with_rows(vf, x);
-          store(head * q_heads + h, x);
         }
       }
-      const float g = power(lg, take);
+      next(now);
 #pragma unroll
-      for (int t = 0; t < AT; ++t) st[t] *= g;
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) st[t][r] *= g;
       update(vf);
     } else {
       // q once, heads of k and v in turn
-      __syncthreads();
-      if constexpr (!SUMS) {
-        load_tile<F32, A, NT, false>(qt, a.q, head, 0, row0, dir, take);
-      }
-      if constexpr (!SUMS) {
-        bool odd = false;
-        for (int h = 0; h < k_heads; ++h) {  // (as above, for any of the heads)
-          if (h > 0) __syncthreads();
-          odd |= load_tile<F32, B, NT, true>(vt, a.v, head * k_heads + h, slice * B, row0, dir, take);
-        }
-        if (__syncthreads_or(odd && take > 1)) take = 1;
-      }
-      if (take != up_for) {
-        set_up(take);
-        up_for = take;
-      }
       f32x16_t x[RT];
-      if constexpr (!SUMS) with_state(x);
-      const float g = power(lg, take);
+      if constexpr (!SUMS) {
+        f32x16_t p[RT * (RT + 1) / 2];
+        products(true, false, x, p);
+      }
 #pragma unroll
-      for (int t = 0; t < AT; ++t) st[t] *= g;
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) st[t][r] *= g;
       for (int h = 0; h < k_heads; ++h) {
-        __syncthreads();
-        load_tile<F32, A, NT, false>(kt, a.k, head * k_heads + h, 0, row0, dir, take);
-        load_tile<F32, B, NT, false>(vt, a.v, head * k_heads + h, slice * B, row0, dir, take);
-        __syncthreads();
-        uint4 vf[C / KB];
+        if (h > 0) {
+          __syncthreads();
+          fk.template put<false>(kt);
+          fv.template put<false>(vt);
+          __syncthreads();
+        }
         load_v(vf);
-        if constexpr (!SUMS) with_rows(vf, x);
+        if constexpr (!SUMS) {
+          f32x16_t p[RT * (RT + 1) / 2];
+          products(false, true, x, p);
+#pragma unroll
+          for (int it = 0; it < RT; ++it) weigh(it, vf, p + it * (it + 1) / 2, x[it]);
+        }
+        const int more = h + 1 < k_heads ? now : 0;
+        fk.get(a.k, head * k_heads + h + 1, 0, row_now, dir, more);
+        fv.get(a.v, head * k_heads + h + 1, slice * B, row_now, dir, more);
+        __builtin_amdgcn_sched_barrier(0);
         update(vf);
       }
-      if constexpr (!SUMS) store(head, x);
+      next(now);
+      if constexpr (!SUMS) {
+#pragma unroll
+        for (int it = 0; it < RT; ++it) store(it, head, x[it], row_now, now);
+      }
     }
-    t0 += take;
   }
 
   if (a.out != nullptr && (SUMS || last)) {
-    float* e = a.out + seq * a.out_seq + head * a.out_head + part * a.out_part;
+    float* e = a.out + seq * a.out_seq + head * a.out_head + part * a.out_part + (int64_t)state_hf * b_all + b0;
 #pragma unroll
     for (int t = 0; t < AT; ++t)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        e[(int64_t)(32 * t + 8 * (r >> 2) + 4 * hf + (r & 3)) * b_all + b0] = st[t][r];
+      for (int r = 0; r < 16; ++r) e[(32 * t + state_row(r)) * b_all] = st[t][r];
   }
 }
 
