@@ -148,6 +148,25 @@ struct Reader {
   }
 };
 
+// x and y as T bf16 terms (each the rounding of what those before it leave), in
+// pairs. What a rounding leaves is exact, and dot2 with (-1, 0) or (0, -1) gives
+// it without unpacking the pair. (A NaN or an infinity of one of the two makes
+// the other NaN: both go into the same sums.) The pairs are registers: the bits
+// of (0, -1) are those of fp32's -1, which the compiler would put into the
+// instruction as a constant that means another pair there.
+template <int T>
+__device__ __forceinline__ void terms(float x, float y, uint32_t (&w)[T]) {
+  uint32_t low = 0x0000bf80u, high = 0xbf800000u;
+  asm("" : "+s"(low), "+s"(high));
+  w[0] = pack_bf16(x, y);
+#pragma unroll
+  for (int t = 1; t < T; ++t) {
+    x = dot2(w[t - 1], low, x);
+    y = dot2(w[t - 1], high, y);
+    w[t] = pack_bf16(x, y);
+  }
+}
+
 // Values of a product's result (kb of its rows) as an operand: fp32 as they
 // are; as T terms of bf16.
 template <bool F32, int T>
@@ -158,7 +177,7 @@ __device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4 (&f)[
   } else {
     uint32_t w[4][T];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2<T>(x[8 * u + 2 * e], x[8 * u + 2 * e + 1], w[e]);
+    for (int e = 0; e < 4; ++e) terms<T>(x[8 * u + 2 * e], x[8 * u + 2 * e + 1], w[e]);
 #pragma unroll
     for (int t = 0; t < T; ++t) f[t] = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
   }
@@ -232,7 +251,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
   __shared__ __attribute__((aligned(16))) char kt[kBytesA];
   __shared__ __attribute__((aligned(16))) char vt[kBytesB];
   __shared__ __attribute__((aligned(16))) char qt[SUMS ? 16 : kBytesA];
-  __shared__ __attribute__((aligned(16))) float up_f[C], off_f[32];
+  __shared__ __attribute__((aligned(16))) float up_f[C];
   Reader<F32, A> ra;
   Reader<F32, B> rb;
 
@@ -264,24 +283,24 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
   float row_f[RT];  // of the lane's row of x
 #pragma unroll
   for (int it = 0; it < RT; ++it) row_f[it] = a.s_out * power(lg, 32 * it + col + a.lead);
-  for (int i = threadIdx.x; i < 32; i += NT) off_f[i] = a.s_in * power(lg, 32 - i);
   auto set_up = [&](int count) {
     for (int i = threadIdx.x; i < C; i += NT) up_f[i] = a.s_up * power(lg, max(count - a.lead - i, 0));
   };
   set_up(C);
   int up_for = C;
-  // s_in g^(i - j) of a 32 x 32 block on the diagonal, as the lanes hold it
-  __shared__ float4 diag[SUMS ? 1 : 4][64];
-  const float far = power(lg, col);
-  if (!SUMS && wave == 0) {
+  // s_in g^(i - j) of 32 x 32 blocks on the diagonal (0 for j > i) and beside it,
+  // as the lanes hold the weights
+  __shared__ float4 decay[SUMS ? 1 : RT][4][64];
+  if (!SUMS && wave < RT) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int n = col - 8 * u - 4 * hf;
-      diag[SUMS ? 0 : u][lane] = make_float4(a.s_in * power(lg, max(n, 0)), a.s_in * power(lg, max(n - 1, 0)),
-                                             a.s_in * power(lg, max(n - 2, 0)), a.s_in * power(lg, max(n - 3, 0)));
+      const int n = 32 * wave + col - 8 * u - 4 * hf;
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = n < e ? 0.f : a.s_in * power(lg, max(n - e, 0));
+      decay[SUMS ? 0 : wave][u][lane] = make_float4(f[0], f[1], f[2], f[3]);
     }
   }
-
   // value r of a lane's 16 of a state is row state_row(r) + state_hf of the 32
   auto state_row = [](int r) { return F32 ? 8 * (r >> 2) + (r & 3) : 16 * (r >> 3) + (r & 7); };
   const int state_hf = (F32 ? 4 : 8) * hf;
@@ -364,20 +383,13 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
     auto weigh = [&](int it, const uint4(&vf)[C / KB], f32x16_t* p, f32x16_t& x) {
 #pragma unroll
       for (int jt = 0; jt <= it; ++jt) {
-        if (jt == it) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float4 f = diag[SUMS ? 0 : u][lane];
-            const int n = col - 8 * u - 4 * hf;  // (a weight that is not taken may be a NaN)
-            p[jt][4 * u] = n < 0 ? 0.f : p[jt][4 * u] * f.x, p[jt][4 * u + 1] = n < 1 ? 0.f : p[jt][4 * u + 1] * f.y;
-            p[jt][4 * u + 2] = n < 2 ? 0.f : p[jt][4 * u + 2] * f.z, p[jt][4 * u + 3] = n < 3 ? 0.f : p[jt][4 * u + 3] * f.w;
-          }
-        } else {
+        for (int u = 0; u < 4; ++u) {
+          const float4 f = decay[SUMS ? 0 : it - jt][u][lane];
+          p[jt][4 * u] *= f.x, p[jt][4 * u + 1] *= f.y, p[jt][4 * u + 2] *= f.z, p[jt][4 * u + 3] *= f.w;
+          if (jt == it) {  // (a weight that is not taken may be a NaN)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float4 f = *reinterpret_cast<const float4*>(&off_f[8 * u + 4 * hf]);
-            p[jt][4 * u] *= f.x * far, p[jt][4 * u + 1] *= f.y * far;
-            p[jt][4 * u + 2] *= f.z * far, p[jt][4 * u + 3] *= f.w * far;
+            for (int e = 0; e < 4; ++e) p[jt][4 * u + e] = 8 * u + 4 * hf + e > col ? 0.f : p[jt][4 * u + e];
           }
         }
 #pragma unroll
@@ -426,7 +438,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
           uint32_t z[4][TU];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            split2<TU>(__uint_as_float(w[e] << 16) * m[2 * e], __uint_as_float(w[e] & 0xffff0000u) * m[2 * e + 1], z[e]);
+            terms<TU>(__uint_as_float(w[e] << 16) * m[2 * e], __uint_as_float(w[e] & 0xffff0000u) * m[2 * e + 1], z[e]);
 #pragma unroll
           for (int t = 0; t < TU; ++t) u[t] = make_uint4(z[0][t], z[1][t], z[2][t], z[3][t]);
         }
@@ -559,7 +571,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
 
 // The states before every part from the parts' own sums, in their place: E_0
 // is the state before the sequence (or zero), E_{p+1} = g^rows E_p + U_p.
-constexpr int kScanThreads = 256;
+constexpr int kScanThreads = 256, kScanAhead = 8;
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(float* sums, const float* first, const float* log_decay,
                                                             const int32_t* starts, int batch, int tokens, int heads,
                                                             int parts, int part_rows, int size) {
@@ -576,14 +588,23 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(float* sums, const f
   float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
   if (first) e = *reinterpret_cast<const float4*>(first + sh * size + i);
   float* p = sums + sh * parts * size + i;
-  for (int n = 0; n < parts; ++n, p += size) {
-    const bool more = n < parts - 1 && (int64_t)(n + 1) * part_rows < len;
-    float4 u;
-    if (more) u = *reinterpret_cast<const float4*>(p);
-    *reinterpret_cast<float4*>(p) = e;
-    if (!more) break;
-    e = make_float4(g * e.x + u.x, g * e.y + u.y, g * e.z + u.z, g * e.w + u.w);
+  // of these parts the sums are read, several at once; the one behind them only
+  // gets its state
+  const int whole = (int)min((int64_t)(parts - 1), max((len - 1) / part_rows, (int64_t)0));
+  for (int n = 0; n < whole; n += kScanAhead) {
+    float4 u[kScanAhead];
+#pragma unroll
+    for (int j = 0; j < kScanAhead; ++j)
+      if (n + j < whole) u[j] = *reinterpret_cast<const float4*>(p + (int64_t)j * size);
+#pragma unroll
+    for (int j = 0; j < kScanAhead; ++j)
+      if (n + j < whole) {
+        *reinterpret_cast<float4*>(p) = e;
+        e = make_float4(g * e.x + u[j].x, g * e.y + u[j].y, g * e.z + u[j].z, g * e.w + u[j].w);
+        p += size;
+      }
   }
+  *reinterpret_cast<float4*>(p) = e;
 }
 
 // A few tokens a sequence: the state's slice of SB columns is read once, kept
