@@ -230,6 +230,11 @@ struct Fetch {
   }
 };
 
+// A barrier for what the waves share through LDS alone. __syncthreads() also
+// waits for every load and store on its way to memory: those of the tiles that
+// are fetched ahead, and of the rows that leave, would stand in the way of each.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // One part of a sequence's rows for one state head and a slice of NW * 32 of
 // the B columns; wave w has columns 32 w .. of the slice, with its part of the
 // state in registers (fp32, 16 values a lane for each 32 of A).
@@ -252,6 +257,18 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
   __shared__ __attribute__((aligned(16))) char vt[kBytesB];
   __shared__ __attribute__((aligned(16))) char qt[SUMS ? 16 : kBytesA];
   __shared__ __attribute__((aligned(16))) float up_f[C];
+  __shared__ int votes[NW];
+  // A barrier, and whether x holds for any lane.
+  auto any_of = [&](bool x) {
+    if ((threadIdx.x & 63) == 0) votes[threadIdx.x >> 6] = 0;
+    if (x) votes[threadIdx.x >> 6] = 1;
+    lds_barrier();
+    int any = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) any |= votes[w];
+    return __builtin_amdgcn_readfirstlane(any) != 0;
+  };
+  __shared__ uint4 shared[SUMS ? 1 : F32 ? 4 * NW : RT * (RT + 1) / 2 * PER][64];
   Reader<F32, A> ra;
   Reader<F32, B> rb;
 
@@ -332,72 +349,93 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
     rb.forget();
 
     // x of every row tile (column i: its row) = its product with the state before
-    // the chunk, and p (rows j of tile jt <= it, column i) = that with k, side by
-    // side: what is read of the next values of A has the time of seven products
-    auto products = [&](bool state, bool rows, f32x16_t(&x)[RT], f32x16_t(&p)[RT * (RT + 1) / 2]) {
-      uint4 qn[RT], kn[RT];
+    // the chunk
+    auto with_state = [&](f32x16_t(&x)[RT]) {
+      uint4 qn[RT];
 #pragma unroll
-      for (int it = 0; it < RT; ++it) {
-        qn[it] = ra.row(qt, it, 0);
-        if (rows) kn[it] = ra.row(kt, it, 0);
-        if (state) x[it] = f32x16_t{};
-#pragma unroll
-        for (int jt = 0; jt <= it; ++jt)
-          if (rows) p[it * (it + 1) / 2 + jt] = f32x16_t{};
-      }
+      for (int it = 0; it < RT; ++it) qn[it] = ra.row(qt, it, 0), x[it] = f32x16_t{};
 #pragma unroll
       for (int kb = 0; kb < A / KB; ++kb) {
-        uint4 qf[RT], kf[RT], sf[TS];
+        uint4 qf[RT], sf[TS];
 #pragma unroll
         for (int it = 0; it < RT; ++it) {
-          qf[it] = qn[it], kf[it] = kn[it];
-          if (kb + 1 < A / KB) {
-            qn[it] = ra.row(qt, it, kb + 1);
-            if (rows) kn[it] = ra.row(kt, it, kb + 1);
-          }
+          qf[it] = qn[it];
+          if (kb + 1 < A / KB) qn[it] = ra.row(qt, it, kb + 1);
         }
-        if (rows) {
+        as_operand<F32, TS>(st[kb / PER], kb % PER, sf);
 #pragma unroll
-          for (int it = 0; it < RT; ++it)
+        for (int t = 0; t < TS; ++t)
 #pragma unroll
-            for (int jt = 0; jt <= it; ++jt)
-              p[it * (it + 1) / 2 + jt] = mma<F32>(kf[jt], qf[it], p[it * (it + 1) / 2 + jt]);
-        }
-        if (state) {
-          as_operand<F32, TS>(st[kb / PER], kb % PER, sf);
-#pragma unroll
-          for (int t = 0; t < TS; ++t)
-#pragma unroll
-            for (int it = 0; it < RT; ++it) x[it] = mma<F32>(sf[t], qf[it], x[it]);
-        }
+          for (int it = 0; it < RT; ++it) x[it] = mma<F32>(sf[t], qf[it], x[it]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (state) {
+#pragma unroll
+      for (int it = 0; it < RT; ++it)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[it][r] *= row_f[it];
+    };
+    // The weights of a chunk's rows (rows j of tile jt <= it, column i of tile it),
+    // shared by the waves through LDS as the lanes will hold them: bf16 tiles a
+    // wave each, decayed and rounded; of fp32's one tile, each wave a part of the
+    // contraction over A.
+    auto give_weights = [&]() {
+      if constexpr (F32) {
+        constexpr int N = A / KB / NW;
+        f32x16_t p = {};
+#pragma unroll
+        for (int n = 0; n < N; ++n) p = mma<true>(ra.row(kt, 0, wave * N + n), ra.row(qt, 0, wave * N + n), p);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          shared[wave * 4 + u][lane] = make_uint4(__float_as_uint(p[4 * u]), __float_as_uint(p[4 * u + 1]),
+                                                  __float_as_uint(p[4 * u + 2]), __float_as_uint(p[4 * u + 3]));
+      } else {
+        for (int b = wave; b < RT * (RT + 1) / 2; b += NW) {
+          const int it = b > 0, jt = b > 1;
+          const char *kp = kt + 32 * jt * ra.row_bytes, *qp = qt + 32 * it * ra.row_bytes;
+          f32x16_t p = {};
+#pragma unroll
+          for (int kb = 0; kb < A / KB; ++kb) p = mma<false>(ra.row(kp, 0, kb), ra.row(qp, 0, kb), p);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float4 f = decay[SUMS ? 0 : it - jt][u][lane];
+            const float w[4] = {f.x, f.y, f.z, f.w};
+            // (a weight that is not taken may be a NaN)
+            const int n = 32 * (it - jt) + col - 8 * u - 4 * hf;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[4 * u + e] = e > n ? 0.f : p[4 * u + e] * w[e];
+          }
+#pragma unroll
+          for (int u = 0; u < PER; ++u) {
+            uint4 w[1];
+            as_operand<false, 1>(p, u, w);
+            shared[b * PER + u][lane] = w[0];
+          }
+        }
+      }
+    };
+    // x += those weights times v
+    auto take_weights = [&](const uint4(&vf)[C / KB], f32x16_t(&x)[RT]) {
+      if constexpr (F32) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 f = decay[0][u][lane];
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const uint4 p = shared[w * 4 + u][lane];
+            s[0] += __uint_as_float(p.x), s[1] += __uint_as_float(p.y), s[2] += __uint_as_float(p.z), s[3] += __uint_as_float(p.w);
+          }
+          const float g[4] = {f.x, f.y, f.z, f.w};
+          const int n = col - 8 * u - 4 * hf;  // (a weight that is not taken may be a NaN)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = e > n ? 0.f : s[e] * g[e];
+          x[0] = mma<true>(vf[u], make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])), x[0]);
+        }
+      } else {
 #pragma unroll
         for (int it = 0; it < RT; ++it)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[it][r] *= row_f[it];
-      }
-    };
-    // x += the weights p times their decays, times v
-    auto weigh = [&](int it, const uint4(&vf)[C / KB], f32x16_t* p, f32x16_t& x) {
-#pragma unroll
-      for (int jt = 0; jt <= it; ++jt) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 f = decay[SUMS ? 0 : it - jt][u][lane];
-          p[jt][4 * u] *= f.x, p[jt][4 * u + 1] *= f.y, p[jt][4 * u + 2] *= f.z, p[jt][4 * u + 3] *= f.w;
-          if (jt == it) {  // (a weight that is not taken may be a NaN)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[jt][4 * u + e] = 8 * u + 4 * hf + e > col ? 0.f : p[jt][4 * u + e];
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < PER; ++u) {
-          uint4 w[1];
-          as_operand<F32, 1>(p[jt], u, w);
-          x = mma<F32>(vf[jt * PER + u], w[0], x);
-        }
+          for (int kb = 0; kb < (it + 1) * PER; ++kb) x[it] = mma<false>(vf[kb], shared[it * PER + kb][lane], x[it]);
       }
     };
     auto load_v = [&](uint4(&vf)[C / KB]) {
@@ -466,12 +504,12 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
     };
     int now = take;
     uint4 vf[C / KB];
-    __syncthreads();  // (the tiles' last readers are done)
+    lds_barrier();  // (the tiles' last readers are done)
     fk.template put<false>(kt);
     bool odd = fv.template put<!SUMS && !MANY>(vt);
     if constexpr (!SUMS) fq.template put<false>(qt);
     if constexpr (!SUMS && !MANY) {
-      if (__syncthreads_or(odd && now > 1)) {
+      if (any_of(odd && now > 1)) {
         // an infinity or a NaN times a later row's weight of 0 would be NaN:
         // such a chunk is taken a row at a time
         now = 1;
@@ -479,15 +517,15 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
         fv.get(a.v, head, slice * B, row0, dir, now);
         fk.template put<false>(kt);
         fv.template put<false>(vt);
-        __syncthreads();
+        lds_barrier();
       }
     } else {
-      __syncthreads();
+      lds_barrier();
     }
     if (now != up_for) {
       set_up(now);
       up_for = now;
-      __syncthreads();
+      lds_barrier();
     }
     const float g = power(lg, now);
     if constexpr (!MANY) {
@@ -501,18 +539,15 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
           // heads it would take as many registers again)
 #pragma unroll
           for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
-          f32x16_t x[RT], p[RT * (RT + 1) / 2];
-          products(true, true, x, p);
+          f32x16_t x[RT];
+          give_weights();
+          with_state(x);
+          lds_barrier();
+          if (h + 1 < q_heads) fq.template put<false>(qt);
+          take_weights(vf, x);
 #pragma unroll
-          for (int it = 0; it < RT; ++it) {
-            weigh(it, vf, p + it * (it + 1) / 2, x[it]);
-            store(it, head * q_heads + h, x[it], row_now, now);
-          }
-          if (h + 1 < q_heads) {
-            __syncthreads();
-            fq.template put<false>(qt);
-            __syncthreads();
-          }
+          for (int it = 0; it < RT; ++it) store(it, head * q_heads + h, x[it], row_now, now);
+          if (h + 1 < q_heads) lds_barrier();
         }
       }
       next(now);
@@ -524,27 +559,23 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
     } else {
       // q once, heads of k and v in turn
       f32x16_t x[RT];
-      if constexpr (!SUMS) {
-        f32x16_t p[RT * (RT + 1) / 2];
-        products(true, false, x, p);
-      }
+      if constexpr (!SUMS) with_state(x);
 #pragma unroll
       for (int t = 0; t < AT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) st[t][r] *= g;
       for (int h = 0; h < k_heads; ++h) {
         if (h > 0) {
-          __syncthreads();
+          lds_barrier();
           fk.template put<false>(kt);
           fv.template put<false>(vt);
-          __syncthreads();
+          lds_barrier();
         }
         load_v(vf);
         if constexpr (!SUMS) {
-          f32x16_t p[RT * (RT + 1) / 2];
-          products(false, true, x, p);
-#pragma unroll
-          for (int it = 0; it < RT; ++it) weigh(it, vf, p + it * (it + 1) / 2, x[it]);
+          give_weights();
+          lds_barrier();
+          take_weights(vf, x);
         }
         const int more = h + 1 < k_heads ? now : 0;
         fk.get(a.k, head * k_heads + h + 1, 0, row_now, dir, more);
