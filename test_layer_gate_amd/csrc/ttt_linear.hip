@@ -532,25 +532,34 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
       // k and v once, heads of q in turn
       load_v(vf);
       if constexpr (!SUMS) {
-        for (int h = 0; h < q_heads; ++h) {
-          fq.get(a.q, head * q_heads + h + 1, 0, row0, dir, h + 1 < q_heads ? now : 0);
+        f32x16_t x[RT];
+        int h = 0;
+        for (; h + 1 < q_heads; ++h) {
+          fq.get(a.q, head * q_heads + h + 1, 0, row_now, dir, now);
           __builtin_amdgcn_sched_barrier(0);
           // (so that the state's conversion stays inside the loop: kept over the
           // heads it would take as many registers again)
 #pragma unroll
           for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
-          f32x16_t x[RT];
           give_weights();
           with_state(x);
           lds_barrier();
-          if (h + 1 < q_heads) fq.template put<false>(qt);
+          fq.template put<false>(qt);
           take_weights(vf, x);
 #pragma unroll
           for (int it = 0; it < RT; ++it) store(it, head * q_heads + h, x[it], row_now, now);
-          if (h + 1 < q_heads) lds_barrier();
+          lds_barrier();
         }
+        next(now);
+        give_weights();
+        with_state(x);
+        lds_barrier();
+        take_weights(vf, x);
+#pragma unroll
+        for (int it = 0; it < RT; ++it) store(it, head * q_heads + h, x[it], row_now, now);
+      } else {
+        next(now);
       }
-      next(now);
 #pragma unroll
       for (int t = 0; t < AT; ++t)
 #pragma unroll
