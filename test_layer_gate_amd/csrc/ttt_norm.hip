@@ -36,19 +36,25 @@ constexpr int kMaxWaves = 16;
 
 // The workgroup's sums of N values, in every lane. `red` alternates between
 // two buffers from call to call, so that one barrier is enough: nobody writes
-// a buffer again before everybody has passed the other one's barrier.
-template <int N>
+// a buffer again before everybody has passed the other one's barrier. Of the
+// backward's six, those that its norms need.
+template <int N, bool PRE = true, bool POST = true>
 __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[kMaxWaves], int waves) {
+  constexpr auto on = [](int i) { return N != 6 || (i < 2 ? PRE : i < 4 ? POST : PRE && POST); };
+  if constexpr (N == 6 && !PRE && !POST) return;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  for (int i = 0; i < N; ++i)
+    if (on(i)) v[i] = wave_sum(v[i]);
   if (waves == 1) return;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i][threadIdx.x >> 6] = v[i];
+    for (int i = 0; i < N; ++i)
+      if (on(i)) red[i][threadIdx.x >> 6] = v[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
+    if (!on(i)) continue;
     float s = red[i][0];
     for (int w = 1; w < waves; ++w) s += red[i][w];
     v[i] = s;
@@ -68,61 +74,94 @@ __device__ __forceinline__ void load_weight(const void* p, bool f32, int64_t i, 
 
 __device__ __forceinline__ float rounded(float x, bool f32) { return f32 ? x : bf16_f32(bf16_rne(x)); }
 
+// Eight values on their way: loaded as they are, unpacked where they are used.
+template <bool F32>
+struct Raw {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (F32 ? 4 : 2));
+    v[0] = q[0];
+    if constexpr (F32) v[1] = q[1];
+  }
+  // Keeps the compiler from knowing the values from before.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) asm volatile("" : "+v"(v[i].x), "+v"(v[i].y), "+v"(v[i].z), "+v"(v[i].w));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint4& u = v[F32 ? e >> 1 : 0];
+      if constexpr (F32) {
+        x[2 * e] = __uint_as_float(e & 1 ? u.z : u.x), x[2 * e + 1] = __uint_as_float(e & 1 ? u.w : u.y);
+      } else {
+        const uint32_t w = e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
+        x[2 * e] = __uint_as_float(w << 16), x[2 * e + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+    }
+  }
+};
+
 // A workgroup of `waves` waves takes a row at a time, a lane K vectors of 8
 // neighbouring values of it, so that a row is read once and stays in registers
-// through both norms.
+// through both norms; the next row is loaded meanwhile. Bound by HBM.
 template <bool AF32, bool RF32, int K>
-__global__ void norm_kernel(NormLaunch a, int waves) {
+__global__ __launch_bounds__(512) void norm_kernel(NormLaunch a, int waves) {
   __shared__ float red[2][1][kMaxWaves];
   const int vecs = a.d >> 3, step = waves << 6;
   const float inv_d = 1.f / (float)a.d;
-  for (int64_t n = blockIdx.x; n < a.rows; n += gridDim.x) {
-    float x[K][8], f[K][8];
-    const bool has_f = a.f.p != nullptr;
+  const bool has_f = a.f.p != nullptr;
+  Raw<RF32> xn[K];
+  Raw<AF32> fn[K], gn[K];
+  auto fetch = [&](int n) {
+    const int64_t gate = a.gate.p ? (int64_t)(n / a.per_gate) * a.gate.ts : 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = k * step + threadIdx.x;
-      if (v < vecs) {
-        load8<RF32>(a.x.p, n * a.x.ts + v * 8, x[k]);
-        if (has_f) load8<AF32>(a.f.p, n * a.f.ts + v * 8, f[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = f[k][e] = 0.f;
-      }
+      const int v = min(k * step + (int)threadIdx.x, vecs - 1);
+      xn[k].load(a.x.p, (int64_t)n * a.x.ts + v * 8);
+      if (has_f) fn[k].load(a.f.p, (int64_t)n * a.f.ts + v * 8);
+      if (a.gate.p) gn[k].load(a.gate.p, gate + v * 8);
     }
+  };
+  float post[K][8], pre[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int v = min(k * step + (int)threadIdx.x, vecs - 1);
+    load_weight(a.norm_post ? a.post : nullptr, a.w_f32, v * 8, post[k]);
+    load_weight(a.norm_pre ? a.pre : nullptr, a.w_f32, v * 8, pre[k]);
+  }
+  fetch(blockIdx.x);
+  for (int n = blockIdx.x; n < a.rows; n += gridDim.x) {
+    float x[K][8], f[K][8], g[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      xn[k].get(x[k]);
+      if (has_f) fn[k].get(f[k]);
+      if (a.gate.p) gn[k].get(g[k]);
+    }
+    fetch(min(n + (int)gridDim.x, a.rows - 1));
     if (has_f) {
+      float by = a.scale;
       if (a.norm_post) {
         float s[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < K; ++k)
+          if (k * step + (int)threadIdx.x < vecs) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] += f[k][e] * f[k][e];
-        block_sum(s, red[0], waves);
-        const float phi = 1.f / sqrtf(s[0] * inv_d + a.eps);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const int v = k * step + threadIdx.x;
-          if (v < vecs) {
-            float w[8];
-            load_weight(a.post, a.w_f32, v * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[k][e] = f[k][e] * phi * w[e];
+            for (int e = 0; e < 8; ++e) s[0] += f[k][e] * f[k][e];
           }
-        }
+        block_sum(s, red[0], waves);
+        by *= 1.f / sqrtf(s[0] * inv_d + a.eps);
       }
-      const int64_t gate = a.gate.p ? n / a.per_gate * a.gate.ts : 0;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int v = k * step + threadIdx.x;
         if (v < vecs) {
-          if (a.gate.p) {
-            float g[8];
-            load8<AF32>(a.gate.p, gate + v * 8, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[k][e] *= g[e];
+          for (int e = 0; e < 8; ++e) {
+            const float y = f[k][e] * post[k][e];
+            x[k][e] = rounded(x[k][e] + by * (a.gate.p ? y * g[k][e] : y), RF32);
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][e] = rounded(x[k][e] + a.scale * f[k][e], RF32);
           store8<RF32>(a.r.p, n * a.r.ts + v * 8, x[k]);
         }
       }
@@ -134,19 +173,19 @@ __global__ void norm_kernel(NormLaunch a, int waves) {
     float s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k)
+      if (k * step + (int)threadIdx.x < vecs) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += x[k][e] * x[k][e];
+        for (int e = 0; e < 8; ++e) s[0] += x[k][e] * x[k][e];
+      }
     block_sum(s, red[1], waves);
     const float rho = 1.f / sqrtf(s[0] * inv_d + a.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int v = k * step + threadIdx.x;
       if (v < vecs) {
-        float w[8];
-        load_weight(a.pre, a.w_f32, v * 8, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] *= x[k][e] * rho;
-        store8<AF32>(a.h.p, n * a.h.ts + v * 8, w);
+        for (int e = 0; e < 8; ++e) x[k][e] *= rho * pre[k][e];
+        store8<AF32>(a.h.p, n * a.h.ts + v * 8, x[k]);
       }
     }
     // with one of the two sums alone, the next row writes its buffer again with
@@ -157,86 +196,102 @@ __global__ void norm_kernel(NormLaunch a, int waves) {
 
 // The gradients of a row, with rho and phi the two norms' factors:
 //   t = pre dh;  D = dr + rho (t - r rho^2 mean(r t))            dx
-//   a = f post scale gate;  df = phi (post dn - f phi^2 mean(a D)),  dn = scale gate D
-// mean(a D) is taken apart into sums of a dr, a t and a r, so that all sums of
+//   c = f post scale gate;  df = phi (post dn - f phi^2 mean(c D)),  dn = scale gate D
+// mean(c D) is taken apart into sums of c dr, c t and c r, so that all sums of
 // a row are joined at once. The sums over rows are kept in registers over a
-// workgroup's rows.
-template <bool AF32, bool RF32, int K>
-__global__ void norm_backward_kernel(NormBackLaunch b, NormPlan plan, int waves) {
+// workgroup's rows; the next row is loaded meanwhile.
+//
+// PRE, POST, GATED: whether the norms and the gate can be there (registers are
+// kept for what can).
+template <bool AF32, bool RF32, int K, bool PRE, bool POST, bool GATED>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackLaunch b, NormPlan plan, int waves) {
   __shared__ float red[2][6][kMaxWaves];
   const NormLaunch& a = b.n;
   const int vecs = a.d >> 3, step = waves << 6, w = blockIdx.x;
   const float inv_d = 1.f / (float)a.d;
-  const bool has_f = a.f.p != nullptr, gated = a.gate.p != nullptr;
-  int64_t lo, hi;
+  const bool has_f = a.f.p != nullptr, gated = GATED && a.gate.p != nullptr;
+  const bool has_pre = PRE && a.norm_pre, has_post = POST && has_f && a.norm_post;
+  int lo, hi, gate = 0;  // its rows, and the first one's gate
   if (plan.slices > 1) {
-    const int64_t g = w / plan.slices, first = g * a.per_gate;
-    lo = first + (int64_t)(w % plan.slices) * plan.each;
-    hi = min(lo + plan.each, first + a.per_gate);
+    gate = w / plan.slices;
+    lo = gate * a.per_gate + w % plan.slices * plan.each;
+    hi = min(lo + plan.each, (gate + 1) * a.per_gate);
   } else {
-    lo = (int64_t)w * plan.each;
-    hi = min(lo + plan.each, (int64_t)a.rows);
+    lo = w * plan.each;
+    hi = min(lo + plan.each, a.rows);
+    if (gated) gate = lo / a.per_gate;
   }
-  float d_post[K][8], d_pre[K][8], d_gate[K][8], g[K][8];
+  int left = gated ? (gate + 1) * a.per_gate - lo : 0;  // rows of that gate
+  Raw<RF32> rn[K], drn[K];
+  Raw<AF32> fn[K], dhn[K], gn[K];
+  auto fetch = [&](int row, int gate) {
+    const int64_t n = row;
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) d_post[k][e] = d_pre[k][e] = d_gate[k][e] = 0.f, g[k][e] = 1.f;
-  int turn = 0;
-  for (int64_t n = lo; n < hi; ++n, turn ^= 1) {
-    const int64_t gi = gated ? n / a.per_gate : 0;
-    if (gated && (n == lo || n % a.per_gate == 0)) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int v = k * step + threadIdx.x;
-        if (v < vecs) load8<AF32>(a.gate.p, gi * a.gate.ts + v * 8, g[k]);
+    for (int k = 0; k < K; ++k) {
+      const int v = min(k * step + (int)threadIdx.x, vecs - 1);
+      if (has_pre) {
+        rn[k].load(a.x.p, n * a.x.ts + v * 8);
+        dhn[k].load(b.dh.p, n * b.dh.ts + v * 8);
       }
+      if (b.dr.p) drn[k].load(b.dr.p, n * b.dr.ts + v * 8);
+      if (has_f) fn[k].load(a.f.p, n * a.f.ts + v * 8);
+      if (gated) gn[k].load(a.gate.p, gate * a.gate.ts + v * 8);
     }
-    float r[K][8], f[K][8], dr[K][8], dh[K][8], post[K][8];
+  };
+  float d_post[K][8], d_pre[K][8], d_gate[K][8], post[K][8], pre[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d_post[k][e] = d_pre[k][e] = d_gate[k][e] = 0.f;
+    const int v = min(k * step + (int)threadIdx.x, vecs - 1);
+    load_weight(has_post ? a.post : nullptr, a.w_f32, v * 8, post[k]);
+    load_weight(has_pre ? a.pre : nullptr, a.w_f32, v * 8, pre[k]);
+  }
+  int turn = 0;
+  if (lo < hi) fetch(lo, gate);
+  for (int64_t n = lo; n < hi; ++n, turn ^= 1) {
+    // the row stays as it was loaded, and is unpacked again behind the sums
+    Raw<RF32> rc[K], drc[K];
+    Raw<AF32> fc[K], dhc[K], gc[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) rc[k] = rn[k], drc[k] = drn[k], fc[k] = fn[k], dhc[k] = dhn[k], gc[k] = gn[k];
+    auto unpack = [&](int k, float (&r)[8], float (&f)[8], float (&dr)[8], float (&dh)[8], float (&g)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = f[e] = dr[e] = dh[e] = 0.f, g[e] = 1.f;
+      if (has_pre) rc[k].get(r), dhc[k].get(dh);
+      if (b.dr.p) drc[k].get(dr);
+      if (has_f) fc[k].get(f);
+      if (gated) gc[k].get(g);
+    };
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = k * step + threadIdx.x;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[k][e] = f[k][e] = dr[k][e] = dh[k][e] = post[k][e] = 0.f;
-      if (v < vecs) {
-        if (a.norm_pre) {
-          load8<RF32>(a.x.p, n * a.x.ts + v * 8, r[k]);
-          load8<AF32>(b.dh.p, n * b.dh.ts + v * 8, dh[k]);
-        }
-        if (b.dr.p) load8<RF32>(b.dr.p, n * b.dr.ts + v * 8, dr[k]);
-        if (has_f) {
-          load8<AF32>(a.f.p, n * a.f.ts + v * 8, f[k]);
-          load_weight(a.norm_post ? a.post : nullptr, a.w_f32, v * 8, post[k]);
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = k * step + threadIdx.x;
-      float pre[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) pre[e] = 0.f;
-      if (v < vecs && a.norm_pre) load_weight(a.pre, a.w_f32, v * 8, pre);
+      if (k * step + (int)threadIdx.x >= vecs) continue;
+      float r[8], f[8], dr[8], dh[8], g[8];
+      unpack(k, r, f, dr, dh, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float t = pre[e] * dh[k][e];
-        const float c = f[k][e] * post[k][e] * g[k][e];
-        s[0] += r[k][e] * r[k][e];
-        s[1] += r[k][e] * t;
-        s[2] += f[k][e] * f[k][e];
-        s[3] += c * dr[k][e];
-        s[4] += c * t;
-        s[5] += c * r[k][e];
+        const float t = pre[k][e] * dh[e];
+        const float c = f[e] * post[k][e] * g[e];
+        if constexpr (PRE) s[0] += r[e] * r[e], s[1] += r[e] * t;
+        if constexpr (POST) s[2] += f[e] * f[e], s[3] += c * dr[e];
+        if constexpr (PRE && POST) s[4] += c * t, s[5] += c * r[e];
       }
     }
-    block_sum(s, red[turn], waves);
+    const int64_t this_gate = gate;
+    const bool gate_done = gated && --left == 0;
+    if (gate_done && n + 1 < hi) ++gate, left = a.per_gate;
+    fetch(min((int)n + 1, hi - 1), gate);
+    // (unpacked at once, the values would take twice the registers)
+#pragma unroll
+    for (int k = 0; k < K; ++k) rc[k].forget(), drc[k].forget(), fc[k].forget(), dhc[k].forget(), gc[k].forget();
+    block_sum<6, PRE, POST>(s, red[turn], waves);
     float rho = 0.f, back = 0.f, phi = 1.f, fall = 0.f;
-    if (a.norm_pre) {
+    if (has_pre) {
       rho = 1.f / sqrtf(s[0] * inv_d + a.eps);
       back = rho * rho * rho * (s[1] * inv_d);
     }
-    if (has_f && a.norm_post) {
+    if (has_post) {
       phi = 1.f / sqrtf(s[2] * inv_d + a.eps);
       fall = phi * phi * phi * a.scale * ((s[3] + rho * s[4] - back * s[5]) * inv_d);
     }
@@ -244,33 +299,33 @@ __global__ void norm_backward_kernel(NormBackLaunch b, NormPlan plan, int waves)
     for (int k = 0; k < K; ++k) {
       const int v = k * step + threadIdx.x;
       if (v < vecs) {
-        float pre[8], df[8], dg[8];
-        if (a.norm_pre) load_weight(a.pre, a.w_f32, v * 8, pre);
+        float r[8], f[8], dr[8], dh[8], g[8], df[8], dg[8];
+        unpack(k, r, f, dr, dh, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float D = dr[k][e];
-          if (a.norm_pre) {
-            D += rho * (pre[e] * dh[k][e]) - back * r[k][e];
-            d_pre[k][e] += dh[k][e] * (r[k][e] * rho);
+          float D = dr[e];
+          if (has_pre) {
+            D += rho * (pre[k][e] * dh[e]) - back * r[e];
+            d_pre[k][e] += dh[e] * (r[e] * rho);
           }
-          dr[k][e] = D;
-          const float fn = f[k][e] * phi, sD = a.scale * D;
+          dr[e] = D;
+          const float fn = f[e] * phi, sD = a.scale * D;
           dg[e] = fn * post[k][e] * sD;
-          d_gate[k][e] += dg[e];
-          const float dn = g[k][e] * sD;
-          d_post[k][e] += dn * fn;
-          df[e] = phi * (post[k][e] * dn) - fall * f[k][e];
+          if constexpr (GATED) d_gate[k][e] += dg[e];
+          const float dn = g[e] * sD;
+          if constexpr (POST) d_post[k][e] += dn * fn;
+          df[e] = phi * (post[k][e] * dn) - fall * f[e];
         }
-        store8<RF32>(b.dx.p, n * b.dx.ts + v * 8, dr[k]);
+        store8<RF32>(b.dx.p, n * b.dx.ts + v * 8, dr);
         if (has_f) store8<AF32>(b.df.p, n * b.df.ts + v * 8, df);
         if (gated && a.per_gate == 1) store8<AF32>(b.dgate.p, n * b.dgate.ts + v * 8, dg);
       }
     }
-    if (gated && a.per_gate > 1 && plan.slices == 1 && (n + 1) % a.per_gate == 0) {
+    if (gate_done && a.per_gate > 1 && plan.slices == 1) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int v = k * step + threadIdx.x;
-        if (v < vecs) store8<true>(b.dgate.p, gi * b.dgate.ts + v * 8, d_gate[k]);
+        if (v < vecs) store8<true>(b.dgate.p, this_gate * b.dgate.ts + v * 8, d_gate[k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) d_gate[k][e] = 0.f;
       }
@@ -281,8 +336,8 @@ __global__ void norm_backward_kernel(NormBackLaunch b, NormPlan plan, int waves)
     const int v = k * step + threadIdx.x;
     if (v < vecs) {
       const int64_t at = (int64_t)w * a.d + v * 8;
-      if (b.dpost) store8<true>(b.part_post, at, d_post[k]);
-      if (b.dpre) store8<true>(b.part_pre, at, d_pre[k]);
+      if (POST && b.dpost) store8<true>(b.part_post, at, d_post[k]);
+      if (PRE && b.dpre) store8<true>(b.part_pre, at, d_pre[k]);
       if (gated && plan.slices > 1) store8<true>(b.part_gate, at, d_gate[k]);
     }
   }
@@ -327,34 +382,46 @@ int waves_of(int d, int k) { return (d / 8 + 64 * k - 1) / (64 * k); }
 
 template <bool AF32, bool RF32>
 hipError_t norm_of(const NormLaunch& a, hipStream_t s) {
-  const int vecs = a.d / 8;
-  const int K = vecs <= 64 ? 1 : vecs <= 128 ? 2 : vecs <= 192 ? 3 : vecs <= 320 ? 5 : 8;
-  const int waves = waves_of(a.d, K);
-  const int grid = (int)std::min<int64_t>(a.rows, 256 * 32 / waves);
-  const dim3 g(grid), t(64 * waves);
-  switch (K) {
-    case 1: norm_kernel<AF32, RF32, 1><<<g, t, 0, s>>>(a, waves); break;
-    case 2: norm_kernel<AF32, RF32, 2><<<g, t, 0, s>>>(a, waves); break;
-    case 3: norm_kernel<AF32, RF32, 3><<<g, t, 0, s>>>(a, waves); break;
-    case 5: norm_kernel<AF32, RF32, 5><<<g, t, 0, s>>>(a, waves); break;
-    default: norm_kernel<AF32, RF32, 8><<<g, t, 0, s>>>(a, waves); break;
-  }
+  const int K = a.d <= 4096 ? 1 : a.d <= 8192 ? 2 : 4, waves = waves_of(a.d, K);
+  const dim3 g((uint32_t)std::min(a.rows, 256 * 24 / waves)), t(64 * waves);
+  if (K == 1)
+    norm_kernel<AF32, RF32, 1><<<g, t, 0, s>>>(a, waves);
+  else if (K == 2)
+    norm_kernel<AF32, RF32, 2><<<g, t, 0, s>>>(a, waves);
+  else
+    norm_kernel<AF32, RF32, 4><<<g, t, 0, s>>>(a, waves);
   return hipGetLastError();
 }
 
 // Vectors of a lane in the backward: its sums over rows take 24 registers for
 // each.
-int back_vecs(int d) { return d <= 4096 ? 1 : 2; }
+int back_vecs(int d) { return d <= 8192 ? 1 : 2; }
+
+template <bool AF32, bool RF32, bool PRE, bool POST>
+void back_of(const NormBackLaunch& b, const NormPlan& plan, int waves, hipStream_t s) {
+  const dim3 g(plan.groups), t(64 * waves);
+  if (b.n.gate.p)
+    norm_backward_kernel<AF32, RF32, 1, PRE, POST, true><<<g, t, 0, s>>>(b, plan, waves);
+  else
+    norm_backward_kernel<AF32, RF32, 1, PRE, POST, false><<<g, t, 0, s>>>(b, plan, waves);
+}
 
 template <bool AF32, bool RF32>
 hipError_t back_of(const NormBackLaunch& b, hipStream_t s) {
   const NormPlan plan = norm_plan(b.n.rows, b.n.d, b.n.gate.p ? b.n.per_gate : 0);
   const int K = back_vecs(b.n.d), waves = waves_of(b.n.d, K);
-  const dim3 g(plan.groups), t(64 * waves);
-  if (K == 1)
-    norm_backward_kernel<AF32, RF32, 1><<<g, t, 0, s>>>(b, plan, waves);
-  else
-    norm_backward_kernel<AF32, RF32, 2><<<g, t, 0, s>>>(b, plan, waves);
+  if (K == 1) {
+    if (b.n.norm_pre && b.n.norm_post)
+      back_of<AF32, RF32, true, true>(b, plan, waves, s);
+    else if (b.n.norm_pre)
+      back_of<AF32, RF32, true, false>(b, plan, waves, s);
+    else if (b.n.norm_post)
+      back_of<AF32, RF32, false, true>(b, plan, waves, s);
+    else
+      back_of<AF32, RF32, false, false>(b, plan, waves, s);
+  } else {
+    norm_backward_kernel<AF32, RF32, 2, true, true, true><<<plan.groups, 64 * waves, 0, s>>>(b, plan, waves);
+  }
   return hipGetLastError();
 }
 
