@@ -61,6 +61,17 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[kMaxWaves]
   }
 }
 
+// Eight values of a row that leaves: whole lines of bf16 pass the caches by
+// (64k rows of 2560 took 258 us so and 294 with plain stores); of fp32 a lane's
+// two pieces are half lines, which would each cost a read.
+template <bool F32>
+__device__ __forceinline__ void store_row(void* p, int64_t i, const float (&v)[8]) {
+  if constexpr (F32)
+    store8<true>(p, i, v);
+  else
+    stream_store<false>(p, i, v);
+}
+
 __device__ __forceinline__ void load_weight(const void* p, bool f32, int64_t i, float (&v)[8]) {
   if (p == nullptr) {
 #pragma unroll
@@ -73,6 +84,81 @@ __device__ __forceinline__ void load_weight(const void* p, bool f32, int64_t i, 
 }
 
 __device__ __forceinline__ float rounded(float x, bool f32) { return f32 ? x : bf16_f32(bf16_rne(x)); }
+
+// A workgroup of `waves` waves takes a row, a lane K vectors of 8 neighbouring
+// values of it, so that the row is read once and stays in registers through both
+// norms. Bound by HBM: 64k rows of 2560 in bf16, with a gate vector and the norm
+// before the next block, take 253 us, 5.3 TB/s. (Workgroups that stay for more
+// rows and load the next one ahead took 256 us, and more of them 271: there are
+// enough rows on their way.)
+template <bool AF32, bool RF32, int K>
+__global__ __launch_bounds__(512) void norm_kernel(NormLaunch a, int waves) {
+  __shared__ float red[2][1][kMaxWaves];
+  const int vecs = a.d >> 3, step = waves << 6;
+  const float inv_d = 1.f / (float)a.d;
+  const int64_t n = blockIdx.x;
+  const bool has_f = a.f.p != nullptr;
+  float x[K][8], f[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int v = k * step + threadIdx.x;
+    if (v < vecs) {
+      load8<RF32>(a.x.p, n * a.x.ts + v * 8, x[k]);
+      if (has_f) load8<AF32>(a.f.p, n * a.f.ts + v * 8, f[k]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k][e] = f[k][e] = 0.f;
+    }
+  }
+  if (has_f) {
+    float by = a.scale;
+    if (a.norm_post) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0] += f[k][e] * f[k][e];
+      block_sum(s, red[0], waves);
+      by *= 1.f / sqrtf(s[0] * inv_d + a.eps);
+    }
+    const int64_t gate = a.gate.p ? (int64_t)((int)blockIdx.x / a.per_gate) * a.gate.ts : 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = k * step + threadIdx.x;
+      if (v < vecs) {
+        float w[8], g[8];
+        load_weight(a.norm_post ? a.post : nullptr, a.w_f32, v * 8, w);
+        if (a.gate.p) {
+          load8<AF32>(a.gate.p, gate + v * 8, g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] *= g[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = rounded(x[k][e] + by * (f[k][e] * w[e]), RF32);
+        store_row<RF32>(a.r.p, n * a.r.ts + v * 8, x[k]);
+      }
+    }
+  }
+  if (!a.norm_pre) return;
+  float s[1] = {0.f};
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] += x[k][e] * x[k][e];
+  block_sum(s, red[1], waves);
+  const float rho = 1.f / sqrtf(s[0] * inv_d + a.eps);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int v = k * step + threadIdx.x;
+    if (v < vecs) {
+      float w[8];
+      load_weight(a.pre, a.w_f32, v * 8, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= x[k][e] * rho;
+      store_row<AF32>(a.h.p, n * a.h.ts + v * 8, w);
+    }
+  }
+}
 
 // Eight values on their way: loaded as they are, unpacked where they are used.
 template <bool F32>
@@ -101,98 +187,6 @@ struct Raw {
     }
   }
 };
-
-// A workgroup of `waves` waves takes a row at a time, a lane K vectors of 8
-// neighbouring values of it, so that a row is read once and stays in registers
-// through both norms; the next row is loaded meanwhile. Bound by HBM.
-template <bool AF32, bool RF32, int K>
-__global__ __launch_bounds__(512) void norm_kernel(NormLaunch a, int waves) {
-  __shared__ float red[2][1][kMaxWaves];
-  const int vecs = a.d >> 3, step = waves << 6;
-  const float inv_d = 1.f / (float)a.d;
-  const bool has_f = a.f.p != nullptr;
-  Raw<RF32> xn[K];
-  Raw<AF32> fn[K], gn[K];
-  auto fetch = [&](int n) {
-    const int64_t gate = a.gate.p ? (int64_t)(n / a.per_gate) * a.gate.ts : 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = min(k * step + (int)threadIdx.x, vecs - 1);
-      xn[k].load(a.x.p, (int64_t)n * a.x.ts + v * 8);
-      if (has_f) fn[k].load(a.f.p, (int64_t)n * a.f.ts + v * 8);
-      if (a.gate.p) gn[k].load(a.gate.p, gate + v * 8);
-    }
-  };
-  float post[K][8], pre[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int v = min(k * step + (int)threadIdx.x, vecs - 1);
-    load_weight(a.norm_post ? a.post : nullptr, a.w_f32, v * 8, post[k]);
-    load_weight(a.norm_pre ? a.pre : nullptr, a.w_f32, v * 8, pre[k]);
-  }
-  fetch(blockIdx.x);
-  for (int n = blockIdx.x; n < a.rows; n += gridDim.x) {
-    float x[K][8], f[K][8], g[K][8];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      xn[k].get(x[k]);
-      if (has_f) fn[k].get(f[k]);
-      if (a.gate.p) gn[k].get(g[k]);
-    }
-    fetch(min(n + (int)gridDim.x, a.rows - 1));
-    if (has_f) {
-      float by = a.scale;
-      if (a.norm_post) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (k * step + (int)threadIdx.x < vecs) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] += f[k][e] * f[k][e];
-          }
-        block_sum(s, red[0], waves);
-        by *= 1.f / sqrtf(s[0] * inv_d + a.eps);
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int v = k * step + threadIdx.x;
-        if (v < vecs) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float y = f[k][e] * post[k][e];
-            x[k][e] = rounded(x[k][e] + by * (a.gate.p ? y * g[k][e] : y), RF32);
-          }
-          store8<RF32>(a.r.p, n * a.r.ts + v * 8, x[k]);
-        }
-      }
-    }
-    if (!a.norm_pre) {
-      if (waves > 1 && has_f && a.norm_post) __syncthreads();  // (see below)
-      continue;
-    }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (k * step + (int)threadIdx.x < vecs) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += x[k][e] * x[k][e];
-      }
-    block_sum(s, red[1], waves);
-    const float rho = 1.f / sqrtf(s[0] * inv_d + a.eps);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = k * step + threadIdx.x;
-      if (v < vecs) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] *= rho * pre[k][e];
-        store8<AF32>(a.h.p, n * a.h.ts + v * 8, x[k]);
-      }
-    }
-    // with one of the two sums alone, the next row writes its buffer again with
-    // no barrier of the other's between
-    if (waves > 1 && !(has_f && a.norm_post)) __syncthreads();
-  }
-}
 
 // The gradients of a row, with rho and phi the two norms' factors:
 //   t = pre dh;  D = dr + rho (t - r rho^2 mean(r t))            dx
@@ -316,9 +310,9 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackLaunch b, N
           if constexpr (POST) d_post[k][e] += dn * fn;
           df[e] = phi * (post[k][e] * dn) - fall * f[e];
         }
-        store8<RF32>(b.dx.p, n * b.dx.ts + v * 8, dr);
-        if (has_f) store8<AF32>(b.df.p, n * b.df.ts + v * 8, df);
-        if (gated && a.per_gate == 1) store8<AF32>(b.dgate.p, n * b.dgate.ts + v * 8, dg);
+        store_row<RF32>(b.dx.p, n * b.dx.ts + v * 8, dr);
+        if (has_f) store_row<AF32>(b.df.p, n * b.df.ts + v * 8, df);
+        if (gated && a.per_gate == 1) store_row<AF32>(b.dgate.p, n * b.dgate.ts + v * 8, dg);
       }
     }
     if (gate_done && a.per_gate > 1 && plan.slices == 1) {
@@ -383,7 +377,7 @@ int waves_of(int d, int k) { return (d / 8 + 64 * k - 1) / (64 * k); }
 template <bool AF32, bool RF32>
 hipError_t norm_of(const NormLaunch& a, hipStream_t s) {
   const int K = a.d <= 4096 ? 1 : a.d <= 8192 ? 2 : 4, waves = waves_of(a.d, K);
-  const dim3 g((uint32_t)std::min(a.rows, 256 * 24 / waves)), t(64 * waves);
+  const dim3 g(a.rows), t(64 * waves);
   if (K == 1)
     norm_kernel<AF32, RF32, 1><<<g, t, 0, s>>>(a, waves);
   else if (K == 2)
