@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import struct
 
 import torch
@@ -86,14 +87,18 @@ def _alone(t, *others):
         raise ValueError("all tensors must be on the GPU")
     d = t.get_device()
     for o in others:
-        if o is not None and (not o.is_cuda or o.get_device() != d):
+        if o is not None and o.get_device() != d:
             raise ValueError("all tensors must be on one GPU")
     if d != torch.cuda.current_device():
         raise ValueError("the tensors must be on the current GPU (torch.cuda.device selects it)")
 
 
 def _new(shape, dtype, like, stream):
-    return _s._on(stream, torch.empty, shape, dtype=dtype, device=like.device)
+    if dtype is like.dtype:
+        if shape == like.shape:
+            return _s._empty(like, stream)
+        return _s._on(stream, like.new_empty, shape)
+    return _s._on(stream, like.new_empty, shape, dtype=dtype)
 
 
 def _workspace(need, like, workspace, stream):
@@ -135,6 +140,8 @@ def _row_view(t, what):
 def _pack_view(t, what, rows, d, dtype):
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous() and t.shape[-1:] == (d,) and t.numel() == rows * d:
+        return _s._pack_rows(t.data_ptr(), d, d, 1, 0)
     n, m, stride = _row_view(t, what)
     if n != rows or m != d:
         raise ValueError(f"{what} must have {rows} rows of {d}, got {n} of {m}")
@@ -145,6 +152,7 @@ def _out(t, what, like, rows, d, dtype, stream):
     """(tensor, packed view) of an output that the caller gives, or a new one."""
     if t is None:
         t = _new(like.shape, dtype, like, stream)
+        return t, _s._pack_rows(t.data_ptr(), d, d, 1, 0)
     return t, _pack_view(t, what, rows, d, dtype)
 
 
@@ -379,22 +387,27 @@ def linear_attention_backward(do, q, k, v, log_decay, *, state=None, d_state=Non
 # ------------------------------------------------------------------- AdamW
 
 
+_T = torch.Tensor
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _list(ts, what, dtype=None, sizes=None):
     """(addresses, sizes, dtype) of dense tensors of one dtype, the current
-    GPU's."""
+    GPU's. (Maps of methods: with some hundred tensors a comprehension's steps
+    would take longer than the kernel.)"""
     ts = list(ts)
     if not ts:
         return [], [], dtype
+    dtypes = set(map(_dtype_of, ts))
     if dtype is None:
         dtype = ts[0].dtype
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous {dtype} tensors on the current GPU")
-    n = [t.numel() for t in ts]
+    if (dtypes != {dtype} or set(map(_T.get_device, ts)) != {torch.cuda.current_device()}
+            or not all(map(_T.is_contiguous, ts))):
+        raise ValueError(f"{what} must be contiguous {dtype} tensors on the current GPU")
+    n = list(map(_T.numel, ts))
     if sizes is not None and n != sizes:
         raise ValueError(f"{what} must have the parameters' sizes")
-    return [t.data_ptr() for t in ts], n, dtype
+    return list(map(_T.data_ptr, ts)), n, dtype
 
 
 def _scalar(x, what, dtype):
