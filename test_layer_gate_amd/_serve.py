@@ -138,7 +138,7 @@ def _rows_of(t, what):
         n *= b
     else:
         raise ValueError(f"{what} must be [rows, heads, dim] or [B, T, heads, dim]")
-    if vs != 1 and d > 1:
+    if vs != 1 and d > 1 and t.numel():
         raise ValueError(f"{what}: the values of a head must be contiguous")
     if n >> 31:  # ctypes would cut it to 32 bits
         raise ValueError(f"{what} has {n} rows; the library counts them in 32 bits")
