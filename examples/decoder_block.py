@@ -6,9 +6,9 @@ a server would, then tokens one at a time.
     y  = x1 + layer(H = norm(x1), X0 = x0)
 
 kv_append rotates a segment's queries and keys and puts keys and values into
-the cache in one launch; kv_attention reads them there; the layer carries its
-state from segment to segment and into decode_step. The projections and norms
-are torch's.
+the cache in one launch; kv_attention reads them there; block_norm adds what it
+returns and takes the next norm in one pass; the layer carries its state from
+segment to segment and into decode_step. The projections are torch's.
 
     python examples/decoder_block.py --tokens 16384 --new 64
 """
@@ -23,11 +23,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import test_layer_gate_amd as ttt  # noqa: E402
 import synth  # noqa: E402
-
-
-def norm(x):
-    y = x.float()
-    return (y * torch.rsqrt(y.square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
 
 
 class DecoderBlock:
@@ -53,25 +48,26 @@ class DecoderBlock:
         self.decode_state = None
 
     def attention(self, x):
-        """x [batch, T, d] -> x + attention, the T tokens appended."""
+        """x [batch, T, d] -> x1 = x + attention and norm(x1), the T tokens appended."""
         B, T, d = x.shape
         h, g, D = self.heads, self.kv_heads, self.dim
-        qkv = (norm(x).reshape(B * T, d) @ self.Wqkv).reshape(B * T, h + 2 * g, D)
+        n = ttt.block_norm(x, pre=True)[1]
+        qkv = (n.reshape(B * T, d) @ self.Wqkv).reshape(B * T, h + 2 * g, D)
         q, k, v = qkv[:, :h], qkv[:, h:h + g], qkv[:, h + g:]
         self.seen += T
         self.lens += T
         # q is rotated in place, in the projection's own rows
         ttt.kv_append(self.pages, self.table, self.lens, k, v, q=q, q_out=q, rope_table=self.rope)
         o = ttt.kv_attention(q, self.pages, self.table, self.lens, max_new=T, max_kv=self.seen)
-        return x + (o.reshape(B * T, h * D) @ self.w["Wo"].t()).reshape(B, T, d)
+        return ttt.block_norm(x, (o.reshape(B * T, h * D) @ self.w["Wo"].t()).reshape(B, T, d), pre=True)
 
     def segment(self, x, x0):
         """The next T tokens of every sequence, T a multiple of the chunk."""
         if x.shape[1] % self.chunk or self.decode_state is not None:
             raise ValueError("segments are whole chunks, and come before decoding")
-        x1 = self.attention(x)
+        x1, h = self.attention(x)
         m = self.mlp
-        return x1 + ttt.layer_forward_continue(norm(x1), x0, None, m["Wg"], m["Wu"], self.W_state, m["taps"],
+        return x1 + ttt.layer_forward_continue(h, x0, None, m["Wg"], m["Wu"], self.W_state, m["taps"],
                                                m["W_target"], self.eta, self.chunk, pad="chunk")
 
     def step(self, x, x0):
@@ -84,8 +80,8 @@ class DecoderBlock:
             self.decode_state = torch.empty(ttt.decode_state_size(desc, self.chunk), dtype=torch.uint8, device="cuda")
             ttt.decode_begin(self.W_state, self.chunk, self.decode_state, act_dtype=x.dtype,
                              weight_dtype=m["Wg"].dtype, conv_k=m["taps"].shape[0])
-        x1 = self.attention(x[:, None])[:, 0]
-        return x1 + ttt.decode_step(norm(x1), x0, m["Wg"], m["Wu"], m["taps"], m["W_target"], self.eta, self.chunk,
+        x1, h = (t[:, 0] for t in self.attention(x[:, None]))
+        return x1 + ttt.decode_step(h, x0, m["Wg"], m["Wu"], m["taps"], m["W_target"], self.eta, self.chunk,
                                     self.seen - 1, self.W_state, self.decode_state)
 
 
