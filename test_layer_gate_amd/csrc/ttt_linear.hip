@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "ttt_attention.h"
 #include "ttt_block.h"
@@ -36,7 +37,17 @@ struct Chunks {
   int state_turned;             // state is [B][A]
   int batch, tokens, heads, parts, part_rows, slices;
   int lead, back;
+  int fine;                     // the state behind the last row is a result, here or of what follows
   float s_in, s_out, s_up;
+};
+
+// Up to three of them in one launch, where they are of one kind: what one leaves
+// idle while its first tiles are on their way, and when its last parts end,
+// another uses. The parts of all follow each other by eights, one a die, so that
+// what reads the same rows does so at about the same time.
+struct Roles {
+  Chunks c[3];
+  int n;
 };
 
 // Tiles of rows in LDS, swizzled by 16-byte pieces. LDS takes a wave's 16-byte
@@ -168,19 +179,15 @@ __device__ __forceinline__ void terms(float x, float y, uint32_t (&w)[T]) {
 }
 
 // Values of a product's result (kb of its rows) as an operand: fp32 as they
-// are; as T terms of bf16.
-template <bool F32, int T>
-__device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4 (&f)[T]) {
-  if constexpr (F32) {
-    f[0] = make_uint4(__float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]), __float_as_uint(x[4 * u + 2]),
-                      __float_as_uint(x[4 * u + 3]));
-  } else {
-    uint32_t w[4][T];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) terms<T>(x[8 * u + 2 * e], x[8 * u + 2 * e + 1], w[e]);
-#pragma unroll
-    for (int t = 0; t < T; ++t) f[t] = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
-  }
+// are, bf16 rounded.
+template <bool F32>
+__device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4& f) {
+  if constexpr (F32)
+    f = make_uint4(__float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]), __float_as_uint(x[4 * u + 2]),
+                   __float_as_uint(x[4 * u + 3]));
+  else
+    f = make_uint4(pack_bf16(x[8 * u], x[8 * u + 1]), pack_bf16(x[8 * u + 2], x[8 * u + 3]),
+                   pack_bf16(x[8 * u + 4], x[8 * u + 5]), pack_bf16(x[8 * u + 6], x[8 * u + 7]));
 }
 
 // g^n for a whole n >= 0; 1 for n = 0 whatever g is.
@@ -242,15 +249,16 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // MANY: heads of k and v share the state (else heads of q do). SUMS: the
 // part's own sum alone, from zero.
 //
-// bf16: weights (q k) enter the product with v rounded to bf16 (they carry the
-// 2^-9 of a value that is rounded to bf16 once more at the end); states as two
-// bf16 terms (16 bits: each row reads every state again); in the update, whose
-// sums stay, v times its decay as three (24 bits). fp32: the matrix cores' fp32
-// products throughout.
+// bf16: weights (q k) and states enter their products with v and q rounded to
+// bf16, the precision of what they meet and of the result (2-norm error against
+// 64 bits 0.0023, 0.0017 of it the result's own rounding; with the state as two
+// terms 0.0018, for 16 products and 96 vector instructions a chunk more). In the
+// update, whose sums stay in fp32 from chunk to chunk, v times its decay is three
+// terms (24 bits) where the state is a result, else two (16). fp32: the matrix
+// cores' fp32 products throughout.
 template <bool F32, int A, int NW, bool MANY, bool SUMS>
-__global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks a) {
+__global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles roles) {
   constexpr int C = Elem<F32>::rows, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
-  constexpr int TS = F32 ? 1 : 2, TU = F32 ? 1 : 3;  // terms of states, of updates
   constexpr int RT = C / 32, AT = A / 32, PER = 32 / KB;
   constexpr int kBytesA = C * A * Elem<F32>::size, kBytesB = C * B * Elem<F32>::size;
   __shared__ __attribute__((aligned(16))) char kt[kBytesA];
@@ -272,12 +280,15 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
   Reader<F32, A> ra;
   Reader<F32, B> rb;
 
-  int id = blockIdx.x;
+  const int eights = blockIdx.x / 8, turn = __builtin_amdgcn_readfirstlane(eights / roles.n);
+  const Chunks& a = roles.c[eights - turn * roles.n];
+  int id = turn * 8 + blockIdx.x % 8;
   const int slice = id % a.slices;
   id /= a.slices;
   const int part = id % a.parts;
   id /= a.parts;
   const int head = id % a.heads, seq = id / a.heads;
+  if (seq >= a.batch) return;
   int64_t base, len;
   if (a.starts) {
     const int lo = min(max(a.starts[seq], 0), a.tokens), hi = min(max(a.starts[seq + 1], 0), a.tokens);
@@ -356,17 +367,15 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
       for (int it = 0; it < RT; ++it) qn[it] = ra.row(qt, it, 0), x[it] = f32x16_t{};
 #pragma unroll
       for (int kb = 0; kb < A / KB; ++kb) {
-        uint4 qf[RT], sf[TS];
+        uint4 qf[RT], sf;
 #pragma unroll
         for (int it = 0; it < RT; ++it) {
           qf[it] = qn[it];
           if (kb + 1 < A / KB) qn[it] = ra.row(qt, it, kb + 1);
         }
-        as_operand<F32, TS>(st[kb / PER], kb % PER, sf);
+        as_operand<F32>(st[kb / PER], kb % PER, sf);
 #pragma unroll
-        for (int t = 0; t < TS; ++t)
-#pragma unroll
-          for (int it = 0; it < RT; ++it) x[it] = mma<F32>(sf[t], qf[it], x[it]);
+        for (int it = 0; it < RT; ++it) x[it] = mma<F32>(sf, qf[it], x[it]);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -406,9 +415,9 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
           }
 #pragma unroll
           for (int u = 0; u < PER; ++u) {
-            uint4 w[1];
-            as_operand<false, 1>(p, u, w);
-            shared[b * PER + u][lane] = w[0];
+            uint4 w;
+            as_operand<false>(p, u, w);
+            shared[b * PER + u][lane] = w;
           }
         }
       }
@@ -453,14 +462,16 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
               make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
       } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          *reinterpret_cast<uint4*>(static_cast<u16*>(a.o.p) + to + 16 * u + 8 * hf) =
-              make_uint4(pack_bf16(x[8 * u], x[8 * u + 1]), pack_bf16(x[8 * u + 2], x[8 * u + 3]),
-                         pack_bf16(x[8 * u + 4], x[8 * u + 5]), pack_bf16(x[8 * u + 6], x[8 * u + 7]));
+        for (int u = 0; u < 2; ++u) {
+          uint4 w;
+          as_operand<false>(x, u, w);
+          *reinterpret_cast<uint4*>(static_cast<u16*>(a.o.p) + to + 16 * u + 8 * hf) = w;
+        }
       }
     };
     // st += (k decayed)^T v of the chunk in LDS
     auto update = [&](const uint4(&vf)[C / KB]) {
+      constexpr int TU = F32 ? 1 : 3;
 #pragma unroll
       for (int kb = 0; kb < C / KB; ++kb) {
         uint4 u[TU];
@@ -484,7 +495,11 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
         for (int t = 0; t < AT; ++t) {
           const uint4 kf = ra.col(kt, kb, t);
 #pragma unroll
-          for (int x = 0; x < TU; ++x) st[t] = mma<F32>(kf, u[x], st[t]);
+          for (int x = 0; x < (F32 ? 1 : 2); ++x) st[t] = mma<F32>(kf, u[x], st[t]);
+        }
+        if (!F32 && a.fine) {
+#pragma unroll
+          for (int t = 0; t < AT; ++t) st[t] = mma<F32>(ra.col(kt, kb, t), u[TU - 1], st[t]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -612,10 +627,16 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Chunks
 // The states before every part from the parts' own sums, in their place: E_0
 // is the state before the sequence (or zero), E_{p+1} = g^rows E_p + U_p.
 constexpr int kScanThreads = 256, kScanAhead = 8;
-__global__ __launch_bounds__(kScanThreads) void scan_kernel(float* sums, const float* first, const float* log_decay,
+struct Scan {
+  float* sums;
+  const float* first;
+};
+__global__ __launch_bounds__(kScanThreads) void scan_kernel(Scan one, Scan two, const float* log_decay,
                                                             const int32_t* starts, int batch, int tokens, int heads,
                                                             int parts, int part_rows, int size) {
   const int blocks = size / (4 * kScanThreads);
+  float* const sums = blockIdx.y == 0 ? one.sums : two.sums;
+  const float* const first = blockIdx.y == 0 ? one.first : two.first;
   const int64_t sh = blockIdx.x / blocks;
   const int i = ((blockIdx.x % blocks) * kScanThreads + threadIdx.x) * 4;
   const int seq = (int)(sh / heads), head = (int)(sh % heads);
@@ -742,23 +763,29 @@ __global__ __launch_bounds__(256) void through_kernel(const float* from, float* 
 }
 
 template <bool F32, bool MANY, bool SUMS>
-hipError_t chunks_of(const Chunks& a, int A, int B, hipStream_t s) {
-  const dim3 g((uint32_t)((int64_t)a.batch * a.heads * a.parts * a.slices));
+hipError_t chunks_of(const Roles& r, int A, int B, hipStream_t s) {
+  const Chunks& a = r.c[0];
+  int64_t n = (int64_t)a.batch * a.heads * a.parts * a.slices;
+  if (r.n > 1) n = (n + 7) / 8 * 8 * r.n;
+  const dim3 g((uint32_t)n);
   if (B == 64) {
-    if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS><<<g, 128, 0, s>>>(a);
-    else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS><<<g, 128, 0, s>>>(a);
-    else chunk_kernel<F32, 256, 2, MANY, SUMS><<<g, 128, 0, s>>>(a);
+    if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS><<<g, 128, 0, s>>>(r);
+    else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS><<<g, 128, 0, s>>>(r);
+    else chunk_kernel<F32, 256, 2, MANY, SUMS><<<g, 128, 0, s>>>(r);
   } else {
-    if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS><<<g, 256, 0, s>>>(a);
-    else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS><<<g, 256, 0, s>>>(a);
-    else chunk_kernel<F32, 256, 4, MANY, SUMS><<<g, 256, 0, s>>>(a);
+    if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS><<<g, 256, 0, s>>>(r);
+    else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS><<<g, 256, 0, s>>>(r);
+    else chunk_kernel<F32, 256, 4, MANY, SUMS><<<g, 256, 0, s>>>(r);
   }
   return hipGetLastError();
 }
 
+// (all of the same parts and slices)
 template <bool MANY, bool SUMS>
-hipError_t chunks(const Chunks& a, int A, int B, bool f32, hipStream_t s) {
-  return f32 ? chunks_of<true, MANY, SUMS>(a, A, B, s) : chunks_of<false, MANY, SUMS>(a, A, B, s);
+hipError_t chunks(std::initializer_list<Chunks> c, int A, int B, bool f32, hipStream_t s) {
+  Roles r = {};
+  for (const Chunks& x : c) r.c[r.n++] = x;
+  return f32 ? chunks_of<true, MANY, SUMS>(r, A, B, s) : chunks_of<false, MANY, SUMS>(r, A, B, s);
 }
 
 int slices_of(int B) { return B == 256 ? 2 : 1; }
@@ -773,15 +800,17 @@ Chunks base_of(const LinearLaunch& a, int B) {
   return c;
 }
 
-// The parts' sums in `sums`, then what stands before each part.
-template <bool MANY>
-hipError_t before_parts(Chunks c, const LinearLaunch& a, const float* first, float* sums, hipStream_t s) {
+// The same rows' launch for the parts' own sums, in `sums`.
+Chunks sums_of(Chunks c, const LinearLaunch& a, float* sums) {
+  const int64_t size = (int64_t)a.dk * a.dv;
+  c.out = sums, c.out_part = size, c.out_head = size * a.parts, c.out_seq = c.out_head * a.kv_heads;
+  return c;
+}
+hipError_t scan(const LinearLaunch& a, int n, Scan one, Scan two, hipStream_t s) {
   const int size = a.dk * a.dv;
-  c.out = sums, c.out_part = size, c.out_head = (int64_t)size * a.parts, c.out_seq = c.out_head * a.kv_heads;
-  hipError_t e = chunks<MANY, true>(c, a.dk, a.dv, a.f32, s);
-  if (e != hipSuccess) return e;
-  scan_kernel<<<(uint32_t)((int64_t)a.batch * a.kv_heads * (size / (4 * kScanThreads))), kScanThreads, 0, s>>>(
-      sums, first, a.log_decay, a.starts, a.batch, a.tokens, a.kv_heads, a.parts, a.part_rows, size);
+  const dim3 g((uint32_t)((int64_t)a.batch * a.kv_heads * (size / (4 * kScanThreads))), (uint32_t)n);
+  scan_kernel<<<g, kScanThreads, 0, s>>>(one, two, a.log_decay, a.starts, a.batch, a.tokens, a.kv_heads, a.parts,
+                                         a.part_rows, size);
   return hipGetLastError();
 }
 
@@ -811,7 +840,7 @@ bool linear_few(int max_new) { return max_new <= 8; }
 void linear_parts(LinearLaunch* a) {
   const int rows = a->f32 ? 32 : 64;
   const int64_t states = (int64_t)a->batch * a->kv_heads * slices_of(a->dv);
-  const int64_t want = std::max<int64_t>(1, 512 / states);
+  const int64_t want = std::max<int64_t>(1, (a->dv == 64 ? 1024 : 512) / states);
   const int64_t most = std::max<int64_t>(1, a->max_new / (4 * rows));
   const int64_t parts = std::min(want, most);
   a->part_rows = (int)((((int64_t)a->max_new + parts - 1) / parts + rows - 1) / rows * rows);
@@ -826,45 +855,55 @@ hipError_t launch_linear(const LinearLaunch& a, hipStream_t s) {
   }
   Chunks c = base_of(a, a.dv);
   c.q = a.q, c.k = a.k, c.v = a.v, c.o = a.o;
-  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f;
-  if (a.parts > 1) {
-    const hipError_t e = before_parts<false>(c, a, a.first, a.sums, s);
-    if (e != hipSuccess) return e;
-  }
+  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f, c.fine = a.last != nullptr;
+  hipError_t e;
+  if (a.parts > 1 && ((e = chunks<false, true>({sums_of(c, a, a.sums)}, a.dk, a.dv, a.f32, s)) != hipSuccess ||
+                      (e = scan(a, 1, {a.sums, a.first}, {}, s)) != hipSuccess))
+    return e;
   states_from(&c, a, a.first, a.sums);
   c.out = a.last;
-  return chunks<false, false>(c, a.dk, a.dv, a.f32, s);
+  return chunks<false, false>({c}, a.dk, a.dv, a.f32, s);
 }
 
 hipError_t launch_linear_backward(const LinearBackLaunch& b, hipStream_t s) {
   const LinearLaunch& a = b.f;
-  hipError_t e;
-  // dq, from the states before each part
-  Chunks c = base_of(a, a.dv);
-  c.k = a.k, c.v = a.v;
-  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f;
-  if (a.parts > 1 && (e = before_parts<false>(c, a, a.first, a.sums, s)) != hipSuccess) return e;
-  states_from(&c, a, a.first, a.sums);
-  c.slices = slices_of(a.dk);
-  c.q = b.d_o, c.k = a.v, c.v = a.k, c.o = b.dq, c.state_turned = 1;
-  if ((e = chunks<false, false>(c, a.dv, a.dk, a.f32, s)) != hipSuccess) return e;
-  // dk and dv, from the gradients of the states behind each part
-  c = base_of(a, a.dv);
-  c.k = a.q, c.v = b.d_o;
-  c.lead = 0, c.back = 1, c.s_in = a.scale, c.s_out = 1.f, c.s_up = a.scale;
   const bool many = a.q.heads > a.kv_heads;
+  hipError_t e;
+  // the states before each part, and the gradients of those behind each part
+  Chunks f = base_of(a, a.dv), r = f;
+  f.k = a.k, f.v = a.v;
+  f.lead = 1, f.s_in = f.s_out = a.scale, f.s_up = 1.f;
+  r.k = a.q, r.v = b.d_o;
+  r.lead = 0, r.back = 1, r.s_in = a.scale, r.s_out = 1.f, r.s_up = a.scale, r.fine = b.d_first != nullptr;
   if (a.parts > 1) {
-    e = many ? before_parts<true>(c, a, b.d_last, b.back_sums, s) : before_parts<false>(c, a, b.d_last, b.back_sums, s);
-    if (e != hipSuccess) return e;
+    const Chunks u = sums_of(f, a, a.sums), w = sums_of(r, a, b.back_sums);
+    if (many) {
+      if ((e = chunks<false, true>({u}, a.dk, a.dv, a.f32, s)) != hipSuccess) return e;
+      e = chunks<true, true>({w}, a.dk, a.dv, a.f32, s);
+    } else {
+      e = chunks<false, true>({u, w}, a.dk, a.dv, a.f32, s);
+    }
+    if (e != hipSuccess || (e = scan(a, 2, {a.sums, a.first}, {b.back_sums, b.d_last}, s)) != hipSuccess) return e;
   }
-  states_from(&c, a, b.d_last, b.back_sums);
-  Chunks d = c;
-  d.slices = slices_of(a.dk);
-  d.q = a.v, d.k = b.d_o, d.v = a.q, d.o = b.dk, d.state_turned = 1;
-  e = many ? chunks<true, false>(d, a.dv, a.dk, a.f32, s) : chunks<false, false>(d, a.dv, a.dk, a.f32, s);
-  if (e != hipSuccess) return e;
-  c.q = a.k, c.o = b.dv, c.out = b.d_first;
-  return many ? chunks<true, false>(c, a.dk, a.dv, a.f32, s) : chunks<false, false>(c, a.dk, a.dv, a.f32, s);
+  states_from(&f, a, a.first, a.sums);
+  states_from(&r, a, b.d_last, b.back_sums);
+  Chunks q = f, k = r, v = r;
+  q.slices = k.slices = slices_of(a.dk);
+  q.q = b.d_o, q.k = a.v, q.v = a.k, q.o = b.dq, q.state_turned = 1;
+  k.q = a.v, k.k = b.d_o, k.v = a.q, k.o = b.dk, k.state_turned = 1, k.fine = 0;
+  v.q = a.k, v.o = b.dv, v.out = b.d_first;
+  // (dv's launch writes d_first: with one part, where the others would read d_last
+  // or the first state at the same time, it may be one of them)
+  const bool with_v = a.dk == a.dv && (a.parts > 1 || (b.d_first != b.d_last && b.d_first != a.first));
+  if (many) {
+    if ((e = chunks<false, false>({q}, a.dv, a.dk, a.f32, s)) != hipSuccess) return e;
+    if (with_v) return chunks<true, false>({k, v}, a.dv, a.dk, a.f32, s);
+    if ((e = chunks<true, false>({k}, a.dv, a.dk, a.f32, s)) != hipSuccess) return e;
+    return chunks<true, false>({v}, a.dk, a.dv, a.f32, s);
+  }
+  if (with_v) return chunks<false, false>({q, k, v}, a.dv, a.dk, a.f32, s);
+  if ((e = chunks<false, false>({q, k}, a.dv, a.dk, a.f32, s)) != hipSuccess) return e;
+  return chunks<false, false>({v}, a.dk, a.dv, a.f32, s);
 }
 
 hipError_t launch_linear_through(const LinearBackLaunch& b, hipStream_t s) {
