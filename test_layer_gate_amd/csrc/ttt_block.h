@@ -64,7 +64,7 @@ struct LinearBackLaunch {
 };
 // Rows a sequence from which the chunked kernel takes them.
 bool linear_few(int max_new);
-void linear_parts(LinearLaunch* a);
+void linear_parts(LinearLaunch* a, bool back);
 hipError_t launch_linear(const LinearLaunch& a, hipStream_t s);
 hipError_t launch_linear_backward(const LinearBackLaunch& a, hipStream_t s);
 // d_last (or zeros) to d_first: the backward of a call without rows.

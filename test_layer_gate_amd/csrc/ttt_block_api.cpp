@@ -315,7 +315,7 @@ ttt_status ttt_linear_attention_workspace_size(const ttt_linear* linear, size_t*
   if (bytes == nullptr) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
   tttk::LinearLaunch a = {};
   TTT_TRY(check_linear(linear, &a));
-  tttk::linear_parts(&a);
+  tttk::linear_parts(&a, false);
   *bytes = tttk::linear_few(a.max_new) ? 0 : part_bytes(a);
   return TTT_OK;
   TTT_ENTRY_END
@@ -338,7 +338,7 @@ ttt_status ttt_linear_attention(const ttt_linear* linear, const ttt_rows* q, con
     all.out.push_back(reach_of("state", state, state_bytes(a)));
   }
   if (a.tokens == 0) return TTT_OK;
-  tttk::linear_parts(&a);
+  tttk::linear_parts(&a, false);
   const size_t need = tttk::linear_few(a.max_new) ? 0 : part_bytes(a);
   TTT_TRY(check_workspace(workspace, workspace_bytes, need));
   if (need > 0) all.out.push_back(reach_of("workspace", workspace, need));
@@ -354,7 +354,7 @@ ttt_status ttt_linear_attention_backward_workspace_size(const ttt_linear* linear
   if (bytes == nullptr) return fail(TTT_ERR_INVALID_ARG, "bytes is NULL");
   tttk::LinearLaunch a = {};
   TTT_TRY(check_linear(linear, &a));
-  tttk::linear_parts(&a);
+  tttk::linear_parts(&a, true);
   *bytes = 2 * part_bytes(a);
   return TTT_OK;
   TTT_ENTRY_END
@@ -390,7 +390,7 @@ ttt_status ttt_linear_attention_backward(const ttt_linear* linear, const ttt_row
     TTT_TRY(check_ptr(d_state0, "d_state0", 16));
     all.out.push_back(reach_of("d_state0", d_state0, state_bytes(a)));
   }
-  tttk::linear_parts(&a);
+  tttk::linear_parts(&a, true);
   const size_t need = a.tokens > 0 ? part_bytes(a) : 0;
   TTT_TRY(check_workspace(workspace, workspace_bytes, 2 * need));
   if (need > 0) all.out.push_back(reach_of("workspace", workspace, 2 * need));

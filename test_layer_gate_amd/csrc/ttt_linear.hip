@@ -37,7 +37,6 @@ struct Chunks {
   int state_turned;             // state is [B][A]
   int batch, tokens, heads, parts, part_rows, slices;
   int lead, back;
-  int fine;                     // the state behind the last row is a result, here or of what follows
   float s_in, s_out, s_up;
 };
 
@@ -195,23 +194,32 @@ __device__ __forceinline__ float power(float lg, int n) { return n == 0 ? 1.f : 
 
 // A tile on its way: its rows are loaded to registers (get) while the kernel
 // works on others, and written to LDS (put) when their place is free. Rows
-// from `count` on are zero; dir -1 goes backwards from row0. put() tells, if
-// asked, whether a value is infinite or NaN.
+// from `count` on are zero; dir -1 goes backwards; heads count from the first
+// one's. put() tells, if asked, whether a value is infinite or NaN.
 template <bool F32, int W, int NT>
 struct Fetch {
   static constexpr int P = W * Elem<F32>::size / 16, R = NT / P;  // R rows at a time
   static constexpr int N = Elem<F32>::rows / R;
   static_assert(NT % P == 0 && Elem<F32>::rows % R == 0, "whole passes");
   uint4 v[N];
-  __device__ __forceinline__ void get(const Rows& x, int head, int col, int64_t row0, int dir, int count) {
-    const int r = threadIdx.x / P, c = threadIdx.x % P;
-    const int64_t stride = x.ts * Elem<F32>::size * dir;
-    const char* p = static_cast<const char*>(x.p) + (head * x.hs + col + row0 * x.ts) * Elem<F32>::size + r * stride + c * 16;
+  const char* at;  // the lane's place in the next chunk, of the first head
+  __device__ __forceinline__ Fetch(const Rows& x, int head, int col, int64_t row0, int dir)
+      : at(static_cast<const char*>(x.p) +
+           (head * x.hs + col + (row0 + (int)(threadIdx.x / P) * dir) * x.ts) * Elem<F32>::size + threadIdx.x % P * 16) {}
+  __device__ __forceinline__ void on(const Rows& x, int rows) { at += rows * x.ts * Elem<F32>::size; }
+  __device__ __forceinline__ void get(const Rows& x, int head, int dir, int count) {
+    const int64_t step = x.ts * Elem<F32>::size * (dir * R);
+    const char* p = at + head * x.hs * Elem<F32>::size;
+    if (count >= Elem<F32>::rows) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r + i * R < count) v[i] = *reinterpret_cast<const uint4*>(p);
-      p += R * stride;
+      for (int i = 0; i < N; ++i, p += step) v[i] = *reinterpret_cast<const uint4*>(p);
+    } else {
+      const int r = threadIdx.x / P;
+#pragma unroll
+      for (int i = 0; i < N; ++i, p += step) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r + i * R < count) v[i] = *reinterpret_cast<const uint4*>(p);
+      }
     }
   }
   template <bool CHECK>
@@ -254,8 +262,7 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // 64 bits 0.0023, 0.0017 of it the result's own rounding; with the state as two
 // terms 0.0018, for 16 products and 96 vector instructions a chunk more). In the
 // update, whose sums stay in fp32 from chunk to chunk, v times its decay is three
-// terms (24 bits) where the state is a result, else two (16). fp32: the matrix
-// cores' fp32 products throughout.
+// terms (24 bits). fp32: the matrix cores' fp32 products throughout.
 template <bool F32, int A, int NW, bool MANY, bool SUMS>
 __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles roles) {
   constexpr int C = Elem<F32>::rows, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
@@ -303,9 +310,52 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
   if (SUMS && last) return;  // (nobody reads it)
   const int64_t end = last ? len : mine + a.part_rows;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hf = lane >> 5, col = lane & 31;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hf = lane >> 5, col = lane & 31;
   const int b0 = slice * B + wave * 32 + column_of<F32>(col);  // the lane's column of the state
   const int b_all = a.slices * B;
+  // (the first loads before what is computed from the decay: it takes as long)
+  const int q_heads = MANY ? 1 : a.q.heads / a.heads, k_heads = MANY ? a.k.heads / a.heads : 1;
+  const int dir = a.back ? -1 : 1;
+  int64_t t0 = mine;
+  const int64_t row0 = a.back ? base + len - 1 - t0 : base + t0;
+  int take = (int)min((int64_t)C, end - t0);
+  Fetch<F32, A, NT> fk(a.k, head * k_heads, 0, row0, dir), fq(a.q, head * q_heads, 0, row0, dir);
+  Fetch<F32, B, NT> fv(a.v, head * k_heads, slice * B, row0, dir);
+  fk.get(a.k, 0, dir, take);
+  fv.get(a.v, 0, dir, take);
+  if constexpr (!SUMS) fq.get(a.q, 0, dir, take);
+  char* o_at = static_cast<char*>(a.o.p) +
+               (head * q_heads * a.o.hs + slice * B + wave * 32 + (row0 + col * dir) * a.o.ts) * Elem<F32>::size + 16 * hf;
+  // value r of a lane's 16 of a state is row state_row(r) + state_hf of the 32
+  auto state_row = [](int r) { return F32 ? 8 * (r >> 2) + (r & 3) : 16 * (r >> 3) + (r & 7); };
+  const int state_hf = (F32 ? 4 : 8) * hf;
+  f32x16_t st[AT];
+  if (!SUMS && a.state != nullptr) {
+    const float* e = a.state + seq * a.state_seq + head * a.state_head + part * a.state_part;
+    if (a.state_turned) {
+      e += (int64_t)b0 * A + state_hf;
+#pragma unroll
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(e + 32 * t + state_row(r));
+          st[t][r] = w.x, st[t][r + 1] = w.y, st[t][r + 2] = w.z, st[t][r + 3] = w.w;
+        }
+    } else {
+      e += (int64_t)state_hf * b_all + b0;
+#pragma unroll
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) st[t][r] = e[(32 * t + state_row(r)) * b_all];
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < AT; ++t) st[t] = f32x16_t{};
+  }
+
+  __builtin_amdgcn_sched_barrier(0);
+
   const float lg = a.log_decay[head] * kLog2e;
 
   float row_f[RT];  // of the lane's row of x
@@ -329,32 +379,6 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       decay[SUMS ? 0 : wave][u][lane] = make_float4(f[0], f[1], f[2], f[3]);
     }
   }
-  // value r of a lane's 16 of a state is row state_row(r) + state_hf of the 32
-  auto state_row = [](int r) { return F32 ? 8 * (r >> 2) + (r & 3) : 16 * (r >> 3) + (r & 7); };
-  const int state_hf = (F32 ? 4 : 8) * hf;
-  f32x16_t st[AT];
-  if (!SUMS && a.state != nullptr) {
-    const float* e = a.state + seq * a.state_seq + head * a.state_head + part * a.state_part;
-    e += a.state_turned ? (int64_t)b0 * A + state_hf : (int64_t)state_hf * b_all + b0;
-    const int step = a.state_turned ? 1 : b_all;
-#pragma unroll
-    for (int t = 0; t < AT; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) st[t][r] = e[(32 * t + state_row(r)) * step];
-  } else {
-#pragma unroll
-    for (int t = 0; t < AT; ++t) st[t] = f32x16_t{};
-  }
-
-  const int q_heads = MANY ? 1 : a.q.heads / a.heads, k_heads = MANY ? a.k.heads / a.heads : 1;
-  const int dir = a.back ? -1 : 1;
-  int64_t t0 = mine, row0 = a.back ? base + len - 1 - t0 : base + t0;
-  int take = (int)min((int64_t)C, end - t0);
-  Fetch<F32, A, NT> fk, fq;
-  Fetch<F32, B, NT> fv;
-  fk.get(a.k, head * k_heads, 0, row0, dir, take);
-  fv.get(a.v, head * k_heads, slice * B, row0, dir, take);
-  if constexpr (!SUMS) fq.get(a.q, head * q_heads, 0, row0, dir, take);
   while (t0 < end) {
     ra.forget();
     rb.forget();
@@ -362,22 +386,26 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
     // x of every row tile (column i: its row) = its product with the state before
     // the chunk
     auto with_state = [&](f32x16_t(&x)[RT]) {
-      uint4 qn[RT];
+      uint4 qf[2][RT];
 #pragma unroll
-      for (int it = 0; it < RT; ++it) qn[it] = ra.row(qt, it, 0), x[it] = f32x16_t{};
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int it = 0; it < RT; ++it) qf[kb][it] = ra.row(qt, it, kb);
+#pragma unroll
+      for (int it = 0; it < RT; ++it) x[it] = f32x16_t{};
 #pragma unroll
       for (int kb = 0; kb < A / KB; ++kb) {
-        uint4 qf[RT], sf;
-#pragma unroll
-        for (int it = 0; it < RT; ++it) {
-          qf[it] = qn[it];
-          if (kb + 1 < A / KB) qn[it] = ra.row(qt, it, kb + 1);
-        }
+        uint4 sf;
         as_operand<F32>(st[kb / PER], kb % PER, sf);
 #pragma unroll
-        for (int it = 0; it < RT; ++it) x[it] = mma<F32>(sf, qf[it], x[it]);
+        for (int it = 0; it < RT; ++it) {
+          x[it] = mma<F32>(sf, qf[kb & 1][it], x[it]);
+          if (kb + 2 < A / KB) qf[kb & 1][it] = ra.row(qt, it, kb + 2);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    auto decay_rows = [&](f32x16_t(&x)[RT]) {
 #pragma unroll
       for (int it = 0; it < RT; ++it)
 #pragma unroll
@@ -387,29 +415,44 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
     // shared by the waves through LDS as the lanes will hold them: bf16 tiles a
     // wave each, decayed and rounded; of fp32's one tile, each wave a part of the
     // contraction over A.
-    auto give_weights = [&]() {
+    // (x, the product with the state, while the first ones are under way)
+    auto weights_and_state = [&](bool state, f32x16_t(&x)[RT]) {
       if constexpr (F32) {
         constexpr int N = A / KB / NW;
         f32x16_t p = {};
 #pragma unroll
         for (int n = 0; n < N; ++n) p = mma<true>(ra.row(kt, 0, wave * N + n), ra.row(qt, 0, wave * N + n), p);
+        if (state) with_state(x);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           shared[wave * 4 + u][lane] = make_uint4(__float_as_uint(p[4 * u]), __float_as_uint(p[4 * u + 1]),
                                                   __float_as_uint(p[4 * u + 2]), __float_as_uint(p[4 * u + 3]));
       } else {
-        for (int b = wave; b < RT * (RT + 1) / 2; b += NW) {
-          const int it = b > 0, jt = b > 1;
-          const char *kp = kt + 32 * jt * ra.row_bytes, *qp = qt + 32 * it * ra.row_bytes;
-          f32x16_t p = {};
+        constexpr int blocks = RT * (RT + 1) / 2;
+        f32x16_t p = {};
+        auto begin = [&](int b) {
+          const char *kp = kt + 32 * (b > 1) * ra.row_bytes, *qp = qt + 32 * (b > 0) * ra.row_bytes;
+          p = f32x16_t{};
+          constexpr int D = 4;  // so many reads ahead: their latency is that of as many products
+          uint4 kf[D], qf[D];
 #pragma unroll
-          for (int kb = 0; kb < A / KB; ++kb) p = mma<false>(ra.row(kp, 0, kb), ra.row(qp, 0, kb), p);
+          for (int kb = 0; kb < D; ++kb) kf[kb] = ra.row(kp, 0, kb), qf[kb] = ra.row(qp, 0, kb);
+#pragma unroll
+          for (int kb = 0; kb < A / KB; ++kb) {
+            p = mma<false>(kf[kb % D], qf[kb % D], p);
+            if (kb + D < A / KB) kf[kb % D] = ra.row(kp, 0, kb + D), qf[kb % D] = ra.row(qp, 0, kb + D);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        };
+        auto finish = [&](int b) {
+          const int d = b == 1;  // the block below the diagonal's
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float4 f = decay[SUMS ? 0 : it - jt][u][lane];
-            const float w[4] = {f.x, f.y, f.z, f.w};
+            const float4 f = decay[SUMS ? 0 : d][u][lane];
+            float w[4] = {f.x, f.y, f.z, f.w};
+            asm("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));  // (no branches around their reads)
             // (a weight that is not taken may be a NaN)
-            const int n = 32 * (it - jt) + col - 8 * u - 4 * hf;
+            const int n = 32 * d + col - 8 * u - 4 * hf;
 #pragma unroll
             for (int e = 0; e < 4; ++e) p[4 * u + e] = e > n ? 0.f : p[4 * u + e] * w[e];
           }
@@ -419,12 +462,17 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
             as_operand<false>(p, u, w);
             shared[b * PER + u][lane] = w;
           }
-        }
+        };
+        if (wave < blocks) begin(wave);
+        if (state) with_state(x);
+        if (wave < blocks) finish(wave);
+        for (int b = wave + NW; b < blocks; b += NW) begin(b), finish(b);
       }
     };
     // x += those weights times v
     auto take_weights = [&](const uint4(&vf)[C / KB], f32x16_t(&x)[RT]) {
       if constexpr (F32) {
+        if constexpr (!MANY) decay_rows(x);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float4 f = decay[0][u][lane];
@@ -441,10 +489,16 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
           x[0] = mma<true>(vf[u], make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])), x[0]);
         }
       } else {
+        constexpr int N = RT * (RT + 1) / 2 * PER;
+        uint4 w[N];
 #pragma unroll
-        for (int it = 0; it < RT; ++it)
+        for (int n = 0; n < N; ++n) w[n] = shared[n][lane];
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!MANY) decay_rows(x);
 #pragma unroll
-          for (int kb = 0; kb < (it + 1) * PER; ++kb) x[it] = mma<false>(vf[kb], shared[it * PER + kb][lane], x[it]);
+        for (int kb = 0; kb < RT * PER; ++kb)
+#pragma unroll
+          for (int it = kb / PER; it < RT; ++it) x[it] = mma<false>(vf[kb], w[it * PER + kb], x[it]);
       }
     };
     auto load_v = [&](uint4(&vf)[C / KB]) {
@@ -452,36 +506,41 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       for (int kb = 0; kb < C / KB; ++kb) vf[kb] = rb.col(vt, kb, wave);
     };
     // Row tile `it` of a head's outputs.
-    auto store = [&](int it, int q_head, const f32x16_t& x, int64_t row0, int take) {
+    auto store = [&](int it, int q_head, const f32x16_t& x, int take) {
       if (32 * it + col >= take) return;
-      const int64_t to = (row0 + (int64_t)((32 * it + col) * dir)) * a.o.ts + q_head * a.o.hs + slice * B + wave * 32;
+      char* to = o_at + (32 * it * dir * a.o.ts + q_head * a.o.hs) * Elem<F32>::size;
       if constexpr (F32) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.o.p) + to + 8 * u + 4 * hf) =
-              make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+          *reinterpret_cast<float4*>(to + 32 * u) = make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint4 w;
           as_operand<false>(x, u, w);
-          *reinterpret_cast<uint4*>(static_cast<u16*>(a.o.p) + to + 16 * u + 8 * hf) = w;
+          *reinterpret_cast<uint4*>(to + 32 * u) = w;
         }
       }
     };
-    // st += (k decayed)^T v of the chunk in LDS
+    // st += (k decayed)^T v of the chunk in LDS. What a block's products take is
+    // read and computed in the shadow of those before it: with one block after the
+    // other a chunk's update took 3400 cycles, for 1000 to 1500 of products.
     auto update = [&](const uint4(&vf)[C / KB]) {
-      constexpr int TU = F32 ? 1 : 3;
+      constexpr int TU = F32 ? 1 : 3;  // terms
+      uint4 u[2][TU], kf[2][AT];
+      float4 f, g;
+      auto read = [&](int kb, uint4(&kf)[AT]) {
+        f = *reinterpret_cast<const float4*>(&up_f[KB * kb + 4 * hf]);
+        if constexpr (!F32) g = *reinterpret_cast<const float4*>(&up_f[KB * kb + 8 + 4 * hf]);
 #pragma unroll
-      for (int kb = 0; kb < C / KB; ++kb) {
-        uint4 u[TU];
+        for (int t = 0; t < AT; ++t) kf[t] = ra.col(kt, kb, t);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto ready = [&](int kb, uint4(&u)[TU]) {
         if constexpr (F32) {
-          const float4 f = *reinterpret_cast<const float4*>(&up_f[8 * kb + 4 * hf]);
           u[0] = make_uint4(__float_as_uint(__uint_as_float(vf[kb].x) * f.x), __float_as_uint(__uint_as_float(vf[kb].y) * f.y),
                             __float_as_uint(__uint_as_float(vf[kb].z) * f.z), __float_as_uint(__uint_as_float(vf[kb].w) * f.w));
         } else {
-          const float4 f = *reinterpret_cast<const float4*>(&up_f[16 * kb + 4 * hf]);
-          const float4 g = *reinterpret_cast<const float4*>(&up_f[16 * kb + 8 + 4 * hf]);
           const uint32_t w[4] = {vf[kb].x, vf[kb].y, vf[kb].z, vf[kb].w};
           const float m[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
           uint32_t z[4][TU];
@@ -491,30 +550,35 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
 #pragma unroll
           for (int t = 0; t < TU; ++t) u[t] = make_uint4(z[0][t], z[1][t], z[2][t], z[3][t]);
         }
+      };
+      read(0, kf[0]);
+      ready(0, u[0]);
 #pragma unroll
-        for (int t = 0; t < AT; ++t) {
-          const uint4 kf = ra.col(kt, kb, t);
-#pragma unroll
-          for (int x = 0; x < (F32 ? 1 : 2); ++x) st[t] = mma<F32>(kf, u[x], st[t]);
+      for (int kb = 0; kb < C / KB; ++kb) {
+        if (kb + 1 < C / KB) {
+          read(kb + 1, kf[(kb + 1) & 1]);
+          ready(kb + 1, u[(kb + 1) & 1]);
         }
-        if (!F32 && a.fine) {
 #pragma unroll
-          for (int t = 0; t < AT; ++t) st[t] = mma<F32>(ra.col(kt, kb, t), u[TU - 1], st[t]);
-        }
+        for (int x = 0; x < TU; ++x)
+#pragma unroll
+          for (int t = 0; t < AT; ++t) st[t] = mma<F32>(kf[kb & 1][t], u[kb & 1][x], st[t]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    // the next chunk's tiles, behind this one's `take` rows
-    const int64_t row_now = row0;
+    // the next chunk's tiles, behind this one's `now` rows
     auto next = [&](int now) {
-      t0 += now, row0 += now * dir;
+      t0 += now;
       // (a count of 0 behind the end: without a value of their own here, the
       // registers would be taken through the whole loop)
       take = (int)min((int64_t)C, end - t0);
-      fk.get(a.k, head * k_heads, 0, row0, dir, take);
-      fv.get(a.v, head * k_heads, slice * B, row0, dir, take);
-      if constexpr (!SUMS) fq.get(a.q, head * q_heads, 0, row0, dir, take);
+      fk.on(a.k, now * dir);
+      fv.on(a.v, now * dir);
+      if constexpr (!SUMS) fq.on(a.q, now * dir);
+      fk.get(a.k, 0, dir, take);
+      fv.get(a.v, 0, dir, take);
+      if constexpr (!SUMS) fq.get(a.q, 0, dir, take);
       __builtin_amdgcn_sched_barrier(0);
     };
     int now = take;
@@ -528,8 +592,8 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
         // an infinity or a NaN times a later row's weight of 0 would be NaN:
         // such a chunk is taken a row at a time
         now = 1;
-        fk.get(a.k, head, 0, row0, dir, now);
-        fv.get(a.v, head, slice * B, row0, dir, now);
+        fk.get(a.k, 0, dir, now);
+        fv.get(a.v, 0, dir, now);
         fk.template put<false>(kt);
         fv.template put<false>(vt);
         lds_barrier();
@@ -550,28 +614,26 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
         f32x16_t x[RT];
         int h = 0;
         for (; h + 1 < q_heads; ++h) {
-          fq.get(a.q, head * q_heads + h + 1, 0, row_now, dir, now);
+          fq.get(a.q, h + 1, dir, now);
           __builtin_amdgcn_sched_barrier(0);
           // (so that the state's conversion stays inside the loop: kept over the
           // heads it would take as many registers again)
 #pragma unroll
           for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
-          give_weights();
-          with_state(x);
+          weights_and_state(true, x);
           lds_barrier();
           fq.template put<false>(qt);
           take_weights(vf, x);
 #pragma unroll
-          for (int it = 0; it < RT; ++it) store(it, head * q_heads + h, x[it], row_now, now);
+          for (int it = 0; it < RT; ++it) store(it, h, x[it], now);
           lds_barrier();
         }
         next(now);
-        give_weights();
-        with_state(x);
+        weights_and_state(true, x);
         lds_barrier();
         take_weights(vf, x);
 #pragma unroll
-        for (int it = 0; it < RT; ++it) store(it, head * q_heads + h, x[it], row_now, now);
+        for (int it = 0; it < RT; ++it) store(it, h, x[it], now);
       } else {
         next(now);
       }
@@ -583,7 +645,10 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
     } else {
       // q once, heads of k and v in turn
       f32x16_t x[RT];
-      if constexpr (!SUMS) with_state(x);
+      if constexpr (!SUMS) {
+        with_state(x);
+        decay_rows(x);
+      }
 #pragma unroll
       for (int t = 0; t < AT; ++t)
 #pragma unroll
@@ -597,22 +662,23 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
         }
         load_v(vf);
         if constexpr (!SUMS) {
-          give_weights();
+          weights_and_state(false, x);
           lds_barrier();
           take_weights(vf, x);
         }
         const int more = h + 1 < k_heads ? now : 0;
-        fk.get(a.k, head * k_heads + h + 1, 0, row_now, dir, more);
-        fv.get(a.v, head * k_heads + h + 1, slice * B, row_now, dir, more);
+        fk.get(a.k, h + 1, dir, more);
+        fv.get(a.v, h + 1, dir, more);
         __builtin_amdgcn_sched_barrier(0);
         update(vf);
       }
       next(now);
       if constexpr (!SUMS) {
 #pragma unroll
-        for (int it = 0; it < RT; ++it) store(it, head, x[it], row_now, now);
+        for (int it = 0; it < RT; ++it) store(it, 0, x[it], now);
       }
     }
+    o_at += now * dir * a.o.ts * Elem<F32>::size;
   }
 
   if (a.out != nullptr && (SUMS || last)) {
@@ -837,10 +903,10 @@ hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
 
 bool linear_few(int max_new) { return max_new <= 8; }
 
-void linear_parts(LinearLaunch* a) {
+void linear_parts(LinearLaunch* a, bool back) {
   const int rows = a->f32 ? 32 : 64;
   const int64_t states = (int64_t)a->batch * a->kv_heads * slices_of(a->dv);
-  const int64_t want = std::max<int64_t>(1, (a->dv == 64 ? 1024 : 512) / states);
+  const int64_t want = std::max<int64_t>(1, (a->dv == 64 ? 1024 : 512) / (back ? 2 : 1) / states);
   const int64_t most = std::max<int64_t>(1, a->max_new / (4 * rows));
   const int64_t parts = std::min(want, most);
   a->part_rows = (int)((((int64_t)a->max_new + parts - 1) / parts + rows - 1) / rows * rows);
@@ -855,7 +921,7 @@ hipError_t launch_linear(const LinearLaunch& a, hipStream_t s) {
   }
   Chunks c = base_of(a, a.dv);
   c.q = a.q, c.k = a.k, c.v = a.v, c.o = a.o;
-  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f, c.fine = a.last != nullptr;
+  c.lead = 1, c.s_in = c.s_out = a.scale, c.s_up = 1.f;
   hipError_t e;
   if (a.parts > 1 && ((e = chunks<false, true>({sums_of(c, a, a.sums)}, a.dk, a.dv, a.f32, s)) != hipSuccess ||
                       (e = scan(a, 1, {a.sums, a.first}, {}, s)) != hipSuccess))
@@ -874,7 +940,7 @@ hipError_t launch_linear_backward(const LinearBackLaunch& b, hipStream_t s) {
   f.k = a.k, f.v = a.v;
   f.lead = 1, f.s_in = f.s_out = a.scale, f.s_up = 1.f;
   r.k = a.q, r.v = b.d_o;
-  r.lead = 0, r.back = 1, r.s_in = a.scale, r.s_out = 1.f, r.s_up = a.scale, r.fine = b.d_first != nullptr;
+  r.lead = 0, r.back = 1, r.s_in = a.scale, r.s_out = 1.f, r.s_up = a.scale;
   if (a.parts > 1) {
     const Chunks u = sums_of(f, a, a.sums), w = sums_of(r, a, b.back_sums);
     if (many) {
@@ -890,11 +956,11 @@ hipError_t launch_linear_backward(const LinearBackLaunch& b, hipStream_t s) {
   Chunks q = f, k = r, v = r;
   q.slices = k.slices = slices_of(a.dk);
   q.q = b.d_o, q.k = a.v, q.v = a.k, q.o = b.dq, q.state_turned = 1;
-  k.q = a.v, k.k = b.d_o, k.v = a.q, k.o = b.dk, k.state_turned = 1, k.fine = 0;
+  k.q = a.v, k.k = b.d_o, k.v = a.q, k.o = b.dk, k.state_turned = 1;
   v.q = a.k, v.o = b.dv, v.out = b.d_first;
-  // (dv's launch writes d_first: with one part, where the others would read d_last
-  // or the first state at the same time, it may be one of them)
-  const bool with_v = a.dk == a.dv && (a.parts > 1 || (b.d_first != b.d_last && b.d_first != a.first));
+  // (dv's writes d_first, which may be d_last: with one part the others read that
+  // at the same time)
+  const bool with_v = a.dk == a.dv && (a.parts > 1 || b.d_first == nullptr || b.d_first != b.d_last);
   if (many) {
     if ((e = chunks<false, false>({q}, a.dv, a.dk, a.f32, s)) != hipSuccess) return e;
     if (with_v) return chunks<true, false>({k, v}, a.dv, a.dk, a.f32, s);
