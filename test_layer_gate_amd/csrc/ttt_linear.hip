@@ -903,12 +903,18 @@ hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
 
 bool linear_few(int max_new) { return max_new <= 8; }
 
+// Parts of the sequences: as many workgroups as have a place at once, two a
+// compute unit (of two waves for dim_v 64, else of four), of a chunk at least. The
+// parts' states cost a read or write of their own each, so that the gradients,
+// whose launches have two or three roles, take half as many. Measured, us:
+//   64k rows, 8/32 heads of 128:  512 parts 377, 256 418;  dim 64: 1024 parts 104, 512 115
+//   gradients of 2 x 8k rows, 16 heads of 128: 512 312, 256 292, 128 322
+//   2048 rows, 8/32 heads: parts of one chunk 35, of two 38, of four 54
 void linear_parts(LinearLaunch* a, bool back) {
   const int rows = a->f32 ? 32 : 64;
   const int64_t states = (int64_t)a->batch * a->kv_heads * slices_of(a->dv);
-  const int64_t want = std::max<int64_t>(1, (a->dv == 64 ? 1024 : 512) / (back ? 2 : 1) / states);
-  const int64_t most = std::max<int64_t>(1, a->max_new / (4 * rows));
-  const int64_t parts = std::min(want, most);
+  const int64_t places = (a->dv == 64 ? 1024 : 512) / (back ? 2 : 1);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(places / states, a->max_new / rows));
   a->part_rows = (int)((((int64_t)a->max_new + parts - 1) / parts + rows - 1) / rows * rows);
   a->parts = (int)(((int64_t)a->max_new + a->part_rows - 1) / a->part_rows);
 }

