@@ -250,6 +250,14 @@ struct Fetch {
 // are fetched ahead, and of the rows that leave, would stand in the way of each.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Bound by memory. A second pass over k and v, and the parts' states, are what a
+// parallel form reads beyond the operator's own rows: 64k rows of 8/32 heads of
+// 128 take 377 us for 1.74 GB, 4.6 TB/s; the gradients of 2 x 8k rows of 16 heads
+// 291 us for 1.2 GB, with the rows that several roles read in the caches. Beside
+// it a chunk of 64 rows waits, of 12400 cycles, 1800 for its tiles and their way to
+// LDS, 1500 to issue the next loads; weights and the product with the state take
+// 1800, the update 3600, with the matrix unit busy for a third of it.
+//
 // One part of a sequence's rows for one state head and a slice of NW * 32 of
 // the B columns; wave w has columns 32 w .. of the slice, with its part of the
 // state in registers (fp32, 16 values a lane for each 32 of A).
@@ -522,9 +530,8 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
         }
       }
     };
-    // st += (k decayed)^T v of the chunk in LDS. What a block's products take is
-    // read and computed in the shadow of those before it: with one block after the
-    // other a chunk's update took 3400 cycles, for 1000 to 1500 of products.
+    // st += (k decayed)^T v of the chunk in LDS; what a block's products take is
+    // read and computed beside those before it.
     auto update = [&](const uint4(&vf)[C / KB]) {
       constexpr int TU = F32 ? 1 : 3;  // terms
       uint4 u[2][TU], kf[2][AT];
@@ -736,8 +743,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(Scan one, Scan two, 
 
 // A few tokens a sequence: the state's slice of SB columns is read once, kept
 // in registers over the tokens, and written once: bound by HBM. Eight lanes
-// hold 32 neighbouring columns of a row of the state; 32 rows at a time.
-constexpr int kStepGroup = 8;   // heads of q at a time
+// hold 32 neighbouring columns of a row of the state; 32 rows at a time. A token
+// of 48 sequences, 8/32 heads of 128: 12.3 us for 51 MB, 4.2 TB/s.
 template <bool F32, int A, int G>
 __global__ __launch_bounds__(256) void token_kernel(LinearLaunch a) {
   constexpr int SB = 32, R = A / 32;
@@ -901,7 +908,11 @@ hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
 
 }  // namespace
 
-bool linear_few(int max_new) { return max_new <= 8; }
+// Token by token for one or two rows a sequence, whose state is read and written
+// by any kernel. Measured, us (8/32 heads of 128, bf16; token by token, in chunks):
+// 48 sequences of 2 rows 16.1, 20.2, of 4 29.6, 20.3; one of 2 rows 6.7, 13.3, of
+// 4 10.2, 13.2, of 8 17.5, 13.3.
+bool linear_few(int max_new) { return max_new <= 2; }
 
 // Parts of the sequences: as many workgroups as have a place at once, two a
 // compute unit (of two waves for dim_v 64, else of four), of a chunk at least. The

@@ -6,9 +6,9 @@ Tolerances, u = 2^-24, relative to the same sums with every term's magnitude
 each chunk multiplies once and adds to twice: dim_k + 64 + 3 chunks roundings;
 g^n is 2^(n lg): the exponent is within 3 u of itself, so g^n within 3 u n
 |log_decay| + 2 u of itself, and where that passes 64 u the term is below 2^-30 of
-the others. bf16 rows in chunks: the weights are rounded (half a step, 2^-8), the
-state enters as two terms (2^-17), the result is rounded (2^-8 of it). Those
-roundings are spread evenly, so of all values together (2-norm) the error is
+the others. bf16 rows in chunks: the weights or the state are rounded (half a step,
+2^-8 of their part of A each, so of A together), and the result (2^-8 of it).
+Those roundings are spread evenly, so of all values together (2-norm) the error is
 within sqrt(2 / 3) 2^-8 < 2^-8; fp32's is within 16 sqrt(dim_k) u of it. States
 have fp32's in either type (v times its decay enters as 24 bits)."""
 import math
@@ -22,6 +22,7 @@ import oracle.block_oracle as bo
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 U = 2.0 ** -24
+FEW = 2      # rows a sequence that are taken one by one, in fp32: no weights are rounded
 
 
 @pytest.fixture(scope="module")
@@ -71,7 +72,7 @@ class Case:
     def check(self, ttt, few=None, **kw):
         s = None if self.state is None else self.state.clone()
         o = self.run(ttt, s, **kw)
-        few = max(self.lens) <= 8 if few is None else few
+        few = max(self.lens) <= FEW if few is None else few
         for b in range(len(self.lens)):
             at = self.rows(b)
             args = [host(x[at]) for x in (self.q, self.k, self.v)]
@@ -155,10 +156,10 @@ def test_parts_of_long_sequences(ttt, dtype):
     Case([700], hk=1, group=2, dtype=dtype, state=False).check(ttt)
 
 
-@pytest.mark.parametrize("max_new", [1, 8, 64, 5000])
+@pytest.mark.parametrize("max_new", [1, 2, 8, 64, 5000])
 def test_a_wrong_bound_changes_no_result(ttt, max_new):
     Case([333, 20], group=2, dtype=F32).check(ttt, max_new=max_new)
-    Case([333, 20], group=2).check(ttt, max_new=max_new, few=max_new <= 8)
+    Case([333, 20], group=2).check(ttt, max_new=max_new, few=max_new <= FEW)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -233,7 +234,7 @@ def test_what_is_not_finite_reaches_no_earlier_row(ttt, dtype, bad, which):
         clean = np.ones(c.n, bool)
         clean[at:lens[0]] = False
         for rows, hs in ((clean, slice(0, heads)), (np.ones(c.n, bool), slice(heads, None))):
-            close(host(o)[rows, hs], ref[rows, hs], size[rows, hs], c.coef, dtype, "few" if lens[0] <= 8 else "o", c.dk)
+            close(host(o)[rows, hs], ref[rows, hs], size[rows, hs], c.coef, dtype, "few" if lens[0] <= FEW else "o", c.dk)
         if which == "q":
             assert not torch.isfinite(o[at, 0]).all() and torch.isfinite(o[at + 1:]).all() and torch.isfinite(s).all()
         else:
