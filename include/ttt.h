@@ -666,9 +666,9 @@ ttt_status ttt_block_norm_backward(const ttt_norm* norm, const ttt_rows* dr, con
  * A NaN or an infinity in a token reaches the tokens from it on, of its
  * sequence, and no others. Arithmetic: states and sums are fp32. bf16 rows
  * (more than 8 a sequence): products of bf16 operands; q k^T times its decays
- * is rounded to bf16, the state enters o as two bf16 terms (16 bits), v times
- * its decay enters the state as three (24 bits). fp32 rows, and up to 8 rows a
- * sequence: fp32 throughout. */
+ * and the state enter o as two bf16 terms each (16 bits), v times its decay
+ * enters the state as three (24 bits). fp32 rows, and up to 8 rows a sequence:
+ * fp32 throughout. */
 typedef struct ttt_linear {
   const float* log_decay;     /* [kv heads] device memory, <= 0 (-inf: nothing is kept) */
   const int32_t* q_starts;    /* [batch + 1] device memory, or NULL: tokens / batch each */

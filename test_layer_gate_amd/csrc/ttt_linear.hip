@@ -178,15 +178,19 @@ __device__ __forceinline__ void terms(float x, float y, uint32_t (&w)[T]) {
 }
 
 // Values of a product's result (kb of its rows) as an operand: fp32 as they
-// are, bf16 rounded.
-template <bool F32>
-__device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4& f) {
-  if constexpr (F32)
-    f = make_uint4(__float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]), __float_as_uint(x[4 * u + 2]),
-                   __float_as_uint(x[4 * u + 3]));
-  else
-    f = make_uint4(pack_bf16(x[8 * u], x[8 * u + 1]), pack_bf16(x[8 * u + 2], x[8 * u + 3]),
-                   pack_bf16(x[8 * u + 4], x[8 * u + 5]), pack_bf16(x[8 * u + 6], x[8 * u + 7]));
+// are, bf16 as T terms.
+template <bool F32, int T>
+__device__ __forceinline__ void as_operand(const f32x16_t& x, int u, uint4 (&f)[T]) {
+  if constexpr (F32) {
+    f[0] = make_uint4(__float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]), __float_as_uint(x[4 * u + 2]),
+                      __float_as_uint(x[4 * u + 3]));
+  } else {
+    uint32_t w[4][T];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) terms<T>(x[8 * u + 2 * e], x[8 * u + 2 * e + 1], w[e]);
+#pragma unroll
+    for (int t = 0; t < T; ++t) f[t] = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
+  }
 }
 
 // g^n for a whole n >= 0; 1 for n = 0 whatever g is.
@@ -265,16 +269,17 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // MANY: heads of k and v share the state (else heads of q do). SUMS: the
 // part's own sum alone, from zero.
 //
-// bf16: weights (q k) and states enter their products with v and q rounded to
-// bf16, the precision of what they meet and of the result (2-norm error against
-// 64 bits 0.0023, 0.0017 of it the result's own rounding; with the state as two
-// terms 0.0018, for 16 products and 96 vector instructions a chunk more). In the
-// update, whose sums stay in fp32 from chunk to chunk, v times its decay is three
-// terms (24 bits). fp32: the matrix cores' fp32 products throughout.
+// bf16: weights (q k) and states enter their products with v and q as two bf16
+// terms (16 bits), so that what is left of a result's error is its own rounding:
+// 2-norm error against 64 bits 0.0017, as of fp32 sums. (One term each: 0.0023, and
+// 374 us for the prompt's 433; the state alone as two: 0.0018 and 415; three each:
+// 501.) In the update, whose sums stay in fp32 from chunk to chunk, v times its
+// decay is three terms (24 bits). fp32: the matrix cores' fp32 products throughout.
 template <bool F32, int A, int NW, bool MANY, bool SUMS>
 __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles roles) {
   constexpr int C = Elem<F32>::rows, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
   constexpr int RT = C / 32, AT = A / 32, PER = 32 / KB;
+  constexpr int T = F32 ? 1 : 2;  // terms of weights, and of a state that meets q
   constexpr int kBytesA = C * A * Elem<F32>::size, kBytesB = C * B * Elem<F32>::size;
   __shared__ __attribute__((aligned(16))) char kt[kBytesA];
   __shared__ __attribute__((aligned(16))) char vt[kBytesB];
@@ -291,7 +296,8 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
     for (int w = 0; w < NW; ++w) any |= votes[w];
     return __builtin_amdgcn_readfirstlane(any) != 0;
   };
-  __shared__ uint4 shared[SUMS ? 1 : F32 ? 4 * NW : RT * (RT + 1) / 2 * PER][64];
+  constexpr int NB = RT * (RT + 1) / 2 * PER;  // pieces of a chunk's weights
+  __shared__ uint4 shared[SUMS ? 1 : F32 ? 4 * NW : T * NB][64];
   Reader<F32, A> ra;
   Reader<F32, B> rb;
 
@@ -403,13 +409,15 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       for (int it = 0; it < RT; ++it) x[it] = f32x16_t{};
 #pragma unroll
       for (int kb = 0; kb < A / KB; ++kb) {
-        uint4 sf;
-        as_operand<F32>(st[kb / PER], kb % PER, sf);
+        uint4 sf[T];
+        as_operand<F32, T>(st[kb / PER], kb % PER, sf);
 #pragma unroll
-        for (int it = 0; it < RT; ++it) {
-          x[it] = mma<F32>(sf, qf[kb & 1][it], x[it]);
-          if (kb + 2 < A / KB) qf[kb & 1][it] = ra.row(qt, it, kb + 2);
-        }
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int it = 0; it < RT; ++it) {
+            x[it] = mma<F32>(sf[t], qf[kb & 1][it], x[it]);
+            if (t == T - 1 && kb + 2 < A / KB) qf[kb & 1][it] = ra.row(qt, it, kb + 2);
+          }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -421,7 +429,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
     };
     // The weights of a chunk's rows (rows j of tile jt <= it, column i of tile it),
     // shared by the waves through LDS as the lanes will hold them: bf16 tiles a
-    // wave each, decayed and rounded; of fp32's one tile, each wave a part of the
+    // wave each, decayed and in terms; of fp32's one tile, each wave a part of the
     // contraction over A.
     // (x, the product with the state, while the first ones are under way)
     auto weights_and_state = [&](bool state, f32x16_t(&x)[RT]) {
@@ -466,9 +474,10 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
           }
 #pragma unroll
           for (int u = 0; u < PER; ++u) {
-            uint4 w;
-            as_operand<false>(p, u, w);
-            shared[b * PER + u][lane] = w;
+            uint4 w[T];
+            as_operand<false, T>(p, u, w);
+#pragma unroll
+            for (int t = 0; t < T; ++t) shared[t * NB + b * PER + u][lane] = w[t];
           }
         };
         if (wave < blocks) begin(wave);
@@ -497,16 +506,18 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
           x[0] = mma<true>(vf[u], make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])), x[0]);
         }
       } else {
-        constexpr int N = RT * (RT + 1) / 2 * PER;
-        uint4 w[N];
 #pragma unroll
-        for (int n = 0; n < N; ++n) w[n] = shared[n][lane];
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!MANY) decay_rows(x);
+        for (int t = 0; t < T; ++t) {
+          uint4 w[NB];
 #pragma unroll
-        for (int kb = 0; kb < RT * PER; ++kb)
+          for (int n = 0; n < NB; ++n) w[n] = shared[t * NB + n][lane];
+          __builtin_amdgcn_sched_barrier(0);
+          if (!MANY && t == 0) decay_rows(x);
 #pragma unroll
-          for (int it = kb / PER; it < RT; ++it) x[it] = mma<false>(vf[kb], w[it * PER + kb], x[it]);
+          for (int kb = 0; kb < RT * PER; ++kb)
+#pragma unroll
+            for (int it = kb / PER; it < RT; ++it) x[it] = mma<false>(vf[kb], w[it * PER + kb], x[it]);
+        }
       }
     };
     auto load_v = [&](uint4(&vf)[C / KB]) {
@@ -524,9 +535,9 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          uint4 w;
-          as_operand<false>(x, u, w);
-          *reinterpret_cast<uint4*>(to + 32 * u) = w;
+          uint4 w[1];
+          as_operand<false, 1>(x, u, w);
+          *reinterpret_cast<uint4*>(to + 32 * u) = w[0];
         }
       }
     };
