@@ -664,17 +664,18 @@ ttt_status ttt_block_norm_backward(const ttt_norm* norm, const ttt_rows* dr, con
  *   workspace  ttt_linear_attention_workspace_size() bytes, 256-byte aligned
  *      (may be NULL where that is 0)
  * A NaN or an infinity in a token reaches the tokens from it on, of its
- * sequence, and no others. Arithmetic: states and sums are fp32. bf16 rows
- * (more than 8 a sequence): products of bf16 operands; q k^T times its decays
- * and the state enter o as two bf16 terms each (16 bits), v times its decay
- * enters the state as three (24 bits). fp32 rows, and up to 8 rows a sequence:
- * fp32 throughout. */
+ * sequence, and no others. Arithmetic: states and sums are fp32. fp32 rows, and
+ * bf16 rows where max_new is at most 32: fp32 throughout (of bf16's products with
+ * what is fp32, 24 bits: three bf16 terms). Other bf16 rows: q k^T times its
+ * decays and the state enter o as two bf16 terms each (16 bits), v times its decay
+ * enters the state as three. */
 typedef struct ttt_linear {
   const float* log_decay;     /* [kv heads] device memory, <= 0 (-inf: nothing is kept) */
   const int32_t* q_starts;    /* [batch + 1] device memory, or NULL: tokens / batch each */
   int32_t batch, tokens;
   int32_t max_new;            /* an upper bound of a sequence's tokens: it sizes the launch;
-                                 a wrong one costs time, not results */
+                                 a wrong one costs time, not results (but for
+                                 the terms above) */
   int32_t act_dtype;
   int32_t kv_heads, q_heads;
   int32_t dim_k, dim_v;       /* 64, 128 or 256 */

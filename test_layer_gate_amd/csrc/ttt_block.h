@@ -62,8 +62,8 @@ struct LinearBackLaunch {
   float* d_first;               // or null
   float* back_sums;             // like f.sums
 };
-// Rows a sequence from which the chunked kernel takes them.
-bool linear_few(int max_new);
+// Whether a call goes token by token (and needs no parts).
+bool linear_by_token(const LinearLaunch& a);
 void linear_parts(LinearLaunch* a, bool back);
 hipError_t launch_linear(const LinearLaunch& a, hipStream_t s);
 hipError_t launch_linear_backward(const LinearBackLaunch& a, hipStream_t s);

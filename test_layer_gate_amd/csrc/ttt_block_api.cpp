@@ -316,7 +316,7 @@ ttt_status ttt_linear_attention_workspace_size(const ttt_linear* linear, size_t*
   tttk::LinearLaunch a = {};
   TTT_TRY(check_linear(linear, &a));
   tttk::linear_parts(&a, false);
-  *bytes = tttk::linear_few(a.max_new) ? 0 : part_bytes(a);
+  *bytes = tttk::linear_by_token(a) ? 0 : part_bytes(a);
   return TTT_OK;
   TTT_ENTRY_END
 }
@@ -339,7 +339,7 @@ ttt_status ttt_linear_attention(const ttt_linear* linear, const ttt_rows* q, con
   }
   if (a.tokens == 0) return TTT_OK;
   tttk::linear_parts(&a, false);
-  const size_t need = tttk::linear_few(a.max_new) ? 0 : part_bytes(a);
+  const size_t need = tttk::linear_by_token(a) ? 0 : part_bytes(a);
   TTT_TRY(check_workspace(workspace, workspace_bytes, need));
   if (need > 0) all.out.push_back(reach_of("workspace", workspace, need));
   TTT_TRY(all.check());

@@ -59,7 +59,6 @@ struct Elem {
   static constexpr int size = F32 ? 4 : 2;
   static constexpr int per16 = 16 / size;
   static constexpr int kb = F32 ? 8 : 16;       // contraction of one mma()
-  static constexpr int rows = F32 ? 32 : 64;    // of a chunk
 };
 
 template <bool F32, int W>  // W values a row
@@ -200,11 +199,11 @@ __device__ __forceinline__ float power(float lg, int n) { return n == 0 ? 1.f : 
 // works on others, and written to LDS (put) when their place is free. Rows
 // from `count` on are zero; dir -1 goes backwards; heads count from the first
 // one's. put() tells, if asked, whether a value is infinite or NaN.
-template <bool F32, int W, int NT>
+template <bool F32, int W, int NT, int C>
 struct Fetch {
   static constexpr int P = W * Elem<F32>::size / 16, R = NT / P;  // R rows at a time
-  static constexpr int N = Elem<F32>::rows / R;
-  static_assert(NT % P == 0 && Elem<F32>::rows % R == 0, "whole passes");
+  static constexpr int N = C / R;
+  static_assert(NT % P == 0 && C % R == 0, "whole passes");
   uint4 v[N];
   const char* at;  // the lane's place in the next chunk, of the first head
   __device__ __forceinline__ Fetch(const Rows& x, int head, int col, int64_t row0, int dir)
@@ -214,7 +213,7 @@ struct Fetch {
   __device__ __forceinline__ void get(const Rows& x, int head, int dir, int count) {
     const int64_t step = x.ts * Elem<F32>::size * (dir * R);
     const char* p = at + head * x.hs * Elem<F32>::size;
-    if (count >= Elem<F32>::rows) {
+    if (count >= C) {
 #pragma unroll
       for (int i = 0; i < N; ++i, p += step) v[i] = *reinterpret_cast<const uint4*>(p);
     } else {
@@ -275,11 +274,12 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // 374 us for the prompt's 433; the state alone as two: 0.0018 and 415; three each:
 // 501.) In the update, whose sums stay in fp32 from chunk to chunk, v times its
 // decay is three terms (24 bits). fp32: the matrix cores' fp32 products throughout.
-template <bool F32, int A, int NW, bool MANY, bool SUMS>
+// FEW: a chunk is 32 rows of bf16, and weights and states are three terms (24 bits).
+template <bool F32, int A, int NW, bool MANY, bool SUMS, bool FEW>
 __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles roles) {
-  constexpr int C = Elem<F32>::rows, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
+  constexpr int C = F32 || FEW ? 32 : 64, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
   constexpr int RT = C / 32, AT = A / 32, PER = 32 / KB;
-  constexpr int T = F32 ? 1 : 2;  // terms of weights, and of a state that meets q
+  constexpr int T = F32 ? 1 : FEW ? 3 : 2;  // terms of weights, and of a state that meets q
   constexpr int kBytesA = C * A * Elem<F32>::size, kBytesB = C * B * Elem<F32>::size;
   __shared__ __attribute__((aligned(16))) char kt[kBytesA];
   __shared__ __attribute__((aligned(16))) char vt[kBytesB];
@@ -334,8 +334,8 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
   int64_t t0 = mine;
   const int64_t row0 = a.back ? base + len - 1 - t0 : base + t0;
   int take = (int)min((int64_t)C, end - t0);
-  Fetch<F32, A, NT> fk(a.k, head * k_heads, 0, row0, dir), fq(a.q, head * q_heads, 0, row0, dir);
-  Fetch<F32, B, NT> fv(a.v, head * k_heads, slice * B, row0, dir);
+  Fetch<F32, A, NT, C> fk(a.k, head * k_heads, 0, row0, dir), fq(a.q, head * q_heads, 0, row0, dir);
+  Fetch<F32, B, NT, C> fv(a.v, head * k_heads, slice * B, row0, dir);
   fk.get(a.k, 0, dir, take);
   fv.get(a.v, 0, dir, take);
   if constexpr (!SUMS) fq.get(a.q, 0, dir, take);
@@ -756,9 +756,10 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(Scan one, Scan two, 
 // in registers over the tokens, and written once: bound by HBM. Eight lanes
 // hold 32 neighbouring columns of a row of the state; 32 rows at a time. A token
 // of 48 sequences, 8/32 heads of 128: 12.3 us for 51 MB, 4.2 TB/s.
+constexpr int kTokenColumns = 32;
 template <bool F32, int A, int G>
 __global__ __launch_bounds__(256) void token_kernel(LinearLaunch a) {
-  constexpr int SB = 32, R = A / 32;
+  constexpr int SB = kTokenColumns, R = A / 32;
   __shared__ float kq[(1 + G) * A], vv[SB];
   __shared__ float4 red[4][G][8];
   const int slices = a.dv / SB;
@@ -846,20 +847,20 @@ __global__ __launch_bounds__(256) void through_kernel(const float* from, float* 
     reinterpret_cast<float4*>(to)[i] = from ? reinterpret_cast<const float4*>(from)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-template <bool F32, bool MANY, bool SUMS>
+template <bool F32, bool MANY, bool SUMS, bool FEW>
 hipError_t chunks_of(const Roles& r, int A, int B, hipStream_t s) {
   const Chunks& a = r.c[0];
   int64_t n = (int64_t)a.batch * a.heads * a.parts * a.slices;
   if (r.n > 1) n = (n + 7) / 8 * 8 * r.n;
   const dim3 g((uint32_t)n);
   if (B == 64) {
-    if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS><<<g, 128, 0, s>>>(r);
-    else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS><<<g, 128, 0, s>>>(r);
-    else chunk_kernel<F32, 256, 2, MANY, SUMS><<<g, 128, 0, s>>>(r);
+    if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r);
+    else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r);
+    else chunk_kernel<F32, 256, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r);
   } else {
-    if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS><<<g, 256, 0, s>>>(r);
-    else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS><<<g, 256, 0, s>>>(r);
-    else chunk_kernel<F32, 256, 4, MANY, SUMS><<<g, 256, 0, s>>>(r);
+    if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r);
+    else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r);
+    else chunk_kernel<F32, 256, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r);
   }
   return hipGetLastError();
 }
@@ -869,7 +870,7 @@ template <bool MANY, bool SUMS>
 hipError_t chunks(std::initializer_list<Chunks> c, int A, int B, bool f32, hipStream_t s) {
   Roles r = {};
   for (const Chunks& x : c) r.c[r.n++] = x;
-  return f32 ? chunks_of<true, MANY, SUMS>(r, A, B, s) : chunks_of<false, MANY, SUMS>(r, A, B, s);
+  return f32 ? chunks_of<true, MANY, SUMS, false>(r, A, B, s) : chunks_of<false, MANY, SUMS, false>(r, A, B, s);
 }
 
 int slices_of(int B) { return B == 256 ? 2 : 1; }
@@ -910,7 +911,7 @@ void states_from(Chunks* c, const LinearLaunch& a, const float* first, const flo
 
 template <bool F32, int G>
 hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
-  const dim3 g((uint32_t)((int64_t)a.batch * a.kv_heads * (a.dv / 32)));
+  const dim3 g((uint32_t)((int64_t)a.batch * a.kv_heads * (a.dv / kTokenColumns)));
   if (a.dk == 64) token_kernel<F32, 64, G><<<g, 256, 0, s>>>(a);
   else if (a.dk == 128) token_kernel<F32, 128, G><<<g, 256, 0, s>>>(a);
   else token_kernel<F32, 256, G><<<g, 256, 0, s>>>(a);
@@ -919,11 +920,27 @@ hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
 
 }  // namespace
 
-// Token by token for one or two rows a sequence, whose state is read and written
-// by any kernel. Measured, us (8/32 heads of 128, bf16; token by token, in chunks):
-// 48 sequences of 2 rows 16.1, 20.2, of 4 29.6, 20.3; one of 2 rows 6.7, 13.3, of
-// 4 10.2, 13.2, of 8 17.5, 13.3.
-bool linear_few(int max_new) { return max_new <= 2; }
+// Token by token for a few rows a sequence, whose state is read and written by any
+// kernel: its time grows by the row, a chunk's does not. Measured, us (token by
+// token for 2, 3, 4, 6 and 8 rows a sequence; a chunk of 32 rows):
+//   8/32 heads of 128, one sequence   6.8,  8.6, 10.4, 14.0, 17.7; 14.7
+//   8/32 heads of 128, 48            15.6, 22.3, 28.9, 38.9, 48.8; 23.0
+//   16/16 heads of 128, one           4.6,  5.2,  6.0,  7.4,  9.0;  9.2
+//   16/16 heads of 128, 48           20.8, 22.6, 25.0, 30.3, 35.6; 26.5
+//   8/16 heads of 256, 48            38.1, 42.9, 45.2, 54.0, 64.0; 66.5
+//   8/32 heads of 128, fp32, one      6.7,  8.5, 10.2, 13.7, 17.6; 23.5
+//   8/32 heads of 128, fp32, 48      17.5, 24.4, 31.0, 39.6, 49.4; 40.7
+// so up to 6 rows, but where there are more than two workgroups a compute unit, and
+// a chunk is faster (bf16, and two of its workgroups to a unit), up to 3.
+bool linear_by_token(const LinearLaunch& a) {
+  const int64_t groups = (int64_t)a.batch * a.kv_heads * (a.dv / kTokenColumns);
+  return a.max_new <= (a.f32 || a.dk == 256 || groups <= 512 ? 6 : 3);
+}
+
+// Rows a sequence up to which bf16 takes a chunk of 32 rows and three terms: fp32's
+// precision, and for one sequence of 8/32 heads of 128 14.7 us for the 16.8 of a
+// chunk of 64 and two terms, for 48 22.8 for 25.2.
+constexpr int kFewRows = 32;
 
 // Parts of the sequences: as many workgroups as have a place at once, two a
 // compute unit (of two waves for dim_v 64, else of four), of a chunk at least. The
@@ -942,7 +959,7 @@ void linear_parts(LinearLaunch* a, bool back) {
 }
 
 hipError_t launch_linear(const LinearLaunch& a, hipStream_t s) {
-  if (linear_few(a.max_new)) {
+  if (linear_by_token(a)) {
     const int group = a.q.heads / a.kv_heads;
     if (group == 1) return a.f32 ? tokens_of<true, 1>(a, s) : tokens_of<false, 1>(a, s);
     return a.f32 ? tokens_of<true, 4>(a, s) : tokens_of<false, 4>(a, s);
@@ -956,6 +973,7 @@ hipError_t launch_linear(const LinearLaunch& a, hipStream_t s) {
     return e;
   states_from(&c, a, a.first, a.sums);
   c.out = a.last;
+  if (!a.f32 && a.max_new <= kFewRows) return chunks_of<false, false, false, true>({{c}, 1}, a.dk, a.dv, s);
   return chunks<false, false>({c}, a.dk, a.dv, a.f32, s);
 }
 
