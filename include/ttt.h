@@ -691,7 +691,8 @@ ttt_status ttt_linear_attention(const ttt_linear* linear, const ttt_rows* q, con
  *   d_o      [tokens, q heads, dim_v], the gradient of o
  *   state    S before the first token, or NULL: zero
  *   d_state  the gradient of S after the last token, or NULL: zero
- *   dq, dk, dv  out, in act_dtype (dk and dv are sums over a kv head's query heads)
+ *   dq, dk, dv  out, in act_dtype (dk and dv are sums over a kv head's query
+ *            heads); zero in rows that no sequence claims
  *   d_state0 out, fp32: the gradient of S before the first token, or NULL; may
  *            be d_state
  * log_decay and scale get no gradient. Arithmetic as in the forward, for any

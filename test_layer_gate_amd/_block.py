@@ -359,7 +359,8 @@ def linear_attention_backward(do, q, k, v, log_decay, *, state=None, d_state=Non
     dk, dv, d_state0). do: the gradient of o; state: S before the first token
     (the forward's, before it was updated; None: zero); d_state: the gradient of
     S after the last (None: zero). d_state0, the gradient of the first state, is
-    returned where state, d_state or d_state0 is given; it may be d_state."""
+    returned where state, d_state or d_state0 is given; it may be d_state. Rows that
+    no sequence claims have gradients of zero."""
     desc, sizes, rq, rk, rv = _linear_desc(q, k, v, log_decay, q_starts, max_new, scale,
                                            state if state is not None else d_state)
     _alone(q, do, k, v, log_decay, q_starts, state, d_state, d_state0)
@@ -372,9 +373,6 @@ def linear_attention_backward(do, q, k, v, log_decay, *, state=None, d_state=Non
         d_state0 = _new((batch, hk, dk, dv), torch.float32, q, stream)
     p2 = _state_of(d_state0, "d_state0", sizes)
     dq, g_k, g_v = (_s._empty(t, stream) for t in (q, k, v))
-    if q_starts is not None:  # rows that no sequence claims have no part in o
-        for t in (dq, g_k, g_v):
-            _s._on(stream, t.zero_)
     workspace, ws, size = _workspace(_linear_workspace(sizes, True), q, workspace, stream)
     st = _L().ttt_linear_attention_backward(desc, rdo, rq, rk, rv, p0, p1, _s._dense(dq, hq, dk),
                                             _s._dense(g_k, hk, dk), _s._dense(g_v, hk, dv), p2, ws, size,

@@ -847,6 +847,32 @@ __global__ __launch_bounds__(256) void through_kernel(const float* from, float* 
     reinterpret_cast<float4*>(to)[i] = from ? reinterpret_cast<const float4*>(from)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+// Zeros for the gradients of rows that no sequence claims: those before the first
+// start and from the last one on (what lies between is within a sequence, whatever
+// the starts between them are). Ahead of the gradients' own launches: of starts out
+// of order it may write more. A few us where there are none.
+struct Outside {
+  Rows x[3];
+  int dim[3];
+  const int32_t* starts;
+  int batch, tokens, size;      // size: bytes of a value
+};
+__global__ __launch_bounds__(256) void outside_kernel(Outside a) {
+  const int lo = min(max(a.starts[0], 0), a.tokens), hi = min(max(a.starts[a.batch], 0), a.tokens);
+  const int rows = lo + a.tokens - hi;
+  for (int n = blockIdx.x; n < rows; n += gridDim.x) {
+    const int64_t row = n < lo ? n : n - lo + hi;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const Rows& x = a.x[i];
+      const int per = a.dim[i] * a.size / 16;
+      for (int e = threadIdx.x; e < x.heads * per; e += 256)
+        *reinterpret_cast<uint4*>(static_cast<char*>(x.p) + (row * x.ts + e / per * x.hs) * a.size + e % per * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
 template <bool F32, bool MANY, bool SUMS, bool FEW>
 hipError_t chunks_of(const Roles& r, int A, int B, hipStream_t s) {
   const Chunks& a = r.c[0];
@@ -981,6 +1007,11 @@ hipError_t launch_linear_backward(const LinearBackLaunch& b, hipStream_t s) {
   const LinearLaunch& a = b.f;
   const bool many = a.q.heads > a.kv_heads;
   hipError_t e;
+  if (a.starts) {
+    const Outside o = {{b.dq, b.dk, b.dv}, {a.dk, a.dk, a.dv}, a.starts, a.batch, a.tokens, a.f32 ? 4 : 2};
+    outside_kernel<<<std::min(a.tokens, 512), 256, 0, s>>>(o);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   // the states before each part, and the gradients of those behind each part
   Chunks f = base_of(a, a.dv), r = f;
   f.k = a.k, f.v = a.v;
