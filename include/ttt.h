@@ -711,8 +711,8 @@ ttt_status ttt_linear_attention_backward(const ttt_linear* linear, const ttt_row
  *   g' = g * min(1, max_norm / *norm)                  where norm is given
  *   m = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2
  *   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
- * in fp32, rounded once to p's type. Where *norm is infinite or NaN, nothing is
- * changed. p is updated in place; with a master, the master is p's fp32 value
+ * in fp32, rounded once to p's type. Where *norm is infinite or NaN, or
+ * *step_device below 1, nothing is changed. p is updated in place; with a master, the master is p's fp32 value
  * and p its rounding.
  *
  * The states of n tensors of n_i values are N = sum of n_i, each rounded up to

@@ -438,7 +438,7 @@ def adamw_step(params, grads, state, *, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     `grads` (bfloat16 or float32, the params' sizes), with the states of
     adamw_state(params, bits) (ttt_adamw_step). step counts from 1; lr and step
     may be a float32 and an int32 value on the GPU, which a captured call reads
-    again at every replay. masters: float32 values of bfloat16 params, which
+    again at every replay (a step below 1 there changes nothing). masters: float32 values of bfloat16 params, which
     take the step in their place. norm: grad_norm(grads), to limit the
     gradients to max_norm; where it is infinite or NaN, nothing changes."""
     pp, sizes, pt = _list(params, "params")

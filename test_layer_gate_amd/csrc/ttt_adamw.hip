@@ -134,6 +134,7 @@ __global__ __launch_bounds__(kStepThreads) void adamw_kernel(StepLaunch a) {
     k = 1.f - lr * a.wd;
     float c1 = a.a, c2 = a.rs;  // (a is 1 / (1 - b1^t) then)
     if (a.step_dev != nullptr) {
+      if (*a.step_dev < 1) return;  // (its 1 - b^0 would divide by 0)
       const float n = (float)*a.step_dev;
       c1 = 1.f / -expm1f(n * a.ln1);
       c2 = 1.f / sqrtf(-expm1f(n * a.ln2));
