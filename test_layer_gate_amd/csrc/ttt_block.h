@@ -10,6 +10,15 @@
 
 namespace tttk {
 
+// Workgroups of one launch, of up to 1024 threads: a launch holds fewer than 2^32
+// threads. More of them are launched one after the other: f(workgroups, first).
+constexpr int64_t kMostGroups = (int64_t)1 << 21;
+template <class F>
+void in_pieces(int64_t groups, const F& f) {
+  for (int64_t at = 0; at < groups; at += kMostGroups)
+    f((uint32_t)(groups - at < kMostGroups ? groups - at : kMostGroups), at);
+}
+
 // ------------------------------------------------------------------ norms
 
 // Rows of one head: row n of a view at p + n * ts elements.

@@ -92,11 +92,11 @@ __device__ __forceinline__ float rounded(float x, bool f32) { return f32 ? x : b
 // rows and load the next one ahead took 256 us, and more of them 271: there are
 // enough rows on their way.)
 template <bool AF32, bool RF32, int K>
-__global__ __launch_bounds__(512) void norm_kernel(NormLaunch a, int waves) {
+__global__ __launch_bounds__(512) void norm_kernel(NormLaunch a, int waves, int64_t first) {
   __shared__ float red[2][1][kMaxWaves];
   const int vecs = a.d >> 3, step = waves << 6;
   const float inv_d = 1.f / (float)a.d;
-  const int64_t n = blockIdx.x;
+  const int64_t n = first + blockIdx.x;
   const bool has_f = a.f.p != nullptr;
   float x[K][8], f[K][8];
 #pragma unroll
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(512) void norm_kernel(NormLaunch a, int waves) {
       block_sum(s, red[0], waves);
       by *= 1.f / sqrtf(s[0] * inv_d + a.eps);
     }
-    const int64_t gate = a.gate.p ? (int64_t)((int)blockIdx.x / a.per_gate) * a.gate.ts : 0;
+    const int64_t gate = a.gate.p ? (int64_t)((int)n / a.per_gate) * a.gate.ts : 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int v = k * step + threadIdx.x;
@@ -344,10 +344,10 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackLaunch b, N
 // rows of threads each take every 16th part.
 constexpr int kSumRows = 16;
 __global__ __launch_bounds__(64 * kSumRows) void norm_sums_kernel(NormBackLaunch b, NormPlan plan, int blocks,
-                                                                  int jobs_w) {
+                                                                  int jobs_w, int64_t first) {
   __shared__ float red[kSumRows][64];
-  const int d = b.n.d, job = blockIdx.x / blocks;
-  const int col = (blockIdx.x % blocks) * 64 + (threadIdx.x & 63), row = threadIdx.x >> 6;
+  const int d = b.n.d, job = (int)((first + blockIdx.x) / blocks);
+  const int col = (int)((first + blockIdx.x) % blocks) * 64 + (threadIdx.x & 63), row = threadIdx.x >> 6;
   const float* part;
   float* out;
   int count = plan.groups;
@@ -380,13 +380,15 @@ int waves_of(int d, int k) { return (d / 8 + 64 * k - 1) / (64 * k); }
 template <bool AF32, bool RF32>
 hipError_t norm_of(const NormLaunch& a, hipStream_t s) {
   const int K = a.d <= 4096 ? 1 : a.d <= 8192 ? 2 : 4, waves = waves_of(a.d, K);
-  const dim3 g(a.rows), t(64 * waves);
-  if (K == 1)
-    norm_kernel<AF32, RF32, 1><<<g, t, 0, s>>>(a, waves);
-  else if (K == 2)
-    norm_kernel<AF32, RF32, 2><<<g, t, 0, s>>>(a, waves);
-  else
-    norm_kernel<AF32, RF32, 4><<<g, t, 0, s>>>(a, waves);
+  const dim3 t(64 * waves);
+  in_pieces(a.rows, [&](uint32_t g, int64_t first) {
+    if (K == 1)
+      norm_kernel<AF32, RF32, 1><<<g, t, 0, s>>>(a, waves, first);
+    else if (K == 2)
+      norm_kernel<AF32, RF32, 2><<<g, t, 0, s>>>(a, waves, first);
+    else
+      norm_kernel<AF32, RF32, 4><<<g, t, 0, s>>>(a, waves, first);
+  });
   return hipGetLastError();
 }
 
@@ -454,7 +456,9 @@ hipError_t launch_norm_sums(const NormBackLaunch& b, hipStream_t s) {
   const int64_t jobs = jobs_w + (b.n.gate.p && plan.slices != 1 ? b.dgate.heads : 0);
   if (jobs == 0) return hipSuccess;
   const int blocks = (b.n.d + 63) / 64;
-  norm_sums_kernel<<<(uint32_t)(jobs * blocks), 64 * kSumRows, 0, s>>>(b, plan, blocks, jobs_w);
+  in_pieces(jobs * blocks, [&](uint32_t g, int64_t first) {
+    norm_sums_kernel<<<g, 64 * kSumRows, 0, s>>>(b, plan, blocks, jobs_w, first);
+  });
   return hipGetLastError();
 }
 

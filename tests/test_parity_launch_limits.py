@@ -1,0 +1,63 @@
+"""GPU: calls whose kernels have more threads than one launch holds (fewer than
+2^32), and calls on either side of where launches are cut (2^21 workgroups)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+CUT = 1 << 21
+
+
+@pytest.fixture(scope="module")
+def ttt():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test run without a GPU")
+    import test_layer_gate_amd as m
+    m.lib()
+    return m
+
+
+@pytest.fixture(autouse=True)
+def give_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_norm_rows_behind_the_first_launch(ttt):
+    """The last rows and the first ones are those of calls of their own."""
+    rows, d = CUT + 1003, 64
+    g = torch.Generator("cuda").manual_seed(1)
+    x, f = (torch.randn(rows, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    gate = torch.randn(rows // 3, d, generator=g, device="cuda").to(BF)      # a gate for three rows
+    assert rows % 3 == 0
+    w = torch.randn(d, generator=g, device="cuda").to(BF)
+    r, h = ttt.block_norm(x, f, post=w, pre=w, gate=gate, scale=0.5)
+    for rows_, gates in ((slice(0, 300), slice(0, 100)), (slice(rows - 3000, rows), slice(rows // 3 - 1000, rows // 3))):
+        r2, h2 = ttt.block_norm(x[rows_], f[rows_], post=w, pre=w, gate=gate[gates], scale=0.5)
+        assert torch.equal(r[rows_], r2) and torch.equal(h[rows_], h2)
+    at = slice(CUT - 2 - (CUT - 2) % 3, CUT + 31 - (CUT + 31) % 3)           # over the cut
+    r2, h2 = ttt.block_norm(x[at], f[at], post=w, pre=w, gate=gate[at.start // 3:at.stop // 3], scale=0.5)
+    assert torch.equal(r[at], r2) and torch.equal(h[at], h2)
+
+
+def test_norm_of_more_threads_than_a_launch_holds(ttt):
+    """2^23 + 3 rows, 512 threads each (60 GB of results; all rows are one)."""
+    rows, d = (1 << 23) + 3, 3592
+    one = torch.randn(1, d, device="cuda").to(BF)
+    want = ttt.block_norm(one, pre=True)[1]
+    h = ttt.block_norm(one.expand(rows, d), pre=True)[1]
+    assert h.shape == (rows, d)
+    for lo in range(0, rows, 1 << 19):
+        part = h[lo:lo + (1 << 19)]
+        assert torch.equal(part, want.expand_as(part)), lo
+
+
+def test_norm_sums_of_no_rows(ttt):
+    """More gates than one launch's workgroups, and no row: sums of zero."""
+    gates, d = 16385, 16384
+    empty = torch.zeros(0, d, dtype=BF, device="cuda")
+    gate = torch.ones(1, d, dtype=BF, device="cuda").expand(gates, d)
+    held = torch.full((gates, d), 7.0, device="cuda")      # whose memory the sums get
+    del held
+    got = ttt.block_norm_backward(empty, None, None, empty, gate=gate)
+    assert got["dgate"].shape == (gates, d) and got["dgate"].dtype is F32 and not got["dgate"].any()
