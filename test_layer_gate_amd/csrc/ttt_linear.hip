@@ -276,7 +276,7 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // decay is three terms (24 bits). fp32: the matrix cores' fp32 products throughout.
 // FEW: a chunk is 32 rows of bf16, and weights and states are three terms (24 bits).
 template <bool F32, int A, int NW, bool MANY, bool SUMS, bool FEW>
-__global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles roles) {
+__global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles roles, int first) {
   constexpr int C = F32 || FEW ? 32 : 64, KB = Elem<F32>::kb, NT = NW * 64, B = NW * 32;
   constexpr int RT = C / 32, AT = A / 32, PER = 32 / KB;
   constexpr int T = F32 ? 1 : FEW ? 3 : 2;  // terms of weights, and of a state that meets q
@@ -301,9 +301,10 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
   Reader<F32, A> ra;
   Reader<F32, B> rb;
 
-  const int eights = blockIdx.x / 8, turn = __builtin_amdgcn_readfirstlane(eights / roles.n);
+  const int group = first + blockIdx.x;
+  const int eights = group / 8, turn = __builtin_amdgcn_readfirstlane(eights / roles.n);
   const Chunks& a = roles.c[eights - turn * roles.n];
-  int id = turn * 8 + blockIdx.x % 8;
+  int id = turn * 8 + group % 8;
   const int slice = id % a.slices;
   id /= a.slices;
   const int part = id % a.parts;
@@ -758,12 +759,12 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(Scan one, Scan two, 
 // of 48 sequences, 8/32 heads of 128: 12.3 us for 51 MB, 4.2 TB/s.
 constexpr int kTokenColumns = 32;
 template <bool F32, int A, int G>
-__global__ __launch_bounds__(256) void token_kernel(LinearLaunch a) {
+__global__ __launch_bounds__(256) void token_kernel(LinearLaunch a, int first) {
   constexpr int SB = kTokenColumns, R = A / 32;
   __shared__ float kq[(1 + G) * A], vv[SB];
   __shared__ float4 red[4][G][8];
   const int slices = a.dv / SB;
-  int id = blockIdx.x;
+  int id = first + blockIdx.x;
   const int slice = id % slices;
   id /= slices;
   const int head = id % a.kv_heads, seq = id / a.kv_heads;
@@ -878,16 +879,18 @@ hipError_t chunks_of(const Roles& r, int A, int B, hipStream_t s) {
   const Chunks& a = r.c[0];
   int64_t n = (int64_t)a.batch * a.heads * a.parts * a.slices;
   if (r.n > 1) n = (n + 7) / 8 * 8 * r.n;
-  const dim3 g((uint32_t)n);
-  if (B == 64) {
-    if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r);
-    else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r);
-    else chunk_kernel<F32, 256, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r);
-  } else {
-    if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r);
-    else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r);
-    else chunk_kernel<F32, 256, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r);
-  }
+  in_pieces(n, [&](uint32_t g, int64_t at) {
+    const int first = (int)at;  // (n is below 2^25)
+    if (B == 64) {
+      if (A == 64) chunk_kernel<F32, 64, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r, first);
+      else if (A == 128) chunk_kernel<F32, 128, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r, first);
+      else chunk_kernel<F32, 256, 2, MANY, SUMS, FEW><<<g, 128, 0, s>>>(r, first);
+    } else {
+      if (A == 64) chunk_kernel<F32, 64, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r, first);
+      else if (A == 128) chunk_kernel<F32, 128, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r, first);
+      else chunk_kernel<F32, 256, 4, MANY, SUMS, FEW><<<g, 256, 0, s>>>(r, first);
+    }
+  });
   return hipGetLastError();
 }
 
@@ -937,10 +940,12 @@ void states_from(Chunks* c, const LinearLaunch& a, const float* first, const flo
 
 template <bool F32, int G>
 hipError_t tokens_of(const LinearLaunch& a, hipStream_t s) {
-  const dim3 g((uint32_t)((int64_t)a.batch * a.kv_heads * (a.dv / kTokenColumns)));
-  if (a.dk == 64) token_kernel<F32, 64, G><<<g, 256, 0, s>>>(a);
-  else if (a.dk == 128) token_kernel<F32, 128, G><<<g, 256, 0, s>>>(a);
-  else token_kernel<F32, 256, G><<<g, 256, 0, s>>>(a);
+  in_pieces((int64_t)a.batch * a.kv_heads * (a.dv / kTokenColumns), [&](uint32_t g, int64_t at) {
+    const int first = (int)at;  // (at most 2^25 of them)
+    if (a.dk == 64) token_kernel<F32, 64, G><<<g, 256, 0, s>>>(a, first);
+    else if (a.dk == 128) token_kernel<F32, 128, G><<<g, 256, 0, s>>>(a, first);
+    else token_kernel<F32, 256, G><<<g, 256, 0, s>>>(a, first);
+  });
   return hipGetLastError();
 }
 

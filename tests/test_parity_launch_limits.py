@@ -61,3 +61,46 @@ def test_norm_sums_of_no_rows(ttt):
     del held
     got = ttt.block_norm_backward(empty, None, None, empty, gate=gate)
     assert got["dgate"].shape == (gates, d) and got["dgate"].dtype is F32 and not got["dgate"].any()
+
+
+def linear_inputs(batch, rows, heads, dk, dv):
+    g = torch.Generator("cuda").manual_seed(3)
+    q, k, v = (torch.empty(batch * rows, heads, d, dtype=BF, device="cuda").normal_(generator=g) for d in (dk, dk, dv))
+    return q, k, v, -torch.rand(heads, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("rows", [1, 8])
+def test_linear_sequences_behind_the_first_launch(ttt, rows):
+    """2^22 - 64 states of 8 slices (token by token: more than 2^32 threads) or 2:
+    some sequences from all over are those of calls of their own."""
+    batch, heads, dk, dv = 65535, 64, 64, 256 if rows == 1 else 64
+    q, k, v, ld = linear_inputs(batch, rows, heads, dk, dv)
+    out = torch.full((batch * rows, heads, dv), 7.0, dtype=BF, device="cuda")
+    ttt.linear_attention(q, k, v, ld, q_starts=torch.arange(0, batch * rows + 1, rows, dtype=torch.int32, device="cuda"),
+                         max_new=rows, out=out)
+    for lo in (0, 4000, 32767, 32768, 65500):
+        cut = slice(lo * rows, min(lo + 40, batch) * rows)
+        n = (cut.stop - cut.start) // rows
+        want = ttt.linear_attention(q[cut], k[cut], v[cut], ld,
+                                    q_starts=torch.arange(0, n * rows + 1, rows, dtype=torch.int32, device="cuda"), max_new=rows)
+        assert torch.equal(out[cut], want), lo
+    assert not (out == 7).all(-1).any()
+
+
+def test_linear_gradients_of_more_threads_than_a_launch_holds(ttt):
+    """2^22 - 64 states of heads of 256: three roles of two slices, 1.5 times 2^32 threads."""
+    batch, heads, d = 65535, 64, 256
+    q, k, v, ld = linear_inputs(batch, 1, heads, d, d)
+    do = torch.empty_like(v).normal_(generator=torch.Generator("cuda").manual_seed(4))
+    dq, dk, dv, _ = ttt.linear_attention_backward(do, q, k, v, ld, q_starts=torch.arange(batch + 1, dtype=torch.int32, device="cuda"),
+                                                  max_new=1, scale=0.0625)
+    for lo in (0, 4000, 32767, 43000, 65500):
+        cut = slice(lo, min(lo + 30, batch))
+        n = cut.stop - lo
+        want = ttt.linear_attention_backward(do[cut], q[cut], k[cut], v[cut], ld,
+                                             q_starts=torch.arange(n + 1, dtype=torch.int32, device="cuda"), max_new=1, scale=0.0625)
+        for g, w in zip((dq, dk, dv), want):
+            assert torch.equal(g[cut], w), lo
+    # dv of one row: scale (k q) do, of dq and dk likewise: none is left as it was
+    for g in (dq, dk, dv):
+        assert all(bool((part != 0).any(-1).all()) for part in g.split(8192))
