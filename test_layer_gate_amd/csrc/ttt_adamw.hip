@@ -115,13 +115,13 @@ __device__ __forceinline__ void load_states(const StepLaunch& a, int64_t i, floa
 // array is read and written once: 2.4 GB of bf16 weights, fp32 masters and states in
 // 452 us, 5.4 TB/s.
 template <bool PF32, bool GF32, bool MASTER, bool BITS8>
-__global__ __launch_bounds__(kStepThreads) void adamw_kernel(StepLaunch a) {
+__global__ __launch_bounds__(kStepThreads) void adamw_kernel(StepLaunch a, int first) {
 #pragma clang fp contract(off)
   // (products are rounded before they are added: what is quantised afterwards
   // does not depend on which of them a fused operation would have kept exact)
-  const int t = tensor_of(a.first, a.count, blockIdx.x);
+  const int chunk = first + (int)blockIdx.x, t = tensor_of(a.first, a.count, chunk);
   const StepTensor x = a.t[t];
-  const int64_t i = (int64_t)(blockIdx.x - a.first[t]) * kStepChunk + threadIdx.x * 8;
+  const int64_t i = (int64_t)(chunk - a.first[t]) * kStepChunk + threadIdx.x * 8;
   float coef = 1.f;
   if (a.norm != nullptr) {
     const float norm = *a.norm;
@@ -200,9 +200,9 @@ __global__ __launch_bounds__(kStepThreads) void adamw_kernel(StepLaunch a) {
 
 // What 8-bit states stand for: m and v, rounded to the outputs' type.
 template <bool F32>
-__global__ __launch_bounds__(256) void state_read_kernel(StateRead a) {
+__global__ __launch_bounds__(256) void state_read_kernel(StateRead a, int64_t first) {
 #pragma clang fp contract(off)
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t i = ((first + blockIdx.x) * 256 + threadIdx.x) * 8;
   if (i >= a.n) return;
   StepLaunch s;
   s.m = const_cast<void*>(a.m), s.v = const_cast<void*>(a.v);
@@ -258,17 +258,20 @@ __global__ __launch_bounds__(256) void grad_norm_join_kernel(GradNormJoin a) {
 
 template <bool PF32, bool MASTER>
 void adamw_of(const StepCall& c, hipStream_t s) {
-  const dim3 g(c.a->first[c.a->count]), t(kStepThreads);
-  if (c.bits8) {
-    if (c.g_f32)
-      adamw_kernel<PF32, true, MASTER, true><<<g, t, 0, s>>>(*c.a);
-    else
-      adamw_kernel<PF32, false, MASTER, true><<<g, t, 0, s>>>(*c.a);
-  } else if (c.g_f32) {
-    adamw_kernel<PF32, true, MASTER, false><<<g, t, 0, s>>>(*c.a);
-  } else {
-    adamw_kernel<PF32, false, MASTER, false><<<g, t, 0, s>>>(*c.a);
-  }
+  const dim3 t(kStepThreads);
+  in_pieces(c.a->first[c.a->count], [&](uint32_t g, int64_t at) {
+    const int first = (int)at;
+    if (c.bits8) {
+      if (c.g_f32)
+        adamw_kernel<PF32, true, MASTER, true><<<g, t, 0, s>>>(*c.a, first);
+      else
+        adamw_kernel<PF32, false, MASTER, true><<<g, t, 0, s>>>(*c.a, first);
+    } else if (c.g_f32) {
+      adamw_kernel<PF32, true, MASTER, false><<<g, t, 0, s>>>(*c.a, first);
+    } else {
+      adamw_kernel<PF32, false, MASTER, false><<<g, t, 0, s>>>(*c.a, first);
+    }
+  });
 }
 
 }  // namespace
@@ -284,11 +287,12 @@ hipError_t launch_adamw(const StepCall& c, hipStream_t s) {
 }
 
 hipError_t launch_state_read(const StateRead& a, hipStream_t s) {
-  const uint32_t grid = (uint32_t)((a.n / 8 + 255) / 256);
-  if (a.out_f32)
-    state_read_kernel<true><<<grid, 256, 0, s>>>(a);
-  else
-    state_read_kernel<false><<<grid, 256, 0, s>>>(a);
+  in_pieces((a.n / 8 + 255) / 256, [&](uint32_t grid, int64_t first) {
+    if (a.out_f32)
+      state_read_kernel<true><<<grid, 256, 0, s>>>(a, first);
+    else
+      state_read_kernel<false><<<grid, 256, 0, s>>>(a, first);
+  });
   return hipGetLastError();
 }
 

@@ -104,3 +104,44 @@ def test_linear_gradients_of_more_threads_than_a_launch_holds(ttt):
     # dv of one row: scale (k q) do, of dq and dk likewise: none is left as it was
     for g in (dq, dk, dv):
         assert all(bool((part != 0).any(-1).all()) for part in g.split(8192))
+
+
+def need_memory(gb):
+    if torch.cuda.mem_get_info()[0] < gb * 10 ** 9:
+        pytest.skip(f"needs {gb} GB of GPU memory")
+
+
+def test_adamw_values_behind_the_first_launch(ttt):
+    """2^32 + 12345 values: steps and states read back, beside a call for the last ones."""
+    n = (1 << 32) + 12345
+    last = n - (1 << 32) + (1 << 20)          # whole chunks and blocks before them
+    gen = torch.Generator("cuda").manual_seed(5)
+    p, g = (torch.empty(n, dtype=BF, device="cuda").normal_(generator=gen) for _ in range(2))
+    p2, g2 = p[-last:].clone(), g[-last:].clone()
+    kw = dict(lr=1e-2, weight_decay=0.1, bits=8)
+    state, state2 = ttt.adamw_state([p], 8), ttt.adamw_state([p2], 8)
+    for step in (1, 2):
+        ttt.adamw_step([p], [g], state, step=step, **kw)
+        ttt.adamw_step([p2], [g2], state2, step=step, **kw)
+    assert torch.equal(p[-last:], p2)
+    del p, g
+    for x, y in zip(ttt.adamw_read(state, 8, dtype=BF), ttt.adamw_read(state2, 8, dtype=BF)):
+        assert torch.equal(x[-y.numel():], y) and bool(y[:last].any())
+
+
+def test_adamw_of_more_threads_than_a_launch_holds(ttt):
+    """17 tensors of 2^31 values with one gradient (144 GB): each becomes what the first does."""
+    need_memory(160)
+    n, count = 1 << 31, 17
+    g = torch.empty(n, dtype=BF, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(6))
+    ps = [torch.ones(n, dtype=BF, device="cuda") for _ in range(count)]
+    state = ttt.adamw_state(ps, 8)
+    ttt.adamw_step(ps, [g] * count, state, lr=0.1, step=1, bits=8)
+    one = torch.ones(1 << 20, dtype=BF, device="cuda")
+    ttt.adamw_step([one], [g[:1 << 20]], ttt.adamw_state([one], 8), lr=0.1, step=1, bits=8)
+    assert torch.equal(ps[0][:1 << 20], one) and not (one == 1).any()
+    codes = state[:n * count].view(count, n)
+    for i in range(1, count):
+        for lo in range(0, n, n // 4):
+            at = slice(lo, lo + n // 4)
+            assert torch.equal(ps[i][at], ps[0][at]) and torch.equal(codes[i, at], codes[0, at]), (i, lo)
