@@ -695,10 +695,9 @@ ttt_status ttt_linear_attention(const ttt_linear* linear, const ttt_rows* q, con
  *            heads); zero in rows that no sequence claims
  *   d_state0 out, fp32: the gradient of S before the first token, or NULL; may
  *            be d_state
- * log_decay and scale get no gradient. Arithmetic as in the forward, for any
- * number of rows. A NaN or an infinity reaches the rows whose gradients depend
- * on it, and where query heads share a state up to 63 rows of dk and dv behind
- * it. */
+ * log_decay and scale get no gradient. Arithmetic as in the forward, with two
+ * bf16 terms for any number of rows. A NaN or an infinity reaches the rows whose
+ * gradients depend on it, and no others. */
 ttt_status ttt_linear_attention_backward_workspace_size(const ttt_linear* linear, size_t* bytes);
 ttt_status ttt_linear_attention_backward(const ttt_linear* linear, const ttt_rows* d_o,
                                          const ttt_rows* q, const ttt_rows* k, const ttt_rows* v,

@@ -198,7 +198,7 @@ __device__ __forceinline__ float power(float lg, int n) { return n == 0 ? 1.f : 
 // A tile on its way: its rows are loaded to registers (get) while the kernel
 // works on others, and written to LDS (put) when their place is free. Rows
 // from `count` on are zero; dir -1 goes backwards; heads count from the first
-// one's. put() tells, if asked, whether a value is infinite or NaN.
+// one's.
 template <bool F32, int W, int NT, int C>
 struct Fetch {
   static constexpr int P = W * Elem<F32>::size / 16, R = NT / P;  // R rows at a time
@@ -225,26 +225,10 @@ struct Fetch {
       }
     }
   }
-  template <bool CHECK>
-  __device__ __forceinline__ bool put(char* tile) const {
+  __device__ __forceinline__ void put(char* tile) const {
     const int r = threadIdx.x / P, c = threadIdx.x % P;
-    uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (CHECK) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // an exponent of all ones carries into the sign's place
-          if constexpr (F32)
-            bits |= (w[e] & 0x7f800000u) + 0x00800000u;
-          else
-            bits |= (w[e] & 0x7f807f80u) + 0x00800080u;
-        }
-      }
-      *reinterpret_cast<uint4*>(tile + Tile<F32, W>::at(r + i * R, c)) = v[i];
-    }
-    return (bits & (F32 ? 0x80000000u : 0x80008000u)) != 0;
+    for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(tile + Tile<F32, W>::at(r + i * R, c)) = v[i];
   }
 };
 
@@ -285,17 +269,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
   __shared__ __attribute__((aligned(16))) char vt[kBytesB];
   __shared__ __attribute__((aligned(16))) char qt[SUMS ? 16 : kBytesA];
   __shared__ __attribute__((aligned(16))) float up_f[C];
-  __shared__ int votes[NW];
-  // A barrier, and whether x holds for any lane.
-  auto any_of = [&](bool x) {
-    if ((threadIdx.x & 63) == 0) votes[threadIdx.x >> 6] = 0;
-    if (x) votes[threadIdx.x >> 6] = 1;
-    lds_barrier();
-    int any = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) any |= votes[w];
-    return __builtin_amdgcn_readfirstlane(any) != 0;
-  };
+  __shared__ __attribute__((aligned(16))) int odd_from[SUMS ? 1 : NW][32];  // see take_odd
   constexpr int NB = RT * (RT + 1) / 2 * PER;  // pieces of a chunk's weights
   __shared__ uint4 shared[SUMS ? 1 : F32 ? 4 * NW : T * NB][64];
   Reader<F32, A> ra;
@@ -525,6 +499,54 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
 #pragma unroll
       for (int kb = 0; kb < C / KB; ++kb) vf[kb] = rb.col(vt, kb, wave);
     };
+    // An infinity or a NaN in v times an earlier row's weight of 0 would be NaN.
+    // Such values become 0 in the wave's columns, whose first rows that held one (C:
+    // none) are kept in LDS. Whether there are any.
+    auto take_odd = [&](uint4(&vf)[C / KB]) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int kb = 0; kb < C / KB; ++kb) {
+        const uint32_t w[4] = {vf[kb].x, vf[kb].y, vf[kb].z, vf[kb].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // (an exponent of all ones carries into the sign's place)
+          bits |= F32 ? (w[e] & 0x7f800000u) + 0x00800000u : (w[e] & 0x7f807f80u) + 0x00800080u;
+      }
+      const bool odd = __any((bits & (F32 ? 0x80000000u : 0x80008000u)) != 0);
+      if (odd) {
+        int first = C;
+#pragma unroll
+        for (int kb = 0; kb < C / KB; ++kb) {
+          uint32_t w[4] = {vf[kb].x, vf[kb].y, vf[kb].z, vf[kb].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int h = 0; h < (F32 ? 1 : 2); ++h) {
+              const uint32_t all = F32 ? 0x7f800000u : h ? 0x7f800000u : 0x7f80u;
+              const int row = KB * kb + (F32 ? e : 8 * (e >> 1) + 2 * (e & 1) + h);
+              if ((w[e] & all) == all) first = min(first, row), w[e] &= F32 ? 0u : h ? 0xffffu : 0xffff0000u;
+            }
+          }
+          vf[kb] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (first < C) first += 4 * hf;  // (rows of the lane's half)
+        first = min(first, __shfl_xor(first, 32));
+        odd_from[SUMS ? 0 : wave][col] = first;
+      }
+      return odd;
+    };
+    // NaN in the columns of x that take_odd found such a value in, from its row on.
+    auto spoil = [&](f32x16_t(&x)[RT]) {
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const int4 n = *reinterpret_cast<const int4*>(&odd_from[SUMS ? 0 : wave][2 * r + 4 * hf]);
+        const int from[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int it = 0; it < RT; ++it)
+            if (32 * it + col >= from[e]) x[it][r + e] = __builtin_nanf("");
+      }
+    };
     // Row tile `it` of a head's outputs.
     auto store = [&](int it, int q_head, const f32x16_t& x, int take) {
       if (32 * it + col >= take) return;
@@ -600,26 +622,13 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       if constexpr (!SUMS) fq.get(a.q, 0, dir, take);
       __builtin_amdgcn_sched_barrier(0);
     };
-    int now = take;
+    const int now = take;
     uint4 vf[C / KB];
     lds_barrier();  // (the tiles' last readers are done)
-    fk.template put<false>(kt);
-    bool odd = fv.template put<!SUMS && !MANY>(vt);
-    if constexpr (!SUMS) fq.template put<false>(qt);
-    if constexpr (!SUMS && !MANY) {
-      if (any_of(odd && now > 1)) {
-        // an infinity or a NaN times a later row's weight of 0 would be NaN:
-        // such a chunk is taken a row at a time
-        now = 1;
-        fk.get(a.k, 0, dir, now);
-        fv.get(a.v, 0, dir, now);
-        fk.template put<false>(kt);
-        fv.template put<false>(vt);
-        lds_barrier();
-      }
-    } else {
-      lds_barrier();
-    }
+    fk.put(kt);
+    fv.put(vt);
+    if constexpr (!SUMS) fq.put(qt);
+    lds_barrier();
     if (now != up_for) {
       set_up(now);
       up_for = now;
@@ -631,6 +640,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       load_v(vf);
       if constexpr (!SUMS) {
         f32x16_t x[RT];
+        const bool odd = take_odd(vf);
         int h = 0;
         for (; h + 1 < q_heads; ++h) {
           fq.get(a.q, h + 1, dir, now);
@@ -641,8 +651,9 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
           for (int t = 0; t < AT; ++t) asm volatile("" : "+v"(st[t]));
           weights_and_state(true, x);
           lds_barrier();
-          fq.template put<false>(qt);
+          fq.put(qt);
           take_weights(vf, x);
+          if (odd) spoil(x);
 #pragma unroll
           for (int it = 0; it < RT; ++it) store(it, h, x[it], now);
           lds_barrier();
@@ -651,6 +662,7 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
         weights_and_state(true, x);
         lds_barrier();
         take_weights(vf, x);
+        if (odd) spoil(x), load_v(vf);
 #pragma unroll
         for (int it = 0; it < RT; ++it) store(it, h, x[it], now);
       } else {
@@ -675,15 +687,17 @@ __global__ __launch_bounds__(NW * 64, A == 256 ? 1 : 2) void chunk_kernel(Roles 
       for (int h = 0; h < k_heads; ++h) {
         if (h > 0) {
           lds_barrier();
-          fk.template put<false>(kt);
-          fv.template put<false>(vt);
+          fk.put(kt);
+          fv.put(vt);
           lds_barrier();
         }
         load_v(vf);
         if constexpr (!SUMS) {
+          const bool odd = take_odd(vf);
           weights_and_state(false, x);
           lds_barrier();
           take_weights(vf, x);
+          if (odd) spoil(x), load_v(vf);
         }
         const int more = h + 1 < k_heads ? now : 0;
         fk.get(a.k, h + 1, dir, more);
