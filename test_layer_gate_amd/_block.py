@@ -362,7 +362,7 @@ def linear_attention_backward(do, q, k, v, log_decay, *, state=None, d_state=Non
     returned where state, d_state or d_state0 is given; it may be d_state. Rows that
     no sequence claims have gradients of zero."""
     desc, sizes, rq, rk, rv = _linear_desc(q, k, v, log_decay, q_starts, max_new, scale,
-                                           state if state is not None else d_state)
+                                           next((s for s in (state, d_state, d_state0) if s is not None), None))
     _alone(q, do, k, v, log_decay, q_starts, state, d_state, d_state0)
     batch, n, _, _, hk, hq, dk, dv = sizes
     rdo = _s._rows(do, "do", n, dv, q.dtype)

@@ -1,0 +1,25 @@
+"""CPU-only: more calls that the Python entry points of norms, linear attention
+and AdamW take or refuse by themselves (nothing is launched, see
+test_block_checks)."""
+import pytest
+
+from test_block_checks import BF, F32, I32, U8, bl, gpu, lib  # noqa: F401
+
+
+def gradients(**kw):
+    a = dict(do=gpu(12, 4, 128), q=gpu(12, 4, 64), k=gpu(12, 2, 64), v=gpu(12, 2, 128), log_decay=gpu(2, dtype=F32))
+    a.update(kw)
+    return bl.linear_attention_backward(**a)
+
+
+def test_sequences_are_known_from_the_state_gradient(lib):  # noqa: F811
+    """Each of three may be the one state that is given."""
+    s = gpu(3, 2, 64, 128, dtype=F32)
+    for kw in (dict(state=s), dict(d_state=s), dict(d_state0=s)):
+        out = gradients(**kw)
+        assert out[3].shape == s.shape and (out[3] is s) == ("d_state0" in kw)
+    assert lib.calls == ["ttt_linear_attention_backward"] * 3
+    for kw in (dict(state=s, d_state0=gpu(1, 2, 64, 128, dtype=F32)), dict(d_state0=gpu(5, 2, 64, 128, dtype=F32))):
+        with pytest.raises(ValueError):
+            gradients(**kw)
+    assert len(lib.calls) == 3
