@@ -246,6 +246,8 @@ def block_norm_backward(dr, dh, r, f=None, *, post=None, pre=None, gate=None, sc
     has_pre, wpre, kind = _weight(pre, "pre", d, kind)
     if has_pre and (dh is None or r is None):
         raise ValueError("pre needs dh and r")
+    if dh is not None and not has_pre:
+        raise ValueError("dh without pre")
     gates, rgate = _gate_view(gate, rows, d, act)
     desc = _norm_desc(rows, d, gates, act, res, kind, has_post, has_pre, scale, eps)
     rdr = None if dr is None else _pack_view(dr, "dr", rows, d, res)

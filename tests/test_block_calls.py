@@ -23,3 +23,14 @@ def test_sequences_are_known_from_the_state_gradient(lib):  # noqa: F811
         with pytest.raises(ValueError):
             gradients(**kw)
     assert len(lib.calls) == 3
+
+
+def test_a_gradient_that_would_be_left_out_is_refused(lib):  # noqa: F811
+    x = gpu(4, 64)
+    for pre in (None, False):
+        with pytest.raises(ValueError, match="dh without pre"):
+            bl.block_norm_backward(x, x, x, x, pre=pre)
+    assert not lib.calls
+    bl.block_norm_backward(x, x, x, x, pre=True)
+    bl.block_norm_backward(x, None, x, x)
+    assert lib.calls == ["ttt_block_norm_backward"] * 2
