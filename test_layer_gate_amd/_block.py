@@ -453,6 +453,7 @@ def adamw_step(params, grads, state, *, lr, step, betas=(0.9, 0.999), eps=1e-8, 
         raise ValueError("state must be a contiguous uint8 tensor on the current GPU")
     lr, plr = _scalar(lr, "lr", torch.float32)
     step, pstep = _scalar(step, "step", torch.int32)
+    step = operator.index(step)  # (a TypeError for what is no whole number)
     pnorm = 0 if norm is None else _scalar(norm, "norm", torch.float32)[1]
     if norm is not None and not pnorm:
         raise ValueError("norm must be on the GPU")

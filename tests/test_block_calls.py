@@ -34,3 +34,14 @@ def test_a_gradient_that_would_be_left_out_is_refused(lib):  # noqa: F811
     bl.block_norm_backward(x, x, x, x, pre=True)
     bl.block_norm_backward(x, None, x, x)
     assert lib.calls == ["ttt_block_norm_backward"] * 2
+
+
+@pytest.mark.parametrize("step", [1.0, "1", None])
+def test_a_step_is_a_whole_number(lib, step):  # noqa: F811
+    p, g, s = [gpu(7)], [gpu(7, dtype=F32)], gpu(4096, dtype=U8)
+    with pytest.raises(TypeError):
+        bl.adamw_step(p, g, s, lr=1e-3, step=step)
+    assert not lib.calls
+    bl.adamw_step(p, g, s, lr=1e-3, step=gpu(1, dtype=I32))
+    bl.adamw_step([gpu(7, dtype=BF)], g, s, lr=1e-3, step=True)
+    assert len(lib.calls) == 2
