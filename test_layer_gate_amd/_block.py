@@ -427,6 +427,12 @@ def adamw_state_size(sizes, bits=32) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=256)  # of sizes alone
+def _state_bytes(sizes, bits):
+    """adamw_state_size, without a call for every step (0 for bits that the library refuses)."""
+    return sum([-(-n // 256) for n in sizes]) * {32: 256 * 8, 8: 256 * 2 + 8}.get(bits, 0)
+
+
 def adamw_state(params, bits=32):
     """Fresh states of adamw_step for `params`: a uint8 buffer of zeros."""
     params = list(params)
@@ -451,6 +457,9 @@ def adamw_step(params, grads, state, *, lr, step, betas=(0.9, 0.999), eps=1e-8, 
     pm = [0] * n if masters is None else _list(masters, "masters", torch.float32, sizes)[0]
     if state.dtype is not torch.uint8 or state.get_device() != torch.cuda.current_device() or not state.is_contiguous():
         raise ValueError("state must be a contiguous uint8 tensor on the current GPU")
+    need = _state_bytes(tuple(sizes), bits)
+    if state.nbytes != need and need:  # (a larger one would be other tensors', or of other bits)
+        raise ValueError(f"state must be adamw_state(params, {bits}), of {need} bytes")
     lr, plr = _scalar(lr, "lr", torch.float32)
     step, pstep = _scalar(step, "step", torch.int32)
     step = operator.index(step)  # (a TypeError for what is no whole number)

@@ -38,10 +38,29 @@ def test_a_gradient_that_would_be_left_out_is_refused(lib):  # noqa: F811
 
 @pytest.mark.parametrize("step", [1.0, "1", None])
 def test_a_step_is_a_whole_number(lib, step):  # noqa: F811
-    p, g, s = [gpu(7)], [gpu(7, dtype=F32)], gpu(4096, dtype=U8)
+    p, g, s = [gpu(7)], [gpu(7, dtype=F32)], gpu(2048, dtype=U8)
     with pytest.raises(TypeError):
         bl.adamw_step(p, g, s, lr=1e-3, step=step)
     assert not lib.calls
     bl.adamw_step(p, g, s, lr=1e-3, step=gpu(1, dtype=I32))
     bl.adamw_step([gpu(7, dtype=BF)], g, s, lr=1e-3, step=True)
     assert len(lib.calls) == 2
+
+
+def test_a_state_of_other_tensors_or_bits_is_refused(lib):  # noqa: F811
+    p, g = [gpu(300), gpu(7)], [gpu(300, dtype=F32), gpu(7, dtype=F32)]
+    for bits, each in ((32, 2048), (8, 520)):
+        s = gpu(3 * each, dtype=U8)
+        bl.adamw_step(p, g, s, lr=1e-3, step=1, bits=bits)
+        for q, h in ((p[:1], g[:1]), (p[1:], g[1:]), (p + p, g + g)):
+            with pytest.raises(ValueError, match="state must be"):
+                bl.adamw_step(q, h, s, lr=1e-3, step=1, bits=bits)
+        with pytest.raises(ValueError, match="state must be"):
+            bl.adamw_step(p, g, s, lr=1e-3, step=1, bits=40 - bits)
+    assert lib.calls == ["ttt_adamw_step"] * 2
+
+
+@pytest.mark.parametrize("sizes", [(), (0,), (1, 256, 257), (5000, 0, 7, 2048)])
+def test_state_sizes_are_the_librarys(sizes):
+    for bits in (8, 32):
+        assert bl._state_bytes(sizes, bits) == bl.adamw_state_size(sizes, bits)
