@@ -51,6 +51,7 @@ class DecoderBlock:
         """x [batch, T, d] -> x1 = x + attention and norm(x1), the T tokens appended."""
         B, T, d = x.shape
         h, g, D = self.heads, self.kv_heads, self.dim
+        x = x.contiguous()  # (of several sequences' segments, rows that are not evenly apart)
         n = ttt.block_norm(x, pre=True)[1]
         qkv = (n.reshape(B * T, d) @ self.Wqkv).reshape(B * T, h + 2 * g, D)
         q, k, v = qkv[:, :h], qkv[:, h:h + g], qkv[:, h + g:]
