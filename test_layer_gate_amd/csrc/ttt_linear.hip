@@ -988,16 +988,20 @@ bool linear_by_token(const LinearLaunch& a) {
 constexpr int kFewRows = 32;
 
 // Parts of the sequences: as many workgroups as have a place at once, two a
-// compute unit (of two waves for dim_v 64, else of four), of a chunk at least. The
-// parts' states cost a read or write of their own each, so that the gradients,
-// whose launches have two or three roles, take half as many. Measured, us:
-//   64k rows, 8/32 heads of 128:  512 parts 377, 256 418;  dim 64: 1024 parts 104, 512 115
-//   gradients of 2 x 8k rows, 16 heads of 128: 512 312, 256 292, 128 322
-//   2048 rows, 8/32 heads: parts of one chunk 35, of two 38, of four 54
+// compute unit (of two waves for dim_v 64, else of four; one where dim_k is 256 and
+// the state takes the registers of two), of a chunk at least. The parts' states
+// cost a read or write of their own each, so that the gradients, whose launches
+// have two or three roles, take half as many, whatever the heads. Measured, us:
+//   64k rows, 8/32 heads of 128:          1024 parts 477, 512 457, 256 510
+//   4 x 8k rows, 16 heads of 64:          2048 parts 120, 1024 118, 512 123
+//   8k rows, 4 heads of 256:              512 parts 112, 256 90, 128 116
+//   gradients of 2 x 8k rows, 16 of 128:  512 parts 305, 256 285, 128 317
+//   gradients of 8k rows, 4/16 of 256:    256 parts 394, 128 494
+//   2048 rows, 8/32 heads of 128: parts of one chunk 37, of two 43, of four 66
 void linear_parts(LinearLaunch* a, bool back) {
   const int rows = a->f32 ? 32 : 64;
   const int64_t states = (int64_t)a->batch * a->kv_heads * slices_of(a->dv);
-  const int64_t places = (a->dv == 64 ? 1024 : 512) / (back ? 2 : 1);
+  const int64_t places = (a->dv == 64 ? 1024 : 512) / (back || a->dk == 256 ? 2 : 1);
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(places / states, a->max_new / rows));
   a->part_rows = (int)((((int64_t)a->max_new + parts - 1) / parts + rows - 1) / rows * rows);
   a->parts = (int)(((int64_t)a->max_new + a->part_rows - 1) / a->part_rows);
