@@ -237,13 +237,14 @@ struct Fetch {
 // are fetched ahead, and of the rows that leave, would stand in the way of each.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Bound by memory. A second pass over k and v, and the parts' states, are what a
-// parallel form reads beyond the operator's own rows: 64k rows of 8/32 heads of
-// 128 take 377 us for 1.74 GB, 4.6 TB/s; the gradients of 2 x 8k rows of 16 heads
-// 291 us for 1.2 GB, with the rows that several roles read in the caches. Beside
-// it a chunk of 64 rows waits, of 12400 cycles, 1800 for its tiles and their way to
-// LDS, 1500 to issue the next loads; weights and the product with the state take
-// 1800, the update 3600, with the matrix unit busy for a third of it.
+// Bound by the chain of a chunk's products, one after the other in a wave, with two
+// waves a SIMD. 64k rows of 8/32 heads of 128 take 433 us, 87 of them the parts' sums:
+// the outputs' launch keeps the matrix unit busy for 37% of its time and the vector
+// unit for 36%, and its waves wait for their turn at either for 45% of theirs, for
+// memory and barriers for 24%. Memory: 1.74 GB with the second pass over k and v and
+// the parts' states, which a parallel form reads beyond the operator's own rows, 4.0
+// TB/s; the sums 3.4 TB/s. The gradients of 2 x 8k rows of 16 heads take 278 us (matrix
+// unit 34%, vector unit 35%), with the rows that several roles read in the caches.
 //
 // One part of a sequence's rows for one state head and a slice of NW * 32 of
 // the B columns; wave w has columns 32 w .. of the slice, with its part of the
