@@ -193,8 +193,9 @@ def block_norm(x, f=None, *, post=None, pre=None, gate=None, scale=1.0, eps=1e-6
     norm, and h the RMS norm of r. x: the residual stream [..., d]; f: what the
     block added to it, likewise (None: h of x alone, r is None). post, pre: the
     norms' weights [d], True for a norm without one, None for no norm (pre:
-    None: h is None). gate: [..., d] of one, of rows / n, or of all rows. r and
-    h may be given; r may be x."""
+    None: h is None). gate: [..., d] of one row, of all rows, or of rows / n, each
+    for n rows that follow each other (a gate a sequence; it does not broadcast
+    over sequences). r and h may be given; r may be x."""
     rows, d, stride = _row_view(x, "x")
     act = x.dtype if f is None else f.dtype
     if f is None and h is not None:
